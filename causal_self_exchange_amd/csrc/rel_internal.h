@@ -132,6 +132,50 @@ constexpr int kDecodeChunk = 256;
 // states (B * H * ceil(L_cap / 256) * (d_h + 2) floats must fit).
 constexpr size_t kDecodeScratchBytes = REL_DECODE_SCRATCH_BYTES;
 
+// Paged Relation Cache: pages [n_pages][H_kv][page][d_h], page = 1 << page_shift.
+struct PageMapArgs {
+  const int32_t* len;
+  const int32_t* n_new;
+  int32_t* table;       // [S][max_pages]
+  int32_t* free_pages;  // [F]
+  const int32_t* n_free;
+  int32_t* n_free_out;
+  int32_t* cu;          // [S + 1]
+  int32_t* total;       // [S]
+  int32_t* slot;        // [N]
+  int32_t* pos;         // [N]
+  int S, N, F, max_pages, page_shift, n_pages;
+};
+
+struct PagedAppendArgs {
+  const void* P1;       // may be null (with P1o)
+  const void* P2;
+  const void* I;
+  int64_t ld1, ld2, ldi;
+  const int32_t* slot;
+  const int32_t* pos;
+  void* P1o;
+  void* cP2;
+  void* cV;
+  int N, H, H_kv, d_h, n_pages, page_shift;
+  int rope, pairing, mix;   // as in PrestepArgs
+};
+
+struct PagedArgs {
+  const void* P1;
+  int64_t ld1;
+  const void* cP2;
+  const void* cV;
+  const int32_t* table;
+  const int32_t* total;
+  const int32_t* cu;
+  void* Y;
+  void* ws;
+  int N, S, H, H_kv, d_h, n_pages, page_shift, max_pages, max_new;
+};
+
+inline size_t paged_ws_bytes(int64_t, int) { return 256; }
+
 // Launchers (return the hipError_t of the launch).
 hipError_t launch_fwd_scan(const FwdArgs& a, const HeadParams& hp, bool bf16, hipStream_t s);
 // Compute units of the current device (queried once per device, then cached:
@@ -169,5 +213,8 @@ hipError_t launch_decode(const DecodeArgs& a, const HeadParams& hp, bool bf16, h
 hipError_t decode_scratch(void** ptr);
 hipError_t launch_cache_append(void* cP2, void* cV, int32_t* len, const void* p2, const void* v,
                                int B, int H, int L_cap, int d_h, bool bf16, hipStream_t s);
+hipError_t launch_page_map(const PageMapArgs& a, hipStream_t s);
+hipError_t launch_paged_append(const PagedAppendArgs& a, const PrestepParams& pp, bool bf16, hipStream_t s);
+hipError_t launch_paged(const PagedArgs& a, const HeadParams& hp, bool bf16, hipStream_t s);
 
 }  // namespace rel

@@ -122,6 +122,27 @@ bool use_bwd_mfma(rel_dtype dt, int d_h, int T) {
 
 size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
+bool prestep_modes_ok(rel_rope rope, float rope_base, const float* theta, rel_pairing pairing, int H) {
+  if (rope != REL_ROPE_NONE && rope != REL_ROPE_INTERLEAVED && rope != REL_ROPE_HALF) return false;
+  if (pairing != REL_PAIRS_A && pairing != REL_PAIRS_B) return false;
+  if (rope != REL_ROPE_NONE && !(std::isfinite(rope_base) && rope_base > 1.0f)) return false;
+  if (theta)
+    for (int k = 0; k < H / 2; ++k)
+      if (!std::isfinite(theta[k])) return false;
+  return true;
+}
+
+// Rotary frequencies and Givens factors of H information heads.
+void fill_prestep_params(rel::PrestepParams& pp, float rope_base, const float* theta, int H, int d_h) {
+  for (int k = 0; k < 64; ++k)
+    pp.inv_freq[k] = k < d_h / 2 ? std::pow(static_cast<double>(rope_base), -2.0 * k / d_h) : 0.0;
+  for (int k = 0; k < 128; ++k) {
+    const double t = (theta && k < H / 2) ? static_cast<double>(theta[k]) : 0.0;
+    pp.cos_theta[k] = static_cast<float>(std::cos(t));
+    pp.sin_theta[k] = static_cast<float>(std::sin(t));
+  }
+}
+
 // Validates a pre-step call and fills its launch arguments (no HIP call).
 rel_status prestep_setup(rel::PrestepArgs& a, rel::PrestepParams& pp, const void* P1, const void* P2,
                          const void* I, const int32_t* pos0, rel_rope rope, float rope_base,
@@ -133,12 +154,7 @@ rel_status prestep_setup(rel::PrestepArgs& a, rel::PrestepParams& pp, const void
   if (theta && (H % 2 != 0)) return REL_E_SHAPE;
   if (!dtype_ok(dt)) return REL_E_DTYPE;
   if (!fwd_head_dim_ok(d_h)) return REL_E_HEADDIM;
-  if (rope != REL_ROPE_NONE && rope != REL_ROPE_INTERLEAVED && rope != REL_ROPE_HALF) return REL_E_PRESTEP;
-  if (pairing != REL_PAIRS_A && pairing != REL_PAIRS_B) return REL_E_PRESTEP;
-  if (rope != REL_ROPE_NONE && !(std::isfinite(rope_base) && rope_base > 1.0f)) return REL_E_PRESTEP;
-  if (theta)
-    for (int k = 0; k < H / 2; ++k)
-      if (!std::isfinite(theta[k])) return REL_E_PRESTEP;
+  if (!prestep_modes_ok(rope, rope_base, theta, pairing, H)) return REL_E_PRESTEP;
   if (!aligned16(P1) || !aligned16(P2) || !aligned16(I) || !aligned16(P1o) || !aligned16(P2o) ||
       !aligned16(Io) || (reinterpret_cast<uintptr_t>(pos0) & 3u))
     return REL_E_ALIGN;
@@ -156,19 +172,156 @@ rel_status prestep_setup(rel::PrestepArgs& a, rel::PrestepParams& pp, const void
   }
   a = rel::PrestepArgs{P1, P2, I, pos0, P1o, P2o, Io, B, H, T, d_h, static_cast<int>(rope),
                        pairing == REL_PAIRS_A ? 0 : 1, theta ? 1 : 0};
-  for (int k = 0; k < 64; ++k)
-    pp.inv_freq[k] = k < d_h / 2 ? std::pow(static_cast<double>(rope_base), -2.0 * k / d_h) : 0.0;
-  for (int k = 0; k < 128; ++k) {
-    const double t = (theta && k < H / 2) ? static_cast<double>(theta[k]) : 0.0;
-    pp.cos_theta[k] = static_cast<float>(std::cos(t));
-    pp.sin_theta[k] = static_cast<float>(std::sin(t));
-  }
+  fill_prestep_params(pp, rope_base, theta, H, d_h);
   return REL_OK;
+}
+
+// ---- paged Relation Cache ----------------------------------------------------
+
+struct Range { const void* p; size_t n; };
+
+// Whether any output range overlaps an input range or another output range
+// (empty ranges, of optional arguments, overlap nothing).
+template <size_t NI, size_t NO>
+bool any_alias(const Range (&ins)[NI], const Range (&outs)[NO]) {
+  for (size_t x = 0; x < NO; ++x) {
+    if (!outs[x].n) continue;
+    for (const Range& i : ins)
+      if (i.n && overlaps(outs[x].p, outs[x].n, i.p, i.n)) return true;
+    for (size_t y = x + 1; y < NO; ++y)
+      if (outs[y].n && overlaps(outs[x].p, outs[x].n, outs[y].p, outs[y].n)) return true;
+  }
+  return false;
+}
+
+// log2 of a supported page size, or -1.
+int page_shift_of(int page_size) {
+  for (int sh = 4; sh <= 8; ++sh)
+    if (page_size == 1 << sh) return sh;
+  return -1;
+}
+
+// Rows and table widths are counted in 32 bits on the device.
+bool page_counts_ok(int64_t n_pages, int page_size) {
+  return n_pages >= 1 && page_shift_of(page_size) >= 0 && n_pages * page_size < (int64_t(1) << 31);
+}
+
+bool stride_ok(int64_t ld, int64_t heads, int d_h, size_t es) {
+  return ld >= heads * d_h && ld % static_cast<int64_t>(16 / es) == 0 && ld < (int64_t(1) << 31);
+}
+
+// Bytes from the first to the last element of N tokens of stride ld.
+size_t strided_bytes(int64_t N, int64_t ld, int64_t heads, int d_h, size_t es) {
+  return static_cast<size_t>((N - 1) * ld + heads * d_h) * es;
 }
 
 }  // namespace
 
 extern "C" {
+
+rel_status relation_page_map(const int32_t* len, const int32_t* n_new, int32_t* block_table,
+                             int32_t* free_pages, const int32_t* n_free, int32_t* n_free_out, int32_t* cu,
+                             int32_t* total, int32_t* slot, int32_t* pos, int S, int N, int F, int max_pages,
+                             int page_size, int n_pages, hipStream_t stream) {
+  if (!len || !n_new || !block_table || !free_pages || !n_free || !n_free_out || !cu || !total || !slot || !pos)
+    return REL_E_NULL;
+  int64_t n = 0;
+  if (S < 1 || S > 65535 || N < 1 || F < 1) return REL_E_SHAPE;
+  if (!page_counts_ok(n_pages, page_size) || !page_counts_ok(max_pages, page_size)) return REL_E_PAGE;
+  if (!count(n, {S, max_pages})) return REL_E_SHAPE;
+  const void* all[] = {len, n_new, block_table, free_pages, n_free, n_free_out, cu, total, slot, pos};
+  for (const void* p : all)
+    if (!aligned4(p)) return REL_E_ALIGN;
+  const size_t sb = static_cast<size_t>(S) * 4, nb = static_cast<size_t>(N) * 4;
+  // n_free_out may be n_free (in place).
+  const Range ins[] = {{len, sb}, {n_new, sb}, {n_free, n_free_out == n_free ? 0u : 4u}};
+  const Range outs[] = {{block_table, static_cast<size_t>(n) * 4}, {free_pages, static_cast<size_t>(F) * 4},
+                        {n_free_out, 4}, {cu, sb + 4}, {total, sb}, {slot, nb}, {pos, nb}};
+  if (any_alias(ins, outs)) return REL_E_ALIAS;
+  const rel::PageMapArgs a{len, n_new, block_table, free_pages, n_free, n_free_out, cu, total, slot, pos,
+                           S, N, F, max_pages, page_shift_of(page_size), n_pages};
+  return rel::launch_page_map(a, stream) == hipSuccess ? REL_OK : REL_E_LAUNCH;
+}
+
+rel_status relation_paged_append(const void* P1, const void* P2, const void* I, int64_t ld1, int64_t ld2,
+                                 int64_t ldi, const int32_t* slot, const int32_t* pos, rel_rope rope,
+                                 float rope_base, const float* theta, rel_pairing pairing, void* P1o,
+                                 void* cache_P2, void* cache_V, int N, int H, int H_kv, int d_h, int n_pages,
+                                 int page_size, rel_dtype dt, hipStream_t stream) {
+  if (!P2 || !I || !slot || !cache_P2 || !cache_V || !P1 != !P1o || (!pos && rope != REL_ROPE_NONE))
+    return REL_E_NULL;
+  if (!P1) H = 0;
+  int64_t nc = 0;
+  if (N < 1 || (P1 && H < 1) || H > REL_MAX_HEADS || H_kv < 1 || H_kv > REL_MAX_HEADS) return REL_E_SHAPE;
+  if (theta && H_kv % 2 != 0) return REL_E_SHAPE;
+  if (!dtype_ok(dt)) return REL_E_DTYPE;
+  if (!fwd_head_dim_ok(d_h)) return REL_E_HEADDIM;
+  if (!page_counts_ok(n_pages, page_size)) return REL_E_PAGE;
+  if (!count(nc, {n_pages, H_kv, page_size, d_h})) return REL_E_SHAPE;
+  const size_t es = elem_size(dt);
+  if ((P1 && !stride_ok(ld1, H, d_h, es)) || !stride_ok(ld2, H_kv, d_h, es) || !stride_ok(ldi, H_kv, d_h, es))
+    return REL_E_STRIDE;
+  if (!prestep_modes_ok(rope, rope_base, theta, pairing, H_kv)) return REL_E_PRESTEP;
+  if (!aligned16(P1) || !aligned16(P2) || !aligned16(I) || !aligned16(P1o) || !aligned16(cache_P2) ||
+      !aligned16(cache_V) || !aligned4(slot) || !aligned4(pos))
+    return REL_E_ALIGN;
+  const bool in_place = P1 && P1o == P1 && ld1 == static_cast<int64_t>(H) * d_h;
+  const size_t nb = static_cast<size_t>(N) * 4, cb = static_cast<size_t>(nc) * es;
+  const Range ins[] = {{P1, P1 && !in_place ? strided_bytes(N, ld1, H, d_h, es) : 0},
+                       {P2, strided_bytes(N, ld2, H_kv, d_h, es)},
+                       {I, strided_bytes(N, ldi, H_kv, d_h, es)},
+                       {slot, nb}, {pos, pos ? nb : 0}};
+  const Range outs[] = {{P1o, P1 ? static_cast<size_t>(N) * H * d_h * es : 0}, {cache_P2, cb}, {cache_V, cb}};
+  if (any_alias(ins, outs)) return REL_E_ALIAS;
+  rel::PrestepParams pp;
+  fill_prestep_params(pp, rope_base, theta, H_kv, d_h);
+  const rel::PagedAppendArgs a{P1, P2, I, ld1, ld2, ldi, slot, pos, P1o, cache_P2, cache_V, N, H, H_kv, d_h,
+                               n_pages, page_shift_of(page_size), static_cast<int>(rope),
+                               pairing == REL_PAIRS_A ? 0 : 1, theta ? 1 : 0};
+  return rel::launch_paged_append(a, pp, dt == REL_BF16, stream) == hipSuccess ? REL_OK : REL_E_LAUNCH;
+}
+
+size_t relation_paged_workspace_bytes(int N, int S, int H, int H_kv, int d_h) {
+  if (N < 1 || S < 1 || S > 65535 || H < 1 || H > REL_MAX_HEADS || H_kv < 1 || H % H_kv != 0 ||
+      !fwd_head_dim_ok(d_h))
+    return 0;
+  return rel::paged_ws_bytes(S, d_h);
+}
+
+rel_status relation_paged_fwd(const void* P1, int64_t ld1, const void* cache_P2, const void* cache_V,
+                              const int32_t* block_table, const int32_t* total, const int32_t* cu,
+                              const float* tau_s, float lambda, void* Y, int N, int S, int H, int H_kv,
+                              int d_h, int n_pages, int page_size, int max_pages, int max_new, rel_dtype dt,
+                              void* workspace, size_t ws_bytes, hipStream_t stream) {
+  if (!P1 || !cache_P2 || !cache_V || !block_table || !total || !cu || !tau_s || !Y) return REL_E_NULL;
+  int64_t nc = 0, ny = 0, nt = 0;
+  if (N < 1 || S < 1 || S > 65535 || H < 1 || H > REL_MAX_HEADS || H_kv < 1 || max_new < 1) return REL_E_SHAPE;
+  if (H % H_kv != 0) return REL_E_GROUP;
+  if (!dtype_ok(dt)) return REL_E_DTYPE;
+  if (!fwd_head_dim_ok(d_h)) return REL_E_HEADDIM;
+  if (!page_counts_ok(n_pages, page_size) || !page_counts_ok(max_pages, page_size)) return REL_E_PAGE;
+  if (!count(nc, {n_pages, H_kv, page_size, d_h}) || !count(ny, {N, H, d_h}) || !count(nt, {S, max_pages}))
+    return REL_E_SHAPE;
+  HeadParams hp;
+  const rel_status st = pack_heads(hp, tau_s, H, d_h, lambda);
+  if (st != REL_OK) return st;
+  const size_t es = elem_size(dt);
+  if (!stride_ok(ld1, H, d_h, es)) return REL_E_STRIDE;
+  const size_t need = relation_paged_workspace_bytes(N, S, H, H_kv, d_h);
+  if (!workspace || ws_bytes < need) return REL_E_WORKSPACE;
+  if (!aligned16(P1) || !aligned16(cache_P2) || !aligned16(cache_V) || !aligned16(Y) || !aligned16(workspace) ||
+      !aligned4(block_table) || !aligned4(total) || !aligned4(cu))
+    return REL_E_ALIGN;
+  const size_t cb = static_cast<size_t>(nc) * es;
+  const Range ins[] = {{P1, strided_bytes(N, ld1, H, d_h, es)}, {cache_P2, cb}, {cache_V, cb},
+                       {block_table, static_cast<size_t>(nt) * 4}, {total, static_cast<size_t>(S) * 4},
+                       {cu, static_cast<size_t>(S) * 4 + 4}};
+  const Range outs[] = {{Y, static_cast<size_t>(ny) * es}, {workspace, need}};
+  if (any_alias(ins, outs)) return REL_E_ALIAS;
+  const rel::PagedArgs a{P1, ld1, cache_P2, cache_V, block_table, total, cu, Y, workspace, N, S, H, H_kv, d_h,
+                         n_pages, page_shift_of(page_size), max_pages, max_new};
+  return rel::launch_paged(a, hp, dt == REL_BF16, stream) == hipSuccess ? REL_OK : REL_E_LAUNCH;
+}
 
 const char* relation_status_str(rel_status s) {
   switch (s) {
@@ -185,6 +338,9 @@ const char* relation_status_str(rel_status s) {
     case REL_E_LAUNCH: return "kernel launch failed";
     case REL_E_PRESTEP: return "invalid rotary mode, base, pairing or Givens angle";
     case REL_E_KERNEL: return "unknown kernel selection";
+    case REL_E_PAGE: return "page size, page count or table width not supported";
+    case REL_E_GROUP: return "H is not a multiple of H_kv";
+    case REL_E_STRIDE: return "token stride too small or not a multiple of 16 bytes";
   }
   return "unknown status";
 }
@@ -302,7 +458,6 @@ rel_status relation_linear_fwd(const void* P1, const void* P2, const void* I, co
   const size_t tb = static_cast<size_t>(n) * elem_size(dt);
   const size_t ab = static_cast<size_t>(n) * sizeof(float);
   const size_t sb = static_cast<size_t>(B) * H * d_h * d_h * sizeof(float);
-  struct Range { const void* p; size_t n; };
   const Range ins[] = {{P1, tb}, {P2, tb}, {I, tb}, {alpha, ab}};
   const Range outs[] = {{Y, tb}, {state_out, state_out ? sb : 0}, {workspace, need}};
   for (const Range& o : outs)
@@ -367,7 +522,6 @@ rel_status relation_bwd(const void* P1, const void* P2, const void* V, const flo
     return REL_E_ALIGN;
   const size_t tb = static_cast<size_t>(n) * elem_size(dt);
   const size_t lb = static_cast<size_t>(B) * H * T * sizeof(float);
-  struct Range { const void* p; size_t n; };
   const Range ins[] = {{P1, tb}, {P2, tb}, {V, tb}, {Y, tb}, {LSE, lb}, {dY, tb}};
   const Range outs[] = {{dP1, tb}, {dP2, tb}, {dV, tb}, {dtau, H * sizeof(float)},
                         {dlambda, sizeof(float)}, {workspace, need}};

@@ -67,6 +67,17 @@ def lib() -> ctypes.CDLL:
         L.relation_decode_noalloc.restype = i
         L.relation_cache_append.argtypes = [vp, vp, vp, vp, vp, i, i, i, i, i, vp]
         L.relation_cache_append.restype = i
+        l64 = ctypes.c_int64
+        L.relation_page_map.argtypes = [vp] * 10 + [i] * 6 + [vp]
+        L.relation_page_map.restype = i
+        L.relation_paged_append.argtypes = [vp, vp, vp, l64, l64, l64, vp, vp, i, f, fp, i, vp, vp, vp,
+                                            i, i, i, i, i, i, i, vp]
+        L.relation_paged_append.restype = i
+        L.relation_paged_workspace_bytes.argtypes = [i, i, i, i, i]
+        L.relation_paged_workspace_bytes.restype = sz
+        L.relation_paged_fwd.argtypes = [vp, l64, vp, vp, vp, vp, vp, fp, f, vp, i, i, i, i, i, i, i, i, i, i,
+                                         vp, sz, vp]
+        L.relation_paged_fwd.restype = i
         L.relation_status_str.argtypes = [i]
         L.relation_status_str.restype = ctypes.c_char_p
         L.relation_select_kernels.argtypes = [i, i]
@@ -79,7 +90,8 @@ EXPORTS = ("relation_fwd", "relation_fwd_ex", "relation_fwd_lse", "relation_bwd_
            "relation_bwd_stored_workspace_bytes", "relation_bwd", "relation_prestep", "relation_fwd_model_workspace_bytes",
            "relation_fwd_model", "relation_linear_workspace_bytes", "relation_linear_fwd",
            "relation_decode_workspace_bytes", "relation_decode", "relation_decode_noalloc",
-           "relation_cache_append", "relation_status_str", "relation_select_kernels")
+           "relation_cache_append", "relation_page_map", "relation_paged_append",
+           "relation_paged_workspace_bytes", "relation_paged_fwd", "relation_status_str", "relation_select_kernels")
 
 KERNELS = {"auto": 0, "scan": 1}
 
@@ -155,7 +167,16 @@ class _Args:
             raise ValueError(f"{self.fn}: {name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
         if dtype is not None and t.dtype != dtype:
             raise TypeError(f"{self.fn}: {name} has dtype {t.dtype}, expected {dtype}")
-        self.ts.append((name, t))
+        self.ts.append((name, t, True))
+        return self
+
+    def tokens(self, name, t, shape, dtype):
+        """A packed token tensor [N, heads, d_h]: each token's heads are
+        contiguous, tokens may be further apart (a slice of a fused projection)."""
+        self(name, t, shape, dtype)
+        self.ts[-1] = (name, t, False)
+        if t.stride()[2] != 1 or (t.shape[1] > 1 and t.stride(1) != t.shape[2]):
+            raise ValueError(f"{self.fn}: the heads of each token of {name} must be contiguous")
         return self
 
     def bytes(self, name, t, need: int):
@@ -167,10 +188,10 @@ class _Args:
 
     def done(self):
         dev = None
-        for name, t in self.ts:
+        for name, t, dense in self.ts:
             if not t.is_cuda:
                 raise ValueError(f"{self.fn}: {name} must be a device tensor")
-            if not t.is_contiguous():
+            if dense and not t.is_contiguous():
                 raise ValueError(f"{self.fn}: {name} must be contiguous")
             if dev is None:
                 dev = t.device
@@ -441,3 +462,140 @@ def cache_append(cache_P2, cache_V, lens, p2, v, stream=None):
     st = lib().relation_cache_append(_ptr(cache_P2), _ptr(cache_V), _ptr(lens), _ptr(p2), _ptr(v),
                                      B, H, L_cap, D, _dtype_code(p2), _stream(stream))
     _check("relation_cache_append", st)
+
+
+def _pages(fn, cache_P2):
+    if not isinstance(cache_P2, torch.Tensor) or cache_P2.dim() != 4:
+        raise ValueError(f"{fn}: cache_P2 must be a [n_pages, H_kv, page_size, d_h] tensor")
+    return tuple(cache_P2.shape)
+
+
+class _On:
+    """The tensors' device made current for a call of the paged entry points, and
+    the stream: the caller's, which has to be of that device, or the current one."""
+
+    def __init__(self, fn, t, stream):
+        if stream is not None and stream.device != t.device:
+            raise ValueError(f"{fn}: the stream is on {stream.device}, the tensors on {t.device}")
+        self.guard, self.stream = torch.cuda.device(t.device), stream
+
+    def __enter__(self):
+        self.guard.__enter__()
+        return _stream(self.stream)
+
+    def __exit__(self, *exc):
+        return self.guard.__exit__(*exc)
+
+
+def _ld(t) -> int:
+    """Elements between consecutive tokens of a packed [N, heads, d_h] tensor."""
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+
+
+def page_map(lens, n_new, block_table, free_pages, n_free, N: int, page_size: int, n_pages: int, out=None,
+             stream=None):
+    """Block table, slots and positions of a packed batch of N token rows, from
+    the request lengths: lens, n_new int32[S] (n_new -1: finished, its pages
+    return to the list), block_table int32[S, max_pages] and free_pages int32[F]
+    (both updated in place), n_free int32[1]. Returns (cu [S+1], total [S], slot
+    [N], pos [N], n_free_out [1]); out: the five tensors (n_free_out may be n_free)."""
+    if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
+        raise ValueError("page_map: block_table must be an [S, max_pages] tensor")
+    if not isinstance(free_pages, torch.Tensor) or free_pages.dim() != 1:
+        raise ValueError("page_map: free_pages must be a 1-d tensor")
+    S, width = block_table.shape
+    N, it = int(N), torch.int32
+    a = _Args("page_map")("block_table", block_table, dtype=it)("free_pages", free_pages, dtype=it)
+    a("lens", lens, (S,), it)("n_new", n_new, (S,), it)("n_free", n_free, (1,), it)
+    shapes = ((S + 1,), (S,), (N,), (N,), (1,))
+    if out is not None:
+        if len(out) != 5:
+            raise ValueError("page_map: out must be (cu, total, slot, pos, n_free_out)")
+        for name, t, shp in zip(("cu", "total", "slot", "pos", "n_free_out"), out, shapes):
+            a(name, t, shp, it)
+    a.done()
+    if out is None:
+        out = tuple(torch.empty(max(shp[0], 0), dtype=it, device=lens.device) for shp in shapes)
+    cu, total, slot, pos, n_free_out = out
+    with _On("page_map", lens, stream) as sp:
+        st = lib().relation_page_map(_ptr(lens), _ptr(n_new), _ptr(block_table), _ptr(free_pages), _ptr(n_free),
+                                     _ptr(n_free_out), _ptr(cu), _ptr(total), _ptr(slot), _ptr(pos), S, N,
+                                     free_pages.numel(), width, int(page_size), int(n_pages), sp)
+    _check("relation_page_map", st)
+    return out
+
+
+def paged_append(P2, I, slot, cache_P2, cache_V, P1=None, pos=None, rope="none", rope_base: float = 1e4, theta=None,
+                 pairing="A", out=None, stream=None):
+    """Pre-steps of a packed batch with P2 and the mixed I stored into the pages:
+    P2, I [N, H_kv, d_h] and optionally P1 [N, H, d_h] (tokens may be slices of a
+    fused projection), slot and pos int32[N] (page_map), caches [n_pages, H_kv,
+    page_size, d_h]. Returns the rotated P1 ([N, H, d_h]; out, which may be P1
+    itself if contiguous) or None. Rows of tokens without a slot are not written."""
+    n_pages, Hkv, ps, D = _pages("paged_append", cache_P2)
+    dt = cache_P2.dtype
+    if not isinstance(P2, torch.Tensor) or P2.dim() != 3:
+        raise ValueError("paged_append: P2 must be an [N, H_kv, d_h] tensor")
+    N, H = P2.shape[0], 0
+    a = _Args("paged_append")("cache_P2", cache_P2)("cache_V", cache_V, cache_P2.shape, dt)
+    a.tokens("P2", P2, (N, Hkv, D), dt).tokens("I", I, (N, Hkv, D), dt)
+    a("slot", slot, (N,), torch.int32)("pos", pos, (N,), torch.int32, optional=True)
+    if P1 is not None:
+        if not isinstance(P1, torch.Tensor) or P1.dim() != 3:
+            raise ValueError("paged_append: P1 must be an [N, H, d_h] tensor")
+        H = P1.shape[1]
+        a.tokens("P1", P1, (N, H, D), dt)("out", out, (N, H, D), dt, optional=True)
+    elif out is not None:
+        raise ValueError("paged_append: out is given without P1")
+    a.done()
+    if P1 is not None and out is None:
+        out = torch.zeros((N, H, D), dtype=dt, device=P1.device)   # rows without a token stay zero
+    th_keep, th_p = _theta_arg(theta, Hkv)
+    with _On("paged_append", P2, stream) as sp:
+        st = lib().relation_paged_append(_ptr(P1), _ptr(P2), _ptr(I), 0 if P1 is None else _ld(P1), _ld(P2), _ld(I),
+                                         _ptr(slot), _ptr(pos), ROPE[rope], float(rope_base), th_p, PAIRS[pairing],
+                                         _ptr(out), _ptr(cache_P2), _ptr(cache_V), N, H, Hkv, D, n_pages, ps,
+                                         _dtype_code(cache_P2), sp)
+    del th_keep
+    _check("relation_paged_append", st)
+    return out
+
+
+def paged_workspace_bytes(N: int, S: int, H: int, H_kv: int, d_h: int) -> int:
+    return int(lib().relation_paged_workspace_bytes(N, S, H, H_kv, d_h))
+
+
+def paged_fwd(P1, cache_P2, cache_V, block_table, total, cu, tau, lam: float = 0.0, max_new=None, out=None,
+              workspace=None, stream=None):
+    """Y [N, H, d_h] of a packed batch of new tokens whose own rows are in the
+    pages already: P1 [N, H, d_h] (rotated), caches [n_pages, H_kv, page_size,
+    d_h], block_table int32[S, max_pages], total int32[S], cu int32[S+1]
+    (page_map). max_new: the most new tokens of one request (default N)."""
+    n_pages, Hkv, ps, D = _pages("paged_fwd", cache_P2)
+    dt = cache_P2.dtype
+    if not isinstance(P1, torch.Tensor) or P1.dim() != 3:
+        raise ValueError("paged_fwd: P1 must be an [N, H, d_h] tensor")
+    if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
+        raise ValueError("paged_fwd: block_table must be an [S, max_pages] tensor")
+    N, H = P1.shape[:2]
+    S, width = block_table.shape
+    a = _Args("paged_fwd")("cache_P2", cache_P2)("cache_V", cache_V, cache_P2.shape, dt)
+    a.tokens("P1", P1, (N, H, D), dt)("block_table", block_table, dtype=torch.int32)
+    a("total", total, (S,), torch.int32)("cu", cu, (S + 1,), torch.int32)("out", out, (N, H, D), dt, optional=True)
+    need = paged_workspace_bytes(N, S, H, Hkv, D)
+    if workspace is not None:
+        a.bytes("workspace", workspace, need)
+    a.done()
+    if out is None:
+        out = torch.zeros((N, H, D), dtype=dt, device=P1.device)   # rows without a token stay zero
+    if workspace is None:
+        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=P1.device)
+    tau_keep, tau_p = _tau_arg(tau, H)
+    with _On("paged_fwd", P1, stream) as sp:
+        st = lib().relation_paged_fwd(_ptr(P1), _ld(P1), _ptr(cache_P2), _ptr(cache_V), _ptr(block_table),
+                                      _ptr(total), _ptr(cu), tau_p, float(lam), _ptr(out), N, S, H, Hkv, D, n_pages,
+                                      ps, width, N if max_new is None else int(max_new), _dtype_code(P1),
+                                      _ptr(workspace), workspace.numel(), sp)
+    del tau_keep
+    _check("relation_paged_fwd", st)
+    return out

@@ -28,5 +28,8 @@ hipError_t launch_cache_append(void*, void*, int32_t*, const void*, const void*,
                                hipStream_t) {
   return hipErrorLaunchFailure;
 }
+hipError_t launch_page_map(const PageMapArgs&, hipStream_t) { return hipErrorLaunchFailure; }
+hipError_t launch_paged_append(const PagedAppendArgs&, const PrestepParams&, bool, hipStream_t) { return hipErrorLaunchFailure; }
+hipError_t launch_paged(const PagedArgs&, const HeadParams&, bool, hipStream_t) { return hipErrorLaunchFailure; }
 
 }  // namespace rel

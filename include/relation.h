@@ -1,8 +1,9 @@
 /*
  * relation.h - C ABI of librelation.so: the causal Self-Exchange Relation
  * forward (FlashRelation form), its backward, the model-side pre-steps
- * (RoPE, Givens head mixing), the Linear Relation forward and the Relation
- * Cache decode step on AMD Instinct MI355X (gfx950).
+ * (RoPE, Givens head mixing), the Linear Relation forward, the Relation Cache
+ * decode step and the paged Relation Cache (tables, append, chunk forward) on
+ * AMD Instinct MI355X (gfx950).
  *
  * Operator ("Ask Self, Ask Others: Relation Is All You Need", Eq. (1)-(3)),
  * per batch entry b and head h, for query row i (one-based) of T:
@@ -20,7 +21,8 @@
  *
  * Common conventions
  *   - Tensors are device memory, contiguous row-major [B, H, T, d_h] (forward)
- *     or [B, H, d_h] / [B, H, L_cap, d_h] (decode); all of one dtype.
+ *     or [B, H, d_h] / [B, H, L_cap, d_h] (decode); all of one dtype. The paged
+ *     entry points have layouts of their own (below).
  *   - tau_s is HOST memory, float[H], read during the call (may be freed on
  *     return). Every tau must be finite and > 0 (the paper requires tau_S > 0).
  *   - lambda is the count-calibration coefficient; 0 gives the operator without
@@ -72,7 +74,10 @@ typedef enum {
   REL_E_WORKSPACE = 9, /* workspace missing or smaller than required         */
   REL_E_LAUNCH = 10,   /* a kernel launch failed                             */
   REL_E_PRESTEP = 11,  /* invalid rotary mode / base, pairing or Givens angle */
-  REL_E_KERNEL = 12    /* unknown kernel selection                           */
+  REL_E_KERNEL = 12,   /* unknown kernel selection                           */
+  REL_E_PAGE = 13,     /* page size, page count or table width not supported */
+  REL_E_GROUP = 14,    /* H is not a multiple of H_kv                        */
+  REL_E_STRIDE = 15    /* a token stride is too small or not 16-byte sized   */
 } rel_status;
 
 typedef enum { REL_F32 = 0, REL_BF16 = 1 } rel_dtype;
@@ -351,6 +356,137 @@ rel_status relation_cache_append(void* cache_P2, void* cache_V, int32_t* len,
                                  const void* p2, const void* v, int B, int H,
                                  int L_cap, int d_h, rel_dtype dt,
                                  hipStream_t stream);
+
+/*
+ * ---- The paged Relation Cache ------------------------------------------------
+ *
+ * A cache of pages shared by many requests: cache_P2 and cache_V are device
+ * [n_pages, H_kv, page_size, d_h], page_size one of 16, 32, 64, 128, 256. Row p
+ * (zero-based position) of request b lies in page block_table[b, p / page_size]
+ * at row p % page_size of every head; block_table is device int32[S, max_pages].
+ * The slot of a row is page * page_size + p % page_size.
+ * A batch packs the new tokens of S requests one after another: request b owns
+ * the packed tokens cu[b] .. cu[b+1]-1 (cu device int32[S+1]), and token tensors
+ * are device [N, heads, d_h], N the packed rows (rows behind the last request's
+ * are padding). The H query heads form groups of H / H_kv consecutive heads that
+ * share one cached head (query head h reads cached head h / (H / H_kv)).
+ * One serving step: relation_page_map, relation_paged_append, relation_paged_fwd.
+ * Limits: S <= 65535; N, n_pages * page_size and max_pages * page_size < 2^31.
+ * A request whose device-side numbers are not valid is skipped as each call
+ * describes, and a page number outside [0, n_pages) is never followed: its rows
+ * read as zeros and are not written. Slots must be distinct: of tokens that
+ * name one slot it is not said whose values the slot holds afterwards.
+ */
+
+/*
+ * relation_page_map - block table, slots and positions of a batch, from the
+ * request lengths, and the list of free pages that they are taken from.
+ * First every finished request (n_new = -1) gives the ceil(len / page_size)
+ * pages of its table row back: they go on top of the free list in request
+ * order, page order within a request. Then the others, in request order, take
+ * the ceil((len + n_new) / page_size) - ceil(len / page_size) pages that they
+ * need from the top of the list (free_pages[n_free - 1] first) into their next
+ * table entries. A request is refused, with nothing taken, when a value of its
+ * own does not fit (len or n_new negative, len + n_new > max_pages * page_size,
+ * its packed tokens past N), or when it needs pages and the list does not hold
+ * all that it and the requests before it need (those that fit themselves).
+ *
+ *   len         : in,  device int32[S], cached tokens per request
+ *   n_new       : in,  device int32[S], new tokens (0: none; -1: finished)
+ *   block_table : in/out, device int32[S, max_pages]; only new entries written
+ *   free_pages  : in/out, device int32[F]; entries at and above *n_free are
+ *                 overwritten by returned pages (those past F are dropped)
+ *   n_free      : in,  device int32[1], free pages (clamped into [0, F])
+ *   n_free_out  : out, device int32[1], free pages afterwards; may be n_free
+ *   cu          : out, device int32[S+1], packed offsets: the exclusive sum of
+ *                 max(n_new, 0), saturating at 2^31 - 1
+ *   total       : out, device int32[S], len + n_new; 0 for a finished request
+ *                 whose len fits its table row; -1 for any other refused one
+ *   slot, pos   : out, device int32[N], slot and position of each packed token;
+ *                 both -1 for tokens of refused requests and behind the last
+ *                 request, slot alone -1 where the page is not in [0, n_pages)
+ */
+rel_status relation_page_map(const int32_t* len, const int32_t* n_new,
+                             int32_t* block_table, int32_t* free_pages,
+                             const int32_t* n_free, int32_t* n_free_out,
+                             int32_t* cu, int32_t* total, int32_t* slot,
+                             int32_t* pos, int S, int N, int F, int max_pages,
+                             int page_size, int n_pages, hipStream_t stream);
+
+/*
+ * relation_paged_append - the pre-steps of relation_prestep on a packed batch,
+ * with P2 and the mixed information state stored straight into the pages: per
+ * token t with 0 <= slot[t] < n_pages * page_size, P2 rotated by pos[t] goes to
+ * the slot's row of cache_P2, I~ to that of cache_V, and P1 rotated by pos[t]
+ * to P1o. Any other token is skipped: its P1o row and the pages stay as they
+ * were.
+ *
+ *   P1          : in,  device [N, H, d_h], or NULL (then P1o is NULL too: only
+ *                 the cache is written, and H is ignored)
+ *   P2, I       : in,  device [N, H_kv, d_h]
+ *   ld1, ld2, ldi : elements between consecutive tokens of P1, P2, I (a token's
+ *                 heads are contiguous), a multiple of 16 bytes, at least
+ *                 heads * d_h: slices of one fused projection go in as they are
+ *   slot, pos   : in,  device int32[N]; pos may be NULL for REL_ROPE_NONE
+ *   rope, rope_base, theta, pairing : as in relation_prestep, theta (host, may
+ *                 be NULL) with H_kv / 2 angles for the H_kv information heads
+ *   P1o         : out, device contiguous [N, H, d_h]; may be P1 if ld1 = H * d_h
+ * Numerics: as relation_prestep.
+ */
+rel_status relation_paged_append(const void* P1, const void* P2, const void* I,
+                                 int64_t ld1, int64_t ld2, int64_t ldi,
+                                 const int32_t* slot, const int32_t* pos,
+                                 rel_rope rope, float rope_base,
+                                 const float* theta, rel_pairing pairing,
+                                 void* P1o, void* cache_P2, void* cache_V,
+                                 int N, int H, int H_kv, int d_h, int n_pages,
+                                 int page_size, rel_dtype dt,
+                                 hipStream_t stream);
+
+/*
+ * relation_paged_workspace_bytes - device workspace relation_paged_fwd needs
+ * (the work plan and the partial states of split histories). 0 on invalid
+ * sizes. Calls that may run at the same time need a workspace each, calls on
+ * one stream may share one; nothing is kept in it between calls.
+ */
+size_t relation_paged_workspace_bytes(int N, int S, int H, int H_kv, int d_h);
+
+/*
+ * relation_paged_fwd - the Relation forward of a packed batch of new tokens
+ * against the paged cache that already holds their own rows
+ * (relation_paged_append first). Token k of request b has the zero-based
+ * position p = total[b] - (cu[b+1] - cu[b]) + k, and its output is row p + 1
+ * (one-based) of relation_fwd_ex on the request's rows 0 .. p:
+ *   R_p = sigmoid(U_p / tau_h),  R_j = SiLU(U_j) - lambda log(p + 1) for j < p,
+ *   Y = sum_{j<=p} softmax(R)_j V_j,   U_j = p1 . p2_j / sqrt(d_h).
+ * One call takes any mix of single tokens, several tokens, chunks of a prompt
+ * over what is cached of it, and whole prompts.
+ *
+ *   P1          : in,  device [N, H, d_h] (rotated), ld1 elements between tokens
+ *                 (a multiple of 16 bytes, at least H * d_h)
+ *   total       : in,  device int32[S], cached rows per request, the new ones
+ *                 included (relation_page_map's)
+ *   cu          : in,  device int32[S+1]
+ *   max_new     : no request has more new tokens (1 for a decode step)
+ *   tau_s, lambda : as in relation_fwd_ex, tau_s host float[H]
+ *   Y           : out, device contiguous [N, H, d_h]
+ *   workspace   : device, >= relation_paged_workspace_bytes
+ * Rows of Y are left as they were for padding, and for a request without new
+ * tokens, with more than max_new, with cu outside [0, N], or with total below
+ * its new tokens (a refused one, -1) or above max_pages * page_size.
+ * Rows at or past total[b] may hold anything and are not used; a row that is
+ * used may not hold NaN or infinities (they reach other rows of its request,
+ * never another request's).
+ * Numerics: as relation_fwd_ex; the same call gives the same bits.
+ */
+rel_status relation_paged_fwd(const void* P1, int64_t ld1, const void* cache_P2,
+                              const void* cache_V, const int32_t* block_table,
+                              const int32_t* total, const int32_t* cu,
+                              const float* tau_s, float lambda, void* Y, int N,
+                              int S, int H, int H_kv, int d_h, int n_pages,
+                              int page_size, int max_pages, int max_new,
+                              rel_dtype dt, void* workspace, size_t ws_bytes,
+                              hipStream_t stream);
 
 /* Human-readable name of a status code (static string, never NULL). */
 const char* relation_status_str(rel_status s);
