@@ -1,9 +1,20 @@
 // Relation forward of a packed batch of new tokens against the paged Relation
-// Cache (semantics in relation.h).
+// Cache (semantics in relation.h; "Ask Self, Ask Others: Relation Is All You
+// Need", Eq. (1)-(3) by the scan of Sec. 5.1, Eq. (12)-(14), and the cache of
+// Sec. 5.3).
 //
-// One work-group per (packed token, query head): its rows of lanes scan the
-// token's history with a running maximum each, the states meet in LDS, and the
-// Self entry and the count term enter once (RowCombine).
+// The rows of a request that share a cached head (its new tokens times the
+// query heads of the group) are taken in blocks of 16 NB rows. A work item is
+// (request, split of its history, cached head, row block); a work-group of four
+// waves scans the item's keys, each wave its own 32 keys at a time, and keeps
+// (m, l, z) per row; the waves' states meet in LDS. Where a history is split,
+// the item leaves a partial state and merge_kernel joins them; otherwise the
+// item finishes the row itself (Self entry, count term, output).
+//
+// Three launches: plan (one work-group: the split length and prefix sums of the
+// work over the requests, from the device-side lengths), scan (persistent), and
+// merge.
+#include "mfma_tile.h"
 #include "rel_internal.h"
 #include "rel_device.h"
 
@@ -11,100 +22,714 @@ namespace rel {
 
 namespace {
 
-constexpr int kThreads = 256;
+using namespace mfma;
+typedef float f32x4 __attribute__((ext_vector_type(4)));
 
-// The request of packed token t: cu[b] <= t < cu[b + 1], the first such b.
-__device__ __forceinline__ int request_of(const PagedArgs& a, int t) {
-  int lo = 0, hi = a.S;
-  while (lo < hi) {
-    const int mid = (lo + hi) >> 1;
-    if (a.cu[mid + 1] > t) hi = mid;
-    else lo = mid + 1;
+constexpr int kWaves = 4;
+constexpr int kThreads = 64 * kWaves;
+constexpr int kStep = 32;                 // keys of a wave's step
+constexpr int kMinChunk = 256;            // keys of the shortest split
+constexpr int kTargetItems = 1024;        // work items wanted of one call
+constexpr float kLazy = 32.0f;            // log2 slack before the stabiliser moves
+
+// Workspace of a call.
+struct Ws {
+  PagedPlan* plan;
+  int* units[2];     // [S + 1] each: exclusive sums of row blocks x splits
+  int* part;         // [S + 1] partial rows
+  int* merge;        // [S + 1] rows to merge
+  float2* ml;        // [kPartialRows] stabiliser (log2) and sum
+  float* z;          // [kPartialRows][d_h]
+  __host__ __device__ Ws(void* ws, int S) {
+    char* p = static_cast<char*>(ws);
+    const int64_t n = ((int64_t)(S + 1) * 4 + 255) / 256 * 256;
+    plan = reinterpret_cast<PagedPlan*>(p);
+    p += kPlanHeader;
+    units[0] = reinterpret_cast<int*>(p);
+    units[1] = reinterpret_cast<int*>(p + n);
+    part = reinterpret_cast<int*>(p + 2 * n);
+    merge = reinterpret_cast<int*>(p + 3 * n);
+    p += kPlanSums * n;
+    ml = reinterpret_cast<float2*>(p);
+    z = reinterpret_cast<float*>(p + kPartialRows * sizeof(float2));
   }
-  return lo;
+};
+
+// What the device-side numbers say of request b; rows = 0 for one that is skipped.
+struct Req {
+  int first, q, total, rows;   // first packed token, new tokens, cached rows, rows per cached head
+  __device__ __forceinline__ Req(const PagedArgs& a, int b) {
+    first = a.cu[b];
+    const int end = a.cu[b + 1];
+    total = a.total[b];
+    const bool ok = first >= 0 && end > first && end <= a.N && end - first <= a.max_new && total >= end - first &&
+                    (long long)total <= ((long long)a.max_pages << a.page_shift);
+    q = ok ? end - first : 0;
+    rows = q * (a.H / a.H_kv);
+  }
+};
+
+// A value that is the same in every lane, in a scalar register: buffer
+// descriptors are formed from it.
+__device__ __forceinline__ int uni(int x) { return __builtin_amdgcn_readfirstlane(x); }
+
+// A split length of kMaxChunk stands for unsplit histories of any length.
+constexpr int kMaxChunk = 0x7fffff80;
+__device__ __forceinline__ int splits_of(int total, int chunk) {
+  return chunk == kMaxChunk ? 1 : (int)(((long long)total + chunk - 1) / chunk);
 }
 
-template <typename Tin, int D>
-__global__ __launch_bounds__(kThreads) void paged_scan_kernel(PagedArgs a, HeadParams hp) {
-  constexpr int VEC = 16 / (int)sizeof(Tin);
-  constexpr int LIVE = D / VEC;
-  constexpr int LPR = LIVE <= 4 ? 4 : (LIVE <= 8 ? 8 : (LIVE <= 16 ? 16 : 32));
-  constexpr int GROUPS = kThreads / LPR;
-  __shared__ float s_m[GROUPS], s_l[GROUPS], s_z[GROUPS][D + 1], s_u;
-  const int t = blockIdx.x, h = blockIdx.y;
-  const int b = request_of(a, t);
-  if (b >= a.S) return;
-  const int c0 = a.cu[b], q = a.cu[b + 1] - c0, total = a.total[b];
-  if (c0 < 0 || c0 > t || a.cu[b + 1] > a.N || q > a.max_new || total < q ||
-      total > ((long long)a.max_pages << a.page_shift))
-    return;
-  const int p = total - q + (t - c0);
-  const int kvh = h / (a.H / a.H_kv);
-  const int tid = threadIdx.x, g = tid / LPR, sl = tid % LPR;
-  const bool live = sl < LIVE;
-  const int so = live ? sl * VEC : 0;
-  const Tin* p1 = static_cast<const Tin*>(a.P1) + (size_t)t * a.ld1 + (size_t)h * D + so;
-  auto row = [&](const void* cache, int j, float (&x)[VEC]) {
-    const int page = a.table[(size_t)b * a.max_pages + (j >> a.page_shift)];
-    const bool in = live && page >= 0 && page < a.n_pages;
-    const Tin* r = static_cast<const Tin*>(cache) +
-                   (((((size_t)(in ? page : 0) * a.H_kv + kvh) << a.page_shift) + (j & ((1 << a.page_shift) - 1))) * D + so);
+// ---- plan ---------------------------------------------------------------------
+
+struct Sum4 { int v[kPlanSums]; };
+
+// Exclusive sums over the work-group of four counts at once, and their totals.
+__device__ __forceinline__ Sum4 block_sums(const Sum4& x, Sum4* red, Sum4* total) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  Sum4 s = x;
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) x[e] = in ? to_f32(r[e]) : 0.0f;
-  };
-  float qv[VEC], z[VEC], x[VEC];
+  for (int o = 1; o < 64; o <<= 1)
 #pragma unroll
-  for (int e = 0; e < VEC; ++e) {
-    qv[e] = live ? to_f32(p1[e]) : 0.0f;
-    z[e] = 0.0f;
-  }
-  float m = kEmptyMax, l = 0.0f;
-  for (int j = g; j <= p; j += GROUPS) {
-    row(a.cP2, j, x);
-    float u = 0.0f;
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) u = fmaf(qv[e], x[e], u);
-#pragma unroll
-    for (int off = LPR / 2; off > 0; off >>= 1) u += __shfl_xor(u, off);
-    u *= hp.scale;
-    if (j == p) {
-      if (sl == 0) s_u = u;
-      break;
+    for (int k = 0; k < kPlanSums; ++k) {
+      const int y = __shfl_up(s.v[k], o, 64);
+      if (lane >= o) s.v[k] += y;
     }
-    const float E = silu_f32(u), mn = fmaxf(m, E);
-    const float w = expf(E - mn), k = expf(m - mn);
-    m = mn;
-    l = l * k + w;
-    row(a.cV, j, x);
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) z[e] = z[e] * k + w * x[e];
-  }
-  if (sl == 0) {
-    s_m[g] = m;
-    s_l[g] = l;
-  }
-  if (live)
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) s_z[g][so + e] = z[e];
   __syncthreads();
-  float M = kEmptyMax, ls = 0.0f;
-  for (int k = 0; k < GROUPS; ++k) M = fmaxf(M, s_m[k]);
-  for (int k = 0; k < GROUPS; ++k) ls += s_l[k] * expf(s_m[k] - M);
-  const RowCombine cmb(sigmoid_f32(s_u * hp.inv_tau[h]), M, ls, hp.lambda * logf((float)(p + 1)));
-  if (g == 0 && live) {
-    row(a.cV, p, x);
+  if (lane == 63) red[wave] = s;
+  __syncthreads();
+  Sum4 out;
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) {
-      float zs = 0.0f;
-      for (int k = 0; k < GROUPS; ++k) zs += s_z[k][so + e] * expf(s_m[k] - M);
-      static_cast<Tin*>(a.Y)[((size_t)t * a.H + h) * D + so + e] = from_f32<Tin>(cmb.w_self * x[e] + cmb.w_hist * zs);
+  for (int k = 0; k < kPlanSums; ++k) {
+    int before = 0, all = 0;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) {
+      before += w < wave ? red[w].v[k] : 0;
+      all += red[w].v[k];
+    }
+    total->v[k] = all;
+    out.v[k] = before + s.v[k] - x.v[k];
+  }
+  return out;
+}
+
+// rb[c]: rows per block of class c; a request belongs to class 0 when one block
+// of 16 holds its rows.
+__global__ __launch_bounds__(kThreads) void plan_kernel(PagedArgs a, int rb0, int rb1) {
+  __shared__ long long red_w[2][kWaves];
+  __shared__ Sum4 red[kWaves];
+  const Ws ws(a.ws, a.S);
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+
+  // Key visits of the row blocks, and rows times keys: the split length spreads
+  // the first over kTargetItems items and keeps the partial rows within the
+  // workspace (a split request has at most 2 total / chunk splits).
+  long long visits = 0, cells = 0;
+  for (int b = tid; b < a.S; b += kThreads) {
+    const Req r(a, b);
+    const int rb = r.rows <= rb0 ? rb0 : rb1;
+    visits += (long long)((r.rows + rb - 1) / rb) * a.H_kv * r.total;
+    cells += (long long)r.q * a.H * r.total;
+  }
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    visits += __shfl_xor(visits, o, 64);
+    cells += __shfl_xor(cells, o, 64);
+  }
+  if (lane == 0) {
+    red_w[0][wave] = visits;
+    red_w[1][wave] = cells;
+  }
+  __syncthreads();
+  visits = cells = 0;
+#pragma unroll
+  for (int w = 0; w < kWaves; ++w) {
+    visits += red_w[0][w];
+    cells += red_w[1][w];
+  }
+  long long c = (visits + kTargetItems - 1) / kTargetItems;
+  const long long c2 = (2 * cells + kPartialRows - 1) / kPartialRows;
+  c = c > c2 ? c : c2;
+  c = c < kMinChunk ? kMinChunk : c;
+  c = (c + 127) / 128 * 128;
+  const int chunk = (int)(c < kMaxChunk ? c : kMaxChunk);
+
+  Sum4 base = {{0, 0, 0, 0}}, all;
+  for (int b0 = 0; b0 < a.S; b0 += kThreads) {
+    const int b = b0 + tid;
+    Sum4 x = {{0, 0, 0, 0}};
+    if (b < a.S) {
+      const Req r(a, b);
+      const int cls = r.rows <= rb0 ? 0 : 1;
+      const int rb = cls ? rb1 : rb0;
+      const int splits = splits_of(r.total, chunk);
+      if (r.rows > 0) {
+        x.v[cls] = (r.rows + rb - 1) / rb * splits;
+        if (splits > 1) {
+          x.v[3] = r.q * a.H;
+          x.v[2] = x.v[3] * splits;
+        }
+      }
+    }
+    const Sum4 at = block_sums(x, red, &all);
+    if (b < a.S) {
+      ws.units[0][b] = base.v[0] + at.v[0];
+      ws.units[1][b] = base.v[1] + at.v[1];
+      ws.part[b] = base.v[2] + at.v[2];
+      ws.merge[b] = base.v[3] + at.v[3];
+    }
+#pragma unroll
+    for (int k = 0; k < kPlanSums; ++k) base.v[k] += all.v[k];
+  }
+  if (tid == 0) {
+    ws.plan->chunk = chunk;
+    ws.plan->units[0] = base.v[0];
+    ws.plan->units[1] = base.v[1];
+    ws.plan->merge_rows = base.v[3];
+  }
+}
+
+// The last request b with off[b] <= i: 64 entries are compared at a time.
+__device__ __forceinline__ int find_request(const int* off, int S, int i) {
+  const int lane = threadIdx.x & 63;
+  int lo = 0, n = S;
+  while (n > 1) {
+    const int stride = (n + 63) >> 6;
+    const int k = lane * stride;
+    const bool le = k < n && off[lo + k] <= i;
+    const int cnt = __popcll(__ballot(le));
+    lo += (cnt - 1) * stride;
+    n = min(stride, n - (cnt - 1) * stride);
+  }
+  return __builtin_amdgcn_readfirstlane(lo);
+}
+
+// ---- rows ---------------------------------------------------------------------
+
+template <typename Tin>
+__device__ __forceinline__ void load8(const Tin* p, float (&x)[8]) {
+  if constexpr (sizeof(Tin) == 2) {
+    const bf16x8 v = *reinterpret_cast<const bf16x8*>(p);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = (float)v[e];
+  } else {
+    const f32x4 v = reinterpret_cast<const f32x4*>(p)[0], w = reinterpret_cast<const f32x4*>(p)[1];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      x[e] = v[e];
+      x[4 + e] = w[e];
+    }
+  }
+}
+
+template <typename Tin>
+__device__ __forceinline__ void store8(Tin* p, const float (&x)[8]) {
+  if constexpr (sizeof(Tin) == 2) {
+    *reinterpret_cast<u32x4*>(p) =
+        u32x4{pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7])};
+  } else {
+    reinterpret_cast<f32x4*>(p)[0] = f32x4{x[0], x[1], x[2], x[3]};
+    reinterpret_cast<f32x4*>(p)[1] = f32x4{x[4], x[5], x[6], x[7]};
+  }
+}
+
+// Output of one row from its history's state, by 16 lanes of 8 columns each:
+// z (sum of weights times V), m (log2 stabiliser) and l (sum of weights); the
+// Self evidence and V come from the row's own cached row.
+template <typename Tin, int D>
+__device__ __forceinline__ void finish_row(const PagedArgs& a, const HeadParams& hp, int b, int t, int h, int pos,
+                                           int sl, float m, float l, const float (&z)[8], bool row_ok) {
+  const bool live = row_ok && sl < D / 8;
+  const int col = live ? 8 * sl : 0;
+  const int kvh = h / (a.H / a.H_kv);
+  float q[8], k[8], v[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) q[e] = k[e] = v[e] = 0.0f;
+  if (live) {
+    load8(static_cast<const Tin*>(a.P1) + (size_t)t * a.ld1 + (size_t)h * D + col, q);
+    const int page = a.table[(size_t)b * a.max_pages + (pos >> a.page_shift)];
+    if (page >= 0 && page < a.n_pages) {
+      const size_t row =
+          ((((size_t)page * a.H_kv + kvh) << a.page_shift) + (pos & ((1 << a.page_shift) - 1))) * D + col;
+      load8(static_cast<const Tin*>(a.cP2) + row, k);
+      load8(static_cast<const Tin*>(a.cV) + row, v);
+    }
+  }
+  float u = 0.0f;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) u = fmaf(q[e], k[e], u);
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) u += __shfl_xor(u, o, 16);
+  if (!live) return;
+  const float S = sigmoid_f32(u * hp.scale * hp.inv_tau[h]);
+  const RowCombine c(S, m * kLn2, l, hp.lambda * logf((float)(pos + 1)));
+  float y[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) y[e] = c.w_self * v[e] + c.w_hist * z[e];
+  store8(static_cast<Tin*>(a.Y) + ((size_t)t * a.H + h) * D + col, y);
+}
+
+// ---- scan ---------------------------------------------------------------------
+//
+// v_mfma_f32_16x16x32_bf16 and v_mfma_f32_16x16x4_f32 (lane l, i = l % 16, j =
+// l / 16): A row i, B column i, the contraction index in the elements and j; C
+// register r holds row 4 j + r of column i. With keys as A rows and query rows
+// as B columns a lane holds 4 keys' scores of one query row, and its own
+// weights are the B operand of the transport O^T[d][row] += V^T[d][key]
+// W[key][row], whose contraction runs over the keys in that same order.
+//   bf16: two 16-key blocks make one transport step; V^T comes from a
+//     wave-private LDS tile (direct loads, transposing reads).
+//   fp32: contraction over d in the order {16 t + 4 j + e}, so each lane loads 16
+//     bytes of a P2 row; output rows in the order {d / 16 i + e}, so each lane
+//     loads d_h / 16 consecutive floats of a V row as the A operands of all
+//     output blocks.
+template <typename Tin, int D>
+struct Geom {
+  static constexpr bool kBf = sizeof(Tin) == 2;
+  static constexpr int kKs = kBf ? (D + 31) / 32 : D / 16;   // 16-byte loads per lane and 16-key block
+  static constexpr int kDb = D / 16;                         // 16-row blocks of O^T
+  static constexpr int kCb = (D + 63) / 64;                  // 64-column blocks of a V tile
+  static constexpr int kVTile = 4 * kCb * 1024;              // 32 rows: blocks of 8 rows x 8 chunks, 1 KB each
+  static constexpr int kRing = kBf ? kWaves * 2 * kVTile : 0;
+  static constexpr int kZStride = D + 4;
+  static constexpr int kZBytes = kWaves * 16 * kZStride * 4;
+  static constexpr int kLds = kRing > kZBytes ? kRing : kZBytes;
+};
+
+template <typename Tin, int D, int NB>
+__global__ __launch_bounds__(kThreads, NB == 1 ? 2 : 1) void scan_kernel(PagedArgs a, HeadParams hp, int cls) {
+  using C = Geom<Tin, D>;
+  constexpr bool kBf = C::kBf;
+  constexpr int kRb = 16 * NB;
+  constexpr int kEs = (int)sizeof(Tin);
+  __shared__ __attribute__((aligned(16))) char smem[C::kLds];
+  __shared__ float s_m[kWaves][16], s_l[kWaves][16];
+
+  const Ws ws(a.ws, a.S);
+  const int n_items = uni(ws.plan->units[cls]) * a.H_kv;
+  const int chunk = uni(ws.plan->chunk);
+  const int G = a.H / a.H_kv;
+  const int tid = threadIdx.x;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int lane = tid & 63;
+  const int li = lane & 15, lj = lane >> 4;
+  const float k2 = hp.scale * kLog2e;
+  const int pmask = (1 << a.page_shift) - 1;
+  const int per = (n_items + 7) >> 3;
+
+  // Work-groups go round the 8 XCDs: each takes a contiguous eighth of the items,
+  // so the row blocks of one (request, split, cached head), which lie together,
+  // read its keys through one L2.
+  for (int it = blockIdx.x; it < 8 * per; it += gridDim.x) {
+    const int item = (it & 7) * per + (it >> 3);
+    if (item >= n_items) continue;
+    const int b = find_request(ws.units[cls], a.S, item / a.H_kv);
+    Req r(a, b);
+    r.first = uni(r.first);
+    r.q = uni(r.q);
+    r.total = uni(r.total);
+    r.rows = uni(r.rows);
+    const int nrb = (r.rows + kRb - 1) / kRb;
+    const int nsplit = splits_of(r.total, chunk);
+    const int local = item - uni(ws.units[cls][b]) * a.H_kv;   // 0 .. nrb * nsplit * H_kv - 1
+    const int rb = local % nrb;
+    const int kvh = (local / nrb) % a.H_kv;
+    const int split = local / nrb / a.H_kv;
+    const int ctx = r.total - r.q;
+    const int row0 = rb * kRb;
+    const int rows = min(kRb, r.rows - row0);
+    const int pos_lo = ctx + row0 / G, pos_hi = ctx + (row0 + rows - 1) / G;
+    const int k0 = split * chunk;
+    if (split > 0 && k0 >= pos_hi) continue;        // no keys; the merge does not read this state
+    const int k1 = (int)min((long long)k0 + chunk, (long long)pos_hi);
+
+    // The query rows as B operands, and their positions (0 for rows past the end:
+    // no key is below it).
+    u32x4 qf[NB][C::kKs];
+    int pos[NB];
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) {
+      const int row = row0 + 16 * nb + li;
+      const bool ok = 16 * nb + li < rows;
+      const int tq = ok ? row / G : 0;
+      const int h = kvh * G + (ok ? row - tq * G : 0);
+      pos[nb] = ok ? ctx + tq : 0;
+      const Tin* p = static_cast<const Tin*>(a.P1) + (size_t)(r.first + tq) * a.ld1 + (size_t)h * D;
+#pragma unroll
+      for (int ks = 0; ks < C::kKs; ++ks) {
+        const int col = kBf ? 32 * ks + 8 * lj : 16 * ks + 4 * lj;
+        qf[nb][ks] = ok && col < D ? *reinterpret_cast<const u32x4*>(p + col) : u32x4{0u, 0u, 0u, 0u};
+      }
+    }
+
+    f32x4 acc[NB][C::kDb];
+    float m2[NB], l[NB];
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) {
+      m2[nb] = l[nb] = 0.0f;
+#pragma unroll
+      for (int db = 0; db < C::kDb; ++db) acc[nb][db] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    }
+
+    // This wave's steps: first + 4 n. Lane x holds the page of half x % 2 of step
+    // n0 + x / 2, for 32 steps at a time.
+    const int first = k0 / kStep + wave;
+    const int nsteps = k1 > k0 + kStep * wave ? ((k1 - k0 + kStep - 1) / kStep - wave + kWaves - 1) / kWaves : 0;
+    int pages = -1;
+    auto load_pages = [&](int n0) {
+      const int key = (first + kWaves * (n0 + (lane >> 1))) * kStep + 16 * (lane & 1);
+      pages = -1;
+      if (n0 + (lane >> 1) < nsteps && key < r.total) {
+        const int pg = a.table[(size_t)b * a.max_pages + (key >> a.page_shift)];
+        pages = pg >= 0 && pg < a.n_pages ? pg : -1;
+      }
+    };
+    // Byte address of the first row of 16-key half hb of step n in a cache, and
+    // the bytes of its rows that exist (0: page outside the cache).
+    auto half_at = [&](const void* cache, int n, int hb, int* bytes) -> const char* {
+      const int key = (first + kWaves * n) * kStep + 16 * hb;
+      const int pg = __builtin_amdgcn_readlane(pages, 2 * (n & 31) + hb);
+      const int left = min(16, r.total - key);
+      *bytes = pg >= 0 && left > 0 ? left * D * kEs : 0;
+      const size_t row = (((size_t)(pg >= 0 ? pg : 0) * a.H_kv + kvh) << a.page_shift) + (key & pmask);
+      return static_cast<const char*>(cache) + row * D * kEs;
+    };
+
+    u32x4 kf[2][2][C::kKs];                         // P2 rows of this step and the next
+    float vf[2][4][C::kDb];                         // fp32: V rows of the step
+    char* const ring = smem + wave * 2 * C::kVTile;
+    auto fetch = [&](int n, int buf) __attribute__((always_inline)) {
+      if ((n & 31) == 0) load_pages(n);
+#pragma unroll
+      for (int hb = 0; hb < 2; ++hb) {
+        int bytes;
+        const char* p = half_at(a.cP2, n, hb, &bytes);
+        const auto rs = rsrc(p, bytes);
+#pragma unroll
+        for (int ks = 0; ks < C::kKs; ++ks) {
+          const int col = kBf ? 32 * ks + 8 * lj : 16 * ks + 4 * lj;
+          const int o = col < D ? (li * D + col) * kEs : kOutOfRange;
+          kf[buf][hb][ks] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rs, o, 0, 0));
+        }
+        const char* v = half_at(a.cV, n, hb, &bytes);
+        if constexpr (kBf) {
+#pragma unroll
+          for (int rg = 0; rg < 2; ++rg) {
+            u32x4 rw = rsrc_words(v + 8 * rg * D * kEs, bytes - 8 * rg * D * kEs);
+#pragma unroll
+            for (int w = 0; w < 3; ++w) rw[w] = (unsigned)uni((int)rw[w]);
+#pragma unroll
+            for (int cb = 0; cb < C::kCb; ++cb) {
+              const int ch = 8 * cb + (lane >> 3);
+              dma16(rw, ring + (n & 1) * C::kVTile + (2 * hb + rg + 4 * cb) * 1024,
+                    ch < D / 8 ? (lane & 7) * D * 2 + 16 * ch : kOutOfRange);
+            }
+          }
+        }
+      }
+    };
+    // fp32: the V rows of 16-key half hb, key 4 j + rr, columns d / 16 i ..
+    auto fetch_v = [&](int n) __attribute__((always_inline)) {
+      if constexpr (!kBf) {
+#pragma unroll
+        for (int hb = 0; hb < 2; ++hb) {
+          int bytes;
+          const char* v = half_at(a.cV, n, hb, &bytes);
+          const auto rs = rsrc(v, bytes);
+#pragma unroll
+          for (int rr = 0; rr < 4; ++rr) {
+            const int o = ((4 * lj + rr) * D + C::kDb * li) * 4;
+#pragma unroll
+            for (int e = 0; e < C::kDb; e += 4) {
+              if constexpr (C::kDb >= 4) {
+                if (e + 4 <= C::kDb) {
+                  const f32x4 x = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(rs, o + 4 * e, 0, 0));
+#pragma unroll
+                  for (int w = 0; w < 4; ++w) vf[hb][rr][e + w] = x[w];
+                  continue;
+                }
+              }
+#pragma unroll
+              for (int w = e; w < C::kDb; ++w)
+                vf[hb][rr][w] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(rs, o + 4 * w, 0, 0));
+            }
+          }
+        }
+      }
+    };
+
+    // Scores, weights and transport of step n from P2 buffer buf. Row blocks past
+    // the item's rows run along: with a branch around their MFMAs the compiler
+    // (ROCm 7.2) left out the wait states between an MFMA and the read of its
+    // result behind the branch, and results were wrong.
+    auto compute = [&](int n, int buf) __attribute__((always_inline)) {
+      const int key0 = (first + kWaves * n) * kStep;
+      const bool full = key0 + kStep <= pos_lo;
+      u32x4 wf[NB];
+      float w32[kBf ? 1 : NB][2][4];
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) {
+        float e2[2][4];
+#pragma unroll
+        for (int hb = 0; hb < 2; ++hb) {
+          f32x4 s = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+          for (int ks = 0; ks < C::kKs; ++ks) {
+            if constexpr (kBf) {
+              s = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, kf[buf][hb][ks]),
+                                                          __builtin_bit_cast(bf16x8, qf[nb][ks]), s, 0, 0, 0);
+            } else {
+              const f32x4 x = __builtin_bit_cast(f32x4, kf[buf][hb][ks]), y = __builtin_bit_cast(f32x4, qf[nb][ks]);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) s = __builtin_amdgcn_mfma_f32_16x16x4f32(x[e], y[e], s, 0, 0, 0);
+            }
+          }
+#pragma unroll
+          for (int rr = 0; rr < 4; ++rr) {
+            // SiLU(u) log2 e = a / (1 + 2^-a), a = u log2 e.
+            const float av = s[rr] * k2;
+            e2[hb][rr] = av * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-av));
+          }
+        }
+        if (!full) {
+#pragma unroll
+          for (int hb = 0; hb < 2; ++hb)
+#pragma unroll
+            for (int rr = 0; rr < 4; ++rr)
+              e2[hb][rr] = key0 + 16 * hb + 4 * lj + rr < pos[nb] ? e2[hb][rr] : -INFINITY;
+        }
+        // The stabiliser starts at 0 (SiLU >= -0.2785, so no weight is small) and
+        // moves only when a score passes it by 2^32.
+        float mx = fmaxf(fmaxf(fmaxf(e2[0][0], e2[0][1]), fmaxf(e2[0][2], e2[0][3])),
+                         fmaxf(fmaxf(e2[1][0], e2[1][1]), fmaxf(e2[1][2], e2[1][3])));
+        if (__any(mx > m2[nb] + kLazy)) {
+          mx = fmaxf(mx, __shfl_xor(mx, 16));
+          mx = fmaxf(mx, __shfl_xor(mx, 32));
+          const float mn = fmaxf(mx, m2[nb]);
+          const float f = __builtin_amdgcn_exp2f(m2[nb] - mn);
+          m2[nb] = mn;
+          l[nb] *= f;
+#pragma unroll
+          for (int db = 0; db < C::kDb; ++db)
+#pragma unroll
+            for (int rr = 0; rr < 4; ++rr) acc[nb][db][rr] *= f;
+        }
+        float w[2][4];
+#pragma unroll
+        for (int hb = 0; hb < 2; ++hb) {
+#pragma unroll
+          for (int rr = 0; rr < 4; ++rr) w[hb][rr] = __builtin_amdgcn_exp2f(e2[hb][rr] - m2[nb]);
+          l[nb] += (w[hb][0] + w[hb][1]) + (w[hb][2] + w[hb][3]);
+        }
+        if constexpr (kBf) {
+          // The transport's operand: weights rounded to bf16, like the other bf16 forwards.
+          wf[nb] = u32x4{pack_bf16(w[0][0], w[0][1]), pack_bf16(w[0][2], w[0][3]), pack_bf16(w[1][0], w[1][1]),
+                         pack_bf16(w[1][2], w[1][3])};
+        } else {
+#pragma unroll
+          for (int hb = 0; hb < 2; ++hb)
+#pragma unroll
+            for (int rr = 0; rr < 4; ++rr) w32[nb][hb][rr] = w[hb][rr];
+        }
+      }
+      if constexpr (kBf) {
+        // Transposing reads: lane m of group j addresses row 4 j + m / 4 of a
+        // 16-row block at columns 16 db + 4 (m % 4).
+        const int q = 4 * lj + (li >> 2), c = (li & 3) >> 1;
+        const char* tb = ring + (n & 1) * C::kVTile + 1024 * (q >> 3) + 16 * ((q & 7) + 8 * c) + 8 * (li & 1);
+#pragma unroll
+        for (int db = 0; db < C::kDb; ++db) {
+          const char* p = tb + 4096 * (db / 4) + 256 * (db % 4);
+          const bf16x4 x = lds_tr_read(p), y = lds_tr_read(p + 2048);
+          const bf16x8 vt = {x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb)
+            acc[nb][db] =
+                __builtin_amdgcn_mfma_f32_16x16x32_bf16(vt, __builtin_bit_cast(bf16x8, wf[nb]), acc[nb][db], 0, 0, 0);
+        }
+      } else {
+#pragma unroll
+        for (int hb = 0; hb < 2; ++hb)
+#pragma unroll
+          for (int rr = 0; rr < 4; ++rr)
+#pragma unroll
+            for (int db = 0; db < C::kDb; ++db)
+#pragma unroll
+              for (int nb = 0; nb < NB; ++nb)
+                acc[nb][db] = __builtin_amdgcn_mfma_f32_16x16x4f32(vf[hb][rr][db], w32[nb][hb][rr], acc[nb][db], 0, 0, 0);
+      }
+    };
+
+    // One step ahead: the next step's loads are issued once this step's have
+    // landed and the LDS reads of the step before are done.
+    if (nsteps > 0) fetch(0, 0);
+    for (int n = 0; n < nsteps; n += 2) {
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        if (n + u < nsteps) {
+          if constexpr (kBf) {
+            asm volatile("" ::: "memory");
+            wait_vm_lgkm<0, 0>();
+            asm volatile("" ::: "memory");
+            __builtin_amdgcn_sched_barrier(0);
+          }
+          fetch_v(n + u);
+          if (n + u + 1 < nsteps) fetch(n + u + 1, u ^ 1);
+          __builtin_amdgcn_sched_barrier(0);
+          compute(n + u, u);
+        }
+      }
+    }
+
+    // The waves' states meet in LDS, 16 rows at a time; then 16 lanes per row.
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) {
+      if (16 * nb >= rows) continue;
+      float ls = l[nb];
+      ls += __shfl_xor(ls, 16);
+      ls += __shfl_xor(ls, 32);
+      __syncthreads();                              // ring or the previous rows' states are no longer read
+      if (lj == 0) {
+        s_m[wave][li] = m2[nb];
+        s_l[wave][li] = ls;
+      }
+      float* z = reinterpret_cast<float*>(smem) + (wave * 16 + li) * C::kZStride;
+#pragma unroll
+      for (int db = 0; db < C::kDb; ++db) {
+        if constexpr (kBf) {
+          *reinterpret_cast<f32x4*>(z + 16 * db + 4 * lj) = acc[nb][db];
+        } else {
+#pragma unroll
+          for (int rr = 0; rr < 4; ++rr) z[C::kDb * (4 * lj + rr) + db] = acc[nb][db][rr];
+        }
+      }
+      __syncthreads();
+      const int rr = tid >> 4, sl = tid & 15;
+      const int row = row0 + 16 * nb + rr;
+      const bool ok = 16 * nb + rr < rows;
+      float M = s_m[0][rr], L = 0.0f, zs[8];
+#pragma unroll
+      for (int w = 1; w < kWaves; ++w) M = fmaxf(M, s_m[w][rr]);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) zs[e] = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kWaves; ++w) {
+        const float f = __builtin_amdgcn_exp2f(s_m[w][rr] - M);
+        L = fmaf(f, s_l[w][rr], L);
+        if (sl < D / 8) {
+          const float* zw = reinterpret_cast<const float*>(smem) + (w * 16 + rr) * C::kZStride + 8 * sl;
+          const f32x4 x = reinterpret_cast<const f32x4*>(zw)[0], y = reinterpret_cast<const f32x4*>(zw)[1];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            zs[e] = fmaf(f, x[e], zs[e]);
+            zs[4 + e] = fmaf(f, y[e], zs[4 + e]);
+          }
+        }
+      }
+      const int tq = ok ? row / G : 0;
+      const int h = kvh * G + (ok ? row - tq * G : 0);
+      if (nsplit == 1) {
+        finish_row<Tin, D>(a, hp, b, r.first + tq, h, ctx + tq, sl, M, L, zs, ok);
+      } else if (ok) {
+        const int64_t p = (int64_t)ws.part[b] + (int64_t)split * r.rows * a.H_kv + (int64_t)kvh * r.rows + row;
+        if (sl == 0) ws.ml[p] = make_float2(M, L);
+        if (sl < D / 8) {
+          reinterpret_cast<f32x4*>(ws.z + p * D + 8 * sl)[0] = f32x4{zs[0], zs[1], zs[2], zs[3]};
+          reinterpret_cast<f32x4*>(ws.z + p * D + 8 * sl)[1] = f32x4{zs[4], zs[5], zs[6], zs[7]};
+        }
+      }
+    }
+    __syncthreads();                                // the states are read before the next item's loads land
+  }
+}
+
+// ---- merge --------------------------------------------------------------------
+
+// One work-group per row: 16 groups of 16 lanes each join every 16th split, the
+// groups join in LDS in their order, and the first group finishes the row.
+template <typename Tin, int D>
+__global__ __launch_bounds__(kThreads) void merge_kernel(PagedArgs a, HeadParams hp) {
+  __shared__ float s_m[16], s_l[16], s_z[16][D + 4];
+  const Ws ws(a.ws, a.S);
+  const int n = ws.plan->merge_rows;
+  const int chunk = ws.plan->chunk;
+  const int G = a.H / a.H_kv;
+  const int g = threadIdx.x >> 4, sl = threadIdx.x & 15;
+  for (int i = blockIdx.x; i < n; i += gridDim.x) {
+    const int b = find_request(ws.merge, a.S, i);
+    const Req r(a, b);
+    const int id = i - ws.merge[b];                 // kvh * rows + row
+    const int kvh = id / r.rows, row = id - kvh * r.rows;
+    const int tq = row / G, h = kvh * G + row - tq * G;
+    const int pos = r.total - r.q + tq;
+    const int ns = (int)(((long long)pos + chunk - 1) / chunk);   // splits with keys of this row
+    float M = kEmptyMax, L = 0.0f, z[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) z[e] = 0.0f;
+    for (int s = g; s < ns; s += 16) {
+      const int64_t p = (int64_t)ws.part[b] + (int64_t)s * r.rows * a.H_kv + id;
+      const float2 ml = ws.ml[p];
+      f32x4 x = {0.0f, 0.0f, 0.0f, 0.0f}, y = x;
+      if (sl < D / 8) {
+        x = reinterpret_cast<const f32x4*>(ws.z + p * D + 8 * sl)[0];
+        y = reinterpret_cast<const f32x4*>(ws.z + p * D + 8 * sl)[1];
+      }
+      const float Mn = fmaxf(M, ml.x);
+      const float fo = __builtin_amdgcn_exp2f(M - Mn), fn = __builtin_amdgcn_exp2f(ml.x - Mn);
+      M = Mn;
+      L = L * fo + ml.y * fn;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        z[e] = z[e] * fo + x[e] * fn;
+        z[4 + e] = z[4 + e] * fo + y[e] * fn;
+      }
+    }
+    __syncthreads();
+    if (sl == 0) {
+      s_m[g] = M;
+      s_l[g] = L;
+    }
+    if (sl < D / 8)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) s_z[g][8 * sl + e] = z[e];
+    __syncthreads();
+    if (threadIdx.x < 64) {                         // the first wave; its groups 1 to 3 only follow
+      M = kEmptyMax;
+      L = 0.0f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) z[e] = 0.0f;
+#pragma unroll
+      for (int k = 0; k < 16; ++k) M = fmaxf(M, s_m[k]);
+      for (int k = 0; k < 16; ++k) {
+        const float f = __builtin_amdgcn_exp2f(s_m[k] - M);
+        L = fmaf(f, s_l[k], L);
+        if (sl < D / 8)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) z[e] = fmaf(f, s_z[k][8 * sl + e], z[e]);
+      }
+      finish_row<Tin, D>(a, hp, b, r.first + tq, h, pos, sl, M, L, z, g == 0);
     }
   }
 }
 
 template <typename Tin, int D>
 hipError_t launch_typed(const PagedArgs& a, const HeadParams& hp, hipStream_t s) {
-  hipLaunchKernelGGL((paged_scan_kernel<Tin, D>), dim3((unsigned)a.N, a.H), dim3(kThreads), 0, s, a, hp);
+  constexpr int kNb1 = sizeof(Tin) == 2 ? 4 : 2;
+  int cu = 0;
+  hipError_t e = device_cu_count(&cu);
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(plan_kernel, dim3(1), dim3(kThreads), 0, s, a, 16, 16 * kNb1);
+  e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  const unsigned grid = 2u * (unsigned)cu;
+  hipLaunchKernelGGL((scan_kernel<Tin, D, 1>), dim3(grid), dim3(kThreads), 0, s, a, hp, 0);
+  e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  if ((long long)a.max_new * (a.H / a.H_kv) > 16) {
+    hipLaunchKernelGGL((scan_kernel<Tin, D, kNb1>), dim3(grid), dim3(kThreads), 0, s, a, hp, 1);
+    e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  hipLaunchKernelGGL((merge_kernel<Tin, D>), dim3(4 * grid), dim3(kThreads), 0, s, a, hp);
   return hipGetLastError();
 }
 

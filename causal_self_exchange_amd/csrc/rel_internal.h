@@ -174,7 +174,21 @@ struct PagedArgs {
   int N, S, H, H_kv, d_h, n_pages, page_shift, max_pages, max_new;
 };
 
-inline size_t paged_ws_bytes(int64_t, int) { return 256; }
+// Workspace of relation_paged_fwd: the work plan (a header and prefix sums over
+// the requests) and the partial states of split histories, at most
+// kPartialRows rows (m, l) and z[d_h].
+struct PagedPlan {
+  int chunk;            // keys per split, a multiple of 128
+  int units[2];         // work units of the two row classes (times H_kv work items)
+  int merge_rows;       // output rows with split histories
+};
+constexpr int kPlanSums = 4;                  // units of both classes, partial rows, merge rows
+constexpr int64_t kPartialRows = 32768;
+constexpr int64_t kPlanHeader = 256;
+inline int64_t paged_sum_bytes(int64_t S) { return ((S + 1) * 4 + 255) / 256 * 256; }
+inline size_t paged_ws_bytes(int64_t S, int d_h) {
+  return static_cast<size_t>(kPlanHeader + kPlanSums * paged_sum_bytes(S) + kPartialRows * (d_h + 2) * 4);
+}
 
 // Launchers (return the hipError_t of the launch).
 hipError_t launch_fwd_scan(const FwdArgs& a, const HeadParams& hp, bool bf16, hipStream_t s);

@@ -300,7 +300,8 @@ rel_status relation_paged_fwd(const void* P1, int64_t ld1, const void* cache_P2,
   if (!dtype_ok(dt)) return REL_E_DTYPE;
   if (!fwd_head_dim_ok(d_h)) return REL_E_HEADDIM;
   if (!page_counts_ok(n_pages, page_size) || !page_counts_ok(max_pages, page_size)) return REL_E_PAGE;
-  if (!count(nc, {n_pages, H_kv, page_size, d_h}) || !count(ny, {N, H, d_h}) || !count(nt, {S, max_pages}))
+  if (!count(nc, {n_pages, H_kv, page_size, d_h}) || !count(ny, {N, H, d_h}) || !count(nt, {S, max_pages}) ||
+      static_cast<int64_t>(N) * H >= (int64_t(1) << 31))
     return REL_E_SHAPE;
   HeadParams hp;
   const rel_status st = pack_heads(hp, tau_s, H, d_h, lambda);

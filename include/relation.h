@@ -371,7 +371,7 @@ rel_status relation_cache_append(void* cache_P2, void* cache_V, int32_t* len,
  * are padding). The H query heads form groups of H / H_kv consecutive heads that
  * share one cached head (query head h reads cached head h / (H / H_kv)).
  * One serving step: relation_page_map, relation_paged_append, relation_paged_fwd.
- * Limits: S <= 65535; N, n_pages * page_size and max_pages * page_size < 2^31.
+ * Limits: S <= 65535; N * H, n_pages * page_size and max_pages * page_size < 2^31.
  * A request whose device-side numbers are not valid is skipped as each call
  * describes, and a page number outside [0, n_pages) is never followed: its rows
  * read as zeros and are not written. Slots must be distinct: of tokens that
