@@ -14,16 +14,13 @@
 // Three launches: plan (one work-group: the split length and prefix sums of the
 // work over the requests, from the device-side lengths), scan (persistent), and
 // merge.
-#include "mfma_tile.h"
-#include "rel_internal.h"
-#include "rel_device.h"
+#include "paged_device.h"
 
 namespace rel {
 
 namespace {
 
-using namespace mfma;
-typedef float f32x4 __attribute__((ext_vector_type(4)));
+using namespace paged;
 
 constexpr int kWaves = 4;
 constexpr int kThreads = 64 * kWaves;
@@ -31,53 +28,6 @@ constexpr int kStep = 32;                 // keys of a wave's step
 constexpr int kMinChunk = 256;            // keys of the shortest split
 constexpr int kTargetItems = 1024;        // work items wanted of one call
 constexpr float kLazy = 32.0f;            // log2 slack before the stabiliser moves
-
-// Workspace of a call.
-struct Ws {
-  PagedPlan* plan;
-  int* units[2];     // [S + 1] each: exclusive sums of row blocks x splits
-  int* part;         // [S + 1] partial rows
-  int* merge;        // [S + 1] rows to merge
-  float2* ml;        // [kPartialRows] stabiliser (log2) and sum
-  float* z;          // [kPartialRows][d_h]
-  __host__ __device__ Ws(void* ws, int S) {
-    char* p = static_cast<char*>(ws);
-    const int64_t n = ((int64_t)(S + 1) * 4 + 255) / 256 * 256;
-    plan = reinterpret_cast<PagedPlan*>(p);
-    p += kPlanHeader;
-    units[0] = reinterpret_cast<int*>(p);
-    units[1] = reinterpret_cast<int*>(p + n);
-    part = reinterpret_cast<int*>(p + 2 * n);
-    merge = reinterpret_cast<int*>(p + 3 * n);
-    p += kPlanSums * n;
-    ml = reinterpret_cast<float2*>(p);
-    z = reinterpret_cast<float*>(p + kPartialRows * sizeof(float2));
-  }
-};
-
-// What the device-side numbers say of request b; rows = 0 for one that is skipped.
-struct Req {
-  int first, q, total, rows;   // first packed token, new tokens, cached rows, rows per cached head
-  __device__ __forceinline__ Req(const PagedArgs& a, int b) {
-    first = a.cu[b];
-    const int end = a.cu[b + 1];
-    total = a.total[b];
-    const bool ok = first >= 0 && end > first && end <= a.N && end - first <= a.max_new && total >= end - first &&
-                    (long long)total <= ((long long)a.max_pages << a.page_shift);
-    q = ok ? end - first : 0;
-    rows = q * (a.H / a.H_kv);
-  }
-};
-
-// A value that is the same in every lane, in a scalar register: buffer
-// descriptors are formed from it.
-__device__ __forceinline__ int uni(int x) { return __builtin_amdgcn_readfirstlane(x); }
-
-// A split length of kMaxChunk stands for unsplit histories of any length.
-constexpr int kMaxChunk = 0x7fffff80;
-__device__ __forceinline__ int splits_of(int total, int chunk) {
-  return chunk == kMaxChunk ? 1 : (int)(((long long)total + chunk - 1) / chunk);
-}
 
 // ---- plan ---------------------------------------------------------------------
 
@@ -112,9 +62,32 @@ __device__ __forceinline__ Sum4 block_sums(const Sum4& x, Sum4* red, Sum4* total
   return out;
 }
 
+// Exclusive sum over the work-group of one 64-bit count, and its total.
+__device__ __forceinline__ long long block_sum(long long x, long long* red, long long* total) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  long long s = x;
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    const long long y = __shfl_up(s, o, 64);
+    if (lane >= o) s += y;
+  }
+  __syncthreads();
+  if (lane == 63) red[wave] = s;
+  __syncthreads();
+  long long before = 0, all = 0;
+#pragma unroll
+  for (int w = 0; w < kWaves; ++w) {
+    before += w < wave ? red[w] : 0;
+    all += red[w];
+  }
+  *total = all;
+  return before + s - x;
+}
+
 // rb[c]: rows per block of class c; a request belongs to class 0 when one block
-// of 16 holds its rows.
-__global__ __launch_bounds__(kThreads) void plan_kernel(PagedArgs a, int rb0, int rb1) {
+// of 16 holds its rows, to the long chunks with chunk_min new tokens (0: to
+// neither), and to class 1 otherwise.
+__global__ __launch_bounds__(kThreads) void plan_kernel(PagedArgs a, int rb0, int rb1, int chunk_min) {
   __shared__ long long red_w[2][kWaves];
   __shared__ Sum4 red[kWaves];
   const Ws ws(a.ws, a.S);
@@ -126,6 +99,7 @@ __global__ __launch_bounds__(kThreads) void plan_kernel(PagedArgs a, int rb0, in
   long long visits = 0, cells = 0;
   for (int b = tid; b < a.S; b += kThreads) {
     const Req r(a, b);
+    if (is_chunk(r, chunk_min)) continue;
     const int rb = r.rows <= rb0 ? rb0 : rb1;
     visits += (long long)((r.rows + rb - 1) / rb) * a.H_kv * r.total;
     cells += (long long)r.q * a.H * r.total;
@@ -162,7 +136,7 @@ __global__ __launch_bounds__(kThreads) void plan_kernel(PagedArgs a, int rb0, in
       const int cls = r.rows <= rb0 ? 0 : 1;
       const int rb = cls ? rb1 : rb0;
       const int splits = splits_of(r.total, chunk);
-      if (r.rows > 0) {
+      if (r.rows > 0 && !is_chunk(r, chunk_min)) {
         x.v[cls] = (r.rows + rb - 1) / rb * splits;
         if (splits > 1) {
           x.v[3] = r.q * a.H;
@@ -186,86 +160,26 @@ __global__ __launch_bounds__(kThreads) void plan_kernel(PagedArgs a, int rb0, in
     ws.plan->units[1] = base.v[1];
     ws.plan->merge_rows = base.v[3];
   }
-}
+  if (chunk_min == 0) return;
 
-// The last request b with off[b] <= i: 64 entries are compared at a time.
-__device__ __forceinline__ int find_request(const int* off, int S, int i) {
-  const int lane = threadIdx.x & 63;
-  int lo = 0, n = S;
-  while (n > 1) {
-    const int stride = (n + 63) >> 6;
-    const int k = lane * stride;
-    const bool le = k < n && off[lo + k] <= i;
-    const int cnt = __popcll(__ballot(le));
-    lo += (cnt - 1) * stride;
-    n = min(stride, n - (cnt - 1) * stride);
-  }
-  return __builtin_amdgcn_readfirstlane(lo);
-}
-
-// ---- rows ---------------------------------------------------------------------
-
-template <typename Tin>
-__device__ __forceinline__ void load8(const Tin* p, float (&x)[8]) {
-  if constexpr (sizeof(Tin) == 2) {
-    const bf16x8 v = *reinterpret_cast<const bf16x8*>(p);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = (float)v[e];
-  } else {
-    const f32x4 v = reinterpret_cast<const f32x4*>(p)[0], w = reinterpret_cast<const f32x4*>(p)[1];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      x[e] = v[e];
-      x[4 + e] = w[e];
+  // Key tiles of the long chunks, all heads.
+  const ChunkWs cw(a.ws, a.S, a.d_h);
+  long long sum = 0, n;
+  for (int b0 = 0; b0 < a.S; b0 += kThreads) {
+    const int b = b0 + tid;
+    long long x = 0;
+    if (b < a.S) {
+      const Req r(a, b);
+      if (is_chunk(r, chunk_min)) {
+        const ChunkTiles t(r.total - r.q, r.total);
+        x = t.before(t.n) * a.H;
+      }
     }
+    const long long at = block_sum(x, red_w[0], &n);
+    if (b < a.S) cw.units[b] = sum + at;
+    sum += n;
   }
-}
-
-template <typename Tin>
-__device__ __forceinline__ void store8(Tin* p, const float (&x)[8]) {
-  if constexpr (sizeof(Tin) == 2) {
-    *reinterpret_cast<u32x4*>(p) =
-        u32x4{pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7])};
-  } else {
-    reinterpret_cast<f32x4*>(p)[0] = f32x4{x[0], x[1], x[2], x[3]};
-    reinterpret_cast<f32x4*>(p)[1] = f32x4{x[4], x[5], x[6], x[7]};
-  }
-}
-
-// Output of one row from its history's state, by 16 lanes of 8 columns each:
-// z (sum of weights times V), m (log2 stabiliser) and l (sum of weights); the
-// Self evidence and V come from the row's own cached row.
-template <typename Tin, int D>
-__device__ __forceinline__ void finish_row(const PagedArgs& a, const HeadParams& hp, int b, int t, int h, int pos,
-                                           int sl, float m, float l, const float (&z)[8], bool row_ok) {
-  const bool live = row_ok && sl < D / 8;
-  const int col = live ? 8 * sl : 0;
-  const int kvh = h / (a.H / a.H_kv);
-  float q[8], k[8], v[8];
-#pragma unroll
-  for (int e = 0; e < 8; ++e) q[e] = k[e] = v[e] = 0.0f;
-  if (live) {
-    load8(static_cast<const Tin*>(a.P1) + (size_t)t * a.ld1 + (size_t)h * D + col, q);
-    const int page = a.table[(size_t)b * a.max_pages + (pos >> a.page_shift)];
-    if (page >= 0 && page < a.n_pages) {
-      const size_t row =
-          ((((size_t)page * a.H_kv + kvh) << a.page_shift) + (pos & ((1 << a.page_shift) - 1))) * D + col;
-      load8(static_cast<const Tin*>(a.cP2) + row, k);
-      load8(static_cast<const Tin*>(a.cV) + row, v);
-    }
-  }
-  float u = 0.0f;
-#pragma unroll
-  for (int e = 0; e < 8; ++e) u = fmaf(q[e], k[e], u);
-#pragma unroll
-  for (int o = 8; o > 0; o >>= 1) u += __shfl_xor(u, o, 16);
-  if (!live) return;
-  const float S = sigmoid_f32(u * hp.scale * hp.inv_tau[h]);
-  const RowCombine c(S, m * kLn2, l, hp.lambda * logf((float)(pos + 1)));
-  float y[8];
-#pragma unroll
-  for (int e = 0; e < 8; ++e) y[e] = c.w_self * v[e] + c.w_hist * z[e];
-  store8(static_cast<Tin*>(a.Y) + ((size_t)t * a.H + h) * D + col, y);
+  if (tid == 0) cw.units[a.S] = sum;
 }
 
 // ---- scan ---------------------------------------------------------------------
@@ -717,9 +631,16 @@ hipError_t launch_typed(const PagedArgs& a, const HeadParams& hp, hipStream_t s)
   int cu = 0;
   hipError_t e = device_cu_count(&cu);
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(plan_kernel, dim3(1), dim3(kThreads), 0, s, a, 16, 16 * kNb1);
+  // Long chunks: bf16, with a token stride whose 256 rows a 31-bit byte offset
+  // reaches.
+  const bool chunks = sizeof(Tin) == 2 && a.max_new >= kChunkMin && a.N >= kChunkMin && a.ld1 < (1 << 22);
+  hipLaunchKernelGGL(plan_kernel, dim3(1), dim3(kThreads), 0, s, a, 16, 16 * kNb1, chunks ? kChunkMin : 0);
   e = hipGetLastError();
   if (e != hipSuccess) return e;
+  if (chunks) {
+    e = launch_paged_chunk(a, hp, cu < kChunkGroups ? cu : kChunkGroups, s);
+    if (e != hipSuccess) return e;
+  }
   const unsigned grid = 2u * (unsigned)cu;
   hipLaunchKernelGGL((scan_kernel<Tin, D, 1>), dim3(grid), dim3(kThreads), 0, s, a, hp, 0);
   e = hipGetLastError();

@@ -214,6 +214,16 @@ def test_paged_fwd_long_history(dt, d):
     check_fwd(P.make(dt, 4, 2, d, 16, [(20001, 1), (9000, 3), (5, 1), (8190, 18)], seed=d), 0.5, dt)
 
 
+@pytest.mark.parametrize("d,page,H,Hkv,reqs", [
+    (128, 16, 2, 1, [(6000, 128), (31, 129), (0, 1)]), (64, 256, 8, 2, [(63, 255), (64, 256), (65, 257), (1, 511)]),
+    (80, 64, 1, 1, [(4097, 300)]), (48, 16, 8, 8, [(0, 256), (3, 1), (0, 64), (100, 900)]),
+    (32, 128, 3, 3, [(10, 1500)]), (128, 32, 16, 4, [(129, 190), (2, 5), (500, 140), (0, 127)]),
+])
+def test_paged_fwd_long_chunks(d, page, H, Hkv, reqs):
+    """Chunks of 128 tokens and more, at and around the tile sizes, mixed with short ones; few and many pieces per tile."""
+    check_fwd(P.make("bf16", H, Hkv, d, page, reqs, seed=d + H, stride_pad=8, pad_rows=2), 0.5, "bf16")
+
+
 @pytest.mark.parametrize("dt,reqs", [("bf16", RAGGED), ("bf16", CHUNKS), ("f32", RAGGED)])
 def test_paged_fwd_large_evidence(dt, reqs):
     """Evidence far beyond the exponent range of an unshifted exponential (|U| to some hundreds): the stabiliser moves.
