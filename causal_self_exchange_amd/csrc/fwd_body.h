@@ -225,11 +225,11 @@ struct StepKind {
 // kRope: P1 is rotated (rotary position encoding, interleaved or half-split
 // pairs) after each query tile's rows are loaded, as the pre-step would have
 // rotated it (same angles, fp32 rotation, one bf16 rounding).
-// kPaged: the paged form of the LSE variant's arithmetic (fp32 evidence and row
-// sum); pg and its source of segments replace a's layout.
+// kPaged: the paged form, with the LSE variant's fp32 evidence and the other's row
+// sum (there is no LSE output); pg and its segments replace a's layout.
 template <int D, int DR, bool kLse, bool kRope, bool kPaged = false>
 __device__ __forceinline__ void fwd_body(const FwdArgs& a, const HeadParams& hp, const RopeParams& rp,
-                                         const PagedArgs& pg = PagedArgs{}) {
+                                         const PagedArgs& pg = PagedArgs{}, const paged::Plan& plan = paged::Plan{}) {
   static_assert(!kPaged || (kLse && !kRope), "the paged form has the LSE variant's arithmetic");
   static_assert(DR % 16 == 0 && DR <= D && DR >= 32, "real head size within the layout");
   using C = Cfg<D>;
@@ -524,7 +524,7 @@ __device__ __forceinline__ void fwd_body(const FwdArgs& a, const HeadParams& hp,
       const float an = kLse ? sW[n] * k2 : sW[n];
       float w = __builtin_amdgcn_exp2f(an * tv[n] - m2);
       if constexpr (K::W == kWDiag) w = key_of(n, hf) < lq ? w : 0.0f;
-      if constexpr (kLse) acc[n & 3] += w;
+      if constexpr (kLse && !kPaged) acc[n & 3] += w;
       if (n & 1) pW[n >> 3][(n & 7) >> 1] = pack_bf16(tv[n - 1], w);
       else tv[n] = w;
     };
@@ -547,7 +547,7 @@ __device__ __forceinline__ void fwd_body(const FwdArgs& a, const HeadParams& hp,
           const int k = i >> 1, ks = k / C::kDb, db = k % C::kDb;
           const bf16x8 w = __builtin_bit_cast(bf16x8, pT[ks]);
           o[db] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(ring[i & 3], w, o[db], 0, 0, 0);
-          if constexpr (!kLse) {
+          if constexpr (!kLse || kPaged) {
             if (db == C::kDb - 1) l16 = __builtin_amdgcn_mfma_f32_16x16x32_bf16(sel, w, l16, 0, 0, 0);
           }
         }
@@ -566,7 +566,7 @@ __device__ __forceinline__ void fwd_body(const FwdArgs& a, const HeadParams& hp,
       }
       __builtin_amdgcn_sched_barrier(0);
     }
-    if constexpr (kLse && K::W != kWOff) lsum += (acc[0] + acc[1]) + (acc[2] + acc[3]);
+    if constexpr (kLse && !kPaged && K::W != kWOff) lsum += (acc[0] + acc[1]) + (acc[2] + acc[3]);
   };
   using SFull = StepKind<true, kWFull, true>;
 
@@ -721,7 +721,7 @@ __device__ __forceinline__ void fwd_body(const FwdArgs& a, const HeadParams& hp,
     wait_vm_lgkm<0, 15>();
 
     // Exactness of the fixed offset: every row sum below 2^100 and O finite.
-    const float lrow = kLse ? lane_pair_sum(lsum) : l16[0];
+    const float lrow = kLse && !kPaged ? lane_pair_sum(lsum) : l16[0];
     float omax = 0.0f;
 #pragma unroll
     for (int db = 0; db < C::kDb; ++db)
@@ -770,12 +770,12 @@ __device__ __forceinline__ void fwd_body(const FwdArgs& a, const HeadParams& hp,
   if constexpr (kPaged) {
     // A segment without all of its query tile's keys: (m, l) and z of its rows.
     if (sg.slot >= 0) {
-      const paged::ChunkWs cw(pg.ws, pg.S, DR);
+      const paged::States st = paged::States::chunk(pg);
       const int ln = lane_now();
       const int row = sg.slot * kBM + wave * 32 + (ln & 31);
-      const float lw = lane_pair_sum(lsum);
-      if (ln < 32) cw.ml[row] = make_float2(m2, lw);
-      float* z = cw.z + (size_t)row * DR + 4 * (ln >> 5);
+      const float lw = l16[0];
+      if (ln < 32) st.ml[row] = make_float2(m2, lw);
+      float* z = st.z + (size_t)row * DR + 4 * (ln >> 5);
 #pragma unroll
       for (int db = 0; db < C::kDb; ++db)
 #pragma unroll
@@ -811,7 +811,7 @@ __device__ __forceinline__ void fwd_body(const FwdArgs& a, const HeadParams& hp,
   }
 
   // ---- epilogue -------------------------------------------------------------
-  const float lrow = kLse ? lane_pair_sum(lsum) : l16[0];
+  const float lrow = kLse && !kPaged ? lane_pair_sum(lsum) : l16[0];
   const float uii = lane_pair_sum(dself) * (kLse ? hp.scale : kLn2);
   const float S = sigmoid_f32(uii * inv_tau);
   const RowCombine c(S, m2 * kLn2, lrow, hp.lambda * logf((float)(qrow + 1)));
@@ -877,7 +877,7 @@ __device__ __forceinline__ void fwd_body(const FwdArgs& a, const HeadParams& hp,
   if constexpr (kPaged) {
     // The work-group's range of units (key tiles of all query tiles), segment by
     // segment.
-    paged::SegmentSource src(pg, blockIdx.x, gridDim.x);
+    paged::SegmentSource src(pg, plan, blockIdx.x, gridDim.x);
     paged::Segment sg = src.next().uniform();
     if (sg.te == 0) return;
     load_q_paged(sg);

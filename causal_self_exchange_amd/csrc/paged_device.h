@@ -12,32 +12,13 @@ namespace paged {
 using namespace mfma;
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 
-// Workspace of a call.
-struct Ws {
-  PagedPlan* plan;
-  int* units[2];     // [S + 1] each: exclusive sums of row blocks x splits
-  int* part;         // [S + 1] partial rows
-  int* merge;        // [S + 1] rows to merge
-  float2* ml;        // [kPartialRows] stabiliser (log2) and sum
-  float* z;          // [kPartialRows][d_h]
-  __host__ __device__ Ws(void* ws, int S) {
-    char* p = static_cast<char*>(ws);
-    const int64_t n = ((int64_t)(S + 1) * 4 + 255) / 256 * 256;
-    plan = reinterpret_cast<PagedPlan*>(p);
-    p += kPlanHeader;
-    units[0] = reinterpret_cast<int*>(p);
-    units[1] = reinterpret_cast<int*>(p + n);
-    part = reinterpret_cast<int*>(p + 2 * n);
-    merge = reinterpret_cast<int*>(p + 3 * n);
-    p += kPlanSums * n;
-    ml = reinterpret_cast<float2*>(p);
-    z = reinterpret_cast<float*>(p + kPartialRows * sizeof(float2));
-  }
-};
+// A value that is the same in every lane, in a scalar register: buffer
+// descriptors are formed from it.
+__device__ __forceinline__ int uni(int x) { return __builtin_amdgcn_readfirstlane(x); }
 
-// What the device-side numbers say of request b; rows = 0 for one that is skipped.
+// What the device-side numbers say of request b; q = 0 for one that is skipped.
 struct Req {
-  int first, q, total, rows;   // first packed token, new tokens, cached rows, rows per cached head
+  int first, q, total;         // first packed token, new tokens, cached rows
   __device__ __forceinline__ Req() {}
   __device__ __forceinline__ Req(const PagedArgs& a, int b) {
     first = a.cu[b];
@@ -46,19 +27,233 @@ struct Req {
     const bool ok = first >= 0 && end > first && end <= a.N && end - first <= a.max_new && total >= end - first &&
                     (long long)total <= ((long long)a.max_pages << a.page_shift);
     q = ok ? end - first : 0;
-    rows = q * (a.H / a.H_kv);
   }
 };
 
-// A value that is the same in every lane, in a scalar register: buffer
-// descriptors are formed from it.
-__device__ __forceinline__ int uni(int x) { return __builtin_amdgcn_readfirstlane(x); }
+// Query tiles of a long chunk: 256 positions each from ctx rounded down to a
+// multiple of 64, so that 64-key tiles never straddle a tile's first position
+// and a tile's own keys are four key tiles. Tile k needs the key tiles up to its
+// last position: all but the last tile base64 + 4 (k + 1). A last tile with
+// fewer than kChunkMin positions would waste more of the long-chunk kernel than
+// the scan kernel is slower: its tokens (rest) go there.
+struct ChunkTiles {
+  int base64, n, last, rest;   // first position / 64, tiles, key tiles of the last one, tokens left to the scan
+  __device__ __forceinline__ ChunkTiles(int ctx, int total) {
+    base64 = ctx >> 6;
+    const long long span = (long long)total - 64LL * base64;
+    rest = (int)(span & 255);
+    rest = rest < kChunkMin ? rest : 0;
+    n = (int)((span - rest + 255) >> 8);
+    last = (int)(((long long)total - rest + 63) >> 6);
+  }
+  // Key tiles of the tiles before k.
+  __device__ __forceinline__ long long before(int k) const {
+    const long long full = (long long)k * base64 + 2LL * k * (k + 1);
+    return k < n ? full : (long long)(n - 1) * base64 + 2LL * (n - 1) * n + last;
+  }
+  __device__ __forceinline__ int keys(int k) const { return k + 1 < n ? base64 + 4 * (k + 1) : last; }
+};
 
-// A split length of kMaxChunk stands for unsplit histories of any length.
-constexpr int kMaxChunk = 0x7fffff80;
+// The part of a request that each kernel takes: its first tokens with
+// chunk_min > 0 and at least that many new ones go to the long-chunk kernel, the
+// rest to the scan kernel, as requests of their own.
+__device__ __forceinline__ Req chunk_part(Req r, int chunk_min) {
+  if (chunk_min == 0 || r.q < chunk_min) r.q = 0;
+  if (r.q > 0) {
+    const int rest = ChunkTiles(r.total - r.q, r.total).rest;
+    r.q -= rest;
+    r.total -= rest;
+  }
+  return r;
+}
+__device__ __forceinline__ Req scan_part(Req r, int chunk_min) {
+  if (chunk_min > 0 && r.q >= chunk_min) {
+    const int rest = ChunkTiles(r.total - r.q, r.total).rest;
+    r.first += r.q - rest;
+    r.q = rest;
+  }
+  return r;
+}
+
+// ---- plan ---------------------------------------------------------------------
+//
+// How the batch's work is cut, from the device-side lengths. Scan kernel: row
+// blocks of row_block rows of a request and cached head, times splits of its
+// history of `chunk` keys; partial states where a history is split. Long chunks:
+// key tiles of all query tiles and heads, in one line. The sums are exclusive,
+// over the requests.
+
+constexpr int kMinChunk = 512;            // keys of the shortest split
+constexpr int kTargetItems = 1024;        // work items wanted of one call
+constexpr int kMaxChunk = 0x7fffff80;     // stands for unsplit histories of any length
+
+struct Plan {
+  int chunk, units, merge_rows;
+  int* unit_sum;          // row blocks x splits (times H_kv work items)
+  int* part_sum;          // partial rows
+  int* merge_sum;         // rows to join
+  long long* tile_sum;    // key tiles of the long chunks; [S] the total
+};
+
 __device__ __forceinline__ int splits_of(int total, int chunk) {
   return chunk == kMaxChunk ? 1 : (int)(((long long)total + chunk - 1) / chunk);
 }
+
+// Exclusive sum over the first four waves of a work-group and its total; every
+// thread of the work-group calls it.
+template <typename Int>
+__device__ __forceinline__ Int sum_256(Int x, Int* red, Int* total) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  Int s = x;
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    const Int y = __shfl_up(s, o, 64);
+    if (lane >= o) s += y;
+  }
+  if (lane == 63 && wave < 4) red[wave] = s;
+  __syncthreads();
+  Int before = 0, all = 0;
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {
+    before += w < wave ? red[w] : 0;
+    all += red[w];
+  }
+  __syncthreads();
+  *total = all;
+  return before + s - x;
+}
+
+struct PlanScratch {
+  long long wide[4];
+  int sum[4];
+};
+
+// Fills p and the arrays it points to, by the work-group's first 256 threads
+// (every thread calls). scan / chunks: which sums are wanted.
+__device__ __forceinline__ void make_plan(const PagedArgs& a, int row_block, int chunk_min, bool scan, bool chunks,
+                                          PlanScratch& sc, Plan& p) {
+  const int tid = threadIdx.x;
+  const int G = a.H / a.H_kv;
+  if (scan) {
+    // Key visits of the row blocks, and rows times keys: the split length spreads
+    // the first over kTargetItems items and keeps the partial rows within the
+    // workspace (a split request has at most 2 total / chunk splits).
+    long long visits = 0, cells = 0;
+    for (int b = tid; b < a.S && tid < 256; b += 256) {
+      const Req r = scan_part(Req(a, b), chunk_min);
+      visits += (long long)((r.q * G + row_block - 1) / row_block) * a.H_kv * r.total;
+      cells += (long long)r.q * a.H * r.total;
+    }
+    long long n;
+    sum_256(visits, sc.wide, &n);
+    long long c = (n + kTargetItems - 1) / kTargetItems;
+    sum_256(cells, sc.wide, &n);
+    const long long c2 = (2 * n + kPartialRows - 1) / kPartialRows;
+    c = c > c2 ? c : c2;
+    c = c < kMinChunk ? kMinChunk : (c + 127) / 128 * 128;
+    p.chunk = (int)(c < kMaxChunk ? c : kMaxChunk);
+  }
+  int units = 0, parts = 0, merges = 0;
+  long long tiles = 0;
+  for (int b0 = 0; b0 < a.S; b0 += 256) {
+    const int b = b0 + tid;
+    const bool in = tid < 256 && b < a.S;
+    Req r;
+    r.q = 0;
+    if (in) r = Req(a, b);
+    if (scan) {
+      const Req s = scan_part(r, chunk_min);
+      const int splits = s.q > 0 ? splits_of(s.total, p.chunk) : 0;
+      const int rows = splits > 1 ? s.q * a.H : 0;
+      int n;
+      const int u = sum_256((s.q * G + row_block - 1) / row_block * splits, &sc.sum[0], &n);
+      if (in) p.unit_sum[b] = units + u;
+      units += n;
+      const int m = sum_256(rows, &sc.sum[0], &n);
+      if (in) p.merge_sum[b] = merges + m;
+      merges += n;
+      const int q = sum_256(rows * splits, &sc.sum[0], &n);
+      if (in) p.part_sum[b] = parts + q;
+      parts += n;
+    }
+    if (chunks) {
+      const Req s = chunk_part(r, chunk_min);
+      long long x = 0, n;
+      if (s.q > 0) {
+        const ChunkTiles t(s.total - s.q, s.total);
+        x = t.before(t.n) * a.H;
+      }
+      const long long at = sum_256(x, sc.wide, &n);
+      if (in) p.tile_sum[b] = tiles + at;
+      tiles += n;
+    }
+  }
+  p.units = units;
+  p.merge_rows = merges;
+  if (chunks && tid == 0) p.tile_sum[a.S] = tiles;
+}
+
+// The plan in the workspace, written by plan_kernel for more than kPlanInline
+// requests.
+struct WsPlan {
+  int* head;              // chunk, units, merge_rows
+  Plan p;
+  __device__ __forceinline__ WsPlan(const PagedArgs& a) {
+    char* w = static_cast<char*>(a.ws);
+    head = reinterpret_cast<int*>(w);
+    w += kPlanHeader;
+    const int64_t n = paged_sum_bytes(a.S, 4);
+    p.unit_sum = reinterpret_cast<int*>(w);
+    p.part_sum = reinterpret_cast<int*>(w + n);
+    p.merge_sum = reinterpret_cast<int*>(w + 2 * n);
+    p.tile_sum = reinterpret_cast<long long*>(w + 3 * n);
+  }
+};
+
+// A kernel's plan: formed in LDS by each work-group for up to kPlanInline
+// requests (2 us; a launch of its own and the wait for it take 5), else read
+// from the workspace.
+struct PlanLds {
+  PlanScratch sc;
+  int unit_sum[kPlanInline + 1], part_sum[kPlanInline + 1], merge_sum[kPlanInline + 1];
+  long long tile_sum[kPlanInline + 1];
+};
+__device__ __forceinline__ Plan load_plan(const PagedArgs& a, int row_block, int chunk_min, bool scan, bool chunks,
+                                          PlanLds& lds) {
+  if (a.S > kPlanInline) {
+    WsPlan w(a);
+    w.p.chunk = uni(w.head[0]);
+    w.p.units = uni(w.head[1]);
+    w.p.merge_rows = uni(w.head[2]);
+    return w.p;
+  }
+  Plan p{};
+  p.unit_sum = lds.unit_sum;
+  p.part_sum = lds.part_sum;
+  p.merge_sum = lds.merge_sum;
+  p.tile_sum = lds.tile_sum;
+  make_plan(a, row_block, chunk_min, scan, chunks, lds.sc, p);
+  __syncthreads();
+  p.chunk = uni(p.chunk);
+  p.units = uni(p.units);
+  p.merge_rows = uni(p.merge_rows);
+  return p;
+}
+
+// Partial states in the workspace: of the scan's split histories, and of the
+// long chunks' divided tiles.
+struct States {
+  float2* ml;
+  float* z;
+  __device__ __forceinline__ static States scan(const PagedArgs& a) {
+    char* w = static_cast<char*>(a.ws) + paged_plan_bytes(a.S);
+    return {reinterpret_cast<float2*>(w), reinterpret_cast<float*>(w + kPartialRows * sizeof(float2))};
+  }
+  __device__ __forceinline__ static States chunk(const PagedArgs& a) {
+    char* w = static_cast<char*>(a.ws) + paged_plan_bytes(a.S) + paged_scan_bytes(a.d_h);
+    return {reinterpret_cast<float2*>(w), reinterpret_cast<float*>(w + (int64_t)kChunkStates * 256 * sizeof(float2))};
+  }
+};
 
 // The last request b with off[b] <= i: 64 entries are compared at a time.
 template <typename Int>
@@ -78,49 +273,11 @@ __device__ __forceinline__ int find_request(const Int* off, int S, Int i) {
 
 // ---- long chunks --------------------------------------------------------------
 
-// Query tiles of a request's chunk: 256 positions each from ctx rounded down to
-// a multiple of 64, so that 64-key tiles never straddle a tile's first position
-// and a tile's own keys are four key tiles. Tile k needs the key tiles below
-// its last position's next: all but the last tile base64 + 4 (k + 1).
-struct ChunkTiles {
-  int base64, n, last;         // first position / 64, tiles, key tiles of the last tile
-  __device__ __forceinline__ ChunkTiles(int ctx, int total) {
-    base64 = ctx >> 6;
-    n = (int)(((long long)total - 64LL * base64 + 255) >> 8);
-    last = (int)(((long long)total + 63) >> 6);
-  }
-  // Key tiles of the tiles before k.
-  __device__ __forceinline__ long long before(int k) const {
-    const long long full = (long long)k * base64 + 2LL * k * (k + 1);
-    return k < n ? full : (long long)(n - 1) * base64 + 2LL * (n - 1) * n + last;
-  }
-  __device__ __forceinline__ int keys(int k) const { return k + 1 < n ? base64 + 4 * (k + 1) : last; }
-};
-
-// Whether the request's rows go to the long-chunk kernel.
-__device__ __forceinline__ bool is_chunk(const Req& r, int chunk_min) { return chunk_min > 0 && r.q >= chunk_min; }
-
-// The long-chunk part of the workspace: exclusive sums of key tiles over the
-// requests (all heads; [S] the total) and the partial states, 256 rows each, two
-// per work-group.
-struct ChunkWs {
-  long long* units;
-  float2* ml;
-  float* z;
-  __host__ __device__ ChunkWs(void* ws, int S, int d_h) {
-    char* p = static_cast<char*>(ws) + paged_scan_bytes(S, d_h);
-    units = reinterpret_cast<long long*>(p);
-    p += paged_chunk_sum_bytes(S);
-    ml = reinterpret_cast<float2*>(p);
-    z = reinterpret_cast<float*>(p + (int64_t)kChunkStates * 256 * sizeof(float2));
-  }
-};
-
 // A unit is one key tile of one query tile; the units of all query tiles (per
-// request, per head, tile by tile) form one line that is cut into equal ranges,
-// one per work-group, whatever the requests' lengths. A segment is the part of a
-// query tile's key tiles in one range: [tb, te), te = 0 for none. slot: the
-// partial state it leaves, or -1 when it holds all of them.
+// request, per head, tile by tile) form one line that is cut into equal ranges
+// of at least 8, one per work-group, whatever the requests' lengths. A segment
+// is the part of a query tile's key tiles in one range: [tb, te), te = 0 for
+// none. slot: the partial state it leaves, or -1 when it holds all of them.
 struct Segment {
   int b, h, kvh;
   int first, ctx, total;       // packed token of the chunk's first row, its position, cached rows
@@ -131,29 +288,23 @@ struct Segment {
   }
 };
 
-// Equal ranges of at least 8 units.
-struct Ranges {
-  long long units, per;
-  __device__ __forceinline__ Ranges(const PagedArgs& a, int groups) {
-    units = ChunkWs(a.ws, a.S, a.d_h).units[a.S];
-    per = (units + groups - 1) / groups;
-    per = per < 8 ? 8 : per;
-  }
-};
+__device__ __forceinline__ long long range_length(long long units, int groups) {
+  const long long per = (units + groups - 1) / groups;
+  return per < 8 ? 8 : per;
+}
 
 // The query tile of unit u: its request and head, its index within them, and
 // the unit of its first key tile.
 struct TileOf {
   int b, h, tile, keys;
   long long start;
-  __device__ __forceinline__ TileOf(const PagedArgs& a, long long u, Req* req) {
-    const long long* sums = ChunkWs(a.ws, a.S, a.d_h).units;
-    b = find_request(sums, a.S, u);
-    const Req r(a, b);
-    *req = r;
+  Req r;
+  __device__ __forceinline__ TileOf(const PagedArgs& a, const Plan& p, long long u) {
+    b = find_request(p.tile_sum, a.S, u);
+    r = chunk_part(Req(a, b), kChunkMin);
     const ChunkTiles t(r.total - r.q, r.total);
     const long long per_head = t.before(t.n);
-    const long long v = u - sums[b];
+    const long long v = u - p.tile_sum[b];
     h = (int)(v / per_head);
     const long long w = v - h * per_head;
     int lo = 0, hi = t.n - 1;                            // the last tile that starts at or before w
@@ -164,7 +315,7 @@ struct TileOf {
     }
     tile = lo;
     keys = t.keys(tile);
-    start = sums[b] + h * per_head + t.before(tile);
+    start = p.tile_sum[b] + h * per_head + t.before(tile);
   }
 };
 
@@ -173,25 +324,26 @@ struct TileOf {
 // which read the same keys, share its L2.
 struct SegmentSource {
   const PagedArgs& a;
+  const Plan& p;
   long long u, end;
   int me;
-  __device__ __forceinline__ SegmentSource(const PagedArgs& args, int group, int groups) : a(args) {
+  __device__ __forceinline__ SegmentSource(const PagedArgs& args, const Plan& plan, int group, int groups)
+      : a(args), p(plan) {
     me = groups % 8 == 0 ? (group & 7) * (groups >> 3) + (group >> 3) : group;
-    const Ranges r(args, groups);
-    u = me * r.per;
-    end = u + r.per < r.units ? u + r.per : r.units;
+    const long long units = p.tile_sum[a.S], per = range_length(units, groups);
+    u = me * per;
+    end = u + per < units ? u + per : units;
   }
   __device__ __forceinline__ Segment next() {
     Segment s{};
     if (u >= end) return s;
-    Req r;
-    const TileOf t(a, u, &r);
+    const TileOf t(a, p, u);
     s.b = t.b;
     s.h = t.h;
     s.kvh = t.h / (a.H / a.H_kv);
-    s.first = r.first;
-    s.total = r.total;
-    s.ctx = r.total - r.q;
+    s.first = t.r.first;
+    s.total = t.r.total;
+    s.ctx = t.r.total - t.r.q;
     s.q0 = (s.ctx & ~63) + 256 * t.tile;
     s.tb = (int)(u - t.start);
     const long long stop = t.start + t.keys < end ? t.start + t.keys : end;
@@ -265,6 +417,26 @@ __device__ __forceinline__ void finish_row(const PagedArgs& a, const HeadParams&
 #pragma unroll
   for (int e = 0; e < 8; ++e) y[e] = c.w_self * v[e] + c.w_hist * z[e];
   store8(static_cast<Tin*>(a.Y) + ((size_t)t * a.H + h) * D + col, y);
+}
+
+// A partial state at row `at` of st joined to (M, L, z), 16 lanes of 8 columns.
+template <int D>
+__device__ __forceinline__ void join_state(const States& st, int64_t at, int sl, float& M, float& L, float (&z)[8]) {
+  const float2 ml = st.ml[at];
+  f32x4 x = {0.0f, 0.0f, 0.0f, 0.0f}, y = x;
+  if (sl < D / 8) {
+    x = reinterpret_cast<const f32x4*>(st.z + at * D + 8 * sl)[0];
+    y = reinterpret_cast<const f32x4*>(st.z + at * D + 8 * sl)[1];
+  }
+  const float Mn = fmaxf(M, ml.x);
+  const float fo = __builtin_amdgcn_exp2f(M - Mn), fn = __builtin_amdgcn_exp2f(ml.x - Mn);
+  M = Mn;
+  L = L * fo + ml.y * fn;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    z[e] = z[e] * fo + x[e] * fn;
+    z[4 + e] = z[4 + e] * fo + y[e] * fn;
+  }
 }
 
 }  // namespace paged

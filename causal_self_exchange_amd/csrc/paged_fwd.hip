@@ -25,161 +25,17 @@ using namespace paged;
 constexpr int kWaves = 4;
 constexpr int kThreads = 64 * kWaves;
 constexpr int kStep = 32;                 // keys of a wave's step
-constexpr int kMinChunk = 256;            // keys of the shortest split
-constexpr int kTargetItems = 1024;        // work items wanted of one call
 constexpr float kLazy = 32.0f;            // log2 slack before the stabiliser moves
 
-// ---- plan ---------------------------------------------------------------------
-
-struct Sum4 { int v[kPlanSums]; };
-
-// Exclusive sums over the work-group of four counts at once, and their totals.
-__device__ __forceinline__ Sum4 block_sums(const Sum4& x, Sum4* red, Sum4* total) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  Sum4 s = x;
-#pragma unroll
-  for (int o = 1; o < 64; o <<= 1)
-#pragma unroll
-    for (int k = 0; k < kPlanSums; ++k) {
-      const int y = __shfl_up(s.v[k], o, 64);
-      if (lane >= o) s.v[k] += y;
-    }
-  __syncthreads();
-  if (lane == 63) red[wave] = s;
-  __syncthreads();
-  Sum4 out;
-#pragma unroll
-  for (int k = 0; k < kPlanSums; ++k) {
-    int before = 0, all = 0;
-#pragma unroll
-    for (int w = 0; w < kWaves; ++w) {
-      before += w < wave ? red[w].v[k] : 0;
-      all += red[w].v[k];
-    }
-    total->v[k] = all;
-    out.v[k] = before + s.v[k] - x.v[k];
+__global__ __launch_bounds__(kThreads) void plan_kernel(PagedArgs a, int row_block, int chunk_min) {
+  __shared__ PlanScratch sc;
+  WsPlan w(a);
+  make_plan(a, row_block, chunk_min, true, chunk_min > 0, sc, w.p);
+  if (threadIdx.x == 0) {
+    w.head[0] = w.p.chunk;
+    w.head[1] = w.p.units;
+    w.head[2] = w.p.merge_rows;
   }
-  return out;
-}
-
-// Exclusive sum over the work-group of one 64-bit count, and its total.
-__device__ __forceinline__ long long block_sum(long long x, long long* red, long long* total) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  long long s = x;
-#pragma unroll
-  for (int o = 1; o < 64; o <<= 1) {
-    const long long y = __shfl_up(s, o, 64);
-    if (lane >= o) s += y;
-  }
-  __syncthreads();
-  if (lane == 63) red[wave] = s;
-  __syncthreads();
-  long long before = 0, all = 0;
-#pragma unroll
-  for (int w = 0; w < kWaves; ++w) {
-    before += w < wave ? red[w] : 0;
-    all += red[w];
-  }
-  *total = all;
-  return before + s - x;
-}
-
-// rb[c]: rows per block of class c; a request belongs to class 0 when one block
-// of 16 holds its rows, to the long chunks with chunk_min new tokens (0: to
-// neither), and to class 1 otherwise.
-__global__ __launch_bounds__(kThreads) void plan_kernel(PagedArgs a, int rb0, int rb1, int chunk_min) {
-  __shared__ long long red_w[2][kWaves];
-  __shared__ Sum4 red[kWaves];
-  const Ws ws(a.ws, a.S);
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-
-  // Key visits of the row blocks, and rows times keys: the split length spreads
-  // the first over kTargetItems items and keeps the partial rows within the
-  // workspace (a split request has at most 2 total / chunk splits).
-  long long visits = 0, cells = 0;
-  for (int b = tid; b < a.S; b += kThreads) {
-    const Req r(a, b);
-    if (is_chunk(r, chunk_min)) continue;
-    const int rb = r.rows <= rb0 ? rb0 : rb1;
-    visits += (long long)((r.rows + rb - 1) / rb) * a.H_kv * r.total;
-    cells += (long long)r.q * a.H * r.total;
-  }
-#pragma unroll
-  for (int o = 1; o < 64; o <<= 1) {
-    visits += __shfl_xor(visits, o, 64);
-    cells += __shfl_xor(cells, o, 64);
-  }
-  if (lane == 0) {
-    red_w[0][wave] = visits;
-    red_w[1][wave] = cells;
-  }
-  __syncthreads();
-  visits = cells = 0;
-#pragma unroll
-  for (int w = 0; w < kWaves; ++w) {
-    visits += red_w[0][w];
-    cells += red_w[1][w];
-  }
-  long long c = (visits + kTargetItems - 1) / kTargetItems;
-  const long long c2 = (2 * cells + kPartialRows - 1) / kPartialRows;
-  c = c > c2 ? c : c2;
-  c = c < kMinChunk ? kMinChunk : c;
-  c = (c + 127) / 128 * 128;
-  const int chunk = (int)(c < kMaxChunk ? c : kMaxChunk);
-
-  Sum4 base = {{0, 0, 0, 0}}, all;
-  for (int b0 = 0; b0 < a.S; b0 += kThreads) {
-    const int b = b0 + tid;
-    Sum4 x = {{0, 0, 0, 0}};
-    if (b < a.S) {
-      const Req r(a, b);
-      const int cls = r.rows <= rb0 ? 0 : 1;
-      const int rb = cls ? rb1 : rb0;
-      const int splits = splits_of(r.total, chunk);
-      if (r.rows > 0 && !is_chunk(r, chunk_min)) {
-        x.v[cls] = (r.rows + rb - 1) / rb * splits;
-        if (splits > 1) {
-          x.v[3] = r.q * a.H;
-          x.v[2] = x.v[3] * splits;
-        }
-      }
-    }
-    const Sum4 at = block_sums(x, red, &all);
-    if (b < a.S) {
-      ws.units[0][b] = base.v[0] + at.v[0];
-      ws.units[1][b] = base.v[1] + at.v[1];
-      ws.part[b] = base.v[2] + at.v[2];
-      ws.merge[b] = base.v[3] + at.v[3];
-    }
-#pragma unroll
-    for (int k = 0; k < kPlanSums; ++k) base.v[k] += all.v[k];
-  }
-  if (tid == 0) {
-    ws.plan->chunk = chunk;
-    ws.plan->units[0] = base.v[0];
-    ws.plan->units[1] = base.v[1];
-    ws.plan->merge_rows = base.v[3];
-  }
-  if (chunk_min == 0) return;
-
-  // Key tiles of the long chunks, all heads.
-  const ChunkWs cw(a.ws, a.S, a.d_h);
-  long long sum = 0, n;
-  for (int b0 = 0; b0 < a.S; b0 += kThreads) {
-    const int b = b0 + tid;
-    long long x = 0;
-    if (b < a.S) {
-      const Req r(a, b);
-      if (is_chunk(r, chunk_min)) {
-        const ChunkTiles t(r.total - r.q, r.total);
-        x = t.before(t.n) * a.H;
-      }
-    }
-    const long long at = block_sum(x, red_w[0], &n);
-    if (b < a.S) cw.units[b] = sum + at;
-    sum += n;
-  }
-  if (tid == 0) cw.units[a.S] = sum;
 }
 
 // ---- scan ---------------------------------------------------------------------
@@ -209,18 +65,25 @@ struct Geom {
   static constexpr int kLds = kRing > kZBytes ? kRing : kZBytes;
 };
 
+// Work-groups per compute unit: as many as the LDS ring and the registers of
+// the row blocks admit.
 template <typename Tin, int D, int NB>
-__global__ __launch_bounds__(kThreads, NB == 1 ? 2 : 1) void scan_kernel(PagedArgs a, HeadParams hp, int cls) {
+constexpr int kPerCu = sizeof(Tin) == 4 && D == 128 && NB == 2 ? 1 : (D <= 64 && NB == 1 ? 4 : 2);
+
+template <typename Tin, int D, int NB>
+__global__ __launch_bounds__(kThreads, (kPerCu<Tin, D, NB>)) void scan_kernel(PagedArgs a, HeadParams hp, int chunk_min) {
   using C = Geom<Tin, D>;
   constexpr bool kBf = C::kBf;
   constexpr int kRb = 16 * NB;
   constexpr int kEs = (int)sizeof(Tin);
   __shared__ __attribute__((aligned(16))) char smem[C::kLds];
   __shared__ float s_m[kWaves][16], s_l[kWaves][16];
+  __shared__ PlanLds lds;
 
-  const Ws ws(a.ws, a.S);
-  const int n_items = uni(ws.plan->units[cls]) * a.H_kv;
-  const int chunk = uni(ws.plan->chunk);
+  const Plan plan = load_plan(a, kRb, chunk_min, true, false, lds);
+  const int n_items = plan.units * a.H_kv;
+  const int chunk = plan.chunk;
+  const States states = States::scan(a);
   const int G = a.H / a.H_kv;
   const int tid = threadIdx.x;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -236,21 +99,21 @@ __global__ __launch_bounds__(kThreads, NB == 1 ? 2 : 1) void scan_kernel(PagedAr
   for (int it = blockIdx.x; it < 8 * per; it += gridDim.x) {
     const int item = (it & 7) * per + (it >> 3);
     if (item >= n_items) continue;
-    const int b = find_request(ws.units[cls], a.S, item / a.H_kv);
-    Req r(a, b);
+    const int b = find_request(plan.unit_sum, a.S, item / a.H_kv);
+    Req r = scan_part(Req(a, b), chunk_min);
     r.first = uni(r.first);
     r.q = uni(r.q);
     r.total = uni(r.total);
-    r.rows = uni(r.rows);
-    const int nrb = (r.rows + kRb - 1) / kRb;
+    const int all_rows = r.q * G;
+    const int nrb = (all_rows + kRb - 1) / kRb;
     const int nsplit = splits_of(r.total, chunk);
-    const int local = item - uni(ws.units[cls][b]) * a.H_kv;   // 0 .. nrb * nsplit * H_kv - 1
+    const int local = item - uni(plan.unit_sum[b]) * a.H_kv;   // 0 .. nrb * nsplit * H_kv - 1
     const int rb = local % nrb;
     const int kvh = (local / nrb) % a.H_kv;
     const int split = local / nrb / a.H_kv;
     const int ctx = r.total - r.q;
     const int row0 = rb * kRb;
-    const int rows = min(kRb, r.rows - row0);
+    const int rows = min(kRb, all_rows - row0);
     const int pos_lo = ctx + row0 / G, pos_hi = ctx + (row0 + rows - 1) / G;
     const int k0 = split * chunk;
     if (split > 0 && k0 >= pos_hi) continue;        // no keys; the merge does not read this state
@@ -308,7 +171,8 @@ __global__ __launch_bounds__(kThreads, NB == 1 ? 2 : 1) void scan_kernel(PagedAr
       return static_cast<const char*>(cache) + row * D * kEs;
     };
 
-    u32x4 kf[2][2][C::kKs];                         // P2 rows of this step and the next
+    constexpr int kBuf = kBf ? 2 : 1;
+    u32x4 kf[kBuf][2][C::kKs];                      // P2 rows of this step (bf16: and the next)
     float vf[2][4][C::kDb];                         // fp32: V rows of the step
     char* const ring = smem + wave * 2 * C::kVTile;
     auto fetch = [&](int n, int buf) __attribute__((always_inline)) {
@@ -473,24 +337,29 @@ __global__ __launch_bounds__(kThreads, NB == 1 ? 2 : 1) void scan_kernel(PagedAr
       }
     };
 
-    // One step ahead: the next step's loads are issued once this step's have
-    // landed and the LDS reads of the step before are done.
-    if (nsteps > 0) fetch(0, 0);
-    for (int n = 0; n < nsteps; n += 2) {
+    if constexpr (kBf) {
+      // One step ahead: the next step's loads are issued once this step's have
+      // landed and the LDS reads of the step before are done.
+      if (nsteps > 0) fetch(0, 0);
+      for (int n = 0; n < nsteps; n += 2) {
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        if (n + u < nsteps) {
-          if constexpr (kBf) {
+        for (int u = 0; u < 2; ++u) {
+          if (n + u < nsteps) {
             asm volatile("" ::: "memory");
             wait_vm_lgkm<0, 0>();
             asm volatile("" ::: "memory");
             __builtin_amdgcn_sched_barrier(0);
+            if (n + u + 1 < nsteps) fetch(n + u + 1, u ^ 1);
+            __builtin_amdgcn_sched_barrier(0);
+            compute(n + u, u);
           }
-          fetch_v(n + u);
-          if (n + u + 1 < nsteps) fetch(n + u + 1, u ^ 1);
-          __builtin_amdgcn_sched_barrier(0);
-          compute(n + u, u);
         }
+      }
+    } else {
+      for (int n = 0; n < nsteps; ++n) {
+        fetch(n, 0);
+        fetch_v(n);
+        compute(n, 0);
       }
     }
 
@@ -544,11 +413,11 @@ __global__ __launch_bounds__(kThreads, NB == 1 ? 2 : 1) void scan_kernel(PagedAr
       if (nsplit == 1) {
         finish_row<Tin, D>(a, hp, b, r.first + tq, h, ctx + tq, sl, M, L, zs, ok);
       } else if (ok) {
-        const int64_t p = (int64_t)ws.part[b] + (int64_t)split * r.rows * a.H_kv + (int64_t)kvh * r.rows + row;
-        if (sl == 0) ws.ml[p] = make_float2(M, L);
+        const int64_t p = (int64_t)plan.part_sum[b] + (int64_t)split * all_rows * a.H_kv + (int64_t)kvh * all_rows + row;
+        if (sl == 0) states.ml[p] = make_float2(M, L);
         if (sl < D / 8) {
-          reinterpret_cast<f32x4*>(ws.z + p * D + 8 * sl)[0] = f32x4{zs[0], zs[1], zs[2], zs[3]};
-          reinterpret_cast<f32x4*>(ws.z + p * D + 8 * sl)[1] = f32x4{zs[4], zs[5], zs[6], zs[7]};
+          reinterpret_cast<f32x4*>(states.z + p * D + 8 * sl)[0] = f32x4{zs[0], zs[1], zs[2], zs[3]};
+          reinterpret_cast<f32x4*>(states.z + p * D + 8 * sl)[1] = f32x4{zs[4], zs[5], zs[6], zs[7]};
         }
       }
     }
@@ -556,47 +425,32 @@ __global__ __launch_bounds__(kThreads, NB == 1 ? 2 : 1) void scan_kernel(PagedAr
   }
 }
 
-// ---- merge --------------------------------------------------------------------
+// ---- join ---------------------------------------------------------------------
 
-// One work-group per row: 16 groups of 16 lanes each join every 16th split, the
-// groups join in LDS in their order, and the first group finishes the row.
+// One work-group's rows of split histories: per row, 16 groups of 16 lanes join
+// every 16th split, the groups join in LDS in their order, and the first group
+// finishes the row.
 template <typename Tin, int D>
-__global__ __launch_bounds__(kThreads) void merge_kernel(PagedArgs a, HeadParams hp) {
-  __shared__ float s_m[16], s_l[16], s_z[16][D + 4];
-  const Ws ws(a.ws, a.S);
-  const int n = ws.plan->merge_rows;
-  const int chunk = ws.plan->chunk;
+__device__ __forceinline__ void join_rows(const PagedArgs& a, const HeadParams& hp, const Plan& plan, int chunk_min,
+                                          int group, int groups, float (&s_m)[16], float (&s_l)[16],
+                                          float (&s_z)[16][D + 4]) {
+  const States st = States::scan(a);
   const int G = a.H / a.H_kv;
   const int g = threadIdx.x >> 4, sl = threadIdx.x & 15;
-  for (int i = blockIdx.x; i < n; i += gridDim.x) {
-    const int b = find_request(ws.merge, a.S, i);
-    const Req r(a, b);
-    const int id = i - ws.merge[b];                 // kvh * rows + row
-    const int kvh = id / r.rows, row = id - kvh * r.rows;
+  for (int i = group; i < plan.merge_rows; i += groups) {
+    const int b = find_request(plan.merge_sum, a.S, i);
+    const Req r = scan_part(Req(a, b), chunk_min);
+    const int all_rows = r.q * G;
+    const int id = i - plan.merge_sum[b];           // kvh * all_rows + row
+    const int kvh = id / all_rows, row = id - kvh * all_rows;
     const int tq = row / G, h = kvh * G + row - tq * G;
     const int pos = r.total - r.q + tq;
-    const int ns = (int)(((long long)pos + chunk - 1) / chunk);   // splits with keys of this row
+    const int ns = (int)(((long long)pos + plan.chunk - 1) / plan.chunk);   // splits with keys of this row
     float M = kEmptyMax, L = 0.0f, z[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) z[e] = 0.0f;
-    for (int s = g; s < ns; s += 16) {
-      const int64_t p = (int64_t)ws.part[b] + (int64_t)s * r.rows * a.H_kv + id;
-      const float2 ml = ws.ml[p];
-      f32x4 x = {0.0f, 0.0f, 0.0f, 0.0f}, y = x;
-      if (sl < D / 8) {
-        x = reinterpret_cast<const f32x4*>(ws.z + p * D + 8 * sl)[0];
-        y = reinterpret_cast<const f32x4*>(ws.z + p * D + 8 * sl)[1];
-      }
-      const float Mn = fmaxf(M, ml.x);
-      const float fo = __builtin_amdgcn_exp2f(M - Mn), fn = __builtin_amdgcn_exp2f(ml.x - Mn);
-      M = Mn;
-      L = L * fo + ml.y * fn;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        z[e] = z[e] * fo + x[e] * fn;
-        z[4 + e] = z[4 + e] * fo + y[e] * fn;
-      }
-    }
+    for (int s = g; s < ns; s += 16)
+      join_state<D>(st, (int64_t)plan.part_sum[b] + (int64_t)s * all_rows * a.H_kv + id, sl, M, L, z);
     __syncthreads();
     if (sl == 0) {
       s_m[g] = M;
@@ -613,7 +467,7 @@ __global__ __launch_bounds__(kThreads) void merge_kernel(PagedArgs a, HeadParams
       for (int e = 0; e < 8; ++e) z[e] = 0.0f;
 #pragma unroll
       for (int k = 0; k < 16; ++k) M = fmaxf(M, s_m[k]);
-      for (int k = 0; k < 16; ++k) {
+      for (int k = 0; k < min(ns, 16); ++k) {
         const float f = __builtin_amdgcn_exp2f(s_m[k] - M);
         L = fmaf(f, s_l[k], L);
         if (sl < D / 8)
@@ -625,33 +479,81 @@ __global__ __launch_bounds__(kThreads) void merge_kernel(PagedArgs a, HeadParams
   }
 }
 
+// 16 rows of the query tile that the cut before range k divides, if that is the
+// first cut inside it: 16 lanes per row.
 template <typename Tin, int D>
-hipError_t launch_typed(const PagedArgs& a, const HeadParams& hp, hipStream_t s) {
-  constexpr int kNb1 = sizeof(Tin) == 2 ? 4 : 2;
+__device__ __forceinline__ void join_tile(const PagedArgs& a, const HeadParams& hp, const Plan& plan, int k, int rows16,
+                                          int chunk_groups) {
+  const long long units = plan.tile_sum[a.S], per = range_length(units, chunk_groups);
+  const long long cut = k * per;
+  if (cut >= units) return;
+  const TileOf t(a, plan, cut);
+  if (t.start >= cut || cut - per > t.start) return;    // between two tiles, or an earlier cut's tile
+  const States st = States::chunk(a);
+  const int sl = threadIdx.x & 15, i = 16 * rows16 + (threadIdx.x >> 4);
+  const int ctx = t.r.total - t.r.q;
+  const int pos = (ctx & ~63) + 256 * t.tile + i;
+  const int pieces = (int)((t.start + t.keys - cut + per - 1) / per) + 1;
+  float M = kEmptyMax, L = 0.0f, z[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) z[e] = 0.0f;
+  // Piece 0 is the last of range k - 1, the others the first of ranges k, k + 1, ...
+#pragma unroll 4
+  for (int p = 0; p < pieces; ++p)
+    join_state<D>(st, (int64_t)(p == 0 ? 2 * (k - 1) + 1 : 2 * (k - 1 + p)) * 256 + i, sl, M, L, z);
+  finish_row<Tin, D>(a, hp, t.b, t.r.first + (pos - ctx), t.h, pos, sl, M, L, z, pos >= ctx && pos < t.r.total);
+}
+
+// The first row_groups work-groups join the scan's split histories, the others
+// 16 rows each of the long chunks' divided tiles.
+template <typename Tin, int D>
+__global__ __launch_bounds__(kThreads) void join_kernel(PagedArgs a, HeadParams hp, int row_block, int chunk_min,
+                                                        int row_groups, int chunk_groups) {
+  __shared__ PlanLds lds;
+  __shared__ float s_m[16], s_l[16], s_z[16][D + 4];
+  const bool rows = (int)blockIdx.x < row_groups;
+  const Plan plan = load_plan(a, row_block, chunk_min, rows, !rows, lds);
+  if (rows) {
+    join_rows<Tin, D>(a, hp, plan, chunk_min, blockIdx.x, row_groups, s_m, s_l, s_z);
+  } else if constexpr (sizeof(Tin) == 2) {
+    const int i = (int)blockIdx.x - row_groups;
+    join_tile<Tin, D>(a, hp, plan, 1 + i / 16, i % 16, chunk_groups);
+  }
+}
+
+template <typename Tin, int D, int NB>
+hipError_t launch_rows(const PagedArgs& a, const HeadParams& hp, hipStream_t s) {
   int cu = 0;
   hipError_t e = device_cu_count(&cu);
   if (e != hipSuccess) return e;
   // Long chunks: bf16, with a token stride whose 256 rows a 31-bit byte offset
   // reaches.
   const bool chunks = sizeof(Tin) == 2 && a.max_new >= kChunkMin && a.N >= kChunkMin && a.ld1 < (1 << 22);
-  hipLaunchKernelGGL(plan_kernel, dim3(1), dim3(kThreads), 0, s, a, 16, 16 * kNb1, chunks ? kChunkMin : 0);
-  e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  if (chunks) {
-    e = launch_paged_chunk(a, hp, cu < kChunkGroups ? cu : kChunkGroups, s);
-    if (e != hipSuccess) return e;
-  }
-  const unsigned grid = 2u * (unsigned)cu;
-  hipLaunchKernelGGL((scan_kernel<Tin, D, 1>), dim3(grid), dim3(kThreads), 0, s, a, hp, 0);
-  e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  if ((long long)a.max_new * (a.H / a.H_kv) > 16) {
-    hipLaunchKernelGGL((scan_kernel<Tin, D, kNb1>), dim3(grid), dim3(kThreads), 0, s, a, hp, 1);
+  const int chunk_min = chunks ? kChunkMin : 0;
+  const int chunk_groups = chunks ? (cu < kChunkGroups ? cu : kChunkGroups) : 0;
+  if (a.S > kPlanInline) {
+    hipLaunchKernelGGL(plan_kernel, dim3(1), dim3(kThreads), 0, s, a, 16 * NB, chunk_min);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  hipLaunchKernelGGL((merge_kernel<Tin, D>), dim3(4 * grid), dim3(kThreads), 0, s, a, hp);
+  if (chunks) {
+    e = launch_paged_chunk(a, hp, chunk_groups, s);
+    if (e != hipSuccess) return e;
+  }
+  const unsigned grid = (unsigned)cu * kPerCu<Tin, D, NB>;
+  hipLaunchKernelGGL((scan_kernel<Tin, D, NB>), dim3(grid), dim3(kThreads), 0, s, a, hp, chunk_min);
+  e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  const int row_groups = 4 * cu;
+  hipLaunchKernelGGL((join_kernel<Tin, D>), dim3(row_groups + (chunks ? 16 * (chunk_groups - 1) : 0)), dim3(kThreads), 0, s,
+                     a, hp, 16 * NB, chunk_min, row_groups, chunk_groups);
   return hipGetLastError();
+}
+
+template <typename Tin, int D>
+hipError_t launch_typed(const PagedArgs& a, const HeadParams& hp, hipStream_t s) {
+  const long long rows = (long long)a.max_new * (a.H / a.H_kv);
+  return rows <= 16 ? launch_rows<Tin, D, 1>(a, hp, s) : launch_rows<Tin, D, 2>(a, hp, s);
 }
 
 }  // namespace

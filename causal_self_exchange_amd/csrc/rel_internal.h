@@ -174,30 +174,26 @@ struct PagedArgs {
   int N, S, H, H_kv, d_h, n_pages, page_shift, max_pages, max_new;
 };
 
-// Workspace of relation_paged_fwd: the work plan (a header and prefix sums over
-// the requests) and the partial states of split histories, at most
-// kPartialRows rows (m, l) and z[d_h].
-struct PagedPlan {
-  int chunk;            // keys per split, a multiple of 128
-  int units[2];         // work units of the two row classes (times H_kv work items)
-  int merge_rows;       // output rows with split histories
-};
-constexpr int kPlanSums = 4;                  // units of both classes, partial rows, merge rows
-constexpr int64_t kPartialRows = 32768;
+// Workspace of relation_paged_fwd (paged_device.h): the work plan of batches of
+// more than kPlanInline requests, the partial states of split histories, at
+// most kPartialRows rows (m, l) and z[d_h], and those of the long-chunk kernel
+// (bf16, requests with at least kChunkMin new tokens), 256 rows each, two per
+// work-group.
+constexpr int kPlanInline = 256;
 constexpr int64_t kPlanHeader = 256;
-inline __host__ __device__ int64_t paged_sum_bytes(int64_t S) { return ((S + 1) * 4 + 255) / 256 * 256; }
-inline __host__ __device__ int64_t paged_scan_bytes(int64_t S, int d_h) {
-  return (kPlanHeader + kPlanSums * paged_sum_bytes(S) + kPartialRows * (d_h + 2) * 4 + 255) / 256 * 256;
-}
-// The long-chunk kernel (bf16): requests with at least kChunkMin new tokens, on
-// at most kChunkGroups work-groups with two partial states of 256 rows each.
+constexpr int64_t kPartialRows = 32768;
 constexpr int kChunkMin = 128;
 constexpr int kChunkGroups = 256;
 constexpr int kChunkStates = 2 * kChunkGroups;
-inline __host__ __device__ int64_t paged_chunk_sum_bytes(int64_t S) { return ((S + 1) * 8 + 255) / 256 * 256; }
+// Three 32-bit and one 64-bit prefix sum over the requests.
+inline __host__ __device__ int64_t paged_sum_bytes(int64_t S, int size) { return ((S + 1) * size + 255) / 256 * 256; }
+inline __host__ __device__ int64_t paged_plan_bytes(int64_t S) {
+  return kPlanHeader + 3 * paged_sum_bytes(S, 4) + paged_sum_bytes(S, 8);
+}
+inline __host__ __device__ int64_t paged_scan_bytes(int d_h) { return kPartialRows * (d_h + 2) * 4; }
 inline size_t paged_ws_bytes(int64_t N, int64_t S, int d_h) {
-  const int64_t chunk = paged_chunk_sum_bytes(S) + (int64_t)kChunkStates * 256 * (d_h + 2) * 4;
-  return static_cast<size_t>(paged_scan_bytes(S, d_h) + (N >= kChunkMin ? chunk : 0));
+  return static_cast<size_t>(paged_plan_bytes(S) + paged_scan_bytes(d_h) +
+                             (N >= kChunkMin ? (int64_t)kChunkStates * 256 * (d_h + 2) * 4 : 0));
 }
 
 // Launchers (return the hipError_t of the launch).
@@ -240,7 +236,7 @@ hipError_t launch_cache_append(void* cP2, void* cV, int32_t* len, const void* p2
 hipError_t launch_page_map(const PageMapArgs& a, hipStream_t s);
 hipError_t launch_paged_append(const PagedAppendArgs& a, const PrestepParams& pp, bool bf16, hipStream_t s);
 hipError_t launch_paged(const PagedArgs& a, const HeadParams& hp, bool bf16, hipStream_t s);
-// The long chunks of the batch (bf16; the plan is in the workspace).
+// The long chunks of the batch (bf16), without the joining of divided tiles.
 hipError_t launch_paged_chunk(const PagedArgs& a, const HeadParams& hp, int groups, hipStream_t s);
 
 }  // namespace rel
