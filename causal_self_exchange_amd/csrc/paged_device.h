@@ -84,8 +84,15 @@ __device__ __forceinline__ Req scan_part(Req r, int chunk_min) {
 // over the requests.
 
 constexpr int kMinChunk = 512;            // keys of the shortest split
-constexpr int kTargetItems = 1024;        // work items wanted of one call
 constexpr int kMaxChunk = 0x7fffff80;     // stands for unsplit histories of any length
+
+// What the host fixes of it.
+struct Cut {
+  int row_block;          // rows per scan item
+  int chunk_min;          // new tokens from which a request is a long chunk; 0: none is
+  int scan_groups;        // work-groups of the scan kernel
+  int chunk_groups;       // and of the long-chunk kernel
+};
 
 struct Plan {
   int chunk, units, merge_rows;
@@ -130,23 +137,31 @@ struct PlanScratch {
 
 // Fills p and the arrays it points to, by the work-group's first 256 threads
 // (every thread calls). scan / chunks: which sums are wanted.
-__device__ __forceinline__ void make_plan(const PagedArgs& a, int row_block, int chunk_min, bool scan, bool chunks,
-                                          PlanScratch& sc, Plan& p) {
+__device__ __forceinline__ void make_plan(const PagedArgs& a, const Cut& cut, bool scan, bool chunks, PlanScratch& sc,
+                                          Plan& p) {
+  const int row_block = cut.row_block, chunk_min = cut.chunk_min;
   const int tid = threadIdx.x;
   const int G = a.H / a.H_kv;
   if (scan) {
-    // Key visits of the row blocks, and rows times keys: the split length spreads
-    // the first over kTargetItems items and keeps the partial rows within the
-    // workspace (a split request has at most 2 total / chunk splits).
-    long long visits = 0, cells = 0;
+    // Key visits of the row blocks, rows times keys, and the items without splits:
+    // a split length c makes at most visits / c + base items. They should fill the
+    // scan's work-groups a whole number of times, with as many again as there are
+    // at least: a few items past a round cost a round. The length also keeps the
+    // partial rows within the workspace (a split request has at most 2 total /
+    // chunk splits).
+    long long visits = 0, cells = 0, base = 0;
     for (int b = tid; b < a.S && tid < 256; b += 256) {
       const Req r = scan_part(Req(a, b), chunk_min);
-      visits += (long long)((r.q * G + row_block - 1) / row_block) * a.H_kv * r.total;
+      const long long blocks = (long long)((r.q * G + row_block - 1) / row_block) * a.H_kv;
+      visits += blocks * r.total;
+      base += blocks;
       cells += (long long)r.q * a.H * r.total;
     }
     long long n;
+    sum_256(base, sc.wide, &base);
     sum_256(visits, sc.wide, &n);
-    long long c = (n + kTargetItems - 1) / kTargetItems;
+    const long long room = (2 * base + cut.scan_groups - 1) / cut.scan_groups * cut.scan_groups - base;
+    long long c = room > 0 ? (n + room - 1) / room : 0;
     sum_256(cells, sc.wide, &n);
     const long long c2 = (2 * n + kPartialRows - 1) / kPartialRows;
     c = c > c2 ? c : c2;
@@ -218,8 +233,7 @@ struct PlanLds {
   int unit_sum[kPlanInline + 1], part_sum[kPlanInline + 1], merge_sum[kPlanInline + 1];
   long long tile_sum[kPlanInline + 1];
 };
-__device__ __forceinline__ Plan load_plan(const PagedArgs& a, int row_block, int chunk_min, bool scan, bool chunks,
-                                          PlanLds& lds) {
+__device__ __forceinline__ Plan load_plan(const PagedArgs& a, const Cut& cut, bool scan, bool chunks, PlanLds& lds) {
   if (a.S > kPlanInline) {
     WsPlan w(a);
     w.p.chunk = uni(w.head[0]);
@@ -232,7 +246,7 @@ __device__ __forceinline__ Plan load_plan(const PagedArgs& a, int row_block, int
   p.part_sum = lds.part_sum;
   p.merge_sum = lds.merge_sum;
   p.tile_sum = lds.tile_sum;
-  make_plan(a, row_block, chunk_min, scan, chunks, lds.sc, p);
+  make_plan(a, cut, scan, chunks, lds.sc, p);
   __syncthreads();
   p.chunk = uni(p.chunk);
   p.units = uni(p.units);
@@ -250,7 +264,7 @@ struct States {
     return {reinterpret_cast<float2*>(w), reinterpret_cast<float*>(w + kPartialRows * sizeof(float2))};
   }
   __device__ __forceinline__ static States chunk(const PagedArgs& a) {
-    char* w = static_cast<char*>(a.ws) + paged_plan_bytes(a.S) + paged_scan_bytes(a.d_h);
+    char* w = static_cast<char*>(a.ws) + paged_plan_bytes(a.S) + paged_scan_bytes(a.d_h) + kCutBytes;
     return {reinterpret_cast<float2*>(w), reinterpret_cast<float*>(w + (int64_t)kChunkStates * 256 * sizeof(float2))};
   }
 };
@@ -287,6 +301,14 @@ struct Segment {
     return Segment{uni(b), uni(h), uni(kvh), uni(first), uni(ctx), uni(total), uni(q0), uni(tb), uni(te), uni(slot)};
   }
 };
+
+// The query tile that the end of a work-group's range divides, for the join:
+// pieces = 0 when there is none. Piece 0 is the last segment of range k, the
+// others the first segments of the ranges after it.
+struct CutTile {
+  int pieces, b, h, first, ctx, total, q0, pad;
+};
+static_assert(sizeof(CutTile) == 32 && kChunkGroups * sizeof(CutTile) == kCutBytes, "workspace layout");
 
 __device__ __forceinline__ long long range_length(long long units, int groups) {
   const long long per = (units + groups - 1) / groups;
@@ -325,14 +347,19 @@ struct TileOf {
 struct SegmentSource {
   const PagedArgs& a;
   const Plan& p;
-  long long u, end;
+  long long u, end, per;
   int me;
   __device__ __forceinline__ SegmentSource(const PagedArgs& args, const Plan& plan, int group, int groups)
       : a(args), p(plan) {
     me = groups % 8 == 0 ? (group & 7) * (groups >> 3) + (group >> 3) : group;
-    const long long units = p.tile_sum[a.S], per = range_length(units, groups);
+    const long long units = p.tile_sum[a.S];
+    per = range_length(units, groups);
     u = me * per;
     end = u + per < units ? u + per : units;
+    if (threadIdx.x == 0) cuts()[me].pieces = 0;
+  }
+  __device__ __forceinline__ CutTile* cuts() const {
+    return reinterpret_cast<CutTile*>(static_cast<char*>(a.ws) + paged_plan_bytes(a.S) + paged_scan_bytes(a.d_h));
   }
   __device__ __forceinline__ Segment next() {
     Segment s{};
@@ -349,6 +376,8 @@ struct SegmentSource {
     const long long stop = t.start + t.keys < end ? t.start + t.keys : end;
     s.te = (int)(stop - t.start);
     s.slot = s.tb == 0 && s.te == t.keys ? -1 : (s.tb > 0 ? 2 * me : 2 * me + 1);
+    if (s.slot == 2 * me + 1 && threadIdx.x == 0)
+      cuts()[me] = CutTile{1 + (int)((t.start + t.keys - end + per - 1) / per), s.b, s.h, s.first, s.ctx, s.total, s.q0, 0};
     u = stop;
     return s;
   }

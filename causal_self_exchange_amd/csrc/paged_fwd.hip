@@ -27,10 +27,10 @@ constexpr int kThreads = 64 * kWaves;
 constexpr int kStep = 32;                 // keys of a wave's step
 constexpr float kLazy = 32.0f;            // log2 slack before the stabiliser moves
 
-__global__ __launch_bounds__(kThreads) void plan_kernel(PagedArgs a, int row_block, int chunk_min) {
+__global__ __launch_bounds__(kThreads) void plan_kernel(PagedArgs a, Cut cut) {
   __shared__ PlanScratch sc;
   WsPlan w(a);
-  make_plan(a, row_block, chunk_min, true, chunk_min > 0, sc, w.p);
+  make_plan(a, cut, true, cut.chunk_min > 0, sc, w.p);
   if (threadIdx.x == 0) {
     w.head[0] = w.p.chunk;
     w.head[1] = w.p.units;
@@ -71,7 +71,7 @@ template <typename Tin, int D, int NB>
 constexpr int kPerCu = sizeof(Tin) == 4 && D == 128 && NB == 2 ? 1 : (D <= 64 && NB == 1 ? 4 : 2);
 
 template <typename Tin, int D, int NB>
-__global__ __launch_bounds__(kThreads, (kPerCu<Tin, D, NB>)) void scan_kernel(PagedArgs a, HeadParams hp, int chunk_min) {
+__global__ __launch_bounds__(kThreads, (kPerCu<Tin, D, NB>)) void scan_kernel(PagedArgs a, HeadParams hp, Cut cut) {
   using C = Geom<Tin, D>;
   constexpr bool kBf = C::kBf;
   constexpr int kRb = 16 * NB;
@@ -80,7 +80,8 @@ __global__ __launch_bounds__(kThreads, (kPerCu<Tin, D, NB>)) void scan_kernel(Pa
   __shared__ float s_m[kWaves][16], s_l[kWaves][16];
   __shared__ PlanLds lds;
 
-  const Plan plan = load_plan(a, kRb, chunk_min, true, false, lds);
+  const int chunk_min = cut.chunk_min;
+  const Plan plan = load_plan(a, cut, true, false, lds);
   const int n_items = plan.units * a.H_kv;
   const int chunk = plan.chunk;
   const States states = States::scan(a);
@@ -427,17 +428,15 @@ __global__ __launch_bounds__(kThreads, (kPerCu<Tin, D, NB>)) void scan_kernel(Pa
 
 // ---- join ---------------------------------------------------------------------
 
-// One work-group's rows of split histories: per row, 16 groups of 16 lanes join
-// every 16th split, the groups join in LDS in their order, and the first group
-// finishes the row.
+// Rows of split histories, a wave each: four groups of 16 lanes join every
+// fourth split, then the groups join.
 template <typename Tin, int D>
 __device__ __forceinline__ void join_rows(const PagedArgs& a, const HeadParams& hp, const Plan& plan, int chunk_min,
-                                          int group, int groups, float (&s_m)[16], float (&s_l)[16],
-                                          float (&s_z)[16][D + 4]) {
+                                          int wave, int waves) {
   const States st = States::scan(a);
   const int G = a.H / a.H_kv;
-  const int g = threadIdx.x >> 4, sl = threadIdx.x & 15;
-  for (int i = group; i < plan.merge_rows; i += groups) {
+  const int lane = threadIdx.x & 63, g = lane >> 4, sl = lane & 15;
+  for (int i = wave; i < plan.merge_rows; i += waves) {
     const int b = find_request(plan.merge_sum, a.S, i);
     const Req r = scan_part(Req(a, b), chunk_min);
     const int all_rows = r.q * G;
@@ -449,75 +448,53 @@ __device__ __forceinline__ void join_rows(const PagedArgs& a, const HeadParams& 
     float M = kEmptyMax, L = 0.0f, z[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) z[e] = 0.0f;
-    for (int s = g; s < ns; s += 16)
+#pragma unroll 4
+    for (int s = g; s < ns; s += 4)
       join_state<D>(st, (int64_t)plan.part_sum[b] + (int64_t)s * all_rows * a.H_kv + id, sl, M, L, z);
-    __syncthreads();
-    if (sl == 0) {
-      s_m[g] = M;
-      s_l[g] = L;
+#pragma unroll
+    for (int o = 16; o < 64; o <<= 1) {
+      const float Mo = __shfl_xor(M, o), Mn = fmaxf(M, Mo);
+      const float f = __builtin_amdgcn_exp2f(M - Mn), fo = __builtin_amdgcn_exp2f(Mo - Mn);
+      L = L * f + __shfl_xor(L, o) * fo;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) z[e] = z[e] * f + __shfl_xor(z[e], o) * fo;
+      M = Mn;
     }
-    if (sl < D / 8)
-#pragma unroll
-      for (int e = 0; e < 8; ++e) s_z[g][8 * sl + e] = z[e];
-    __syncthreads();
-    if (threadIdx.x < 64) {                         // the first wave; its groups 1 to 3 only follow
-      M = kEmptyMax;
-      L = 0.0f;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) z[e] = 0.0f;
-#pragma unroll
-      for (int k = 0; k < 16; ++k) M = fmaxf(M, s_m[k]);
-      for (int k = 0; k < min(ns, 16); ++k) {
-        const float f = __builtin_amdgcn_exp2f(s_m[k] - M);
-        L = fmaf(f, s_l[k], L);
-        if (sl < D / 8)
-#pragma unroll
-          for (int e = 0; e < 8; ++e) z[e] = fmaf(f, s_z[k][8 * sl + e], z[e]);
-      }
-      finish_row<Tin, D>(a, hp, b, r.first + tq, h, pos, sl, M, L, z, g == 0);
-    }
+    finish_row<Tin, D>(a, hp, b, r.first + tq, h, pos, sl, M, L, z, g == 0);
   }
 }
 
-// 16 rows of the query tile that the cut before range k divides, if that is the
-// first cut inside it: 16 lanes per row.
+// 16 rows of the query tile that the end of range k of the long chunks divides,
+// 16 lanes per row.
 template <typename Tin, int D>
-__device__ __forceinline__ void join_tile(const PagedArgs& a, const HeadParams& hp, const Plan& plan, int k, int rows16,
-                                          int chunk_groups) {
-  const long long units = plan.tile_sum[a.S], per = range_length(units, chunk_groups);
-  const long long cut = k * per;
-  if (cut >= units) return;
-  const TileOf t(a, plan, cut);
-  if (t.start >= cut || cut - per > t.start) return;    // between two tiles, or an earlier cut's tile
+__device__ __forceinline__ void join_tile(const PagedArgs& a, const HeadParams& hp, int k, int rows16) {
+  const CutTile t = reinterpret_cast<const CutTile*>(static_cast<const char*>(a.ws) + paged_plan_bytes(a.S) +
+                                                     paged_scan_bytes(a.d_h))[k];
+  if (t.pieces == 0) return;
   const States st = States::chunk(a);
   const int sl = threadIdx.x & 15, i = 16 * rows16 + (threadIdx.x >> 4);
-  const int ctx = t.r.total - t.r.q;
-  const int pos = (ctx & ~63) + 256 * t.tile + i;
-  const int pieces = (int)((t.start + t.keys - cut + per - 1) / per) + 1;
+  const int pos = t.q0 + i;
+  const bool ok = pos >= t.ctx && pos < t.total;
   float M = kEmptyMax, L = 0.0f, z[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) z[e] = 0.0f;
-  // Piece 0 is the last of range k - 1, the others the first of ranges k, k + 1, ...
 #pragma unroll 4
-  for (int p = 0; p < pieces; ++p)
-    join_state<D>(st, (int64_t)(p == 0 ? 2 * (k - 1) + 1 : 2 * (k - 1 + p)) * 256 + i, sl, M, L, z);
-  finish_row<Tin, D>(a, hp, t.b, t.r.first + (pos - ctx), t.h, pos, sl, M, L, z, pos >= ctx && pos < t.r.total);
+  for (int p = 0; p < t.pieces; ++p)
+    join_state<D>(st, (int64_t)(p == 0 ? 2 * k + 1 : 2 * (k + p)) * 256 + i, sl, M, L, z);
+  finish_row<Tin, D>(a, hp, t.b, ok ? t.first + (pos - t.ctx) : 0, t.h, ok ? pos : 0, sl, M, L, z, ok);
 }
 
 // The first row_groups work-groups join the scan's split histories, the others
 // 16 rows each of the long chunks' divided tiles.
 template <typename Tin, int D>
-__global__ __launch_bounds__(kThreads) void join_kernel(PagedArgs a, HeadParams hp, int row_block, int chunk_min,
-                                                        int row_groups, int chunk_groups) {
+__global__ __launch_bounds__(kThreads) void join_kernel(PagedArgs a, HeadParams hp, Cut cut, int row_groups) {
   __shared__ PlanLds lds;
-  __shared__ float s_m[16], s_l[16], s_z[16][D + 4];
-  const bool rows = (int)blockIdx.x < row_groups;
-  const Plan plan = load_plan(a, row_block, chunk_min, rows, !rows, lds);
-  if (rows) {
-    join_rows<Tin, D>(a, hp, plan, chunk_min, blockIdx.x, row_groups, s_m, s_l, s_z);
+  if ((int)blockIdx.x < row_groups) {
+    const Plan plan = load_plan(a, cut, true, false, lds);
+    join_rows<Tin, D>(a, hp, plan, cut.chunk_min, blockIdx.x * kWaves + (threadIdx.x >> 6), row_groups * kWaves);
   } else if constexpr (sizeof(Tin) == 2) {
     const int i = (int)blockIdx.x - row_groups;
-    join_tile<Tin, D>(a, hp, plan, 1 + i / 16, i % 16, chunk_groups);
+    join_tile<Tin, D>(a, hp, i / 16, i % 16);
   }
 }
 
@@ -529,24 +506,22 @@ hipError_t launch_rows(const PagedArgs& a, const HeadParams& hp, hipStream_t s) 
   // Long chunks: bf16, with a token stride whose 256 rows a 31-bit byte offset
   // reaches.
   const bool chunks = sizeof(Tin) == 2 && a.max_new >= kChunkMin && a.N >= kChunkMin && a.ld1 < (1 << 22);
-  const int chunk_min = chunks ? kChunkMin : 0;
-  const int chunk_groups = chunks ? (cu < kChunkGroups ? cu : kChunkGroups) : 0;
+  const Cut cut{16 * NB, chunks ? kChunkMin : 0, cu * kPerCu<Tin, D, NB>, chunks ? (cu < kChunkGroups ? cu : kChunkGroups) : 0};
   if (a.S > kPlanInline) {
-    hipLaunchKernelGGL(plan_kernel, dim3(1), dim3(kThreads), 0, s, a, 16 * NB, chunk_min);
+    hipLaunchKernelGGL(plan_kernel, dim3(1), dim3(kThreads), 0, s, a, cut);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
   if (chunks) {
-    e = launch_paged_chunk(a, hp, chunk_groups, s);
+    e = launch_paged_chunk(a, hp, cut.chunk_groups, s);
     if (e != hipSuccess) return e;
   }
-  const unsigned grid = (unsigned)cu * kPerCu<Tin, D, NB>;
-  hipLaunchKernelGGL((scan_kernel<Tin, D, NB>), dim3(grid), dim3(kThreads), 0, s, a, hp, chunk_min);
+  hipLaunchKernelGGL((scan_kernel<Tin, D, NB>), dim3(cut.scan_groups), dim3(kThreads), 0, s, a, hp, cut);
   e = hipGetLastError();
   if (e != hipSuccess) return e;
-  const int row_groups = 4 * cu;
-  hipLaunchKernelGGL((join_kernel<Tin, D>), dim3(row_groups + (chunks ? 16 * (chunk_groups - 1) : 0)), dim3(kThreads), 0, s,
-                     a, hp, 16 * NB, chunk_min, row_groups, chunk_groups);
+  // The last range has no end inside a tile.
+  const int row_groups = 4 * cu, tile_groups = chunks ? 16 * (cut.chunk_groups - 1) : 0;
+  hipLaunchKernelGGL((join_kernel<Tin, D>), dim3(row_groups + tile_groups), dim3(kThreads), 0, s, a, hp, cut, row_groups);
   return hipGetLastError();
 }
 

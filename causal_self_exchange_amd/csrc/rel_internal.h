@@ -185,6 +185,7 @@ constexpr int64_t kPartialRows = 32768;
 constexpr int kChunkMin = 128;
 constexpr int kChunkGroups = 256;
 constexpr int kChunkStates = 2 * kChunkGroups;
+constexpr int64_t kCutBytes = 32 * kChunkGroups;
 // Three 32-bit and one 64-bit prefix sum over the requests.
 inline __host__ __device__ int64_t paged_sum_bytes(int64_t S, int size) { return ((S + 1) * size + 255) / 256 * 256; }
 inline __host__ __device__ int64_t paged_plan_bytes(int64_t S) {
@@ -193,7 +194,7 @@ inline __host__ __device__ int64_t paged_plan_bytes(int64_t S) {
 inline __host__ __device__ int64_t paged_scan_bytes(int d_h) { return kPartialRows * (d_h + 2) * 4; }
 inline size_t paged_ws_bytes(int64_t N, int64_t S, int d_h) {
   return static_cast<size_t>(paged_plan_bytes(S) + paged_scan_bytes(d_h) +
-                             (N >= kChunkMin ? (int64_t)kChunkStates * 256 * (d_h + 2) * 4 : 0));
+                             (N >= kChunkMin ? kCutBytes + (int64_t)kChunkStates * 256 * (d_h + 2) * 4 : 0));
 }
 
 // Launchers (return the hipError_t of the launch).
