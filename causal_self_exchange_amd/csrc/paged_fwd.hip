@@ -6,7 +6,7 @@
 // The rows of a request that share a cached head (its new tokens times the
 // query heads of the group) are taken in blocks of 16 NB rows. A work item is
 // (request, split of its history, cached head, row block); a work-group of four
-// waves scans the item's keys, each wave its own 32 keys at a time, and keeps
+// waves scans the item's keys, each wave its own steps of 32 (fp32: 16), and keeps
 // (m, l, z) per row; the waves' states meet in LDS. Where a history is split,
 // the item leaves a partial state and merge_kernel joins them; otherwise the
 // item finishes the row itself (Self entry, count term, output).
@@ -24,7 +24,6 @@ using namespace paged;
 
 constexpr int kWaves = 4;
 constexpr int kThreads = 64 * kWaves;
-constexpr int kStep = 32;                 // keys of a wave's step
 constexpr float kLazy = 32.0f;            // log2 slack before the stabiliser moves
 
 __global__ __launch_bounds__(kThreads) void plan_kernel(PagedArgs a, Cut cut) {
@@ -45,37 +44,54 @@ __global__ __launch_bounds__(kThreads) void plan_kernel(PagedArgs a, Cut cut) {
 // register r holds row 4 j + r of column i. With keys as A rows and query rows
 // as B columns a lane holds 4 keys' scores of one query row, and its own
 // weights are the B operand of the transport O^T[d][row] += V^T[d][key]
-// W[key][row], whose contraction runs over the keys in that same order.
-//   bf16: two 16-key blocks make one transport step; V^T comes from a
-//     wave-private LDS tile (direct loads, transposing reads).
-//   fp32: contraction over d in the order {16 t + 4 j + e}, so each lane loads 16
-//     bytes of a P2 row; output rows in the order {d / 16 i + e}, so each lane
-//     loads d_h / 16 consecutive floats of a V row as the A operands of all
-//     output blocks.
+// W[key][row], whose contraction runs over the keys in that same order (bf16:
+// two 16-key blocks to a step; fp32: one, contraction over d in the order
+// {16 t + 4 j + e}).
+//
+// Both operands of the keys pass through a wave-private LDS slot, filled by
+// direct loads of 1 KB of consecutive memory each. The order matters more than
+// the traffic: reading the rows straight into the A layout (16 rows x 64 bytes
+// per instruction), or V in blocks of 8 rows x 128 bytes, the same bytes took
+// eight times as long from the L2 (196 rows over 32,000 keys: 94 us of loads
+// against 12). The 16-byte chunks of a row are stored in an order that depends
+// on the row, so that the operand reads spread over the banks. A wave holds its
+// step's operands in registers, and the slot is refilled while it computes.
 template <typename Tin, int D>
 struct Geom {
   static constexpr bool kBf = sizeof(Tin) == 2;
-  static constexpr int kKs = kBf ? (D + 31) / 32 : D / 16;   // 16-byte loads per lane and 16-key block
+  static constexpr int kEs = (int)sizeof(Tin);
+  static constexpr int kHalves = kBf ? 2 : 1;                // 16-key blocks per step
+  static constexpr int kStep = 16 * kHalves;                 // keys of a wave's step
+  static constexpr int kCh = D * kEs / 16;                   // 16-byte chunks per row
+  static constexpr int kDma = (kCh + 3) / 4;                 // 1 KB loads per 16 rows
+  static constexpr int kHalf = kDma * 1024;
+  static constexpr int kSlot = 2 * kHalves * kHalf;          // P2, then V
+  static constexpr int kKs = (kCh + 3) / 4;                  // A operands of 16 bytes per row block
   static constexpr int kDb = D / 16;                         // 16-row blocks of O^T
-  static constexpr int kCb = (D + 63) / 64;                  // 64-column blocks of a V tile
-  static constexpr int kVTile = 4 * kCb * 1024;              // 32 rows: blocks of 8 rows x 8 chunks, 1 KB each
-  static constexpr int kRing = kBf ? kWaves * 2 * kVTile : 0;
   static constexpr int kZStride = D + 4;
   static constexpr int kZBytes = kWaves * 16 * kZStride * 4;
-  static constexpr int kLds = kRing > kZBytes ? kRing : kZBytes;
+  static constexpr int kLds = kWaves * kSlot > kZBytes ? kWaves * kSlot : kZBytes;
+  // Chunk c of row q lies at position c ^ swz(q). Rows of 160 and 96 bytes spread
+  // over the banks by themselves; wider fp32 rows of 320 and 192 bytes leave
+  // four-way conflicts in the V reads.
+  __device__ static int swz(int q) {
+    if (kBf) return kCh == 16 ? 2 * (q & 7) : (kCh == 8 ? 2 * ((q >> 1) & 3) : (kCh == 4 ? 2 * ((q >> 2) & 1) : 0));
+    return kCh >= 32 || kCh == 16 ? q & 15 : (kCh == 8 ? (q >> 1) & 7 : q & 3);
+  }
 };
 
-// Work-groups per compute unit: as many as the LDS ring and the registers of
+// Work-groups per compute unit: as many as the LDS slots and the registers of
 // the row blocks admit.
 template <typename Tin, int D, int NB>
-constexpr int kPerCu = sizeof(Tin) == 4 && D == 128 && NB == 2 ? 1 : (D <= 64 && NB == 1 ? 4 : 2);
+constexpr int kPerCu = D <= 64 && NB == 1 ? 4 : 2;
 
 template <typename Tin, int D, int NB>
 __global__ __launch_bounds__(kThreads, (kPerCu<Tin, D, NB>)) void scan_kernel(PagedArgs a, HeadParams hp, Cut cut) {
   using C = Geom<Tin, D>;
   constexpr bool kBf = C::kBf;
   constexpr int kRb = 16 * NB;
-  constexpr int kEs = (int)sizeof(Tin);
+  constexpr int kEs = C::kEs;
+  constexpr int kStep = C::kStep;
   __shared__ __attribute__((aligned(16))) char smem[C::kLds];
   __shared__ float s_m[kWaves][16], s_l[kWaves][16];
   __shared__ PlanLds lds;
@@ -93,6 +109,16 @@ __global__ __launch_bounds__(kThreads, (kPerCu<Tin, D, NB>)) void scan_kernel(Pa
   const float k2 = hp.scale * kLog2e;
   const int pmask = (1 << a.page_shift) - 1;
   const int per = (n_items + 7) >> 3;
+  char* const slot = smem + wave * C::kSlot;
+
+  // Source of this lane's 16 bytes in load u of a 16-row block: LDS position
+  // 64 u + lane is row / chunk position of the block.
+  int src[C::kDma];
+#pragma unroll
+  for (int u = 0; u < C::kDma; ++u) {
+    const int p = 64 * u + lane, q = p / C::kCh, c = p - q * C::kCh;
+    src[u] = q < 16 ? q * D * kEs + 16 * (c ^ C::swz(q)) : kOutOfRange;
+  }
 
   // Work-groups go round the 8 XCDs: each takes a contiguous eighth of the items,
   // so the row blocks of one (request, split, cached head), which lie together,
@@ -117,7 +143,7 @@ __global__ __launch_bounds__(kThreads, (kPerCu<Tin, D, NB>)) void scan_kernel(Pa
     const int rows = min(kRb, all_rows - row0);
     const int pos_lo = ctx + row0 / G, pos_hi = ctx + (row0 + rows - 1) / G;
     const int k0 = split * chunk;
-    if (split > 0 && k0 >= pos_hi) continue;        // no keys; the merge does not read this state
+    if (split > 0 && k0 >= pos_hi) continue;        // no keys; the join does not read this state
     const int k1 = (int)min((long long)k0 + chunk, (long long)pos_hi);
 
     // The query rows as B operands, and their positions (0 for rows past the end:
@@ -131,11 +157,11 @@ __global__ __launch_bounds__(kThreads, (kPerCu<Tin, D, NB>)) void scan_kernel(Pa
       const int tq = ok ? row / G : 0;
       const int h = kvh * G + (ok ? row - tq * G : 0);
       pos[nb] = ok ? ctx + tq : 0;
-      const Tin* p = static_cast<const Tin*>(a.P1) + (size_t)(r.first + tq) * a.ld1 + (size_t)h * D;
+      const char* p = static_cast<const char*>(a.P1) + ((size_t)(r.first + tq) * a.ld1 + (size_t)h * D) * kEs;
 #pragma unroll
       for (int ks = 0; ks < C::kKs; ++ks) {
-        const int col = kBf ? 32 * ks + 8 * lj : 16 * ks + 4 * lj;
-        qf[nb][ks] = ok && col < D ? *reinterpret_cast<const u32x4*>(p + col) : u32x4{0u, 0u, 0u, 0u};
+        const int c = 4 * ks + lj;
+        qf[nb][ks] = ok && c < C::kCh ? *reinterpret_cast<const u32x4*>(p + 16 * c) : u32x4{0u, 0u, 0u, 0u};
       }
     }
 
@@ -148,116 +174,99 @@ __global__ __launch_bounds__(kThreads, (kPerCu<Tin, D, NB>)) void scan_kernel(Pa
       for (int db = 0; db < C::kDb; ++db) acc[nb][db] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     }
 
-    // This wave's steps: first + 4 n. Lane x holds the page of half x % 2 of step
-    // n0 + x / 2, for 32 steps at a time.
+    // This wave's steps: first + 4 n. Lane x holds the page of 16-key block x of
+    // its steps, for 64 blocks at a time.
+    constexpr int kWin = 64 / C::kHalves;           // steps per window
     const int first = k0 / kStep + wave;
     const int nsteps = k1 > k0 + kStep * wave ? ((k1 - k0 + kStep - 1) / kStep - wave + kWaves - 1) / kWaves : 0;
     int pages = -1;
     auto load_pages = [&](int n0) {
-      const int key = (first + kWaves * (n0 + (lane >> 1))) * kStep + 16 * (lane & 1);
+      const int n = n0 + lane / C::kHalves;
+      const int key = (first + kWaves * n) * kStep + 16 * (lane % C::kHalves);
       pages = -1;
-      if (n0 + (lane >> 1) < nsteps && key < r.total) {
+      if (n < nsteps && key < r.total) {
         const int pg = a.table[(size_t)b * a.max_pages + (key >> a.page_shift)];
         pages = pg >= 0 && pg < a.n_pages ? pg : -1;
       }
     };
-    // Byte address of the first row of 16-key half hb of step n in a cache, and
-    // the bytes of its rows that exist (0: page outside the cache).
-    auto half_at = [&](const void* cache, int n, int hb, int* bytes) -> const char* {
-      const int key = (first + kWaves * n) * kStep + 16 * hb;
-      const int pg = __builtin_amdgcn_readlane(pages, 2 * (n & 31) + hb);
-      const int left = min(16, r.total - key);
-      *bytes = pg >= 0 && left > 0 ? left * D * kEs : 0;
-      const size_t row = (((size_t)(pg >= 0 ? pg : 0) * a.H_kv + kvh) << a.page_shift) + (key & pmask);
-      return static_cast<const char*>(cache) + row * D * kEs;
+    // Direct loads of step n into the slot. Rows at and past the request's end
+    // and rows of a page outside the cache are zeros.
+    auto fetch = [&](int n) __attribute__((always_inline)) {
+      if (n % kWin == 0) load_pages(n);
+#pragma unroll
+      for (int hb = 0; hb < C::kHalves; ++hb) {
+        const int key = (first + kWaves * n) * kStep + 16 * hb;
+        const int pg = __builtin_amdgcn_readlane(pages, C::kHalves * (n % kWin) + hb);
+        const int left = min(16, r.total - key);
+        const int bytes = pg >= 0 && left > 0 ? left * D * kEs : 0;
+        const size_t row = (((size_t)(pg >= 0 ? pg : 0) * a.H_kv + kvh) << a.page_shift) + (key & pmask);
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+          u32x4 rw = rsrc_words(static_cast<const char*>(w ? a.cV : a.cP2) + row * D * kEs, bytes);
+#pragma unroll
+          for (int x = 0; x < 3; ++x) rw[x] = (unsigned)uni((int)rw[x]);
+#pragma unroll
+          for (int u = 0; u < C::kDma; ++u) dma16(rw, slot + (w * C::kHalves + hb) * C::kHalf + 1024 * u, src[u]);
+        }
+      }
     };
 
-    constexpr int kBuf = kBf ? 2 : 1;
-    u32x4 kf[kBuf][2][C::kKs];                      // P2 rows of this step (bf16: and the next)
-    float vf[2][4][C::kDb];                         // fp32: V rows of the step
-    char* const ring = smem + wave * 2 * C::kVTile;
-    auto fetch = [&](int n, int buf) __attribute__((always_inline)) {
-      if ((n & 31) == 0) load_pages(n);
+    u32x4 kf[C::kHalves][C::kKs];                   // P2 rows as A operands
+    bf16x8 vb[kBf ? C::kDb : 1];                    // V^T as A operands
+    float vs[kBf ? 1 : 4][C::kDb];
+    auto read_operands = [&]() __attribute__((always_inline)) {
 #pragma unroll
-      for (int hb = 0; hb < 2; ++hb) {
-        int bytes;
-        const char* p = half_at(a.cP2, n, hb, &bytes);
-        const auto rs = rsrc(p, bytes);
+      for (int hb = 0; hb < C::kHalves; ++hb)
 #pragma unroll
         for (int ks = 0; ks < C::kKs; ++ks) {
-          const int col = kBf ? 32 * ks + 8 * lj : 16 * ks + 4 * lj;
-          const int o = col < D ? (li * D + col) * kEs : kOutOfRange;
-          kf[buf][hb][ks] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rs, o, 0, 0));
+          const int c = 4 * ks + lj;
+          const bool in = 4 * ks + 3 < C::kCh || c < C::kCh;
+          const u32x4 x = *reinterpret_cast<const u32x4*>(slot + hb * C::kHalf + 16 * (li * C::kCh + ((in ? c : 0) ^ C::swz(li))));
+          kf[hb][ks] = in ? x : u32x4{0u, 0u, 0u, 0u};
         }
-        const char* v = half_at(a.cV, n, hb, &bytes);
-        if constexpr (kBf) {
+      const char* v = slot + C::kHalves * C::kHalf;
+      if constexpr (kBf) {
+        // Transposing reads: lane m of group j addresses row 4 j + m / 4 of a
+        // 16-row block at columns 16 db + 4 (m % 4).
+        const int q = 4 * lj + (li >> 2), h = (li & 3) >> 1;
 #pragma unroll
-          for (int rg = 0; rg < 2; ++rg) {
-            u32x4 rw = rsrc_words(v + 8 * rg * D * kEs, bytes - 8 * rg * D * kEs);
+        for (int db = 0; db < C::kDb; ++db) {
+          const char* p = v + 16 * (q * C::kCh + ((2 * db + h) ^ C::swz(q))) + 8 * (li & 1);
+          const bf16x4 x = lds_tr_read(p), y = lds_tr_read(p + C::kHalf);
+          vb[db] = bf16x8{x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
+        }
+      } else {
 #pragma unroll
-            for (int w = 0; w < 3; ++w) rw[w] = (unsigned)uni((int)rw[w]);
+        for (int rr = 0; rr < 4; ++rr)
 #pragma unroll
-            for (int cb = 0; cb < C::kCb; ++cb) {
-              const int ch = 8 * cb + (lane >> 3);
-              dma16(rw, ring + (n & 1) * C::kVTile + (2 * hb + rg + 4 * cb) * 1024,
-                    ch < D / 8 ? (lane & 7) * D * 2 + 16 * ch : kOutOfRange);
-            }
+          for (int db = 0; db < C::kDb; ++db) {
+            const int q = 4 * lj + rr, c = 4 * db + (li >> 2);
+            vs[rr][db] = *reinterpret_cast<const float*>(v + 16 * (q * C::kCh + (c ^ C::swz(q))) + 4 * (li & 3));
           }
-        }
-      }
-    };
-    // fp32: the V rows of 16-key half hb, key 4 j + rr, columns d / 16 i ..
-    auto fetch_v = [&](int n) __attribute__((always_inline)) {
-      if constexpr (!kBf) {
-#pragma unroll
-        for (int hb = 0; hb < 2; ++hb) {
-          int bytes;
-          const char* v = half_at(a.cV, n, hb, &bytes);
-          const auto rs = rsrc(v, bytes);
-#pragma unroll
-          for (int rr = 0; rr < 4; ++rr) {
-            const int o = ((4 * lj + rr) * D + C::kDb * li) * 4;
-#pragma unroll
-            for (int e = 0; e < C::kDb; e += 4) {
-              if constexpr (C::kDb >= 4) {
-                if (e + 4 <= C::kDb) {
-                  const f32x4 x = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(rs, o + 4 * e, 0, 0));
-#pragma unroll
-                  for (int w = 0; w < 4; ++w) vf[hb][rr][e + w] = x[w];
-                  continue;
-                }
-              }
-#pragma unroll
-              for (int w = e; w < C::kDb; ++w)
-                vf[hb][rr][w] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(rs, o + 4 * w, 0, 0));
-            }
-          }
-        }
       }
     };
 
-    // Scores, weights and transport of step n from P2 buffer buf. Row blocks past
-    // the item's rows run along: with a branch around their MFMAs the compiler
-    // (ROCm 7.2) left out the wait states between an MFMA and the read of its
-    // result behind the branch, and results were wrong.
-    auto compute = [&](int n, int buf) __attribute__((always_inline)) {
+    // Scores, weights and transport of step n. Row blocks past the item's rows
+    // run along: with a branch around their MFMAs the compiler (ROCm 7.2) left
+    // out the wait states between an MFMA and the read of its result behind the
+    // branch, and results were wrong.
+    auto compute = [&](int n) __attribute__((always_inline)) {
       const int key0 = (first + kWaves * n) * kStep;
       const bool full = key0 + kStep <= pos_lo;
-      u32x4 wf[NB];
-      float w32[kBf ? 1 : NB][2][4];
+      float w[NB][C::kHalves][4];
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) {
-        float e2[2][4];
+        float e2[C::kHalves][4];
 #pragma unroll
-        for (int hb = 0; hb < 2; ++hb) {
+        for (int hb = 0; hb < C::kHalves; ++hb) {
           f32x4 s = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
           for (int ks = 0; ks < C::kKs; ++ks) {
             if constexpr (kBf) {
-              s = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, kf[buf][hb][ks]),
+              s = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, kf[hb][ks]),
                                                           __builtin_bit_cast(bf16x8, qf[nb][ks]), s, 0, 0, 0);
             } else {
-              const f32x4 x = __builtin_bit_cast(f32x4, kf[buf][hb][ks]), y = __builtin_bit_cast(f32x4, qf[nb][ks]);
+              const f32x4 x = __builtin_bit_cast(f32x4, kf[hb][ks]), y = __builtin_bit_cast(f32x4, qf[nb][ks]);
 #pragma unroll
               for (int e = 0; e < 4; ++e) s = __builtin_amdgcn_mfma_f32_16x16x4f32(x[e], y[e], s, 0, 0, 0);
             }
@@ -271,15 +280,17 @@ __global__ __launch_bounds__(kThreads, (kPerCu<Tin, D, NB>)) void scan_kernel(Pa
         }
         if (!full) {
 #pragma unroll
-          for (int hb = 0; hb < 2; ++hb)
+          for (int hb = 0; hb < C::kHalves; ++hb)
 #pragma unroll
             for (int rr = 0; rr < 4; ++rr)
               e2[hb][rr] = key0 + 16 * hb + 4 * lj + rr < pos[nb] ? e2[hb][rr] : -INFINITY;
         }
         // The stabiliser starts at 0 (SiLU >= -0.2785, so no weight is small) and
         // moves only when a score passes it by 2^32.
-        float mx = fmaxf(fmaxf(fmaxf(e2[0][0], e2[0][1]), fmaxf(e2[0][2], e2[0][3])),
-                         fmaxf(fmaxf(e2[1][0], e2[1][1]), fmaxf(e2[1][2], e2[1][3])));
+        float mx = -INFINITY;
+#pragma unroll
+        for (int hb = 0; hb < C::kHalves; ++hb)
+          mx = fmaxf(mx, fmaxf(fmaxf(e2[hb][0], e2[hb][1]), fmaxf(e2[hb][2], e2[hb][3])));
         if (__any(mx > m2[nb] + kLazy)) {
           mx = fmaxf(mx, __shfl_xor(mx, 16));
           mx = fmaxf(mx, __shfl_xor(mx, 32));
@@ -292,76 +303,53 @@ __global__ __launch_bounds__(kThreads, (kPerCu<Tin, D, NB>)) void scan_kernel(Pa
 #pragma unroll
             for (int rr = 0; rr < 4; ++rr) acc[nb][db][rr] *= f;
         }
-        float w[2][4];
 #pragma unroll
-        for (int hb = 0; hb < 2; ++hb) {
+        for (int hb = 0; hb < C::kHalves; ++hb) {
 #pragma unroll
-          for (int rr = 0; rr < 4; ++rr) w[hb][rr] = __builtin_amdgcn_exp2f(e2[hb][rr] - m2[nb]);
-          l[nb] += (w[hb][0] + w[hb][1]) + (w[hb][2] + w[hb][3]);
-        }
-        if constexpr (kBf) {
-          // The transport's operand: weights rounded to bf16, like the other bf16 forwards.
-          wf[nb] = u32x4{pack_bf16(w[0][0], w[0][1]), pack_bf16(w[0][2], w[0][3]), pack_bf16(w[1][0], w[1][1]),
-                         pack_bf16(w[1][2], w[1][3])};
-        } else {
-#pragma unroll
-          for (int hb = 0; hb < 2; ++hb)
-#pragma unroll
-            for (int rr = 0; rr < 4; ++rr) w32[nb][hb][rr] = w[hb][rr];
+          for (int rr = 0; rr < 4; ++rr) w[nb][hb][rr] = __builtin_amdgcn_exp2f(e2[hb][rr] - m2[nb]);
+          l[nb] += (w[nb][hb][0] + w[nb][hb][1]) + (w[nb][hb][2] + w[nb][hb][3]);
         }
       }
       if constexpr (kBf) {
-        // Transposing reads: lane m of group j addresses row 4 j + m / 4 of a
-        // 16-row block at columns 16 db + 4 (m % 4).
-        const int q = 4 * lj + (li >> 2), c = (li & 3) >> 1;
-        const char* tb = ring + (n & 1) * C::kVTile + 1024 * (q >> 3) + 16 * ((q & 7) + 8 * c) + 8 * (li & 1);
+        // The transport's operand: weights rounded to bf16, like the other bf16 forwards.
+        u32x4 wf[NB];
 #pragma unroll
-        for (int db = 0; db < C::kDb; ++db) {
-          const char* p = tb + 4096 * (db / 4) + 256 * (db % 4);
-          const bf16x4 x = lds_tr_read(p), y = lds_tr_read(p + 2048);
-          const bf16x8 vt = {x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
+        for (int nb = 0; nb < NB; ++nb)
+          wf[nb] = u32x4{pack_bf16(w[nb][0][0], w[nb][0][1]), pack_bf16(w[nb][0][2], w[nb][0][3]),
+                         pack_bf16(w[nb][1][0], w[nb][1][1]), pack_bf16(w[nb][1][2], w[nb][1][3])};
+#pragma unroll
+        for (int db = 0; db < C::kDb; ++db)
 #pragma unroll
           for (int nb = 0; nb < NB; ++nb)
             acc[nb][db] =
-                __builtin_amdgcn_mfma_f32_16x16x32_bf16(vt, __builtin_bit_cast(bf16x8, wf[nb]), acc[nb][db], 0, 0, 0);
-        }
+                __builtin_amdgcn_mfma_f32_16x16x32_bf16(vb[db], __builtin_bit_cast(bf16x8, wf[nb]), acc[nb][db], 0, 0, 0);
       } else {
 #pragma unroll
-        for (int hb = 0; hb < 2; ++hb)
+        for (int rr = 0; rr < 4; ++rr)
 #pragma unroll
-          for (int rr = 0; rr < 4; ++rr)
+          for (int db = 0; db < C::kDb; ++db)
 #pragma unroll
-            for (int db = 0; db < C::kDb; ++db)
-#pragma unroll
-              for (int nb = 0; nb < NB; ++nb)
-                acc[nb][db] = __builtin_amdgcn_mfma_f32_16x16x4f32(vf[hb][rr][db], w32[nb][hb][rr], acc[nb][db], 0, 0, 0);
+            for (int nb = 0; nb < NB; ++nb)
+              acc[nb][db] = __builtin_amdgcn_mfma_f32_16x16x4f32(vs[rr][db], w[nb][0][rr], acc[nb][db], 0, 0, 0);
       }
     };
 
-    if constexpr (kBf) {
-      // One step ahead: the next step's loads are issued once this step's have
-      // landed and the LDS reads of the step before are done.
-      if (nsteps > 0) fetch(0, 0);
-      for (int n = 0; n < nsteps; n += 2) {
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          if (n + u < nsteps) {
-            asm volatile("" ::: "memory");
-            wait_vm_lgkm<0, 0>();
-            asm volatile("" ::: "memory");
-            __builtin_amdgcn_sched_barrier(0);
-            if (n + u + 1 < nsteps) fetch(n + u + 1, u ^ 1);
-            __builtin_amdgcn_sched_barrier(0);
-            compute(n + u, u);
-          }
-        }
-      }
-    } else {
-      for (int n = 0; n < nsteps; ++n) {
-        fetch(n, 0);
-        fetch_v(n);
-        compute(n, 0);
-      }
+    if (nsteps > 0) fetch(0);
+    for (int n = 0; n < nsteps; ++n) {
+      // The step's loads have landed; then its operands are in registers and the
+      // slot is free.
+      asm volatile("" ::: "memory");
+      wait_vm_lgkm<0, 15>();
+      asm volatile("" ::: "memory");
+      __builtin_amdgcn_sched_barrier(0);
+      read_operands();
+      asm volatile("" ::: "memory");
+      wait_vm_lgkm<63, 0>();
+      asm volatile("" ::: "memory");
+      __builtin_amdgcn_sched_barrier(0);
+      if (n + 1 < nsteps) fetch(n + 1);
+      __builtin_amdgcn_sched_barrier(0);
+      compute(n);
     }
 
     // The waves' states meet in LDS, 16 rows at a time; then 16 lanes per row.
@@ -378,14 +366,7 @@ __global__ __launch_bounds__(kThreads, (kPerCu<Tin, D, NB>)) void scan_kernel(Pa
       }
       float* z = reinterpret_cast<float*>(smem) + (wave * 16 + li) * C::kZStride;
 #pragma unroll
-      for (int db = 0; db < C::kDb; ++db) {
-        if constexpr (kBf) {
-          *reinterpret_cast<f32x4*>(z + 16 * db + 4 * lj) = acc[nb][db];
-        } else {
-#pragma unroll
-          for (int rr = 0; rr < 4; ++rr) z[C::kDb * (4 * lj + rr) + db] = acc[nb][db][rr];
-        }
-      }
+      for (int db = 0; db < C::kDb; ++db) *reinterpret_cast<f32x4*>(z + 16 * db + 4 * lj) = acc[nb][db];
       __syncthreads();
       const int rr = tid >> 4, sl = tid & 15;
       const int row = row0 + 16 * nb + rr;
