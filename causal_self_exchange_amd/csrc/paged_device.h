@@ -103,36 +103,43 @@ struct Plan {
 };
 
 __device__ __forceinline__ int splits_of(int total, int chunk) {
-  return chunk == kMaxChunk ? 1 : (int)(((long long)total + chunk - 1) / chunk);
+  return chunk == kMaxChunk ? 1 : (int)(((unsigned)total + (unsigned)chunk - 1u) / (unsigned)chunk);
 }
 
-// Exclusive sum over the first four waves of a work-group and its total; every
-// thread of the work-group calls it.
-template <typename Int>
-__device__ __forceinline__ Int sum_256(Int x, Int* red, Int* total) {
+// Sums over the first four waves of a work-group, of N values per thread at
+// once: inclusive sums in x, totals in total; every thread of the work-group
+// calls it, and red is free again when it returns.
+template <typename Int, int N>
+__device__ __forceinline__ void sum_256(Int (&x)[N], Int (&total)[N], Int (*red)[N]) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  Int s = x;
 #pragma unroll
-  for (int o = 1; o < 64; o <<= 1) {
-    const Int y = __shfl_up(s, o, 64);
-    if (lane >= o) s += y;
-  }
-  if (lane == 63 && wave < 4) red[wave] = s;
-  __syncthreads();
-  Int before = 0, all = 0;
+  for (int o = 1; o < 64; o <<= 1)
 #pragma unroll
-  for (int w = 0; w < 4; ++w) {
-    before += w < wave ? red[w] : 0;
-    all += red[w];
+    for (int k = 0; k < N; ++k) {
+      const Int y = __shfl_up(x[k], o, 64);
+      if (lane >= o) x[k] += y;
+    }
+  if (lane == 63 && wave < 4)
+#pragma unroll
+    for (int k = 0; k < N; ++k) red[wave][k] = x[k];
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < N; ++k) {
+    Int before = 0, all = 0;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      before += w < wave ? red[w][k] : 0;
+      all += red[w][k];
+    }
+    x[k] += before;
+    total[k] = all;
   }
   __syncthreads();
-  *total = all;
-  return before + s - x;
 }
 
 struct PlanScratch {
-  long long wide[4];
-  int sum[4];
+  long long wide[4][3];
+  int sum[4][3];
 };
 
 // Fills p and the arrays it points to, by the work-group's first 256 threads
@@ -142,77 +149,89 @@ __device__ __forceinline__ void make_plan(const PagedArgs& a, const Cut& cut, bo
   const int row_block = cut.row_block, chunk_min = cut.chunk_min;
   const int tid = threadIdx.x;
   const int G = a.H / a.H_kv;
+  // Up to 256 requests each thread keeps its own.
+  Req mine;
+  mine.q = 0;
+  if (tid < 256 && tid < a.S) mine = Req(a, tid);
   if (scan) {
-    // Key visits of the row blocks, rows times keys, and the items without splits:
+    // Key visits of the row blocks, the items without splits, and rows times keys:
     // a split length c makes at most visits / c + base items. They should fill the
     // scan's work-groups a whole number of times, with as many again as there are
     // at least: a few items past a round cost a round. The length also keeps the
     // partial rows within the workspace (a split request has at most 2 total /
     // chunk splits).
-    long long visits = 0, cells = 0, base = 0;
+    long long x[3] = {0, 0, 0}, n[3];
     for (int b = tid; b < a.S && tid < 256; b += 256) {
-      const Req r = scan_part(Req(a, b), chunk_min);
+      const Req r = scan_part(b < 256 ? mine : Req(a, b), chunk_min);
       const long long blocks = (long long)((r.q * G + row_block - 1) / row_block) * a.H_kv;
-      visits += blocks * r.total;
-      base += blocks;
-      cells += (long long)r.q * a.H * r.total;
+      x[0] += blocks * r.total;
+      x[1] += blocks;
+      x[2] += (long long)r.q * a.H * r.total;
     }
-    long long n;
-    sum_256(base, sc.wide, &base);
-    sum_256(visits, sc.wide, &n);
-    const long long room = (2 * base + cut.scan_groups - 1) / cut.scan_groups * cut.scan_groups - base;
-    long long c = room > 0 ? (n + room - 1) / room : 0;
-    sum_256(cells, sc.wide, &n);
-    const long long c2 = (2 * n + kPartialRows - 1) / kPartialRows;
-    c = c > c2 ? c : c2;
-    c = c < kMinChunk ? kMinChunk : (c + 127) / 128 * 128;
-    p.chunk = (int)(c < kMaxChunk ? c : kMaxChunk);
+    sum_256<long long, 3>(x, n, sc.wide);
+    const long long room = (2 * n[1] + cut.scan_groups - 1) / cut.scan_groups * cut.scan_groups - n[1];
+    float c1 = room > 0 ? (float)n[0] / (float)room : 0.0f;
+    const float c2 = (float)(2 * n[2]) * (1.0f / kPartialRows) * 1.00001f;
+    c1 = fmaxf(fmaxf(c1, c2) + 1.0f, (float)kMinChunk);
+    p.chunk = c1 < 2.0e9f ? ((int)c1 + 127) & ~127 : kMaxChunk;
   }
-  int units = 0, parts = 0, merges = 0;
+  int done[3] = {0, 0, 0};     // units, rows to join, partial rows
   long long tiles = 0;
   for (int b0 = 0; b0 < a.S; b0 += 256) {
     const int b = b0 + tid;
     const bool in = tid < 256 && b < a.S;
     Req r;
     r.q = 0;
-    if (in) r = Req(a, b);
+    if (in) r = b0 == 0 ? mine : Req(a, b);
     if (scan) {
       const Req s = scan_part(r, chunk_min);
       const int splits = s.q > 0 ? splits_of(s.total, p.chunk) : 0;
       const int rows = splits > 1 ? s.q * a.H : 0;
-      int n;
-      const int u = sum_256((s.q * G + row_block - 1) / row_block * splits, &sc.sum[0], &n);
-      if (in) p.unit_sum[b] = units + u;
-      units += n;
-      const int m = sum_256(rows, &sc.sum[0], &n);
-      if (in) p.merge_sum[b] = merges + m;
-      merges += n;
-      const int q = sum_256(rows * splits, &sc.sum[0], &n);
-      if (in) p.part_sum[b] = parts + q;
-      parts += n;
+      const int own[3] = {(s.q * G + row_block - 1) / row_block * splits, rows, rows * splits};
+      int x[3] = {own[0], own[1], own[2]}, n[3];
+      sum_256<int, 3>(x, n, sc.sum);
+      if (in) {
+        p.unit_sum[b] = done[0] + x[0] - own[0];
+        p.merge_sum[b] = done[1] + x[1] - own[1];
+        p.part_sum[b] = done[2] + x[2] - own[2];
+      }
+#pragma unroll
+      for (int k = 0; k < 3; ++k) done[k] += n[k];
     }
     if (chunks) {
       const Req s = chunk_part(r, chunk_min);
-      long long x = 0, n;
+      long long own = 0;
       if (s.q > 0) {
         const ChunkTiles t(s.total - s.q, s.total);
-        x = t.before(t.n) * a.H;
+        own = t.before(t.n) * a.H;
       }
-      const long long at = sum_256(x, sc.wide, &n);
-      if (in) p.tile_sum[b] = tiles + at;
-      tiles += n;
+      long long x[3] = {own, 0, 0}, n[3];
+      sum_256<long long, 3>(x, n, sc.wide);
+      if (in) p.tile_sum[b] = tiles + x[0] - own;
+      tiles += n[0];
     }
   }
-  p.units = units;
-  p.merge_rows = merges;
+  p.units = done[0];
+  p.merge_rows = done[1];
   if (chunks && tid == 0) p.tile_sum[a.S] = tiles;
 }
 
-// The plan in the workspace, written by plan_kernel for more than kPlanInline
-// requests.
+// The plan in the workspace: written by plan_kernel for more than kPlanInline
+// requests, else by the scan kernel's first work-group for the join.
 struct WsPlan {
   int* head;              // chunk, units, merge_rows
   Plan p;
+  __device__ __forceinline__ void put_head(const Plan& q) {
+    head[0] = q.chunk;
+    head[1] = q.units;
+    head[2] = q.merge_rows;
+  }
+  __device__ __forceinline__ Plan get() {
+    p.chunk = uni(head[0]);
+    p.units = uni(head[1]);
+    p.merge_rows = uni(head[2]);
+    return p;
+  }
   __device__ __forceinline__ WsPlan(const PagedArgs& a) {
     char* w = static_cast<char*>(a.ws);
     head = reinterpret_cast<int*>(w);
@@ -226,8 +245,8 @@ struct WsPlan {
 };
 
 // A kernel's plan: formed in LDS by each work-group for up to kPlanInline
-// requests (2 us; a launch of its own and the wait for it take 5), else read
-// from the workspace.
+// requests (a launch of its own and the wait for it take 5 us), else read from
+// the workspace.
 struct PlanLds {
   PlanScratch sc;
   int unit_sum[kPlanInline + 1], part_sum[kPlanInline + 1], merge_sum[kPlanInline + 1];
@@ -236,10 +255,7 @@ struct PlanLds {
 __device__ __forceinline__ Plan load_plan(const PagedArgs& a, const Cut& cut, bool scan, bool chunks, PlanLds& lds) {
   if (a.S > kPlanInline) {
     WsPlan w(a);
-    w.p.chunk = uni(w.head[0]);
-    w.p.units = uni(w.head[1]);
-    w.p.merge_rows = uni(w.head[2]);
-    return w.p;
+    return w.get();
   }
   Plan p{};
   p.unit_sum = lds.unit_sum;

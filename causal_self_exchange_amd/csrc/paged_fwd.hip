@@ -30,11 +30,7 @@ __global__ __launch_bounds__(kThreads) void plan_kernel(PagedArgs a, Cut cut) {
   __shared__ PlanScratch sc;
   WsPlan w(a);
   make_plan(a, cut, true, cut.chunk_min > 0, sc, w.p);
-  if (threadIdx.x == 0) {
-    w.head[0] = w.p.chunk;
-    w.head[1] = w.p.units;
-    w.head[2] = w.p.merge_rows;
-  }
+  if (threadIdx.x == 0) w.put_head(w.p);
 }
 
 // ---- scan ---------------------------------------------------------------------
@@ -98,6 +94,14 @@ __global__ __launch_bounds__(kThreads, (kPerCu<Tin, D, NB>)) void scan_kernel(Pa
 
   const int chunk_min = cut.chunk_min;
   const Plan plan = load_plan(a, cut, true, false, lds);
+  if (a.S <= kPlanInline && blockIdx.x == 0) {      // for the join
+    WsPlan w(a);
+    if ((int)threadIdx.x < a.S) {
+      w.p.part_sum[threadIdx.x] = plan.part_sum[threadIdx.x];
+      w.p.merge_sum[threadIdx.x] = plan.merge_sum[threadIdx.x];
+    }
+    if (threadIdx.x == 0) w.put_head(plan);
+  }
   const int n_items = plan.units * a.H_kv;
   const int chunk = plan.chunk;
   const States states = States::scan(a);
@@ -469,9 +473,9 @@ __device__ __forceinline__ void join_tile(const PagedArgs& a, const HeadParams& 
 // 16 rows each of the long chunks' divided tiles.
 template <typename Tin, int D>
 __global__ __launch_bounds__(kThreads) void join_kernel(PagedArgs a, HeadParams hp, Cut cut, int row_groups) {
-  __shared__ PlanLds lds;
   if ((int)blockIdx.x < row_groups) {
-    const Plan plan = load_plan(a, cut, true, false, lds);
+    WsPlan w(a);
+    const Plan plan = w.get();
     join_rows<Tin, D>(a, hp, plan, cut.chunk_min, blockIdx.x * kWaves + (threadIdx.x >> 6), row_groups * kWaves);
   } else if constexpr (sizeof(Tin) == 2) {
     const int i = (int)blockIdx.x - row_groups;

@@ -167,16 +167,7 @@ class _Args:
             raise ValueError(f"{self.fn}: {name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
         if dtype is not None and t.dtype != dtype:
             raise TypeError(f"{self.fn}: {name} has dtype {t.dtype}, expected {dtype}")
-        self.ts.append((name, t, True))
-        return self
-
-    def tokens(self, name, t, shape, dtype):
-        """A packed token tensor [N, heads, d_h]: each token's heads are
-        contiguous, tokens may be further apart (a slice of a fused projection)."""
-        self(name, t, shape, dtype)
-        self.ts[-1] = (name, t, False)
-        if t.stride()[2] != 1 or (t.shape[1] > 1 and t.stride(1) != t.shape[2]):
-            raise ValueError(f"{self.fn}: the heads of each token of {name} must be contiguous")
+        self.ts.append((name, t))
         return self
 
     def bytes(self, name, t, need: int):
@@ -188,10 +179,10 @@ class _Args:
 
     def done(self):
         dev = None
-        for name, t, dense in self.ts:
+        for name, t in self.ts:
             if not t.is_cuda:
                 raise ValueError(f"{self.fn}: {name} must be a device tensor")
-            if dense and not t.is_contiguous():
+            if not t.is_contiguous():
                 raise ValueError(f"{self.fn}: {name} must be contiguous")
             if dev is None:
                 dev = t.device
@@ -464,27 +455,76 @@ def cache_append(cache_P2, cache_V, lens, p2, v, stream=None):
     _check("relation_cache_append", st)
 
 
+# ---- the paged Relation Cache ------------------------------------------------------
+# These calls run in serving loops, where a step can be shorter than the checks of
+# its arguments: the checks are one pass over (name, tensor, shape, dtype, dense).
+
+_I32 = torch.int32
+
+
+def _check_tensors(fn, specs):
+    """Shapes, dtypes and token layouts of all tensors first, whatever device they
+    are on; then device and contiguity. dense False: a packed token tensor [N, heads, d_h] whose
+    tokens may be further apart (a slice of a fused projection). Returns the device."""
+    for name, t, shape, dtype, dense in specs:
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{fn}: {name} must be a torch.Tensor")
+        if t.shape != shape:
+            raise ValueError(f"{fn}: {name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+        if t.dtype is not dtype:
+            raise TypeError(f"{fn}: {name} has dtype {t.dtype}, expected {dtype}")
+        if not dense and (t.stride(2) != 1 or (shape[1] > 1 and t.stride(1) != shape[2])):
+            raise ValueError(f"{fn}: the heads of each token of {name} must be contiguous")
+    dev = specs[0][1].device
+    for name, t, _, _, dense in specs:
+        if not t.is_cuda:
+            raise ValueError(f"{fn}: {name} must be a device tensor")
+        if t.device != dev:
+            raise ValueError(f"{fn}: {name} is on {t.device}, the inputs on {dev}")
+        if dense and not t.is_contiguous():
+            raise ValueError(f"{fn}: {name} must be contiguous")
+    return dev
+
+
+def _run_on(fn, dev, stream, args):
+    """The library call fn(*args, stream) with the tensors' device current, on the
+    caller's stream (which has to be of that device) or the current one."""
+    if stream is not None and stream.device != dev:
+        raise ValueError(f"{fn}: the stream is on {stream.device}, the tensors on {dev}")
+    f = getattr(lib(), fn)
+    if dev.index == torch.cuda.current_device():
+        st = f(*args, _stream(stream))
+    else:
+        with torch.cuda.device(dev):
+            st = f(*args, _stream(stream))
+    if st != 0:
+        raise RelationError(fn, st)
+
+
+def _host_floats(x, n: int):
+    """Host float[n] from a float or n of them."""
+    if isinstance(x, (list, tuple)) and len(x) == n:
+        return (ctypes.c_float * n)(*x)
+    arr = np.ascontiguousarray(np.broadcast_to(np.asarray(x, dtype=np.float32), (n,)))
+    return (ctypes.c_float * n).from_buffer_copy(arr)
+
+
 def _pages(fn, cache_P2):
     if not isinstance(cache_P2, torch.Tensor) or cache_P2.dim() != 4:
         raise ValueError(f"{fn}: cache_P2 must be a [n_pages, H_kv, page_size, d_h] tensor")
-    return tuple(cache_P2.shape)
+    return cache_P2.shape
 
 
-class _On:
-    """The tensors' device made current for a call of the paged entry points, and
-    the stream: the caller's, which has to be of that device, or the current one."""
+def _tokens(fn, name, t):
+    if not isinstance(t, torch.Tensor) or t.dim() != 3:
+        raise ValueError(f"{fn}: {name} must be an [N, heads, d_h] tensor")
+    return t.shape
 
-    def __init__(self, fn, t, stream):
-        if stream is not None and stream.device != t.device:
-            raise ValueError(f"{fn}: the stream is on {stream.device}, the tensors on {t.device}")
-        self.guard, self.stream = torch.cuda.device(t.device), stream
 
-    def __enter__(self):
-        self.guard.__enter__()
-        return _stream(self.stream)
-
-    def __exit__(self, *exc):
-        return self.guard.__exit__(*exc)
+def _table(fn, t):
+    if not isinstance(t, torch.Tensor) or t.dim() != 2:
+        raise ValueError(f"{fn}: block_table must be an [S, max_pages] tensor")
+    return t.shape
 
 
 def _ld(t) -> int:
@@ -499,29 +539,27 @@ def page_map(lens, n_new, block_table, free_pages, n_free, N: int, page_size: in
     return to the list), block_table int32[S, max_pages] and free_pages int32[F]
     (both updated in place), n_free int32[1]. Returns (cu [S+1], total [S], slot
     [N], pos [N], n_free_out [1]); out: the five tensors (n_free_out may be n_free)."""
-    if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
-        raise ValueError("page_map: block_table must be an [S, max_pages] tensor")
+    fn = "page_map"
+    S, width = _table(fn, block_table)
     if not isinstance(free_pages, torch.Tensor) or free_pages.dim() != 1:
         raise ValueError("page_map: free_pages must be a 1-d tensor")
-    S, width = block_table.shape
-    N, it = int(N), torch.int32
-    a = _Args("page_map")("block_table", block_table, dtype=it)("free_pages", free_pages, dtype=it)
-    a("lens", lens, (S,), it)("n_new", n_new, (S,), it)("n_free", n_free, (1,), it)
-    shapes = ((S + 1,), (S,), (N,), (N,), (1,))
+    N, F = int(N), free_pages.shape[0]
+    specs = [("block_table", block_table, (S, width), _I32, True), ("free_pages", free_pages, (F,), _I32, True),
+             ("lens", lens, (S,), _I32, True), ("n_new", n_new, (S,), _I32, True), ("n_free", n_free, (1,), _I32, True)]
     if out is not None:
         if len(out) != 5:
             raise ValueError("page_map: out must be (cu, total, slot, pos, n_free_out)")
-        for name, t, shp in zip(("cu", "total", "slot", "pos", "n_free_out"), out, shapes):
-            a(name, t, shp, it)
-    a.done()
+        cu, total, slot, pos, n_free_out = out
+        specs += [("cu", cu, (S + 1,), _I32, True), ("total", total, (S,), _I32, True), ("slot", slot, (N,), _I32, True),
+                  ("pos", pos, (N,), _I32, True), ("n_free_out", n_free_out, (1,), _I32, True)]
+    dev = _check_tensors(fn, specs)
     if out is None:
-        out = tuple(torch.empty(max(shp[0], 0), dtype=it, device=lens.device) for shp in shapes)
-    cu, total, slot, pos, n_free_out = out
-    with _On("page_map", lens, stream) as sp:
-        st = lib().relation_page_map(_ptr(lens), _ptr(n_new), _ptr(block_table), _ptr(free_pages), _ptr(n_free),
-                                     _ptr(n_free_out), _ptr(cu), _ptr(total), _ptr(slot), _ptr(pos), S, N,
-                                     free_pages.numel(), width, int(page_size), int(n_pages), sp)
-    _check("relation_page_map", st)
+        out = tuple(torch.empty(max(n, 0), dtype=_I32, device=dev) for n in (S + 1, S, N, N, 1))
+        cu, total, slot, pos, n_free_out = out
+    _run_on("relation_page_map", dev, stream,
+            (lens.data_ptr(), n_new.data_ptr(), block_table.data_ptr(), free_pages.data_ptr(), n_free.data_ptr(),
+             n_free_out.data_ptr(), cu.data_ptr(), total.data_ptr(), slot.data_ptr(), pos.data_ptr(), S, N, F, width,
+             int(page_size), int(n_pages)))
     return out
 
 
@@ -531,33 +569,33 @@ def paged_append(P2, I, slot, cache_P2, cache_V, P1=None, pos=None, rope="none",
     P2, I [N, H_kv, d_h] and optionally P1 [N, H, d_h] (tokens may be slices of a
     fused projection), slot and pos int32[N] (page_map), caches [n_pages, H_kv,
     page_size, d_h]. Returns the rotated P1 ([N, H, d_h]; out, which may be P1
-    itself if contiguous) or None. Rows of tokens without a slot are not written."""
-    n_pages, Hkv, ps, D = _pages("paged_append", cache_P2)
-    dt = cache_P2.dtype
-    if not isinstance(P2, torch.Tensor) or P2.dim() != 3:
-        raise ValueError("paged_append: P2 must be an [N, H_kv, d_h] tensor")
-    N, H = P2.shape[0], 0
-    a = _Args("paged_append")("cache_P2", cache_P2)("cache_V", cache_V, cache_P2.shape, dt)
-    a.tokens("P2", P2, (N, Hkv, D), dt).tokens("I", I, (N, Hkv, D), dt)
-    a("slot", slot, (N,), torch.int32)("pos", pos, (N,), torch.int32, optional=True)
+    itself if contiguous) or None. Rows of tokens without a slot are not written
+    (zero in a P1 that the call allocates)."""
+    fn = "paged_append"
+    n_pages, Hkv, ps, D = shp = _pages(fn, cache_P2)
+    N = _tokens(fn, "P2", P2)[0]
+    dt, H = cache_P2.dtype, 0
+    specs = [("cache_P2", cache_P2, shp, dt, True), ("cache_V", cache_V, shp, dt, True),
+             ("P2", P2, (N, Hkv, D), dt, False), ("I", I, (N, Hkv, D), dt, False), ("slot", slot, (N,), _I32, True)]
+    if pos is not None:
+        specs.append(("pos", pos, (N,), _I32, True))
     if P1 is not None:
-        if not isinstance(P1, torch.Tensor) or P1.dim() != 3:
-            raise ValueError("paged_append: P1 must be an [N, H, d_h] tensor")
-        H = P1.shape[1]
-        a.tokens("P1", P1, (N, H, D), dt)("out", out, (N, H, D), dt, optional=True)
+        H = _tokens(fn, "P1", P1)[1]
+        specs.append(("P1", P1, (N, H, D), dt, False))
+        if out is not None:
+            specs.append(("out", out, (N, H, D), dt, True))
     elif out is not None:
         raise ValueError("paged_append: out is given without P1")
-    a.done()
+    dev = _check_tensors(fn, specs)
     if P1 is not None and out is None:
-        out = torch.zeros((N, H, D), dtype=dt, device=P1.device)   # rows without a token stay zero
-    th_keep, th_p = _theta_arg(theta, Hkv)
-    with _On("paged_append", P2, stream) as sp:
-        st = lib().relation_paged_append(_ptr(P1), _ptr(P2), _ptr(I), 0 if P1 is None else _ld(P1), _ld(P2), _ld(I),
-                                         _ptr(slot), _ptr(pos), ROPE[rope], float(rope_base), th_p, PAIRS[pairing],
-                                         _ptr(out), _ptr(cache_P2), _ptr(cache_V), N, H, Hkv, D, n_pages, ps,
-                                         _dtype_code(cache_P2), sp)
-    del th_keep
-    _check("relation_paged_append", st)
+        out = torch.zeros((N, H, D), dtype=dt, device=dev)
+    if theta is not None and len(theta) != Hkv // 2:
+        raise ValueError(f"theta needs H_kv/2 = {Hkv // 2} angles")
+    _run_on("relation_paged_append", dev, stream,
+            (_ptr(P1), P2.data_ptr(), I.data_ptr(), 0 if P1 is None else _ld(P1), _ld(P2), _ld(I), slot.data_ptr(),
+             _ptr(pos), ROPE[rope], float(rope_base), None if theta is None else _host_floats(theta, Hkv // 2),
+             PAIRS[pairing], _ptr(out), cache_P2.data_ptr(), cache_V.data_ptr(), N, H, Hkv, D, n_pages, ps,
+             _dtype_code(cache_P2)))
     return out
 
 
@@ -570,32 +608,32 @@ def paged_fwd(P1, cache_P2, cache_V, block_table, total, cu, tau, lam: float = 0
     """Y [N, H, d_h] of a packed batch of new tokens whose own rows are in the
     pages already: P1 [N, H, d_h] (rotated), caches [n_pages, H_kv, page_size,
     d_h], block_table int32[S, max_pages], total int32[S], cu int32[S+1]
-    (page_map). max_new: the most new tokens of one request (default N)."""
-    n_pages, Hkv, ps, D = _pages("paged_fwd", cache_P2)
+    (page_map). max_new: the most new tokens of one request (default N). Rows that
+    no request owns are not written (zero in a Y that the call allocates)."""
+    fn = "paged_fwd"
+    n_pages, Hkv, ps, D = shp = _pages(fn, cache_P2)
+    N, H = _tokens(fn, "P1", P1)[:2]
+    S, width = _table(fn, block_table)
     dt = cache_P2.dtype
-    if not isinstance(P1, torch.Tensor) or P1.dim() != 3:
-        raise ValueError("paged_fwd: P1 must be an [N, H, d_h] tensor")
-    if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
-        raise ValueError("paged_fwd: block_table must be an [S, max_pages] tensor")
-    N, H = P1.shape[:2]
-    S, width = block_table.shape
-    a = _Args("paged_fwd")("cache_P2", cache_P2)("cache_V", cache_V, cache_P2.shape, dt)
-    a.tokens("P1", P1, (N, H, D), dt)("block_table", block_table, dtype=torch.int32)
-    a("total", total, (S,), torch.int32)("cu", cu, (S + 1,), torch.int32)("out", out, (N, H, D), dt, optional=True)
+    specs = [("cache_P2", cache_P2, shp, dt, True), ("cache_V", cache_V, shp, dt, True), ("P1", P1, (N, H, D), dt, False),
+             ("block_table", block_table, (S, width), _I32, True), ("total", total, (S,), _I32, True),
+             ("cu", cu, (S + 1,), _I32, True)]
+    if out is not None:
+        specs.append(("out", out, (N, H, D), dt, True))
     need = paged_workspace_bytes(N, S, H, Hkv, D)
     if workspace is not None:
-        a.bytes("workspace", workspace, need)
-    a.done()
+        if not isinstance(workspace, torch.Tensor) or workspace.dtype != torch.uint8 or workspace.dim() != 1:
+            raise TypeError("paged_fwd: workspace must be a 1-d torch.uint8 tensor")
+        if workspace.numel() < need:
+            raise ValueError(f"paged_fwd: workspace holds {workspace.numel()} bytes, {need} needed")
+        specs.append(("workspace", workspace, workspace.shape, torch.uint8, True))
+    dev = _check_tensors(fn, specs)
     if out is None:
-        out = torch.zeros((N, H, D), dtype=dt, device=P1.device)   # rows without a token stay zero
+        out = torch.zeros((N, H, D), dtype=dt, device=dev)
     if workspace is None:
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=P1.device)
-    tau_keep, tau_p = _tau_arg(tau, H)
-    with _On("paged_fwd", P1, stream) as sp:
-        st = lib().relation_paged_fwd(_ptr(P1), _ld(P1), _ptr(cache_P2), _ptr(cache_V), _ptr(block_table),
-                                      _ptr(total), _ptr(cu), tau_p, float(lam), _ptr(out), N, S, H, Hkv, D, n_pages,
-                                      ps, width, N if max_new is None else int(max_new), _dtype_code(P1),
-                                      _ptr(workspace), workspace.numel(), sp)
-    del tau_keep
-    _check("relation_paged_fwd", st)
+        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
+    _run_on("relation_paged_fwd", dev, stream,
+            (P1.data_ptr(), _ld(P1), cache_P2.data_ptr(), cache_V.data_ptr(), block_table.data_ptr(), total.data_ptr(),
+             cu.data_ptr(), _host_floats(tau, H), float(lam), out.data_ptr(), N, S, H, Hkv, D, n_pages, ps, width,
+             N if max_new is None else int(max_new), _dtype_code(P1), workspace.data_ptr(), workspace.numel()))
     return out
