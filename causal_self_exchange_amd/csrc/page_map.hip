@@ -1,15 +1,20 @@
 // Block tables, slots and positions of a packed batch of the paged Relation
 // Cache, from the request lengths (integers only; semantics in relation.h).
 //
-// page_map: one work-group walks the requests 1024 at a time, twice. The first
+// page_map: one work-group takes the requests 1024 at a time, twice. The first
 //   walk numbers the pages that finished requests return (a prefix sum) and
 //   pushes them on the free list; the second sums the new tokens (the packed
-//   offsets) and the pages needed, and moves each request's pages from the top
-//   of the list to its table row. One work-group, because both sums run through
-//   all requests and the second needs the whole first one.
+//   offsets) and the pages needed, and moves pages from the top of the list to
+//   the table rows. One work-group, because both sums run through all requests
+//   and the second needs the whole first one. Pages are moved one per thread,
+//   whichever request they belong to (found by bisection in the sums, in LDS): a
+//   request of 2000 tokens returns 125 pages, which one thread would move in 25 us.
 // page_slots: one thread per packed token finds its request by bisection in
-//   the offsets and its page in the table.
-// The call moves a few KB: it is bound by the latency of its dependent steps.
+//   the offsets and its page in the table. Up to kSlotsInline tokens page_map
+//   does it itself.
+// The call moves a few KB: it is bound by the latency of its dependent steps
+// (256 requests of one token 9 us before the offsets were kept in LDS and the
+// sums taken together, 1024 prompts 37 us).
 #include "rel_internal.h"
 #include "rel_device.h"
 
@@ -20,28 +25,41 @@ namespace {
 constexpr int kMapThreads = 1024;
 constexpr int kMapWaves = kMapThreads / 64;
 constexpr int kSlotThreads = 256;
+constexpr int kSlotsInline = 4096;
+constexpr int kSlotsLds = 4096;           // requests whose offsets page_slots keeps in LDS
 
-// Inclusive sum over the work-group and the work-group's total.
-__device__ __forceinline__ long long block_sum(long long v, long long* red, long long* total) {
+// Inclusive sum over the work-group, and the work-group's total.
+__device__ __forceinline__ long long block_sum(long long x, long long* red, long long* total) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  long long x = v;
 #pragma unroll
   for (int o = 1; o < 64; o <<= 1) {
     const long long y = __shfl_up(x, o, 64);
     if (lane >= o) x += y;
   }
-  __syncthreads();                     // the previous use of red is over
   if (lane == 63) red[wave] = x;
   __syncthreads();
   long long before = 0, all = 0;
-#pragma unroll
+#pragma unroll 4
   for (int w = 0; w < kMapWaves; ++w) {
     const long long r = red[w];
     before += w < wave ? r : 0;
     all += r;
   }
+  __syncthreads();
   *total = all;
   return before + x;
+}
+
+// The first k of n with end[k] > i (n when there is none).
+template <typename Int>
+__device__ __forceinline__ int first_past(const Int* end, int n, Int i) {
+  int lo = 0, hi = n;
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (end[mid] > i) hi = mid;
+    else lo = mid + 1;
+  }
+  return lo;
 }
 
 __device__ __forceinline__ int pages_of(int rows, int shift) {
@@ -66,11 +84,12 @@ struct Request {
   }
 };
 
-// Slot and position of packed token t of request b, whose cached rows are len.
-__device__ __forceinline__ void write_slot(const PageMapArgs& a, int t, int b, int first, bool live) {
+// Slot and position of packed token t, the (t - first)th new one of request b,
+// which is granted its pages (live) and holds len tokens already.
+__device__ __forceinline__ void write_slot(const PageMapArgs& a, int t, int b, int first, int len, bool live) {
   int slot = -1, pos = -1;
   if (live) {
-    pos = a.len[b] + (t - first);
+    pos = len + (t - first);
     const int page = a.table[(size_t)b * a.max_pages + (pos >> a.page_shift)];
     if (page >= 0 && page < a.n_pages) slot = (page << a.page_shift) + (pos & ((1 << a.page_shift) - 1));
   }
@@ -78,41 +97,38 @@ __device__ __forceinline__ void write_slot(const PageMapArgs& a, int t, int b, i
   a.pos[t] = pos;
 }
 
-__device__ __forceinline__ void token_slot(const PageMapArgs& a, int t) {
-  // The request with cu[b] <= t < cu[b + 1]: the first b whose end is past t.
-  int lo = 0, hi = a.S;
-  while (lo < hi) {
-    const int mid = (lo + hi) >> 1;
-    if (a.cu[mid + 1] > t) hi = mid;
-    else lo = mid + 1;
-  }
-  const bool in = lo < a.S;
-  const int b = in ? lo : 0;
-  write_slot(a, t, b, a.cu[b], in && a.total[b] >= 0);
-}
-
 __global__ __launch_bounds__(kMapThreads) void page_map_kernel(PageMapArgs a, int with_slots) {
   __shared__ long long red[kMapWaves];
+  __shared__ int s_end[kMapThreads], s_held[kMapThreads], s_to[kMapThreads], s_ok[kMapThreads], s_taken;
   const int tid = threadIdx.x;
   long long all;
+  if (tid == 0) s_taken = 0;
 
-  // Returned pages.
+  // Returned pages. The sums saturate at F: what is past it is dropped.
   int have = a.n_free[0];
   have = have < 0 ? 0 : (have > a.F ? a.F : have);
   long long back = 0;
   for (int b0 = 0; b0 < a.S; b0 += kMapThreads) {
-    const int b = b0 + tid;
-    const Request r(a, b);
+    const Request r(a, b0 + tid);
     const int held = r.gone ? pages_of(r.len, a.page_shift) : 0;
-    const long long at = have + back + block_sum(held, red, &all) - held;
-    for (int k = 0; k < held && at + k < a.F; ++k) a.free_pages[at + k] = a.table[(size_t)b * a.max_pages + k];
+    const long long sum = block_sum(held, red, &all);
+    const long long room = a.F - have - back;             // entries left above the list
+    const int n = (int)(all < room ? all : (room > 0 ? room : 0));
+    s_end[tid] = (int)(sum < n ? sum : n);
+    s_held[tid] = (int)(sum - held < n ? sum - held : n);
+    __syncthreads();
+    for (int k = tid; k < n; k += kMapThreads) {
+      const int x = first_past(s_end, kMapThreads, k);
+      a.free_pages[have + back + k] = a.table[(size_t)(b0 + x) * a.max_pages + (k - s_held[x])];
+    }
     back += all;
+    __syncthreads();                   // s_end is read; the last time, the list is whole too
   }
   const int top = (int)(have + back > a.F ? (long long)a.F : have + back);
-  __syncthreads();                     // the list is whole before pages are taken from it
 
   // Offsets, totals and pages for the new tokens.
-  long long tokens = 0, needed = 0, taken = 0;
+  long long tokens = 0, needed = 0;
+  constexpr long long kMost = 0x7fffffff;
   for (int b0 = 0; b0 < a.S; b0 += kMapThreads) {
     const int b = b0 + tid;
     const Request r(a, b);
@@ -122,40 +138,65 @@ __global__ __launch_bounds__(kMapThreads) void page_map_kernel(PageMapArgs a, in
     bool ok = r.fits && end <= a.N;
     const int need = ok ? pages_of(r.len + r.q, a.page_shift) - held : 0;
     const long long upto = needed + block_sum(need, red, &all);
-    needed += all;
     ok = ok && (need == 0 || upto <= top);
     if (b < a.S) {
-      constexpr long long kMost = 0x7fffffff;
       a.cu[b + 1] = (int)(end < kMost ? end : kMost);
       a.total[b] = ok ? r.len + r.q : (r.gone ? 0 : -1);
     }
-    if (ok) {
-      int* row = a.table + (size_t)b * a.max_pages + held;
-      const int* from = a.free_pages + (top - 1 - (upto - need));
-      for (int k = 0; k < need; ++k) row[k] = from[-k];
+    // The requests that find their pages come first: the list closes at the first
+    // that does not, and taken is the last one's sum.
+    const bool takes = ok && need > 0;
+    if (takes) atomicMax(&s_taken, (int)upto);
+    s_end[tid] = (int)(upto < kMost ? upto : kMost);      // pages up to and with this request
+    s_to[tid] = held;
+    s_held[tid] = need;
+    __syncthreads();
+    const int taken = s_taken, before = (int)(needed < top ? needed : top);
+    for (int k = before + tid; k < taken; k += kMapThreads) {
+      const int x = first_past(s_end, kMapThreads, k);
+      a.table[(size_t)(b0 + x) * a.max_pages + s_to[x] + (k - (s_end[x] - s_held[x]))] = a.free_pages[top - 1 - k];
     }
-    block_sum(ok ? need : 0, red, &all);
-    taken += all;
+    needed += all;
+    __syncthreads();                   // the lists are read, the pages are in the table
+    if (with_slots && a.S <= kMapThreads) {
+      s_end[tid] = b < a.S ? (int)(end < kMost ? end : kMost) : (int)kMost;
+      s_to[tid] = r.len;
+      s_held[tid] = (int)(end - r.q < kMost ? end - r.q : kMost);
+      s_ok[tid] = ok;
+    }
   }
   if (tid == 0) {
     a.cu[0] = 0;
-    a.n_free_out[0] = top - (int)taken;
+    a.n_free_out[0] = top - s_taken;
   }
   if (!with_slots) return;
-  __threadfence_block();
-  __syncthreads();                     // offsets, totals and table are written
-  for (int t = tid; t < a.N; t += kMapThreads) token_slot(a, t);
+  __syncthreads();
+  for (int t = tid; t < a.N; t += kMapThreads) {
+    const int x = first_past(s_end, a.S, t);
+    const bool in = x < a.S;
+    write_slot(a, t, in ? x : 0, s_held[in ? x : 0], s_to[in ? x : 0], in && s_ok[x]);
+  }
 }
 
 __global__ __launch_bounds__(kSlotThreads) void page_slots_kernel(PageMapArgs a) {
+  __shared__ int s_end[kSlotsLds];
+  const bool lds = a.S <= kSlotsLds;
+  if (lds) {
+    for (int b = threadIdx.x; b < a.S; b += kSlotThreads) s_end[b] = a.cu[b + 1];
+    __syncthreads();
+  }
   const int t = blockIdx.x * kSlotThreads + threadIdx.x;
-  if (t < a.N) token_slot(a, t);
+  if (t >= a.N) return;
+  const int x = lds ? first_past<int>(s_end, a.S, t) : first_past<int>(a.cu + 1, a.S, t);
+  const bool in = x < a.S;
+  const int b = in ? x : 0;
+  write_slot(a, t, b, a.cu[b], a.len[b], in && a.total[b] >= 0);
 }
 
 }  // namespace
 
 hipError_t launch_page_map(const PageMapArgs& a, hipStream_t s) {
-  const int with_slots = a.N <= kMapThreads;
+  const int with_slots = a.N <= kSlotsInline && a.S <= kMapThreads;
   hipLaunchKernelGGL(page_map_kernel, dim3(1), dim3(kMapThreads), 0, s, a, with_slots);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || with_slots) return e;

@@ -462,6 +462,13 @@ def cache_append(cache_P2, cache_V, lens, p2, v, stream=None):
 _I32 = torch.int32
 
 
+def _raw_stream(index: int) -> int:
+    """The current stream of a device (torch.cuda.current_stream builds an object
+    around it first, 3 us)."""
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return raw(index) if raw is not None else torch.cuda.current_stream(index).cuda_stream
+
+
 def _check_tensors(fn, specs):
     """Shapes, dtypes and token layouts of all tensors first, whatever device they
     are on; then device and contiguity. dense False: a packed token tensor [N, heads, d_h] whose
@@ -476,9 +483,9 @@ def _check_tensors(fn, specs):
         if not dense and (t.stride(2) != 1 or (shape[1] > 1 and t.stride(1) != shape[2])):
             raise ValueError(f"{fn}: the heads of each token of {name} must be contiguous")
     dev = specs[0][1].device
+    if dev.type != "cuda":
+        raise ValueError(f"{fn}: {specs[0][0]} must be a device tensor")
     for name, t, _, _, dense in specs:
-        if not t.is_cuda:
-            raise ValueError(f"{fn}: {name} must be a device tensor")
         if t.device != dev:
             raise ValueError(f"{fn}: {name} is on {t.device}, the inputs on {dev}")
         if dense and not t.is_contiguous():
@@ -492,11 +499,12 @@ def _run_on(fn, dev, stream, args):
     if stream is not None and stream.device != dev:
         raise ValueError(f"{fn}: the stream is on {stream.device}, the tensors on {dev}")
     f = getattr(lib(), fn)
+    sp = _raw_stream(dev.index) if stream is None else stream.cuda_stream
     if dev.index == torch.cuda.current_device():
-        st = f(*args, _stream(stream))
+        st = f(*args, sp)
     else:
         with torch.cuda.device(dev):
-            st = f(*args, _stream(stream))
+            st = f(*args, sp)
     if st != 0:
         raise RelationError(fn, st)
 
