@@ -60,8 +60,8 @@
 //
 // The paged form (relation_paged_fwd's long chunks, kPaged) runs the same scan
 // on segments: a query tile is 256 positions of one request, from a multiple
-// of 64, and a segment is a range of the tile's key tiles (semantics and work
-// split in paged_chunk.hip). Tiles are then counted from the segment's first,
+// of 64, and a segment is a range of the tile's key tiles (the cut of the work is
+// in paged_device.h). Tiles are then counted from the segment's first,
 // P2 and V rows are found through the request's block table (a wave moves the
 // same 8-row group of every tile, which lies within one page), and a segment
 // that does not hold all of its query tile's keys leaves a partial state.
@@ -356,8 +356,7 @@ __device__ __forceinline__ void fwd_body(const FwdArgs& a, const HeadParams& hp,
 
   // One query tile (256 rows) of one head, start to finish; then, when nqt >=
   // 0, the P1 rows of query tile nqt of head nbh are loaded.
-  auto run_tile = [&](int qt, int bh, int nqt, int nbh, const paged::Segment& sg, const paged::Segment& nsg)
-                      __attribute__((always_inline)) {
+  auto run_tile = [&](int qt, int bh, int nqt, int nbh, const paged::Segment& sg) __attribute__((always_inline)) {
   const int h = kPaged ? sg.h : bh % a.H;
   const size_t head = (size_t)bh * (size_t)T * DR;
   const long long head_bytes = (long long)T * DR * 2;
@@ -786,7 +785,6 @@ __device__ __forceinline__ void fwd_body(const FwdArgs& a, const HeadParams& hp,
       __builtin_amdgcn_s_barrier();                     // the rings are free for the next segment
       asm volatile("" ::: "memory");
       __builtin_amdgcn_sched_barrier(0);
-      if (nsg.te > 0) load_q_paged(nsg);
       return;
     }
   }
@@ -867,9 +865,7 @@ __device__ __forceinline__ void fwd_body(const FwdArgs& a, const HeadParams& hp,
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
   __builtin_amdgcn_sched_barrier(0);
-  if constexpr (kPaged) {
-    if (nsg.te > 0) load_q_paged(nsg);
-  } else {
+  if constexpr (!kPaged) {
     if (nqt >= 0) load_q(nqt, nbh);
   }
   };
@@ -877,16 +873,13 @@ __device__ __forceinline__ void fwd_body(const FwdArgs& a, const HeadParams& hp,
   if constexpr (kPaged) {
     // The work-group's range of units (key tiles of all query tiles), segment by
     // segment.
-    paged::SegmentSource src(pg, plan, blockIdx.x, gridDim.x);
-    paged::Segment sg = src.next().uniform();
-    if (sg.te == 0) return;
-    load_q_paged(sg);
+    paged::ChunkSource src(pg, plan);
 #pragma nounroll
     while (true) {
-      const paged::Segment nsg = src.next().uniform();
-      run_tile(0, 0, -1, 0, sg, nsg);
-      if (nsg.te == 0) break;
-      sg = nsg;
+      const paged::Segment sg = src.next().uniform();
+      if (sg.te == 0) break;
+      load_q_paged(sg);
+      run_tile(0, 0, -1, 0, sg);
     }
     return;
   }
@@ -912,7 +905,7 @@ __device__ __forceinline__ void fwd_body(const FwdArgs& a, const HeadParams& hp,
       work_of(nw, gridDim.x, npair, a.B * a.H, nbh, npr);
       nqt = nq - 1 - npr;
     }
-    run_tile(qt, bh, nqt, nbh, none, none);
+    run_tile(qt, bh, nqt, nbh, none);
     if (nqt < 0) break;
     w = nw;
     bh = nbh;

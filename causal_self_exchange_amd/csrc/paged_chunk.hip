@@ -2,12 +2,10 @@
 // scan of fwd_body.h in its paged form, on query tiles of 256 positions of one
 // request and one head.
 //
-// The key tiles of all query tiles form one line of units that is cut into equal
-// ranges, one per work-group (paged_device.h): one prompt of 8192, ten ragged
-// ones, or one chunk of 256 rows over 100,000 cached ones keep the same share of
-// the chip busy. A query tile that a cut divides leaves a partial state in each
-// range; the join kernel of paged_fwd.hip finishes it. The scan's stabiliser is 0 unless a
-// segment's evidence overflows it, so joining is mostly a sum.
+// The key tiles of all query tiles are cut into equal ranges (paged_device.h): one
+// prompt of 8192, ten ragged ones, or one chunk of 256 rows over 100,000 cached
+// ones keep every compute unit busy to the end. The scan's stabiliser is 0 unless
+// a segment's evidence overflows it, so joining a divided tile is mostly a sum.
 #include "fwd_body.h"
 
 namespace rel {
@@ -19,7 +17,7 @@ using namespace paged;
 template <int D, int DR>
 __global__ __launch_bounds__(kThreads, 1) void paged_chunk_kernel(PagedArgs a, HeadParams hp) {
   __shared__ PlanLds lds;
-  const Plan plan = load_plan(a, Cut{0, kChunkMin, 0, 0}, false, true, lds);
+  const Plan plan = load_plan(a, 0, kChunkMin, lds);
   const FwdArgs none{};
   const RopeParams no_rope{};
   fwd_body<D, DR, true, false, true>(none, hp, no_rope, a, plan);

@@ -15,6 +15,9 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 // A value that is the same in every lane, in a scalar register: buffer
 // descriptors are formed from it.
 __device__ __forceinline__ int uni(int x) { return __builtin_amdgcn_readfirstlane(x); }
+__device__ __forceinline__ long long uni(long long x) {
+  return (long long)((unsigned long long)(unsigned)uni((int)(x >> 32)) << 32 | (unsigned)uni((int)x));
+}
 
 // What the device-side numbers say of request b; q = 0 for one that is skipped.
 struct Req {
@@ -75,326 +78,274 @@ __device__ __forceinline__ Req scan_part(Req r, int chunk_min) {
   return r;
 }
 
-// ---- plan ---------------------------------------------------------------------
+// ---- work ---------------------------------------------------------------------
 //
-// How the batch's work is cut, from the device-side lengths. Scan kernel: row
-// blocks of row_block rows of a request and cached head, times splits of its
-// history of `chunk` keys; partial states where a history is split. Long chunks:
-// key tiles of all query tiles and heads, in one line. The sums are exclusive,
-// over the requests.
+// Both kernels cut their work the same way, from the device-side lengths. A unit
+// is 128 keys of one row block (scan: row_block rows of a request and cached head)
+// or one 64-key tile of one query tile (long chunks: 256 positions of a request
+// and head). The units of all row blocks or tiles form one line, request by
+// request and head by head, which is cut into equal ranges, one per work-group:
+// one request or many, ragged or not, every work-group reads the same number of
+// keys. A row block or tile that a cut divides leaves a partial state in each
+// range it lies in, at most two per range, and the join kernel finishes it.
 
-constexpr int kMinChunk = 512;            // keys of the shortest split
-constexpr int kMaxChunk = 0x7fffff80;     // stands for unsplit histories of any length
-
-// What the host fixes of it.
-struct Cut {
-  int row_block;          // rows per scan item
-  int chunk_min;          // new tokens from which a request is a long chunk; 0: none is
-  int scan_groups;        // work-groups of the scan kernel
-  int chunk_groups;       // and of the long-chunk kernel
-};
+constexpr int kScanUnit = 128;
+constexpr int kMinRange = 4;              // units of the shortest range: shorter ones cost more in joins than they save
 
 struct Plan {
-  int chunk, units, merge_rows;
-  int* unit_sum;          // row blocks x splits (times H_kv work items)
-  int* part_sum;          // partial rows
-  int* merge_sum;         // rows to join
-  long long* tile_sum;    // key tiles of the long chunks; [S] the total
+  long long* unit_sum;    // exclusive sums over the requests; [S] the total
+  long long* tile_sum;
 };
 
-__device__ __forceinline__ int splits_of(int total, int chunk) {
-  return chunk == kMaxChunk ? 1 : (int)(((unsigned)total + (unsigned)chunk - 1u) / (unsigned)chunk);
-}
-
-// Sums over the first four waves of a work-group, of N values per thread at
-// once: inclusive sums in x, totals in total; every thread of the work-group
-// calls it, and red is free again when it returns.
-template <typename Int, int N>
-__device__ __forceinline__ void sum_256(Int (&x)[N], Int (&total)[N], Int (*red)[N]) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-#pragma unroll
-  for (int o = 1; o < 64; o <<= 1)
-#pragma unroll
-    for (int k = 0; k < N; ++k) {
-      const Int y = __shfl_up(x[k], o, 64);
-      if (lane >= o) x[k] += y;
-    }
-  if (lane == 63 && wave < 4)
-#pragma unroll
-    for (int k = 0; k < N; ++k) red[wave][k] = x[k];
-  __syncthreads();
-#pragma unroll
-  for (int k = 0; k < N; ++k) {
-    Int before = 0, all = 0;
-#pragma unroll
-    for (int w = 0; w < 4; ++w) {
-      before += w < wave ? red[w][k] : 0;
-      all += red[w][k];
-    }
-    x[k] += before;
-    total[k] = all;
+// The scan's part of a request.
+struct ScanRows {
+  int rows, blocks, units;     // rows per cached head, row blocks, units of each
+  __device__ __forceinline__ ScanRows(const PagedArgs& a, const Req& r, int row_block) {
+    rows = r.q * (a.H / a.H_kv);
+    blocks = (rows + row_block - 1) / row_block;
+    units = max(1, (r.total - 1 + kScanUnit - 1) / kScanUnit);
   }
-  __syncthreads();
-}
-
-struct PlanScratch {
-  long long wide[4][3];
-  int sum[4][3];
 };
 
-// Fills p and the arrays it points to, by the work-group's first 256 threads
-// (every thread calls). scan / chunks: which sums are wanted.
-__device__ __forceinline__ void make_plan(const PagedArgs& a, const Cut& cut, bool scan, bool chunks, PlanScratch& sc,
-                                          Plan& p) {
-  const int row_block = cut.row_block, chunk_min = cut.chunk_min;
-  const int tid = threadIdx.x;
-  const int G = a.H / a.H_kv;
-  // Up to 256 requests each thread keeps its own.
-  Req mine;
-  mine.q = 0;
-  if (tid < 256 && tid < a.S) mine = Req(a, tid);
-  if (scan) {
-    // Key visits of the row blocks, the items without splits, and rows times keys:
-    // a split length c makes at most visits / c + base items. They should fill the
-    // scan's work-groups a whole number of times, with as many again as there are
-    // at least: a few items past a round cost a round. The length also keeps the
-    // partial rows within the workspace (a split request has at most 2 total /
-    // chunk splits).
-    long long x[3] = {0, 0, 0}, n[3];
-    for (int b = tid; b < a.S && tid < 256; b += 256) {
-      const Req r = scan_part(b < 256 ? mine : Req(a, b), chunk_min);
-      const long long blocks = (long long)((r.q * G + row_block - 1) / row_block) * a.H_kv;
-      x[0] += blocks * r.total;
-      x[1] += blocks;
-      x[2] += (long long)r.q * a.H * r.total;
-    }
-    sum_256<long long, 3>(x, n, sc.wide);
-    const long long room = (2 * n[1] + cut.scan_groups - 1) / cut.scan_groups * cut.scan_groups - n[1];
-    float c1 = room > 0 ? (float)n[0] / (float)room : 0.0f;
-    const float c2 = (float)(2 * n[2]) * (1.0f / kPartialRows) * 1.00001f;
-    c1 = fmaxf(fmaxf(c1, c2) + 1.0f, (float)kMinChunk);
-    p.chunk = c1 < 2.0e9f ? ((int)c1 + 127) & ~127 : kMaxChunk;
-  }
-  int done[3] = {0, 0, 0};     // units, rows to join, partial rows
-  long long tiles = 0;
+struct PlanScratch { long long red[4][2]; };
+
+// Fills the sums whose arrays p has, by the work-group's first 256 threads; every
+// thread calls. row_block: rows per scan item; chunk_min: new tokens from which a
+// request is a long chunk, 0 when none is.
+__device__ __forceinline__ void make_plan(const PagedArgs& a, int row_block, int chunk_min, PlanScratch& sc, const Plan& p) {
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  long long done[2] = {0, 0};
   for (int b0 = 0; b0 < a.S; b0 += 256) {
     const int b = b0 + tid;
     const bool in = tid < 256 && b < a.S;
-    Req r;
-    r.q = 0;
-    if (in) r = b0 == 0 ? mine : Req(a, b);
-    if (scan) {
-      const Req s = scan_part(r, chunk_min);
-      const int splits = s.q > 0 ? splits_of(s.total, p.chunk) : 0;
-      const int rows = splits > 1 ? s.q * a.H : 0;
-      const int own[3] = {(s.q * G + row_block - 1) / row_block * splits, rows, rows * splits};
-      int x[3] = {own[0], own[1], own[2]}, n[3];
-      sum_256<int, 3>(x, n, sc.sum);
-      if (in) {
-        p.unit_sum[b] = done[0] + x[0] - own[0];
-        p.merge_sum[b] = done[1] + x[1] - own[1];
-        p.part_sum[b] = done[2] + x[2] - own[2];
+    long long own[2] = {0, 0};
+    if (in) {
+      const Req r(a, b);
+      const Req s = scan_part(r, chunk_min), c = chunk_part(r, chunk_min);
+      if (p.unit_sum && s.q > 0) {
+        const ScanRows n(a, s, row_block);
+        own[0] = (long long)n.blocks * a.H_kv * n.units;
       }
+      if (p.tile_sum && c.q > 0) {
+        const ChunkTiles t(c.total - c.q, c.total);
+        own[1] = t.before(t.n) * a.H;
+      }
+    }
+    long long x[2] = {own[0], own[1]};
 #pragma unroll
-      for (int k = 0; k < 3; ++k) done[k] += n[k];
-    }
-    if (chunks) {
-      const Req s = chunk_part(r, chunk_min);
-      long long own = 0;
-      if (s.q > 0) {
-        const ChunkTiles t(s.total - s.q, s.total);
-        own = t.before(t.n) * a.H;
+    for (int o = 1; o < 64; o <<= 1)
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const long long y = __shfl_up(x[k], o, 64);
+        if (lane >= o) x[k] += y;
       }
-      long long x[3] = {own, 0, 0}, n[3];
-      sum_256<long long, 3>(x, n, sc.wide);
-      if (in) p.tile_sum[b] = tiles + x[0] - own;
-      tiles += n[0];
+    if (lane == 63 && wave < 4) {
+      sc.red[wave][0] = x[0];
+      sc.red[wave][1] = x[1];
     }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      long long all = 0;
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        x[k] += w < wave ? sc.red[w][k] : 0;
+        all += sc.red[w][k];
+      }
+      x[k] += done[k] - own[k];
+      done[k] += all;
+    }
+    if (in && p.unit_sum) p.unit_sum[b] = x[0];
+    if (in && p.tile_sum) p.tile_sum[b] = x[1];
+    __syncthreads();
   }
-  p.units = done[0];
-  p.merge_rows = done[1];
-  if (chunks && tid == 0) p.tile_sum[a.S] = tiles;
+  if (tid == 0) {
+    if (p.unit_sum) p.unit_sum[a.S] = done[0];
+    if (p.tile_sum) p.tile_sum[a.S] = done[1];
+  }
 }
 
-// The plan in the workspace: written by plan_kernel for more than kPlanInline
-// requests, else by the scan kernel's first work-group for the join.
-struct WsPlan {
-  int* head;              // chunk, units, merge_rows
-  Plan p;
-  __device__ __forceinline__ void put_head(const Plan& q) {
-    head[0] = q.chunk;
-    head[1] = q.units;
-    head[2] = q.merge_rows;
-  }
-  __device__ __forceinline__ Plan get() {
-    p.chunk = uni(head[0]);
-    p.units = uni(head[1]);
-    p.merge_rows = uni(head[2]);
-    return p;
-  }
-  __device__ __forceinline__ WsPlan(const PagedArgs& a) {
-    char* w = static_cast<char*>(a.ws);
-    head = reinterpret_cast<int*>(w);
-    w += kPlanHeader;
-    const int64_t n = paged_sum_bytes(a.S, 4);
-    p.unit_sum = reinterpret_cast<int*>(w);
-    p.part_sum = reinterpret_cast<int*>(w + n);
-    p.merge_sum = reinterpret_cast<int*>(w + 2 * n);
-    p.tile_sum = reinterpret_cast<long long*>(w + 3 * n);
-  }
-};
+// The sums that plan_kernel left in the workspace (more than kPlanInline requests).
+__device__ __forceinline__ Plan ws_plan(const PagedArgs& a) {
+  char* w = static_cast<char*>(a.ws);
+  return Plan{reinterpret_cast<long long*>(w), reinterpret_cast<long long*>(w + paged_sum_bytes(a.S))};
+}
 
-// A kernel's plan: formed in LDS by each work-group for up to kPlanInline
+// A kernel's sums: formed in LDS by each work-group for up to kPlanInline
 // requests (a launch of its own and the wait for it take 5 us), else read from
 // the workspace.
 struct PlanLds {
   PlanScratch sc;
-  int unit_sum[kPlanInline + 1], part_sum[kPlanInline + 1], merge_sum[kPlanInline + 1];
-  long long tile_sum[kPlanInline + 1];
+  long long sum[kPlanInline + 1];
 };
-__device__ __forceinline__ Plan load_plan(const PagedArgs& a, const Cut& cut, bool scan, bool chunks, PlanLds& lds) {
-  if (a.S > kPlanInline) {
-    WsPlan w(a);
-    return w.get();
-  }
-  Plan p{};
-  p.unit_sum = lds.unit_sum;
-  p.part_sum = lds.part_sum;
-  p.merge_sum = lds.merge_sum;
-  p.tile_sum = lds.tile_sum;
-  make_plan(a, cut, scan, chunks, lds.sc, p);
+__device__ __forceinline__ Plan load_plan(const PagedArgs& a, int row_block, int chunk_min, PlanLds& lds) {
+  if (a.S > kPlanInline) return ws_plan(a);
+  const Plan p = row_block > 0 ? Plan{lds.sum, nullptr} : Plan{nullptr, lds.sum};
+  make_plan(a, row_block, chunk_min, lds.sc, p);
   __syncthreads();
-  p.chunk = uni(p.chunk);
-  p.units = uni(p.units);
-  p.merge_rows = uni(p.merge_rows);
   return p;
 }
 
-// Partial states in the workspace: of the scan's split histories, and of the
-// long chunks' divided tiles.
-struct States {
-  float2* ml;
-  float* z;
-  __device__ __forceinline__ static States scan(const PagedArgs& a) {
-    char* w = static_cast<char*>(a.ws) + paged_plan_bytes(a.S);
-    return {reinterpret_cast<float2*>(w), reinterpret_cast<float*>(w + kPartialRows * sizeof(float2))};
-  }
-  __device__ __forceinline__ static States chunk(const PagedArgs& a) {
-    char* w = static_cast<char*>(a.ws) + paged_plan_bytes(a.S) + paged_scan_bytes(a.d_h) + kCutBytes;
-    return {reinterpret_cast<float2*>(w), reinterpret_cast<float*>(w + (int64_t)kChunkStates * 256 * sizeof(float2))};
-  }
-};
-
-// The last request b with off[b] <= i: 64 entries are compared at a time.
-template <typename Int>
-__device__ __forceinline__ int find_request(const Int* off, int S, Int i) {
+// The last request b with off[b] <= u: 64 entries are compared at a time.
+__device__ __forceinline__ int find_request(const long long* off, int S, long long u) {
   const int lane = threadIdx.x & 63;
   int lo = 0, n = S;
   while (n > 1) {
     const int stride = (n + 63) >> 6;
     const int k = lane * stride;
-    const bool le = k < n && off[lo + k] <= i;
+    const bool le = k < n && off[lo + k] <= u;
     const int cnt = __popcll(__ballot(le));
     lo += (cnt - 1) * stride;
     n = min(stride, n - (cnt - 1) * stride);
   }
-  return __builtin_amdgcn_readfirstlane(lo);
+  return uni(lo);
 }
 
-// ---- long chunks --------------------------------------------------------------
+// The row block or tile that the end of a work-group's range divides, for the
+// join: pieces = 0 when there is none. Piece 0 is the last segment of the range,
+// the others the first segments of the ranges after it.
+struct CutRecord {
+  int pieces, b, head, first, ctx, total, row0, rows;
+};
+static_assert(sizeof(CutRecord) == kCutBytes, "workspace layout");
 
-// A unit is one key tile of one query tile; the units of all query tiles (per
-// request, per head, tile by tile) form one line that is cut into equal ranges
-// of at least 8, one per work-group, whatever the requests' lengths. A segment
-// is the part of a query tile's key tiles in one range: [tb, te), te = 0 for
-// none. slot: the partial state it leaves, or -1 when it holds all of them.
+// Records and partial states of the scan or of the long chunks.
+struct States {
+  CutRecord* cuts;
+  float2* ml;
+  float* z;
+  __device__ __forceinline__ static States scan(const PagedArgs& a) {
+    return at(static_cast<char*>(a.ws) + paged_scan_offset(a.S), kScanGroups, kScanStateRows);
+  }
+  __device__ __forceinline__ static States chunk(const PagedArgs& a) {
+    return at(static_cast<char*>(a.ws) + paged_chunk_offset(a.S, a.d_h), kChunkGroups, kChunkStateRows);
+  }
+  __device__ __forceinline__ static States at(char* w, int groups, int rows) {
+    char* m = w + groups * kCutBytes;
+    return {reinterpret_cast<CutRecord*>(w), reinterpret_cast<float2*>(m),
+            reinterpret_cast<float*>(m + (int64_t)rows * sizeof(float2))};
+  }
+};
+
+// A work-group's range of the line. Work-groups go round the 8 XCDs, and each
+// XCD takes a contiguous eighth of the line: neighbouring row blocks, tiles and
+// heads, which read the same keys, share its L2.
+struct Range {
+  long long u, end, per;
+  int me;
+  __device__ __forceinline__ Range(long long units, int least, int group, int groups) {
+    me = groups % 8 == 0 ? (group & 7) * (groups >> 3) + (group >> 3) : group;
+    per = (units + groups - 1) / groups;
+    per = uni(per < least ? least : per);
+    u = me * per;
+    end = uni(u + per < units ? u + per : units);
+  }
+  // The partial state of the segment [u, stop) of the units [start, start + n):
+  // -1 when it holds all of them.
+  __device__ __forceinline__ int slot(long long start, int n, long long stop) const {
+    return u == start && stop == start + n ? -1 : (u > start ? 2 * me : 2 * me + 1);
+  }
+  __device__ __forceinline__ int pieces(long long start, int n) const {
+    return 1 + (int)((start + n - end + per - 1) / per);
+  }
+};
+
+// A range's part of one row block: keys [k0, k1) (units = 0 for none).
+struct ScanSegment {
+  int b, kvh, first, ctx, total, row0, rows, k0, k1, units, slot;
+};
+
+struct ScanSource {
+  const PagedArgs& a;
+  const Plan& p;
+  Range rg;
+  int row_block, chunk_min;
+  CutRecord* cuts;
+  __device__ __forceinline__ ScanSource(const PagedArgs& args, const Plan& plan, int rows, int least_new)
+      : a(args), p(plan), rg(plan.unit_sum[args.S], kMinRange, blockIdx.x, gridDim.x), row_block(rows),
+        chunk_min(least_new), cuts(States::scan(args).cuts) {
+    if (threadIdx.x == 0) cuts[rg.me].pieces = 0;
+  }
+  __device__ __forceinline__ ScanSegment next() {
+    ScanSegment s{};
+    if (rg.u >= rg.end) return s;
+    s.b = find_request(p.unit_sum, a.S, rg.u);
+    const Req r = scan_part(Req(a, s.b), chunk_min);
+    const ScanRows n(a, r, row_block);
+    const long long v = rg.u - p.unit_sum[s.b];
+    const int block = (int)((unsigned long long)v / (unsigned)n.units);   // cached head, row block
+    const int at = (int)(v - (long long)block * n.units);
+    const long long start = rg.u - at;
+    const long long stop = start + n.units < rg.end ? start + n.units : rg.end;
+    s.kvh = block / n.blocks;
+    s.row0 = (block - s.kvh * n.blocks) * row_block;
+    s.rows = min(row_block, n.rows - s.row0);
+    s.first = r.first;
+    s.ctx = r.total - r.q;
+    s.total = r.total;
+    s.units = (int)(stop - rg.u);
+    // Keys below the block's last row's position.
+    const int last = s.ctx + (s.row0 + s.rows - 1) / (a.H / a.H_kv);
+    s.k0 = at * kScanUnit;
+    s.k1 = (int)min((long long)last, ((long long)at + s.units) * kScanUnit);
+    s.slot = rg.slot(start, n.units, stop);
+    if (s.slot == 2 * rg.me + 1 && threadIdx.x == 0)
+      cuts[rg.me] = CutRecord{rg.pieces(start, n.units), s.b, s.kvh, s.first, s.ctx, s.total, s.row0, s.rows};
+    rg.u = uni(stop);
+    return s;
+  }
+};
+
+// A range's part of one query tile: key tiles [tb, te), te = 0 for none.
 struct Segment {
   int b, h, kvh;
   int first, ctx, total;       // packed token of the chunk's first row, its position, cached rows
-  int q0, tb, te, slot;
+  int q0, tb, te, slot;        // q0: the tile's first position
   // The same, every field in a scalar register.
   __device__ __forceinline__ Segment uniform() const {
     return Segment{uni(b), uni(h), uni(kvh), uni(first), uni(ctx), uni(total), uni(q0), uni(tb), uni(te), uni(slot)};
   }
 };
 
-// The query tile that the end of a work-group's range divides, for the join:
-// pieces = 0 when there is none. Piece 0 is the last segment of range k, the
-// others the first segments of the ranges after it.
-struct CutTile {
-  int pieces, b, h, first, ctx, total, q0, pad;
-};
-static_assert(sizeof(CutTile) == 32 && kChunkGroups * sizeof(CutTile) == kCutBytes, "workspace layout");
-
-__device__ __forceinline__ long long range_length(long long units, int groups) {
-  const long long per = (units + groups - 1) / groups;
-  return per < 8 ? 8 : per;
-}
-
-// The query tile of unit u: its request and head, its index within them, and
-// the unit of its first key tile.
-struct TileOf {
-  int b, h, tile, keys;
-  long long start;
-  Req r;
-  __device__ __forceinline__ TileOf(const PagedArgs& a, const Plan& p, long long u) {
-    b = find_request(p.tile_sum, a.S, u);
-    r = chunk_part(Req(a, b), kChunkMin);
+struct ChunkSource {
+  const PagedArgs& a;
+  const Plan& p;
+  Range rg;
+  CutRecord* cuts;
+  __device__ __forceinline__ ChunkSource(const PagedArgs& args, const Plan& plan)
+      : a(args), p(plan), rg(plan.tile_sum[args.S], 2 * kMinRange, blockIdx.x, gridDim.x), cuts(States::chunk(args).cuts) {
+    if (threadIdx.x == 0) cuts[rg.me].pieces = 0;
+  }
+  __device__ __forceinline__ Segment next() {
+    Segment s{};
+    if (rg.u >= rg.end) return s;
+    s.b = find_request(p.tile_sum, a.S, rg.u);
+    const Req r = chunk_part(Req(a, s.b), kChunkMin);
     const ChunkTiles t(r.total - r.q, r.total);
     const long long per_head = t.before(t.n);
-    const long long v = u - p.tile_sum[b];
-    h = (int)(v / per_head);
-    const long long w = v - h * per_head;
+    const long long v = rg.u - p.tile_sum[s.b];
+    s.h = (int)(v / per_head);
+    const long long w = v - s.h * per_head;
     int lo = 0, hi = t.n - 1;                            // the last tile that starts at or before w
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
       if (t.before(mid) <= w) lo = mid;
       else hi = mid - 1;
     }
-    tile = lo;
-    keys = t.keys(tile);
-    start = p.tile_sum[b] + h * per_head + t.before(tile);
-  }
-};
-
-// The segments of one work-group, in order. Work-groups go round the 8 XCDs, and
-// each XCD takes a contiguous eighth of the line: neighbouring tiles and heads,
-// which read the same keys, share its L2.
-struct SegmentSource {
-  const PagedArgs& a;
-  const Plan& p;
-  long long u, end, per;
-  int me;
-  __device__ __forceinline__ SegmentSource(const PagedArgs& args, const Plan& plan, int group, int groups)
-      : a(args), p(plan) {
-    me = groups % 8 == 0 ? (group & 7) * (groups >> 3) + (group >> 3) : group;
-    const long long units = p.tile_sum[a.S];
-    per = range_length(units, groups);
-    u = me * per;
-    end = u + per < units ? u + per : units;
-    if (threadIdx.x == 0) cuts()[me].pieces = 0;
-  }
-  __device__ __forceinline__ CutTile* cuts() const {
-    return reinterpret_cast<CutTile*>(static_cast<char*>(a.ws) + paged_plan_bytes(a.S) + paged_scan_bytes(a.d_h));
-  }
-  __device__ __forceinline__ Segment next() {
-    Segment s{};
-    if (u >= end) return s;
-    const TileOf t(a, p, u);
-    s.b = t.b;
-    s.h = t.h;
-    s.kvh = t.h / (a.H / a.H_kv);
-    s.first = t.r.first;
-    s.total = t.r.total;
-    s.ctx = t.r.total - t.r.q;
-    s.q0 = (s.ctx & ~63) + 256 * t.tile;
-    s.tb = (int)(u - t.start);
-    const long long stop = t.start + t.keys < end ? t.start + t.keys : end;
-    s.te = (int)(stop - t.start);
-    s.slot = s.tb == 0 && s.te == t.keys ? -1 : (s.tb > 0 ? 2 * me : 2 * me + 1);
-    if (s.slot == 2 * me + 1 && threadIdx.x == 0)
-      cuts()[me] = CutTile{1 + (int)((t.start + t.keys - end + per - 1) / per), s.b, s.h, s.first, s.ctx, s.total, s.q0, 0};
-    u = stop;
+    const int keys = t.keys(lo);
+    s.tb = (int)(w - t.before(lo));
+    const long long start = rg.u - s.tb;
+    const long long stop = start + keys < rg.end ? start + keys : rg.end;
+    s.kvh = s.h / (a.H / a.H_kv);
+    s.first = r.first;
+    s.total = r.total;
+    s.ctx = r.total - r.q;
+    s.q0 = (s.ctx & ~63) + 256 * lo;
+    s.te = (int)(stop - start);
+    s.slot = rg.slot(start, keys, stop);
+    if (s.slot == 2 * rg.me + 1 && threadIdx.x == 0)
+      cuts[rg.me] = CutRecord{rg.pieces(start, keys), s.b, s.h, s.first, s.ctx, s.total, s.q0, 256};
+    rg.u = uni(stop);
     return s;
   }
 };

@@ -4,16 +4,16 @@
 // Sec. 5.3).
 //
 // The rows of a request that share a cached head (its new tokens times the
-// query heads of the group) are taken in blocks of 16 NB rows. A work item is
-// (request, split of its history, cached head, row block); a work-group of four
-// waves scans the item's keys, each wave its own steps of 32 (fp32: 16), and keeps
-// (m, l, z) per row; the waves' states meet in LDS. Where a history is split,
-// the item leaves a partial state and merge_kernel joins them; otherwise the
-// item finishes the row itself (Self entry, count term, output).
+// query heads of the group) are taken in blocks of 16 NB rows. The keys of all
+// row blocks are cut into equal ranges, one per work-group (paged_device.h); a
+// work-group of four waves scans its segments' keys, each wave its own steps of 32
+// (fp32: 16), and keeps (m, l, z) per row; the waves' states meet in LDS. A
+// segment with all of its row block's keys finishes the rows itself (Self entry,
+// count term, output); otherwise it leaves a partial state, and join_kernel
+// finishes the row.
 //
-// Three launches: plan (one work-group: the split length and prefix sums of the
-// work over the requests, from the device-side lengths), scan (persistent), and
-// merge.
+// Launches: plan (more than 256 requests only), the long chunks (paged_chunk.hip,
+// where there can be any), scan, join.
 #include "paged_device.h"
 
 namespace rel {
@@ -26,11 +26,11 @@ constexpr int kWaves = 4;
 constexpr int kThreads = 64 * kWaves;
 constexpr float kLazy = 32.0f;            // log2 slack before the stabiliser moves
 
-__global__ __launch_bounds__(kThreads) void plan_kernel(PagedArgs a, Cut cut) {
+__global__ __launch_bounds__(kThreads) void plan_kernel(PagedArgs a, int row_block, int chunk_min) {
   __shared__ PlanScratch sc;
-  WsPlan w(a);
-  make_plan(a, cut, true, cut.chunk_min > 0, sc, w.p);
-  if (threadIdx.x == 0) w.put_head(w.p);
+  Plan p = ws_plan(a);
+  if (chunk_min == 0) p.tile_sum = nullptr;
+  make_plan(a, row_block, chunk_min, sc, p);
 }
 
 // ---- scan ---------------------------------------------------------------------
@@ -82,7 +82,7 @@ template <typename Tin, int D, int NB>
 constexpr int kPerCu = D <= 64 && NB == 1 ? 4 : 2;
 
 template <typename Tin, int D, int NB>
-__global__ __launch_bounds__(kThreads, (kPerCu<Tin, D, NB>)) void scan_kernel(PagedArgs a, HeadParams hp, Cut cut) {
+__global__ __launch_bounds__(kThreads, (kPerCu<Tin, D, NB>)) void scan_kernel(PagedArgs a, HeadParams hp, int chunk_min) {
   using C = Geom<Tin, D>;
   constexpr bool kBf = C::kBf;
   constexpr int kRb = 16 * NB;
@@ -92,18 +92,7 @@ __global__ __launch_bounds__(kThreads, (kPerCu<Tin, D, NB>)) void scan_kernel(Pa
   __shared__ float s_m[kWaves][16], s_l[kWaves][16];
   __shared__ PlanLds lds;
 
-  const int chunk_min = cut.chunk_min;
-  const Plan plan = load_plan(a, cut, true, false, lds);
-  if (a.S <= kPlanInline && blockIdx.x == 0) {      // for the join
-    WsPlan w(a);
-    if ((int)threadIdx.x < a.S) {
-      w.p.part_sum[threadIdx.x] = plan.part_sum[threadIdx.x];
-      w.p.merge_sum[threadIdx.x] = plan.merge_sum[threadIdx.x];
-    }
-    if (threadIdx.x == 0) w.put_head(plan);
-  }
-  const int n_items = plan.units * a.H_kv;
-  const int chunk = plan.chunk;
+  const Plan plan = load_plan(a, kRb, chunk_min, lds);
   const States states = States::scan(a);
   const int G = a.H / a.H_kv;
   const int tid = threadIdx.x;
@@ -112,7 +101,6 @@ __global__ __launch_bounds__(kThreads, (kPerCu<Tin, D, NB>)) void scan_kernel(Pa
   const int li = lane & 15, lj = lane >> 4;
   const float k2 = hp.scale * kLog2e;
   const int pmask = (1 << a.page_shift) - 1;
-  const int per = (n_items + 7) >> 3;
   char* const slot = smem + wave * C::kSlot;
 
   // Source of this lane's 16 bytes in load u of a 16-row block: LDS position
@@ -124,31 +112,13 @@ __global__ __launch_bounds__(kThreads, (kPerCu<Tin, D, NB>)) void scan_kernel(Pa
     src[u] = q < 16 ? q * D * kEs + 16 * (c ^ C::swz(q)) : kOutOfRange;
   }
 
-  // Work-groups go round the 8 XCDs: each takes a contiguous eighth of the items,
-  // so the row blocks of one (request, split, cached head), which lie together,
-  // read its keys through one L2.
-  for (int it = blockIdx.x; it < 8 * per; it += gridDim.x) {
-    const int item = (it & 7) * per + (it >> 3);
-    if (item >= n_items) continue;
-    const int b = find_request(plan.unit_sum, a.S, item / a.H_kv);
-    Req r = scan_part(Req(a, b), chunk_min);
-    r.first = uni(r.first);
-    r.q = uni(r.q);
-    r.total = uni(r.total);
-    const int all_rows = r.q * G;
-    const int nrb = (all_rows + kRb - 1) / kRb;
-    const int nsplit = splits_of(r.total, chunk);
-    const int local = item - uni(plan.unit_sum[b]) * a.H_kv;   // 0 .. nrb * nsplit * H_kv - 1
-    const int rb = local % nrb;
-    const int kvh = (local / nrb) % a.H_kv;
-    const int split = local / nrb / a.H_kv;
-    const int ctx = r.total - r.q;
-    const int row0 = rb * kRb;
-    const int rows = min(kRb, all_rows - row0);
-    const int pos_lo = ctx + row0 / G, pos_hi = ctx + (row0 + rows - 1) / G;
-    const int k0 = split * chunk;
-    if (split > 0 && k0 >= pos_hi) continue;        // no keys; the join does not read this state
-    const int k1 = (int)min((long long)k0 + chunk, (long long)pos_hi);
+  ScanSource source(a, plan, kRb, chunk_min);
+  while (true) {
+    const ScanSegment sg = source.next();
+    if (uni(sg.units) == 0) break;
+    const int b = uni(sg.b), kvh = uni(sg.kvh), total = uni(sg.total), ctx = uni(sg.ctx), row0 = uni(sg.row0);
+    const int rows = uni(sg.rows), k0 = uni(sg.k0), k1 = uni(sg.k1), first_tok = uni(sg.first), seg_slot = uni(sg.slot);
+    const int pos_lo = ctx + row0 / G;
 
     // The query rows as B operands, and their positions (0 for rows past the end:
     // no key is below it).
@@ -161,7 +131,7 @@ __global__ __launch_bounds__(kThreads, (kPerCu<Tin, D, NB>)) void scan_kernel(Pa
       const int tq = ok ? row / G : 0;
       const int h = kvh * G + (ok ? row - tq * G : 0);
       pos[nb] = ok ? ctx + tq : 0;
-      const char* p = static_cast<const char*>(a.P1) + ((size_t)(r.first + tq) * a.ld1 + (size_t)h * D) * kEs;
+      const char* p = static_cast<const char*>(a.P1) + ((size_t)(first_tok + tq) * a.ld1 + (size_t)h * D) * kEs;
 #pragma unroll
       for (int ks = 0; ks < C::kKs; ++ks) {
         const int c = 4 * ks + lj;
@@ -188,7 +158,7 @@ __global__ __launch_bounds__(kThreads, (kPerCu<Tin, D, NB>)) void scan_kernel(Pa
       const int n = n0 + lane / C::kHalves;
       const int key = (first + kWaves * n) * kStep + 16 * (lane % C::kHalves);
       pages = -1;
-      if (n < nsteps && key < r.total) {
+      if (n < nsteps && key < total) {
         const int pg = a.table[(size_t)b * a.max_pages + (key >> a.page_shift)];
         pages = pg >= 0 && pg < a.n_pages ? pg : -1;
       }
@@ -201,7 +171,7 @@ __global__ __launch_bounds__(kThreads, (kPerCu<Tin, D, NB>)) void scan_kernel(Pa
       for (int hb = 0; hb < C::kHalves; ++hb) {
         const int key = (first + kWaves * n) * kStep + 16 * hb;
         const int pg = __builtin_amdgcn_readlane(pages, C::kHalves * (n % kWin) + hb);
-        const int left = min(16, r.total - key);
+        const int left = min(16, total - key);
         const int bytes = pg >= 0 && left > 0 ? left * D * kEs : 0;
         const size_t row = (((size_t)(pg >= 0 ? pg : 0) * a.H_kv + kvh) << a.page_shift) + (key & pmask);
 #pragma unroll
@@ -396,10 +366,10 @@ __global__ __launch_bounds__(kThreads, (kPerCu<Tin, D, NB>)) void scan_kernel(Pa
       }
       const int tq = ok ? row / G : 0;
       const int h = kvh * G + (ok ? row - tq * G : 0);
-      if (nsplit == 1) {
-        finish_row<Tin, D>(a, hp, b, r.first + tq, h, ctx + tq, sl, M, L, zs, ok);
+      if (seg_slot < 0) {
+        finish_row<Tin, D>(a, hp, b, first_tok + tq, h, ctx + tq, sl, M, L, zs, ok);
       } else if (ok) {
-        const int64_t p = (int64_t)plan.part_sum[b] + (int64_t)split * all_rows * a.H_kv + (int64_t)kvh * all_rows + row;
+        const int64_t p = (int64_t)seg_slot * kRb + 16 * nb + rr;
         if (sl == 0) states.ml[p] = make_float2(M, L);
         if (sl < D / 8) {
           reinterpret_cast<f32x4*>(states.z + p * D + 8 * sl)[0] = f32x4{zs[0], zs[1], zs[2], zs[3]};
@@ -407,35 +377,38 @@ __global__ __launch_bounds__(kThreads, (kPerCu<Tin, D, NB>)) void scan_kernel(Pa
         }
       }
     }
-    __syncthreads();                                // the states are read before the next item's loads land
+    __syncthreads();                                // the states are read before the next segment's loads land
   }
 }
 
 // ---- join ---------------------------------------------------------------------
 
-// Rows of split histories, a wave each: four groups of 16 lanes join every
-// fourth split, then the groups join.
+// Rows of the row block or query tile that the end of range k divides: 16 rows per
+// work-group, 16 lanes per row; up to 4 rows take a wave each, with every fourth
+// piece to a group of 16 lanes.
 template <typename Tin, int D>
-__device__ __forceinline__ void join_rows(const PagedArgs& a, const HeadParams& hp, const Plan& plan, int chunk_min,
-                                          int wave, int waves) {
-  const States st = States::scan(a);
+__device__ __forceinline__ void join_rows(const PagedArgs& a, const HeadParams& hp, const States& st, int k, int first_row,
+                                          int state_rows, bool tile) {
+  const CutRecord c = st.cuts[k];
+  if (c.pieces == 0 || first_row >= c.rows) return;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, sl = lane & 15;
+  const bool few = c.rows <= kWaves;
+  const int i = few ? wave : first_row + (threadIdx.x >> 4);
+  const int from = few ? lane >> 4 : 0, by = few ? 4 : 1;
+  // A tile's rows are positions of one head; a block's are tokens times the heads of a group.
   const int G = a.H / a.H_kv;
-  const int lane = threadIdx.x & 63, g = lane >> 4, sl = lane & 15;
-  for (int i = wave; i < plan.merge_rows; i += waves) {
-    const int b = find_request(plan.merge_sum, a.S, i);
-    const Req r = scan_part(Req(a, b), chunk_min);
-    const int all_rows = r.q * G;
-    const int id = i - plan.merge_sum[b];           // kvh * all_rows + row
-    const int kvh = id / all_rows, row = id - kvh * all_rows;
-    const int tq = row / G, h = kvh * G + row - tq * G;
-    const int pos = r.total - r.q + tq;
-    const int ns = (int)(((long long)pos + plan.chunk - 1) / plan.chunk);   // splits with keys of this row
-    float M = kEmptyMax, L = 0.0f, z[8];
+  const int tq = tile ? c.row0 + i - c.ctx : (c.row0 + i) / G;
+  const int h = tile ? c.head : c.head * G + (c.row0 + i) - tq * G;
+  const bool ok = i < c.rows && tq >= 0 && c.ctx + tq < c.total;
+  float M = kEmptyMax, L = 0.0f, z[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) z[e] = 0.0f;
+  for (int e = 0; e < 8; ++e) z[e] = 0.0f;
+  if (i < c.rows) {
 #pragma unroll 4
-    for (int s = g; s < ns; s += 4)
-      join_state<D>(st, (int64_t)plan.part_sum[b] + (int64_t)s * all_rows * a.H_kv + id, sl, M, L, z);
+    for (int p = from; p < c.pieces; p += by)
+      join_state<D>(st, (int64_t)(p == 0 ? 2 * k + 1 : 2 * (k + p)) * state_rows + i, sl, M, L, z);
+  }
+  if (few) {
 #pragma unroll
     for (int o = 16; o < 64; o <<= 1) {
       const float Mo = __shfl_xor(M, o), Mn = fmaxf(M, Mo);
@@ -445,41 +418,21 @@ __device__ __forceinline__ void join_rows(const PagedArgs& a, const HeadParams& 
       for (int e = 0; e < 8; ++e) z[e] = z[e] * f + __shfl_xor(z[e], o) * fo;
       M = Mn;
     }
-    finish_row<Tin, D>(a, hp, b, r.first + tq, h, pos, sl, M, L, z, g == 0);
   }
+  finish_row<Tin, D>(a, hp, c.b, ok ? c.first + tq : 0, ok ? h : 0, ok ? c.ctx + tq : 0, sl, M, L, z, ok && from == 0);
 }
 
-// 16 rows of the query tile that the end of range k of the long chunks divides,
-// 16 lanes per row.
+// The first scan_groups * row_block / 16 work-groups join the scan's row blocks,
+// the others 16 rows each of the long chunks' tiles.
 template <typename Tin, int D>
-__device__ __forceinline__ void join_tile(const PagedArgs& a, const HeadParams& hp, int k, int rows16) {
-  const CutTile t = reinterpret_cast<const CutTile*>(static_cast<const char*>(a.ws) + paged_plan_bytes(a.S) +
-                                                     paged_scan_bytes(a.d_h))[k];
-  if (t.pieces == 0) return;
-  const States st = States::chunk(a);
-  const int sl = threadIdx.x & 15, i = 16 * rows16 + (threadIdx.x >> 4);
-  const int pos = t.q0 + i;
-  const bool ok = pos >= t.ctx && pos < t.total;
-  float M = kEmptyMax, L = 0.0f, z[8];
-#pragma unroll
-  for (int e = 0; e < 8; ++e) z[e] = 0.0f;
-#pragma unroll 4
-  for (int p = 0; p < t.pieces; ++p)
-    join_state<D>(st, (int64_t)(p == 0 ? 2 * k + 1 : 2 * (k + p)) * 256 + i, sl, M, L, z);
-  finish_row<Tin, D>(a, hp, t.b, ok ? t.first + (pos - t.ctx) : 0, t.h, ok ? pos : 0, sl, M, L, z, ok);
-}
-
-// The first row_groups work-groups join the scan's split histories, the others
-// 16 rows each of the long chunks' divided tiles.
-template <typename Tin, int D>
-__global__ __launch_bounds__(kThreads) void join_kernel(PagedArgs a, HeadParams hp, Cut cut, int row_groups) {
-  if ((int)blockIdx.x < row_groups) {
-    WsPlan w(a);
-    const Plan plan = w.get();
-    join_rows<Tin, D>(a, hp, plan, cut.chunk_min, blockIdx.x * kWaves + (threadIdx.x >> 6), row_groups * kWaves);
+__global__ __launch_bounds__(kThreads) void join_kernel(PagedArgs a, HeadParams hp, int scan_groups, int row_block) {
+  const int blocks = row_block / 16;
+  int i = (int)blockIdx.x;
+  if (i < scan_groups * blocks) {
+    join_rows<Tin, D>(a, hp, States::scan(a), i / blocks, 16 * (i % blocks), row_block, false);
   } else if constexpr (sizeof(Tin) == 2) {
-    const int i = (int)blockIdx.x - row_groups;
-    join_tile<Tin, D>(a, hp, i / 16, i % 16);
+    i -= scan_groups * blocks;
+    join_rows<Tin, D>(a, hp, States::chunk(a), i / 16, 16 * (i % 16), 256, true);
   }
 }
 
@@ -491,22 +444,24 @@ hipError_t launch_rows(const PagedArgs& a, const HeadParams& hp, hipStream_t s) 
   // Long chunks: bf16, with a token stride whose 256 rows a 31-bit byte offset
   // reaches.
   const bool chunks = sizeof(Tin) == 2 && a.max_new >= kChunkMin && a.N >= kChunkMin && a.ld1 < (1 << 22);
-  const Cut cut{16 * NB, chunks ? kChunkMin : 0, cu * kPerCu<Tin, D, NB>, chunks ? (cu < kChunkGroups ? cu : kChunkGroups) : 0};
+  const int chunk_min = chunks ? kChunkMin : 0;
+  const int chunk_groups = chunks ? (cu < kChunkGroups ? cu : kChunkGroups) : 0;
+  int scan_groups = cu * kPerCu<Tin, D, NB>;
+  scan_groups = scan_groups * NB < kScanGroups ? scan_groups : kScanGroups / NB;
   if (a.S > kPlanInline) {
-    hipLaunchKernelGGL(plan_kernel, dim3(1), dim3(kThreads), 0, s, a, cut);
+    hipLaunchKernelGGL(plan_kernel, dim3(1), dim3(kThreads), 0, s, a, 16 * NB, chunk_min);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
   if (chunks) {
-    e = launch_paged_chunk(a, hp, cut.chunk_groups, s);
+    e = launch_paged_chunk(a, hp, chunk_groups, s);
     if (e != hipSuccess) return e;
   }
-  hipLaunchKernelGGL((scan_kernel<Tin, D, NB>), dim3(cut.scan_groups), dim3(kThreads), 0, s, a, hp, cut);
+  hipLaunchKernelGGL((scan_kernel<Tin, D, NB>), dim3(scan_groups), dim3(kThreads), 0, s, a, hp, chunk_min);
   e = hipGetLastError();
   if (e != hipSuccess) return e;
-  // The last range has no end inside a tile.
-  const int row_groups = 4 * cu, tile_groups = chunks ? 16 * (cut.chunk_groups - 1) : 0;
-  hipLaunchKernelGGL((join_kernel<Tin, D>), dim3(row_groups + tile_groups), dim3(kThreads), 0, s, a, hp, cut, row_groups);
+  hipLaunchKernelGGL((join_kernel<Tin, D>), dim3(scan_groups * NB + 16 * chunk_groups), dim3(kThreads), 0, s, a, hp,
+                     scan_groups, 16 * NB);
   return hipGetLastError();
 }
 

@@ -174,27 +174,27 @@ struct PagedArgs {
   int N, S, H, H_kv, d_h, n_pages, page_shift, max_pages, max_new;
 };
 
-// Workspace of relation_paged_fwd (paged_device.h): the work plan of batches of
-// more than kPlanInline requests, the partial states of split histories, at
-// most kPartialRows rows (m, l) and z[d_h], and those of the long-chunk kernel
-// (bf16, requests with at least kChunkMin new tokens), 256 rows each, two per
-// work-group.
+// Workspace of relation_paged_fwd (paged_device.h): the work sums of batches of
+// more than kPlanInline requests (two 64-bit ones), a 32-byte record per
+// work-group and the partial states (m, l) and z[d_h] of the scan kernel's row
+// blocks, and the same of the long-chunk kernel's query tiles of 256 rows (bf16,
+// requests with at least kChunkMin new tokens). A work-group leaves at most two
+// partial states.
 constexpr int kPlanInline = 256;
-constexpr int64_t kPlanHeader = 256;
-constexpr int64_t kPartialRows = 32768;
+constexpr int kScanGroups = 1024;         // at most, with 16 rows each; 512 with 32
+constexpr int kScanStateRows = 2 * kScanGroups * 16;
 constexpr int kChunkMin = 128;
 constexpr int kChunkGroups = 256;
-constexpr int kChunkStates = 2 * kChunkGroups;
-constexpr int64_t kCutBytes = 32 * kChunkGroups;
-// Three 32-bit and one 64-bit prefix sum over the requests.
-inline __host__ __device__ int64_t paged_sum_bytes(int64_t S, int size) { return ((S + 1) * size + 255) / 256 * 256; }
-inline __host__ __device__ int64_t paged_plan_bytes(int64_t S) {
-  return kPlanHeader + 3 * paged_sum_bytes(S, 4) + paged_sum_bytes(S, 8);
+constexpr int kChunkStateRows = 2 * kChunkGroups * 256;
+constexpr int64_t kCutBytes = 32;
+inline __host__ __device__ int64_t paged_sum_bytes(int64_t S) { return ((S + 1) * 8 + 255) / 256 * 256; }
+inline __host__ __device__ int64_t paged_scan_offset(int64_t S) { return 2 * paged_sum_bytes(S); }
+inline __host__ __device__ int64_t paged_chunk_offset(int64_t S, int d_h) {
+  return paged_scan_offset(S) + kScanGroups * kCutBytes + (int64_t)kScanStateRows * (d_h + 2) * 4;
 }
-inline __host__ __device__ int64_t paged_scan_bytes(int d_h) { return kPartialRows * (d_h + 2) * 4; }
 inline size_t paged_ws_bytes(int64_t N, int64_t S, int d_h) {
-  return static_cast<size_t>(paged_plan_bytes(S) + paged_scan_bytes(d_h) +
-                             (N >= kChunkMin ? kCutBytes + (int64_t)kChunkStates * 256 * (d_h + 2) * 4 : 0));
+  const int64_t chunk = kChunkGroups * kCutBytes + (int64_t)kChunkStateRows * (d_h + 2) * 4;
+  return static_cast<size_t>(paged_chunk_offset(S, d_h) + (N >= kChunkMin ? chunk : 0));
 }
 
 // Launchers (return the hipError_t of the launch).
