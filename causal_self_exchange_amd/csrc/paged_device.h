@@ -95,6 +95,7 @@ constexpr int kMinRange = 4;              // units of the shortest range: shorte
 struct Plan {
   long long* unit_sum;    // exclusive sums over the requests; [S] the total
   long long* tile_sum;
+  Req* part;              // the requests' parts that the sums count (null: not kept)
 };
 
 // The scan's part of a request.
@@ -119,9 +120,11 @@ __device__ __forceinline__ void make_plan(const PagedArgs& a, int row_block, int
     const int b = b0 + tid;
     const bool in = tid < 256 && b < a.S;
     long long own[2] = {0, 0};
+    Req part;
     if (in) {
       const Req r(a, b);
       const Req s = scan_part(r, chunk_min), c = chunk_part(r, chunk_min);
+      part = p.unit_sum ? s : c;
       if (p.unit_sum && s.q > 0) {
         const ScanRows n(a, s, row_block);
         own[0] = (long long)n.blocks * a.H_kv * n.units;
@@ -157,6 +160,7 @@ __device__ __forceinline__ void make_plan(const PagedArgs& a, int row_block, int
     }
     if (in && p.unit_sum) p.unit_sum[b] = x[0];
     if (in && p.tile_sum) p.tile_sum[b] = x[1];
+    if (in && p.part) p.part[b] = part;
     __syncthreads();
   }
   if (tid == 0) {
@@ -168,7 +172,7 @@ __device__ __forceinline__ void make_plan(const PagedArgs& a, int row_block, int
 // The sums that plan_kernel left in the workspace (more than kPlanInline requests).
 __device__ __forceinline__ Plan ws_plan(const PagedArgs& a) {
   char* w = static_cast<char*>(a.ws);
-  return Plan{reinterpret_cast<long long*>(w), reinterpret_cast<long long*>(w + paged_sum_bytes(a.S))};
+  return Plan{reinterpret_cast<long long*>(w), reinterpret_cast<long long*>(w + paged_sum_bytes(a.S)), nullptr};
 }
 
 // A kernel's sums: formed in LDS by each work-group for up to kPlanInline
@@ -177,10 +181,11 @@ __device__ __forceinline__ Plan ws_plan(const PagedArgs& a) {
 struct PlanLds {
   PlanScratch sc;
   long long sum[kPlanInline + 1];
+  Req part[kPlanInline];
 };
 __device__ __forceinline__ Plan load_plan(const PagedArgs& a, int row_block, int chunk_min, PlanLds& lds) {
   if (a.S > kPlanInline) return ws_plan(a);
-  const Plan p = row_block > 0 ? Plan{lds.sum, nullptr} : Plan{nullptr, lds.sum};
+  const Plan p = row_block > 0 ? Plan{lds.sum, nullptr, lds.part} : Plan{nullptr, lds.sum, lds.part};
   make_plan(a, row_block, chunk_min, lds.sc, p);
   __syncthreads();
   return p;
@@ -199,6 +204,11 @@ __device__ __forceinline__ int find_request(const long long* off, int S, long lo
     n = min(stride, n - (cnt - 1) * stride);
   }
   return uni(lo);
+}
+
+// v / n; the 64-bit division takes longer than the rest of a segment's numbers.
+__device__ __forceinline__ int divide(long long v, long long n) {
+  return (v | n) >> 32 == 0 ? (int)((unsigned)v / (unsigned)n) : (int)(v / n);
 }
 
 // The row block or tile that the end of a work-group's range divides, for the
@@ -270,10 +280,10 @@ struct ScanSource {
     ScanSegment s{};
     if (rg.u >= rg.end) return s;
     s.b = find_request(p.unit_sum, a.S, rg.u);
-    const Req r = scan_part(Req(a, s.b), chunk_min);
+    const Req r = p.part ? p.part[s.b] : scan_part(Req(a, s.b), chunk_min);
     const ScanRows n(a, r, row_block);
     const long long v = rg.u - p.unit_sum[s.b];
-    const int block = (int)((unsigned long long)v / (unsigned)n.units);   // cached head, row block
+    const int block = divide(v, n.units);                // cached head, row block
     const int at = (int)(v - (long long)block * n.units);
     const long long start = rg.u - at;
     const long long stop = start + n.units < rg.end ? start + n.units : rg.end;
@@ -320,11 +330,11 @@ struct ChunkSource {
     Segment s{};
     if (rg.u >= rg.end) return s;
     s.b = find_request(p.tile_sum, a.S, rg.u);
-    const Req r = chunk_part(Req(a, s.b), kChunkMin);
+    const Req r = p.part ? p.part[s.b] : chunk_part(Req(a, s.b), kChunkMin);
     const ChunkTiles t(r.total - r.q, r.total);
     const long long per_head = t.before(t.n);
     const long long v = rg.u - p.tile_sum[s.b];
-    s.h = (int)(v / per_head);
+    s.h = divide(v, per_head);
     const long long w = v - s.h * per_head;
     int lo = 0, hi = t.n - 1;                            // the last tile that starts at or before w
     while (lo < hi) {

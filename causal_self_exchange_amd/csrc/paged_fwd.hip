@@ -52,7 +52,7 @@ __global__ __launch_bounds__(kThreads) void plan_kernel(PagedArgs a, int row_blo
 // against 12). The 16-byte chunks of a row are stored in an order that depends
 // on the row, so that the operand reads spread over the banks. A wave holds its
 // step's operands in registers, and the slot is refilled while it computes.
-template <typename Tin, int D>
+template <typename Tin, int D, int NB>
 struct Geom {
   static constexpr bool kBf = sizeof(Tin) == 2;
   static constexpr int kEs = (int)sizeof(Tin);
@@ -62,11 +62,16 @@ struct Geom {
   static constexpr int kDma = (kCh + 3) / 4;                 // 1 KB loads per 16 rows
   static constexpr int kHalf = kDma * 1024;
   static constexpr int kSlot = 2 * kHalves * kHalf;          // P2, then V
+  static constexpr int kStepLoads = 2 * kHalves * kDma;      // direct loads of a step
   static constexpr int kKs = (kCh + 3) / 4;                  // A operands of 16 bytes per row block
   static constexpr int kDb = D / 16;                         // 16-row blocks of O^T
   static constexpr int kZStride = D + 4;
   static constexpr int kZBytes = kWaves * 16 * kZStride * 4;
-  static constexpr int kLds = kWaves * kSlot > kZBytes ? kWaves * kSlot : kZBytes;
+  // Work-groups per compute unit (as many as the registers and the LDS admit) and
+  // slots per wave: together about 128 KB of loads in flight on a compute unit.
+  static constexpr int kPerCu = NB == 1 ? (D <= 64 ? 4 : (D == 80 ? 3 : 2)) : 2;
+  static constexpr int kSlots = NB == 2 && kSlot <= 8192 ? 2 : 1;
+  static constexpr int kLds = kWaves * kSlots * kSlot > kZBytes ? kWaves * kSlots * kSlot : kZBytes;
   // Chunk c of row q lies at position c ^ swz(q). Rows of 160 and 96 bytes spread
   // over the banks by themselves; wider fp32 rows of 320 and 192 bytes leave
   // four-way conflicts in the V reads.
@@ -76,14 +81,9 @@ struct Geom {
   }
 };
 
-// Work-groups per compute unit: as many as the LDS slots and the registers of
-// the row blocks admit.
 template <typename Tin, int D, int NB>
-constexpr int kPerCu = D <= 64 && NB == 1 ? 4 : 2;
-
-template <typename Tin, int D, int NB>
-__global__ __launch_bounds__(kThreads, (kPerCu<Tin, D, NB>)) void scan_kernel(PagedArgs a, HeadParams hp, int chunk_min) {
-  using C = Geom<Tin, D>;
+__global__ __launch_bounds__(kThreads, (Geom<Tin, D, NB>::kPerCu)) void scan_kernel(PagedArgs a, HeadParams hp, int chunk_min) {
+  using C = Geom<Tin, D, NB>;
   constexpr bool kBf = C::kBf;
   constexpr int kRb = 16 * NB;
   constexpr int kEs = C::kEs;
@@ -101,7 +101,7 @@ __global__ __launch_bounds__(kThreads, (kPerCu<Tin, D, NB>)) void scan_kernel(Pa
   const int li = lane & 15, lj = lane >> 4;
   const float k2 = hp.scale * kLog2e;
   const int pmask = (1 << a.page_shift) - 1;
-  char* const slot = smem + wave * C::kSlot;
+  char* const ring = smem + wave * C::kSlots * C::kSlot;
 
   // Source of this lane's 16 bytes in load u of a 16-row block: LDS position
   // 64 u + lane is row / chunk position of the block.
@@ -166,6 +166,7 @@ __global__ __launch_bounds__(kThreads, (kPerCu<Tin, D, NB>)) void scan_kernel(Pa
     // Direct loads of step n into the slot. Rows at and past the request's end
     // and rows of a page outside the cache are zeros.
     auto fetch = [&](int n) __attribute__((always_inline)) {
+      char* const slot = ring + (n % C::kSlots) * C::kSlot;
       if (n % kWin == 0) load_pages(n);
 #pragma unroll
       for (int hb = 0; hb < C::kHalves; ++hb) {
@@ -188,7 +189,8 @@ __global__ __launch_bounds__(kThreads, (kPerCu<Tin, D, NB>)) void scan_kernel(Pa
     u32x4 kf[C::kHalves][C::kKs];                   // P2 rows as A operands
     bf16x8 vb[kBf ? C::kDb : 1];                    // V^T as A operands
     float vs[kBf ? 1 : 4][C::kDb];
-    auto read_operands = [&]() __attribute__((always_inline)) {
+    auto read_operands = [&](int n) __attribute__((always_inline)) {
+      const char* const slot = ring + (n % C::kSlots) * C::kSlot;
 #pragma unroll
       for (int hb = 0; hb < C::kHalves; ++hb)
 #pragma unroll
@@ -309,19 +311,22 @@ __global__ __launch_bounds__(kThreads, (kPerCu<Tin, D, NB>)) void scan_kernel(Pa
     };
 
     if (nsteps > 0) fetch(0);
+    if (C::kSlots == 2 && nsteps > 1) fetch(1);
     for (int n = 0; n < nsteps; ++n) {
-      // The step's loads have landed; then its operands are in registers and the
-      // slot is free.
+      // The step's loads have landed (vector memory operations complete in order:
+      // all but the next step's, where two are in flight); then its operands are in
+      // registers and the slot is free.
       asm volatile("" ::: "memory");
-      wait_vm_lgkm<0, 15>();
+      if (C::kSlots == 2 && n + 1 < nsteps) wait_vm_lgkm<C::kStepLoads, 15>();
+      else wait_vm_lgkm<0, 15>();
       asm volatile("" ::: "memory");
       __builtin_amdgcn_sched_barrier(0);
-      read_operands();
+      read_operands(n);
       asm volatile("" ::: "memory");
       wait_vm_lgkm<63, 0>();
       asm volatile("" ::: "memory");
       __builtin_amdgcn_sched_barrier(0);
-      if (n + 1 < nsteps) fetch(n + 1);
+      if (n + C::kSlots < nsteps) fetch(n + C::kSlots);
       __builtin_amdgcn_sched_barrier(0);
       compute(n);
     }
@@ -446,7 +451,7 @@ hipError_t launch_rows(const PagedArgs& a, const HeadParams& hp, hipStream_t s) 
   const bool chunks = sizeof(Tin) == 2 && a.max_new >= kChunkMin && a.N >= kChunkMin && a.ld1 < (1 << 22);
   const int chunk_min = chunks ? kChunkMin : 0;
   const int chunk_groups = chunks ? (cu < kChunkGroups ? cu : kChunkGroups) : 0;
-  int scan_groups = cu * kPerCu<Tin, D, NB>;
+  int scan_groups = cu * Geom<Tin, D, NB>::kPerCu;
   scan_groups = scan_groups * NB < kScanGroups ? scan_groups : kScanGroups / NB;
   if (a.S > kPlanInline) {
     hipLaunchKernelGGL(plan_kernel, dim3(1), dim3(kThreads), 0, s, a, 16 * NB, chunk_min);
