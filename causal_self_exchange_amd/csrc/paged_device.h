@@ -85,12 +85,19 @@ __device__ __forceinline__ Req scan_part(Req r, int chunk_min) {
 // or one 64-key tile of one query tile (long chunks: 256 positions of a request
 // and head). The units of all row blocks or tiles form one line, request by
 // request and head by head, which is cut into equal ranges, one per work-group:
-// one request or many, ragged or not, every work-group reads the same number of
-// keys. A row block or tile that a cut divides leaves a partial state in each
-// range it lies in, at most two per range, and the join kernel finishes it.
+// one request or many, ragged or not, every work-group has the same work. A row
+// block or tile counts kExtra units more than its keys: that is what a segment
+// costs beside them (set-up, the waves' states meeting, the output: 3 to 5 us;
+// without it the work-group with the most short histories came last, 64 us
+// against a median of 43 on drafted tokens of 48 requests). A cut less than kSnap
+// units from either end of the keys moves there. A row block or tile that a cut
+// divides leaves a partial state in each range it lies in, at most two per range,
+// and the join kernel finishes it.
 
 constexpr int kScanUnit = 128;
-constexpr int kMinRange = 4;              // units of the shortest range: shorter ones cost more in joins than they save
+constexpr int kExtra = 2;
+constexpr int kSnap = 2;
+constexpr int kMinRange = 4;              // units of the shortest range
 
 struct Plan {
   long long* unit_sum;    // exclusive sums over the requests; [S] the total
@@ -127,11 +134,11 @@ __device__ __forceinline__ void make_plan(const PagedArgs& a, int row_block, int
       part = p.unit_sum ? s : c;
       if (p.unit_sum && s.q > 0) {
         const ScanRows n(a, s, row_block);
-        own[0] = (long long)n.blocks * a.H_kv * n.units;
+        own[0] = (long long)n.blocks * a.H_kv * (n.units + kExtra);
       }
       if (p.tile_sum && c.q > 0) {
         const ChunkTiles t(c.total - c.q, c.total);
-        own[1] = t.before(t.n) * a.H;
+        own[1] = (t.before(t.n) + (long long)t.n * kExtra) * a.H;
       }
     }
     long long x[2] = {own[0], own[1]};
@@ -241,28 +248,47 @@ struct States {
 // XCD takes a contiguous eighth of the line: neighbouring row blocks, tiles and
 // heads, which read the same keys, share its L2.
 struct Range {
-  long long u, end, per;
+  long long u, end, per, units;
   int me;
-  __device__ __forceinline__ Range(long long units, int least, int group, int groups) {
+  __device__ __forceinline__ Range(long long all, int least, int group, int groups) : units(all) {
     me = groups % 8 == 0 ? (group & 7) * (groups >> 3) + (group >> 3) : group;
     per = (units + groups - 1) / groups;
     per = uni(per < least ? least : per);
-    u = me * per;
+    u = uni(me * per);
     end = uni(u + per < units ? u + per : units);
   }
-  // The partial state of the segment [u, stop) of the units [start, start + n):
-  // -1 when it holds all of them.
-  __device__ __forceinline__ int slot(long long start, int n, long long stop) const {
-    return u == start && stop == start + n ? -1 : (u > start ? 2 * me : 2 * me + 1);
+  // The first cut moves to its place: u is in the item [start, start + kExtra + n).
+  __device__ __forceinline__ void settle(long long start, int n) {
+    const long long k = u - start - kExtra;
+    if (k < kSnap) u = uni(start);
+    else if (n - k < kSnap) u = uni(start + kExtra + n);
   }
-  __device__ __forceinline__ int pieces(long long start, int n) const {
-    return 1 + (int)((start + n - end + per - 1) / per);
+  // The part of an item of n units at `start` that begins at u: units [k0, k1) of
+  // its keys, in the partial state `slot` (-1: all of them). false: the item
+  // belongs to the next range.
+  __device__ __forceinline__ bool take(long long start, int n, int& k0, int& k1, int& slot, int& pieces) {
+    const long long stop = start + kExtra + n;
+    const bool inside = u > start;
+    k0 = inside ? (int)(u - start - kExtra) : 0;
+    k1 = n;
+    pieces = 0;
+    u = uni(stop);
+    if (end < stop) {
+      const long long k = end - start - kExtra;
+      if (k < kSnap) return false;
+      if (n - k >= kSnap) {
+        k1 = (int)k;
+        pieces = 2 + (int)((stop - kSnap - end) / per);     // the cuts from here on that stay in it, and one
+      }
+    }
+    slot = inside ? 2 * me : (pieces ? 2 * me + 1 : -1);
+    return true;
   }
 };
 
-// A range's part of one row block: keys [k0, k1) (units = 0 for none).
+// A range's part of one row block: keys [k0, k1) (any = 0 for none).
 struct ScanSegment {
-  int b, kvh, first, ctx, total, row0, rows, k0, k1, units, slot;
+  int b, kvh, first, ctx, total, row0, rows, k0, k1, slot, any;
 };
 
 struct ScanSource {
@@ -271,37 +297,54 @@ struct ScanSource {
   Range rg;
   int row_block, chunk_min;
   CutRecord* cuts;
+  struct Block {
+    int b, kvh, row0, rows, units;
+    long long start;
+    Req r;
+  };
   __device__ __forceinline__ ScanSource(const PagedArgs& args, const Plan& plan, int rows, int least_new)
       : a(args), p(plan), rg(plan.unit_sum[args.S], kMinRange, blockIdx.x, gridDim.x), row_block(rows),
         chunk_min(least_new), cuts(States::scan(args).cuts) {
     if (threadIdx.x == 0) cuts[rg.me].pieces = 0;
+    if (rg.u < rg.end) {
+      const Block k = block_of(rg.u);
+      rg.settle(k.start, k.units);
+    }
+  }
+  __device__ __forceinline__ Block block_of(long long u) const {
+    Block k;
+    k.b = find_request(p.unit_sum, a.S, u);
+    k.r = p.part ? p.part[k.b] : scan_part(Req(a, k.b), chunk_min);
+    const ScanRows n(a, k.r, row_block);
+    k.units = n.units;
+    const long long v = u - p.unit_sum[k.b];
+    const int block = divide(v, n.units + kExtra);       // cached head, row block
+    k.start = p.unit_sum[k.b] + (long long)block * (n.units + kExtra);
+    k.kvh = block / n.blocks;
+    k.row0 = (block - k.kvh * n.blocks) * row_block;
+    k.rows = min(row_block, n.rows - k.row0);
+    return k;
   }
   __device__ __forceinline__ ScanSegment next() {
     ScanSegment s{};
     if (rg.u >= rg.end) return s;
-    s.b = find_request(p.unit_sum, a.S, rg.u);
-    const Req r = p.part ? p.part[s.b] : scan_part(Req(a, s.b), chunk_min);
-    const ScanRows n(a, r, row_block);
-    const long long v = rg.u - p.unit_sum[s.b];
-    const int block = divide(v, n.units);                // cached head, row block
-    const int at = (int)(v - (long long)block * n.units);
-    const long long start = rg.u - at;
-    const long long stop = start + n.units < rg.end ? start + n.units : rg.end;
-    s.kvh = block / n.blocks;
-    s.row0 = (block - s.kvh * n.blocks) * row_block;
-    s.rows = min(row_block, n.rows - s.row0);
-    s.first = r.first;
-    s.ctx = r.total - r.q;
-    s.total = r.total;
-    s.units = (int)(stop - rg.u);
+    const Block k = block_of(rg.u);
+    int u0, u1, pieces;
+    if (!rg.take(k.start, k.units, u0, u1, s.slot, pieces)) return s;
+    s.any = 1;
+    s.b = k.b;
+    s.kvh = k.kvh;
+    s.row0 = k.row0;
+    s.rows = k.rows;
+    s.first = k.r.first;
+    s.ctx = k.r.total - k.r.q;
+    s.total = k.r.total;
     // Keys below the block's last row's position.
     const int last = s.ctx + (s.row0 + s.rows - 1) / (a.H / a.H_kv);
-    s.k0 = at * kScanUnit;
-    s.k1 = (int)min((long long)last, ((long long)at + s.units) * kScanUnit);
-    s.slot = rg.slot(start, n.units, stop);
+    s.k0 = u0 * kScanUnit;
+    s.k1 = (int)min((long long)last, (long long)u1 * kScanUnit);
     if (s.slot == 2 * rg.me + 1 && threadIdx.x == 0)
-      cuts[rg.me] = CutRecord{rg.pieces(start, n.units), s.b, s.kvh, s.first, s.ctx, s.total, s.row0, s.rows};
-    rg.u = uni(stop);
+      cuts[rg.me] = CutRecord{pieces, s.b, s.kvh, s.first, s.ctx, s.total, s.row0, s.rows};
     return s;
   }
 };
@@ -322,40 +365,57 @@ struct ChunkSource {
   const Plan& p;
   Range rg;
   CutRecord* cuts;
+  struct Tile {
+    int b, h, tile, keys;
+    long long start;
+    Req r;
+  };
   __device__ __forceinline__ ChunkSource(const PagedArgs& args, const Plan& plan)
       : a(args), p(plan), rg(plan.tile_sum[args.S], 2 * kMinRange, blockIdx.x, gridDim.x), cuts(States::chunk(args).cuts) {
     if (threadIdx.x == 0) cuts[rg.me].pieces = 0;
+    if (rg.u < rg.end) {
+      const Tile t = tile_of(rg.u);
+      rg.settle(t.start, t.keys);
+    }
+  }
+  __device__ __forceinline__ Tile tile_of(long long u) const {
+    Tile k;
+    k.b = find_request(p.tile_sum, a.S, u);
+    k.r = p.part ? p.part[k.b] : chunk_part(Req(a, k.b), kChunkMin);
+    const ChunkTiles t(k.r.total - k.r.q, k.r.total);
+    auto at = [&](int i) { return t.before(i) + (long long)i * kExtra; };
+    const long long per_head = at(t.n);
+    const long long v = u - p.tile_sum[k.b];
+    k.h = divide(v, per_head);
+    const long long w = v - k.h * per_head;
+    int lo = 0, hi = t.n - 1;                            // the last tile that starts at or before w
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (at(mid) <= w) lo = mid;
+      else hi = mid - 1;
+    }
+    k.tile = lo;
+    k.keys = t.keys(lo);
+    k.start = u - (w - at(lo));
+    return k;
   }
   __device__ __forceinline__ Segment next() {
     Segment s{};
     if (rg.u >= rg.end) return s;
-    s.b = find_request(p.tile_sum, a.S, rg.u);
-    const Req r = p.part ? p.part[s.b] : chunk_part(Req(a, s.b), kChunkMin);
-    const ChunkTiles t(r.total - r.q, r.total);
-    const long long per_head = t.before(t.n);
-    const long long v = rg.u - p.tile_sum[s.b];
-    s.h = divide(v, per_head);
-    const long long w = v - s.h * per_head;
-    int lo = 0, hi = t.n - 1;                            // the last tile that starts at or before w
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (t.before(mid) <= w) lo = mid;
-      else hi = mid - 1;
-    }
-    const int keys = t.keys(lo);
-    s.tb = (int)(w - t.before(lo));
-    const long long start = rg.u - s.tb;
-    const long long stop = start + keys < rg.end ? start + keys : rg.end;
-    s.kvh = s.h / (a.H / a.H_kv);
-    s.first = r.first;
-    s.total = r.total;
-    s.ctx = r.total - r.q;
-    s.q0 = (s.ctx & ~63) + 256 * lo;
-    s.te = (int)(stop - start);
-    s.slot = rg.slot(start, keys, stop);
+    const Tile t = tile_of(rg.u);
+    int u0, u1, pieces;
+    if (!rg.take(t.start, t.keys, u0, u1, s.slot, pieces)) return s;
+    s.b = t.b;
+    s.h = t.h;
+    s.kvh = t.h / (a.H / a.H_kv);
+    s.first = t.r.first;
+    s.total = t.r.total;
+    s.ctx = t.r.total - t.r.q;
+    s.q0 = (s.ctx & ~63) + 256 * t.tile;
+    s.tb = u0;
+    s.te = u1;
     if (s.slot == 2 * rg.me + 1 && threadIdx.x == 0)
-      cuts[rg.me] = CutRecord{rg.pieces(start, keys), s.b, s.h, s.first, s.ctx, s.total, s.q0, 256};
-    rg.u = uni(stop);
+      cuts[rg.me] = CutRecord{pieces, s.b, s.h, s.first, s.ctx, s.total, s.q0, 256};
     return s;
   }
 };

@@ -26,6 +26,15 @@ constexpr int kWaves = 4;
 constexpr int kThreads = 64 * kWaves;
 constexpr float kLazy = 32.0f;            // log2 slack before the stabiliser moves
 
+// A work-group barrier for LDS data alone: outstanding vector memory operations
+// (the next segment's loads) are not waited for.
+__device__ __forceinline__ void lds_barrier() {
+  asm volatile("" ::: "memory");
+  wait_vm_lgkm<63, 0>();
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
 __global__ __launch_bounds__(kThreads) void plan_kernel(PagedArgs a, int row_block, int chunk_min) {
   __shared__ PlanScratch sc;
   Plan p = ws_plan(a);
@@ -66,12 +75,12 @@ struct Geom {
   static constexpr int kKs = (kCh + 3) / 4;                  // A operands of 16 bytes per row block
   static constexpr int kDb = D / 16;                         // 16-row blocks of O^T
   static constexpr int kZStride = D + 4;
-  static constexpr int kZBytes = kWaves * 16 * kZStride * 4;
+  static constexpr int kZBytes = 16 * kZStride * 4;          // 16 rows where the waves' states meet
   // Work-groups per compute unit (as many as the registers and the LDS admit) and
   // slots per wave: together about 128 KB of loads in flight on a compute unit.
-  static constexpr int kPerCu = NB == 1 ? (D <= 64 ? 4 : (D == 80 ? 3 : 2)) : 2;
+  static constexpr int kPerCu = NB == 1 && D <= 64 ? 4 : 2;
   static constexpr int kSlots = NB == 2 && kSlot <= 8192 ? 2 : 1;
-  static constexpr int kLds = kWaves * kSlots * kSlot > kZBytes ? kWaves * kSlots * kSlot : kZBytes;
+  static constexpr int kRing = kWaves * kSlots * kSlot;
   // Chunk c of row q lies at position c ^ swz(q). Rows of 160 and 96 bytes spread
   // over the banks by themselves; wider fp32 rows of 320 and 192 bytes leave
   // four-way conflicts in the V reads.
@@ -88,7 +97,7 @@ __global__ __launch_bounds__(kThreads, (Geom<Tin, D, NB>::kPerCu)) void scan_ker
   constexpr int kRb = 16 * NB;
   constexpr int kEs = C::kEs;
   constexpr int kStep = C::kStep;
-  __shared__ __attribute__((aligned(16))) char smem[C::kLds];
+  __shared__ __attribute__((aligned(16))) char smem[C::kRing + C::kZBytes];
   __shared__ float s_m[kWaves][16], s_l[kWaves][16];
   __shared__ PlanLds lds;
 
@@ -112,12 +121,65 @@ __global__ __launch_bounds__(kThreads, (Geom<Tin, D, NB>::kPerCu)) void scan_ker
     src[u] = q < 16 ? q * D * kEs + 16 * (c ^ C::swz(q)) : kOutOfRange;
   }
 
+  // A segment's numbers, in scalar registers. This wave's steps are first + 4 n.
+  struct Run {
+    int b, kvh, first_tok, ctx, total, row0, rows, slot, first, nsteps;
+    bool any;
+  };
   ScanSource source(a, plan, kRb, chunk_min);
-  while (true) {
+  auto next_run = [&]() __attribute__((always_inline)) -> Run {
     const ScanSegment sg = source.next();
-    if (uni(sg.units) == 0) break;
-    const int b = uni(sg.b), kvh = uni(sg.kvh), total = uni(sg.total), ctx = uni(sg.ctx), row0 = uni(sg.row0);
-    const int rows = uni(sg.rows), k0 = uni(sg.k0), k1 = uni(sg.k1), first_tok = uni(sg.first), seg_slot = uni(sg.slot);
+    const int k0 = uni(sg.k0), k1 = uni(sg.k1);
+    const int mine = k1 - k0 - kStep * wave;        // keys from this wave's first step on
+    return Run{uni(sg.b), uni(sg.kvh), uni(sg.first), uni(sg.ctx), uni(sg.total), uni(sg.row0), uni(sg.rows), uni(sg.slot),
+               k0 / kStep + wave, mine > 0 ? (mine + kWaves * kStep - 1) / (kWaves * kStep) : 0, uni(sg.any) != 0};
+  };
+  // Lane x holds the table entry of 16-key block x of this wave's steps, for 64
+  // blocks from step n0 on (checked when it is used).
+  constexpr int kWin = 64 / C::kHalves;             // steps per window
+  auto load_pages = [&](const Run& r, int n0) __attribute__((always_inline)) -> int {
+    const int n = n0 + lane / C::kHalves;
+    const int key = (r.first + kWaves * n) * kStep + 16 * (lane % C::kHalves);
+    int pg = -1;
+    if (n < r.nsteps && key < r.total) pg = a.table[(size_t)r.b * a.max_pages + (key >> a.page_shift)];
+    return pg;
+  };
+  // Direct loads of step n of a run into a slot. Rows at and past the request's
+  // end and rows of a page outside the cache are zeros.
+  auto fetch = [&](const Run& r, int pages, int n, int g) __attribute__((always_inline)) {
+    char* const slot = ring + (g % C::kSlots) * C::kSlot;
+#pragma unroll
+    for (int hb = 0; hb < C::kHalves; ++hb) {
+      const int key = (r.first + kWaves * n) * kStep + 16 * hb;
+      const int pg = __builtin_amdgcn_readlane(pages, C::kHalves * (n % kWin) + hb);
+      const bool in = pg >= 0 && pg < a.n_pages;
+      const int left = min(16, r.total - key);
+      const int bytes = in && left > 0 ? left * D * kEs : 0;
+      const size_t row = (((size_t)(in ? pg : 0) * a.H_kv + r.kvh) << a.page_shift) + (key & pmask);
+#pragma unroll
+      for (int w = 0; w < 2; ++w) {
+        u32x4 rw = rsrc_words(static_cast<const char*>(w ? a.cV : a.cP2) + row * D * kEs, bytes);
+#pragma unroll
+        for (int x = 0; x < 3; ++x) rw[x] = (unsigned)uni((int)rw[x]);
+#pragma unroll
+        for (int u = 0; u < C::kDma; ++u) dma16(rw, slot + (w * C::kHalves + hb) * C::kHalf + 1024 * u, src[u]);
+      }
+    }
+  };
+
+  // The segments of the range. The next one's numbers are formed while the first
+  // loads of the current one are in flight, and its own first loads are issued
+  // before the current one's states meet: base counts this wave's steps of the
+  // segments before, got the steps whose loads are issued.
+  Run cur = next_run();
+  if (!cur.any) return;
+  int pages = load_pages(cur, 0);
+  int base = 0, got = 0;
+  for (; got < C::kSlots && got < cur.nsteps; ++got) fetch(cur, pages, got, got);
+  while (true) {
+    const Run nxt = next_run();
+    int npages = load_pages(nxt, 0);
+    const int b = cur.b, kvh = cur.kvh, ctx = cur.ctx, row0 = cur.row0, rows = cur.rows;
     const int pos_lo = ctx + row0 / G;
 
     // The query rows as B operands, and their positions (0 for rows past the end:
@@ -131,7 +193,7 @@ __global__ __launch_bounds__(kThreads, (Geom<Tin, D, NB>::kPerCu)) void scan_ker
       const int tq = ok ? row / G : 0;
       const int h = kvh * G + (ok ? row - tq * G : 0);
       pos[nb] = ok ? ctx + tq : 0;
-      const char* p = static_cast<const char*>(a.P1) + ((size_t)(first_tok + tq) * a.ld1 + (size_t)h * D) * kEs;
+      const char* p = static_cast<const char*>(a.P1) + ((size_t)(cur.first_tok + tq) * a.ld1 + (size_t)h * D) * kEs;
 #pragma unroll
       for (int ks = 0; ks < C::kKs; ++ks) {
         const int c = 4 * ks + lj;
@@ -148,49 +210,11 @@ __global__ __launch_bounds__(kThreads, (Geom<Tin, D, NB>::kPerCu)) void scan_ker
       for (int db = 0; db < C::kDb; ++db) acc[nb][db] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     }
 
-    // This wave's steps: first + 4 n. Lane x holds the page of 16-key block x of
-    // its steps, for 64 blocks at a time.
-    constexpr int kWin = 64 / C::kHalves;           // steps per window
-    const int first = k0 / kStep + wave;
-    const int nsteps = k1 > k0 + kStep * wave ? ((k1 - k0 + kStep - 1) / kStep - wave + kWaves - 1) / kWaves : 0;
-    int pages = -1;
-    auto load_pages = [&](int n0) {
-      const int n = n0 + lane / C::kHalves;
-      const int key = (first + kWaves * n) * kStep + 16 * (lane % C::kHalves);
-      pages = -1;
-      if (n < nsteps && key < total) {
-        const int pg = a.table[(size_t)b * a.max_pages + (key >> a.page_shift)];
-        pages = pg >= 0 && pg < a.n_pages ? pg : -1;
-      }
-    };
-    // Direct loads of step n into the slot. Rows at and past the request's end
-    // and rows of a page outside the cache are zeros.
-    auto fetch = [&](int n) __attribute__((always_inline)) {
-      char* const slot = ring + (n % C::kSlots) * C::kSlot;
-      if (n % kWin == 0) load_pages(n);
-#pragma unroll
-      for (int hb = 0; hb < C::kHalves; ++hb) {
-        const int key = (first + kWaves * n) * kStep + 16 * hb;
-        const int pg = __builtin_amdgcn_readlane(pages, C::kHalves * (n % kWin) + hb);
-        const int left = min(16, total - key);
-        const int bytes = pg >= 0 && left > 0 ? left * D * kEs : 0;
-        const size_t row = (((size_t)(pg >= 0 ? pg : 0) * a.H_kv + kvh) << a.page_shift) + (key & pmask);
-#pragma unroll
-        for (int w = 0; w < 2; ++w) {
-          u32x4 rw = rsrc_words(static_cast<const char*>(w ? a.cV : a.cP2) + row * D * kEs, bytes);
-#pragma unroll
-          for (int x = 0; x < 3; ++x) rw[x] = (unsigned)uni((int)rw[x]);
-#pragma unroll
-          for (int u = 0; u < C::kDma; ++u) dma16(rw, slot + (w * C::kHalves + hb) * C::kHalf + 1024 * u, src[u]);
-        }
-      }
-    };
-
     u32x4 kf[C::kHalves][C::kKs];                   // P2 rows as A operands
     bf16x8 vb[kBf ? C::kDb : 1];                    // V^T as A operands
     float vs[kBf ? 1 : 4][C::kDb];
-    auto read_operands = [&](int n) __attribute__((always_inline)) {
-      const char* const slot = ring + (n % C::kSlots) * C::kSlot;
+    auto read_operands = [&](int g) __attribute__((always_inline)) {
+      const char* const slot = ring + (g % C::kSlots) * C::kSlot;
 #pragma unroll
       for (int hb = 0; hb < C::kHalves; ++hb)
 #pragma unroll
@@ -227,7 +251,7 @@ __global__ __launch_bounds__(kThreads, (Geom<Tin, D, NB>::kPerCu)) void scan_ker
     // out the wait states between an MFMA and the read of its result behind the
     // branch, and results were wrong.
     auto compute = [&](int n) __attribute__((always_inline)) {
-      const int key0 = (first + kWaves * n) * kStep;
+      const int key0 = (cur.first + kWaves * n) * kStep;
       const bool full = key0 + kStep <= pos_lo;
       float w[NB][C::kHalves][4];
 #pragma unroll
@@ -310,71 +334,94 @@ __global__ __launch_bounds__(kThreads, (Geom<Tin, D, NB>::kPerCu)) void scan_ker
       }
     };
 
-    if (nsteps > 0) fetch(0);
-    if (C::kSlots == 2 && nsteps > 1) fetch(1);
-    for (int n = 0; n < nsteps; ++n) {
+    for (int n = 0; n < cur.nsteps; ++n) {
       // The step's loads have landed (vector memory operations complete in order:
-      // all but the next step's, where two are in flight); then its operands are in
-      // registers and the slot is free.
+      // all but the next step's, where they are in flight already); then its
+      // operands are in registers and the slot is free.
       asm volatile("" ::: "memory");
-      if (C::kSlots == 2 && n + 1 < nsteps) wait_vm_lgkm<C::kStepLoads, 15>();
+      if (C::kSlots == 2 && got > base + n + 1) wait_vm_lgkm<C::kStepLoads, 15>();
       else wait_vm_lgkm<0, 15>();
       asm volatile("" ::: "memory");
       __builtin_amdgcn_sched_barrier(0);
-      read_operands(n);
+      read_operands(base + n);
       asm volatile("" ::: "memory");
       wait_vm_lgkm<63, 0>();
       asm volatile("" ::: "memory");
       __builtin_amdgcn_sched_barrier(0);
-      if (n + C::kSlots < nsteps) fetch(n + C::kSlots);
+      const int k = got - base;                     // the next step to load: this run's, or the next one's
+      if (k < cur.nsteps) {
+        if (k % kWin == 0) pages = load_pages(cur, k);
+        fetch(cur, pages, k, got);
+        ++got;
+      } else if (k - cur.nsteps < nxt.nsteps) {
+        fetch(nxt, npages, k - cur.nsteps, got);
+        ++got;
+      }
       __builtin_amdgcn_sched_barrier(0);
       compute(n);
     }
+    base += cur.nsteps;
+    for (; got - base < C::kSlots && got - base < nxt.nsteps; ++got) fetch(nxt, npages, got - base, got);
 
-    // The waves' states meet in LDS, 16 rows at a time; then 16 lanes per row.
+    // The waves' states meet in LDS, 16 rows at a time: each wave adds its share to
+    // a quarter of the columns per phase, so the four add side by side and every
+    // column has its own fixed order; then 16 lanes per row.
+    float* const zrow = reinterpret_cast<float*>(smem + C::kRing);
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
       if (16 * nb >= rows) continue;
       float ls = l[nb];
       ls += __shfl_xor(ls, 16);
       ls += __shfl_xor(ls, 32);
-      __syncthreads();                              // ring or the previous rows' states are no longer read
       if (lj == 0) {
         s_m[wave][li] = m2[nb];
         s_l[wave][li] = ls;
       }
-      float* z = reinterpret_cast<float*>(smem) + (wave * 16 + li) * C::kZStride;
+      lds_barrier();
+      float M = s_m[0][li];
 #pragma unroll
-      for (int db = 0; db < C::kDb; ++db) *reinterpret_cast<f32x4*>(z + 16 * db + 4 * lj) = acc[nb][db];
-      __syncthreads();
+      for (int w = 1; w < kWaves; ++w) M = fmaxf(M, s_m[w][li]);
+      const float f = __builtin_amdgcn_exp2f(m2[nb] - M);
+      f32x4 share[C::kDb];
+#pragma unroll
+      for (int db = 0; db < C::kDb; ++db)
+#pragma unroll
+        for (int rr = 0; rr < 4; ++rr) share[db][rr] = acc[nb][db][rr] * f;
+#pragma unroll
+      for (int ph = 0; ph < kWaves; ++ph) {
+#pragma unroll
+        for (int db = 0; db < C::kDb; ++db) {
+          if (((wave + ph) & 3) != (db & 3)) continue;
+          f32x4* z = reinterpret_cast<f32x4*>(zrow + li * C::kZStride + 16 * db + 4 * lj);
+          *z = ph == 0 ? share[db] : *z + share[db];
+        }
+        lds_barrier();
+      }
       const int rr = tid >> 4, sl = tid & 15;
       const int row = row0 + 16 * nb + rr;
       const bool ok = 16 * nb + rr < rows;
-      float M = s_m[0][rr], L = 0.0f, zs[8];
+      float L = 0.0f, zs[8];
+      M = s_m[0][rr];
 #pragma unroll
       for (int w = 1; w < kWaves; ++w) M = fmaxf(M, s_m[w][rr]);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) zs[e] = 0.0f;
+      for (int w = 0; w < kWaves; ++w) L = fmaf(__builtin_amdgcn_exp2f(s_m[w][rr] - M), s_l[w][rr], L);
+      {
+        const float* zw = zrow + rr * C::kZStride + 8 * (sl < D / 8 ? sl : 0);
+        const f32x4 x = reinterpret_cast<const f32x4*>(zw)[0], y = reinterpret_cast<const f32x4*>(zw)[1];
 #pragma unroll
-      for (int w = 0; w < kWaves; ++w) {
-        const float f = __builtin_amdgcn_exp2f(s_m[w][rr] - M);
-        L = fmaf(f, s_l[w][rr], L);
-        if (sl < D / 8) {
-          const float* zw = reinterpret_cast<const float*>(smem) + (w * 16 + rr) * C::kZStride + 8 * sl;
-          const f32x4 x = reinterpret_cast<const f32x4*>(zw)[0], y = reinterpret_cast<const f32x4*>(zw)[1];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            zs[e] = fmaf(f, x[e], zs[e]);
-            zs[4 + e] = fmaf(f, y[e], zs[4 + e]);
-          }
+        for (int e = 0; e < 4; ++e) {
+          zs[e] = x[e];
+          zs[4 + e] = y[e];
         }
       }
+      lds_barrier();                                // read before the next rows' states
       const int tq = ok ? row / G : 0;
       const int h = kvh * G + (ok ? row - tq * G : 0);
-      if (seg_slot < 0) {
-        finish_row<Tin, D>(a, hp, b, first_tok + tq, h, ctx + tq, sl, M, L, zs, ok);
+      if (cur.slot < 0) {
+        finish_row<Tin, D>(a, hp, b, cur.first_tok + tq, h, ctx + tq, sl, M, L, zs, ok);
       } else if (ok) {
-        const int64_t p = (int64_t)seg_slot * kRb + 16 * nb + rr;
+        const int64_t p = (int64_t)cur.slot * kRb + 16 * nb + rr;
         if (sl == 0) states.ml[p] = make_float2(M, L);
         if (sl < D / 8) {
           reinterpret_cast<f32x4*>(states.z + p * D + 8 * sl)[0] = f32x4{zs[0], zs[1], zs[2], zs[3]};
@@ -382,7 +429,9 @@ __global__ __launch_bounds__(kThreads, (Geom<Tin, D, NB>::kPerCu)) void scan_ker
         }
       }
     }
-    __syncthreads();                                // the states are read before the next segment's loads land
+    if (!nxt.any) break;
+    cur = nxt;
+    pages = npages;
   }
 }
 

@@ -180,7 +180,7 @@ struct PagedArgs {
 // blocks, and the same of the long-chunk kernel's query tiles of 256 rows (bf16,
 // requests with at least kChunkMin new tokens). A work-group leaves at most two
 // partial states.
-constexpr int kPlanInline = 192;
+constexpr int kPlanInline = 128;
 constexpr int kScanGroups = 1024;         // at most, with 16 rows each; 512 with 32
 constexpr int kScanStateRows = 2 * kScanGroups * 16;
 constexpr int kChunkMin = 128;
