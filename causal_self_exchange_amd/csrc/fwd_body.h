@@ -59,9 +59,10 @@
 // j >= i masked there) and skips the blocks right of it.
 //
 // The paged form (relation_paged_fwd's long chunks, kPaged) runs the same scan
-// on segments: a query tile is 256 positions of one request, from a multiple
-// of 64, and a segment is a range of the tile's key tiles (the cut of the work is
-// in paged_device.h). Tiles are then counted from the segment's first,
+// on segments: a query tile is 256 rows of one request (256 positions of one head,
+// from a multiple of 64, or blocks of 32 positions of several heads that share a
+// cached head), and a segment is a range of the tile's key tiles (the
+// cut of the work is in paged_device.h). Tiles are then counted from the segment's first,
 // P2 and V rows are found through the request's block table (a wave moves the
 // same 8-row group of every tile, which lies within one page), and a segment
 // that does not hold all of its query tile's keys leaves a partial state.
@@ -286,20 +287,27 @@ __device__ __forceinline__ void fwd_body(const FwdArgs& a, const HeadParams& hp,
     }
   };
 
-  // The paged form: the rows of a segment's query tile, token rows ld1 apart;
-  // rows before the request's first new token and past its last read 0.
+  // The paged form: this wave's head and first position in a segment's query tile
+  // (rows 32 wave .. of it); a head past the group's is none.
+  const int group = kPaged ? pg.H / pg.H_kv : 1;
+  auto wave_head = [&](const paged::Segment& sg) -> int { return (sg.slot0 + wave) / sg.blocks; };
+  auto wave_pos = [&](const paged::Segment& sg) -> int { return sg.q0 + 32 * ((sg.slot0 + wave) % sg.blocks); };
+  // The rows of a segment's query tile, token rows ld1 apart; rows before the
+  // request's first new token and past its last read 0.
   auto load_q_paged = [&](const paged::Segment& sg) __attribute__((always_inline)) {
     const int lane = lane_now();
     const int r0 = max(sg.q0 - sg.ctx, 0);              // the tile's first new token
-    const int pos = sg.q0 + wave * 32 + (lane & 31);
-    const __bf16* p = static_cast<const __bf16*>(pg.P1) + (size_t)(sg.first + r0) * (size_t)pg.ld1 + (size_t)sg.h * DR;
+    const bool has_head = wave_head(sg) < group;
+    const int pos = wave_pos(sg) + (lane & 31);
+    const __bf16* p = static_cast<const __bf16*>(pg.P1) + (size_t)(sg.first + r0) * (size_t)pg.ld1 +
+                      (size_t)(sg.h + (has_head ? wave_head(sg) : 0)) * DR;
     const int rows = min(sg.total - sg.ctx - r0, kBM);
     const int ldb = (int)pg.ld1 * 2;
     const auto rP1 = rsrc(p, (long long)(rows - 1) * ldb + DR * 2);
     const int qoff = (pos - sg.ctx - r0) * ldb + (lane >> 5) * 16;
 #pragma unroll
     for (int ds = 0; ds < C::kDs; ++ds) {
-      const int o = ds < DR / 16 && pos >= sg.ctx && pos < sg.total ? qoff + ds * 32 : kOutOfRange;
+      const int o = ds < DR / 16 && has_head && pos >= sg.ctx && pos < sg.total ? qoff + ds * 32 : kOutOfRange;
       qf[ds] = __builtin_bit_cast(bf16x8, __builtin_amdgcn_raw_buffer_load_b128(rP1, o, 0, 0));
     }
   };
@@ -357,7 +365,8 @@ __device__ __forceinline__ void fwd_body(const FwdArgs& a, const HeadParams& hp,
   // One query tile (256 rows) of one head, start to finish; then, when nqt >=
   // 0, the P1 rows of query tile nqt of head nbh are loaded.
   auto run_tile = [&](int qt, int bh, int nqt, int nbh, const paged::Segment& sg) __attribute__((always_inline)) {
-  const int h = kPaged ? sg.h : bh % a.H;
+  const bool has_head = !kPaged || wave_head(sg) < group;
+  const int h = kPaged ? sg.h + (has_head ? wave_head(sg) : 0) : bh % a.H;
   const size_t head = (size_t)bh * (size_t)T * DR;
   const long long head_bytes = (long long)T * DR * 2;
   const __bf16* P2 = static_cast<const __bf16*>(a.P2) + head;
@@ -377,8 +386,8 @@ __device__ __forceinline__ void fwd_body(const FwdArgs& a, const HeadParams& hp,
   int dblk = q0 + wave * 32 < T ? q0 / 32 + wave : -1;
   int open_end = 0;
   if constexpr (kPaged) {
-    const int p0 = q0 + wave * 32;
-    dblk = p0 < sg.total && p0 + 31 >= sg.ctx ? p0 / 32 - 2 * sg.tb : -1;
+    const int p0 = wave_pos(sg);
+    dblk = has_head && p0 < sg.total && p0 + 31 >= sg.ctx ? p0 / 32 - 2 * sg.tb : -1;
     if (dblk >= 2 * J) {
       dblk = 2 * J - 1;
       open_end = 32;
@@ -793,7 +802,8 @@ __device__ __forceinline__ void fwd_body(const FwdArgs& a, const HeadParams& hp,
   // four loaded): columns 32 db + 8 g4 + 4 hf .. +3, i.e. half hf of chunk
   // 4 db + g4 of row qrow % 64 in the block layout.
   const int lq = lane_now() & 31, hf = lane_now() >> 5;
-  const int qrow = q0 + wave * 32 + lq;           // may be >= T: the stores drop it
+  // May be >= T: the stores drop it.
+  const int qrow = (kPaged ? wave_pos(sg) : q0 + wave * 32) + lq;
   bf16x4 vv[C::kDb][4];
   {
     const int r = qrow & (kBN - 1);
@@ -848,10 +858,10 @@ __device__ __forceinline__ void fwd_body(const FwdArgs& a, const HeadParams& hp,
       const int rr = i * kRows + rs;
       const u32x4 v = *reinterpret_cast<const u32x4*>(ystage + rr * kYStride + 16 * ch);
       if constexpr (kPaged) {
-        const int pos = q0 + wave * 32 + rr, r0 = max(q0 - sg.ctx, 0);
-        const auto rYp = rsrc(static_cast<__bf16*>(pg.Y) + ((size_t)(sg.first + r0) * pg.H + sg.h) * DR,
+        const int pos = wave_pos(sg) + rr, r0 = max(q0 - sg.ctx, 0);
+        const auto rYp = rsrc(static_cast<__bf16*>(pg.Y) + ((size_t)(sg.first + r0) * pg.H + h) * DR,
                               (long long)kBM * pg.H * DR * 2);
-        const bool in = ch < DR / 8 && pos >= sg.ctx && pos < sg.total;
+        const bool in = ch < DR / 8 && has_head && pos >= sg.ctx && pos < sg.total;
         __builtin_amdgcn_raw_buffer_store_b128(v, rYp, in ? (pos - sg.ctx - r0) * (pg.H * DR * 2) + 16 * ch : kOutOfRange, 0, 0);
         continue;
       }

@@ -1,6 +1,7 @@
-// Long chunks of a packed batch against the paged Relation Cache: the bf16 MFMA
-// scan of fwd_body.h in its paged form, on query tiles of 256 positions of one
-// request and one head.
+// Chunks of new tokens of a packed batch against the paged Relation Cache: the
+// bf16 MFMA scan of fwd_body.h in its paged form, on query tiles of 256 rows of one
+// request: 256 positions of one head, or blocks of 32 positions of several heads
+// that share a cached head.
 //
 // The key tiles of all query tiles are cut into equal ranges (paged_device.h): one
 // prompt of 8192, ten ragged ones, or one chunk of 256 rows over 100,000 cached
@@ -17,7 +18,7 @@ using namespace paged;
 template <int D, int DR>
 __global__ __launch_bounds__(kThreads, 1) void paged_chunk_kernel(PagedArgs a, HeadParams hp) {
   __shared__ PlanLds lds;
-  const Plan plan = load_plan(a, 0, kChunkMin, lds);
+  const Plan plan = load_plan(a, 0, true, lds);
   const FwdArgs none{};
   const RopeParams no_rope{};
   fwd_body<D, DR, true, false, true>(none, hp, no_rope, a, plan);

@@ -33,45 +33,52 @@ struct Req {
   }
 };
 
-// Query tiles of a long chunk: 256 positions each from ctx rounded down to a
-// multiple of 64, so that 64-key tiles never straddle a tile's first position
-// and a tile's own keys are four key tiles. Tile k needs the key tiles up to its
-// last position: all but the last tile base64 + 4 (k + 1). A last tile with
-// fewer than kChunkMin positions would waste more of the long-chunk kernel than
-// the scan kernel is slower: its tokens (rest) go there.
+// The cut of the work (below): keys of a scan unit, units that a segment costs
+// beside its keys, the least that a cut leaves, units of the shortest range.
+constexpr int kScanUnit = 128;
+constexpr int kExtra = 2;
+constexpr int kSnap = 2;
+constexpr int kMinRange = 4;
+
+// Query tiles of a request's new tokens (chunk kernel): 256 rows, 32 for each of 8 waves.
+//   Full tiles: 256 positions of one head, from ctx rounded down to a multiple of
+//   64 (64-key tiles then never straddle a tile's first position, and its own keys
+//   are four key tiles). Full tile k needs base64 + 4 (k + 1) key tiles.
+//   Shared tiles: the positions left, from a multiple of 32, are `blocks` blocks of
+//   32; the blocks of all query heads of a cached head, one head after the other,
+//   fill the 8 waves of `tiles` tiles, so that a short chunk, or the end of a long
+//   one, leaves few waves idle. Where the tiles would hold fewer than kChunkRows
+//   rows each, the scan kernel is as fast, and reads the cache faster: the tokens
+//   left (rest) go there.
 struct ChunkTiles {
-  int base64, n, last, rest;   // first position / 64, tiles, key tiles of the last one, tokens left to the scan
-  __device__ __forceinline__ ChunkTiles(int ctx, int total) {
+  int base64, full;            // first position / 64, full tiles
+  int start, blocks, tiles, keys;   // shared tiles: first position, blocks of a head, per cached head, key tiles each
+  int rest;                    // tokens left to the scan
+  __device__ __forceinline__ ChunkTiles(int ctx, int total, int G) {
     base64 = ctx >> 6;
-    const long long span = (long long)total - 64LL * base64;
-    rest = (int)(span & 255);
-    rest = rest < kChunkMin ? rest : 0;
-    n = (int)((span - rest + 255) >> 8);
-    last = (int)(((long long)total - rest + 63) >> 6);
+    full = (int)(((long long)total - 64LL * base64) >> 8);
+    start = full > 0 ? 64 * base64 + 256 * full : ctx & ~31;
+    const int tokens = total - max(start, ctx);
+    blocks = (total - start + 31) >> 5;
+    tiles = (G * blocks + 7) >> 3;
+    keys = (int)(((long long)total + 63) >> 6);
+    rest = tokens * G < tiles * kChunkRows ? tokens : 0;
+    if (rest > 0) tiles = 0;
   }
-  // Key tiles of the tiles before k.
+  // Key tiles and set-ups of the full tiles before k.
   __device__ __forceinline__ long long before(int k) const {
-    const long long full = (long long)k * base64 + 2LL * k * (k + 1);
-    return k < n ? full : (long long)(n - 1) * base64 + 2LL * (n - 1) * n + last;
+    return (long long)k * (base64 + kExtra) + 2LL * k * (k + 1);
   }
-  __device__ __forceinline__ int keys(int k) const { return k + 1 < n ? base64 + 4 * (k + 1) : last; }
+  __device__ __forceinline__ long long units(int H, int H_kv) const {
+    return before(full) * H + (long long)tiles * H_kv * (keys + kExtra);
+  }
 };
 
-// The part of a request that each kernel takes: its first tokens with
-// chunk_min > 0 and at least that many new ones go to the long-chunk kernel, the
-// rest to the scan kernel, as requests of their own.
-__device__ __forceinline__ Req chunk_part(Req r, int chunk_min) {
-  if (chunk_min == 0 || r.q < chunk_min) r.q = 0;
-  if (r.q > 0) {
-    const int rest = ChunkTiles(r.total - r.q, r.total).rest;
-    r.q -= rest;
-    r.total -= rest;
-  }
-  return r;
-}
-__device__ __forceinline__ Req scan_part(Req r, int chunk_min) {
-  if (chunk_min > 0 && r.q >= chunk_min) {
-    const int rest = ChunkTiles(r.total - r.q, r.total).rest;
+// The scan's part of a request: all of its new tokens, or those that the chunk
+// kernel leaves (chunks), as a request of their own.
+__device__ __forceinline__ Req scan_part(Req r, bool chunks, int G) {
+  if (chunks && r.q > 0) {
+    const int rest = ChunkTiles(r.total - r.q, r.total, G).rest;
     r.first += r.q - rest;
     r.q = rest;
   }
@@ -82,8 +89,7 @@ __device__ __forceinline__ Req scan_part(Req r, int chunk_min) {
 //
 // Both kernels cut their work the same way, from the device-side lengths. A unit
 // is 128 keys of one row block (scan: row_block rows of a request and cached head)
-// or one 64-key tile of one query tile (long chunks: 256 positions of a request
-// and head). The units of all row blocks or tiles form one line, request by
+// or one 64-key tile of one query tile (chunks). The units of all row blocks or tiles form one line, request by
 // request and head by head, which is cut into equal ranges, one per work-group:
 // one request or many, ragged or not, every work-group has the same work. A row
 // block or tile counts kExtra units more than its keys: that is what a segment
@@ -93,11 +99,6 @@ __device__ __forceinline__ Req scan_part(Req r, int chunk_min) {
 // units from either end of the keys moves there. A row block or tile that a cut
 // divides leaves a partial state in each range it lies in, at most two per range,
 // and the join kernel finishes it.
-
-constexpr int kScanUnit = 128;
-constexpr int kExtra = 2;
-constexpr int kSnap = 2;
-constexpr int kMinRange = 4;              // units of the shortest range
 
 struct Plan {
   long long* unit_sum;    // exclusive sums over the requests; [S] the total
@@ -118,9 +119,10 @@ struct ScanRows {
 struct PlanScratch { long long red[4][2]; };
 
 // Fills the sums whose arrays p has, by the work-group's first 256 threads; every
-// thread calls. row_block: rows per scan item; chunk_min: new tokens from which a
-// request is a long chunk, 0 when none is.
-__device__ __forceinline__ void make_plan(const PagedArgs& a, int row_block, int chunk_min, PlanScratch& sc, const Plan& p) {
+// thread calls. row_block: rows per scan item; chunks: whether the chunk kernel
+// runs.
+__device__ __forceinline__ void make_plan(const PagedArgs& a, int row_block, bool chunks, PlanScratch& sc, const Plan& p) {
+  const int G = a.H / a.H_kv;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   long long done[2] = {0, 0};
   for (int b0 = 0; b0 < a.S; b0 += 256) {
@@ -130,16 +132,13 @@ __device__ __forceinline__ void make_plan(const PagedArgs& a, int row_block, int
     Req part;
     if (in) {
       const Req r(a, b);
-      const Req s = scan_part(r, chunk_min), c = chunk_part(r, chunk_min);
-      part = p.unit_sum ? s : c;
+      const Req s = scan_part(r, chunks, G);
+      part = p.unit_sum ? s : r;
       if (p.unit_sum && s.q > 0) {
         const ScanRows n(a, s, row_block);
         own[0] = (long long)n.blocks * a.H_kv * (n.units + kExtra);
       }
-      if (p.tile_sum && c.q > 0) {
-        const ChunkTiles t(c.total - c.q, c.total);
-        own[1] = (t.before(t.n) + (long long)t.n * kExtra) * a.H;
-      }
+      if (p.tile_sum && r.q > 0) own[1] = ChunkTiles(r.total - r.q, r.total, G).units(a.H, a.H_kv);
     }
     long long x[2] = {own[0], own[1]};
 #pragma unroll
@@ -190,10 +189,10 @@ struct PlanLds {
   long long sum[kPlanInline + 1];
   Req part[kPlanInline];
 };
-__device__ __forceinline__ Plan load_plan(const PagedArgs& a, int row_block, int chunk_min, PlanLds& lds) {
+__device__ __forceinline__ Plan load_plan(const PagedArgs& a, int row_block, bool chunks, PlanLds& lds) {
   if (a.S > kPlanInline) return ws_plan(a);
   const Plan p = row_block > 0 ? Plan{lds.sum, nullptr, lds.part} : Plan{nullptr, lds.sum, lds.part};
-  make_plan(a, row_block, chunk_min, lds.sc, p);
+  make_plan(a, row_block, chunks, lds.sc, p);
   __syncthreads();
   return p;
 }
@@ -223,6 +222,7 @@ __device__ __forceinline__ int divide(long long v, long long n) {
 // the others the first segments of the ranges after it.
 struct CutRecord {
   int pieces, b, head, first, ctx, total, row0, rows;
+  int blocks, slot0;      // of a query tile
 };
 static_assert(sizeof(CutRecord) == kCutBytes, "workspace layout");
 
@@ -295,16 +295,17 @@ struct ScanSource {
   const PagedArgs& a;
   const Plan& p;
   Range rg;
-  int row_block, chunk_min;
+  int row_block;
+  bool chunks;
   CutRecord* cuts;
   struct Block {
     int b, kvh, row0, rows, units;
     long long start;
     Req r;
   };
-  __device__ __forceinline__ ScanSource(const PagedArgs& args, const Plan& plan, int rows, int least_new)
+  __device__ __forceinline__ ScanSource(const PagedArgs& args, const Plan& plan, int rows, bool with_chunks)
       : a(args), p(plan), rg(plan.unit_sum[args.S], kMinRange, blockIdx.x, gridDim.x), row_block(rows),
-        chunk_min(least_new), cuts(States::scan(args).cuts) {
+        chunks(with_chunks), cuts(States::scan(args).cuts) {
     if (threadIdx.x == 0) cuts[rg.me].pieces = 0;
     if (rg.u < rg.end) {
       const Block k = block_of(rg.u);
@@ -314,7 +315,7 @@ struct ScanSource {
   __device__ __forceinline__ Block block_of(long long u) const {
     Block k;
     k.b = find_request(p.unit_sum, a.S, u);
-    k.r = p.part ? p.part[k.b] : scan_part(Req(a, k.b), chunk_min);
+    k.r = p.part ? p.part[k.b] : scan_part(Req(a, k.b), chunks, a.H / a.H_kv);
     const ScanRows n(a, k.r, row_block);
     k.units = n.units;
     const long long v = u - p.unit_sum[k.b];
@@ -344,78 +345,104 @@ struct ScanSource {
     s.k0 = u0 * kScanUnit;
     s.k1 = (int)min((long long)last, (long long)u1 * kScanUnit);
     if (s.slot == 2 * rg.me + 1 && threadIdx.x == 0)
-      cuts[rg.me] = CutRecord{pieces, s.b, s.kvh, s.first, s.ctx, s.total, s.row0, s.rows};
+      cuts[rg.me] = CutRecord{pieces, s.b, s.kvh, s.first, s.ctx, s.total, s.row0, s.rows, 0, 0};
     return s;
   }
 };
 
-// A range's part of one query tile: key tiles [tb, te), te = 0 for none.
+// A range's part of one query tile: key tiles [tb, te), te = 0 for none. Rows
+// 32 w .. 32 w + 31 of the tile are block (slot0 + w) % blocks of positions from q0
+// of the group's head h + (slot0 + w) / blocks (none past the group).
 struct Segment {
   int b, h, kvh;
   int first, ctx, total;       // packed token of the chunk's first row, its position, cached rows
-  int q0, tb, te, slot;        // q0: the tile's first position
+  int q0, blocks, slot0;
+  int tb, te, slot;
   // The same, every field in a scalar register.
   __device__ __forceinline__ Segment uniform() const {
-    return Segment{uni(b), uni(h), uni(kvh), uni(first), uni(ctx), uni(total), uni(q0), uni(tb), uni(te), uni(slot)};
+    return Segment{uni(b),  uni(h),      uni(kvh),   uni(first), uni(ctx), uni(total),
+                   uni(q0), uni(blocks), uni(slot0), uni(tb),    uni(te),  uni(slot)};
   }
 };
 
+// The end of a tile that the range before began comes last (late): then all
+// work-groups start at a request's first keys and go through them side by side,
+// and the tiles of an XCD find them in its L2.
 struct ChunkSource {
   const PagedArgs& a;
   const Plan& p;
   Range rg;
+  long long late = 0, late_end = 0;
   CutRecord* cuts;
-  struct Tile {
-    int b, h, tile, keys;
-    long long start;
-    Req r;
-  };
   __device__ __forceinline__ ChunkSource(const PagedArgs& args, const Plan& plan)
       : a(args), p(plan), rg(plan.tile_sum[args.S], 2 * kMinRange, blockIdx.x, gridDim.x), cuts(States::chunk(args).cuts) {
     if (threadIdx.x == 0) cuts[rg.me].pieces = 0;
     if (rg.u < rg.end) {
-      const Tile t = tile_of(rg.u);
-      rg.settle(t.start, t.keys);
+      Segment s;
+      int keys;
+      const long long start = tile_of(rg.u, s, keys);
+      rg.settle(start, keys);
+      const long long stop = start + kExtra + keys;
+      if (rg.u > start && rg.u < stop && stop < rg.end) {
+        late = rg.u;
+        late_end = stop;
+        rg.u = uni(stop);
+      }
     }
   }
-  __device__ __forceinline__ Tile tile_of(long long u) const {
-    Tile k;
-    k.b = find_request(p.tile_sum, a.S, u);
-    k.r = p.part ? p.part[k.b] : chunk_part(Req(a, k.b), kChunkMin);
-    const ChunkTiles t(k.r.total - k.r.q, k.r.total);
-    auto at = [&](int i) { return t.before(i) + (long long)i * kExtra; };
-    const long long per_head = at(t.n);
-    const long long v = u - p.tile_sum[k.b];
-    k.h = divide(v, per_head);
-    const long long w = v - k.h * per_head;
-    int lo = 0, hi = t.n - 1;                            // the last tile that starts at or before w
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (at(mid) <= w) lo = mid;
-      else hi = mid - 1;
+  // The query tile of unit u in s, its key tiles, and the unit it starts at.
+  __device__ __forceinline__ long long tile_of(long long u, Segment& s, int& keys) const {
+    const int G = a.H / a.H_kv;
+    s.b = find_request(p.tile_sum, a.S, u);
+    const Req r = p.part ? p.part[s.b] : Req(a, s.b);
+    s.first = r.first;
+    s.total = r.total;
+    s.ctx = r.total - r.q;
+    const ChunkTiles t(s.ctx, s.total, G);
+    const long long v = u - p.tile_sum[s.b], per_head = t.before(t.full), all_full = per_head * a.H;
+    if (v < all_full) {
+      s.h = divide(v, per_head);
+      const long long w = v - s.h * per_head;
+      int lo = 0, hi = t.full - 1;                       // the last tile that starts at or before w
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (t.before(mid) <= w) lo = mid;
+        else hi = mid - 1;
+      }
+      s.kvh = s.h / G;
+      s.q0 = 64 * t.base64 + 256 * lo;
+      s.blocks = 8;
+      s.slot0 = 0;
+      keys = t.base64 + 4 * (lo + 1);
+      return u - (w - t.before(lo));
     }
-    k.tile = lo;
-    k.keys = t.keys(lo);
-    k.start = u - (w - at(lo));
-    return k;
+    const int item = divide(v - all_full, t.keys + kExtra);   // cached head, tile
+    s.kvh = item / t.tiles;
+    s.h = s.kvh * G;
+    s.q0 = t.start;
+    s.blocks = t.blocks;
+    s.slot0 = 8 * (item - s.kvh * t.tiles);
+    keys = t.keys;
+    return p.tile_sum[s.b] + all_full + (long long)item * (t.keys + kExtra);
   }
   __device__ __forceinline__ Segment next() {
     Segment s{};
-    if (rg.u >= rg.end) return s;
-    const Tile t = tile_of(rg.u);
-    int u0, u1, pieces;
-    if (!rg.take(t.start, t.keys, u0, u1, s.slot, pieces)) return s;
-    s.b = t.b;
-    s.h = t.h;
-    s.kvh = t.h / (a.H / a.H_kv);
-    s.first = t.r.first;
-    s.total = t.r.total;
-    s.ctx = t.r.total - t.r.q;
-    s.q0 = (s.ctx & ~63) + 256 * t.tile;
-    s.tb = u0;
-    s.te = u1;
-    if (s.slot == 2 * rg.me + 1 && threadIdx.x == 0)
-      cuts[rg.me] = CutRecord{pieces, s.b, s.h, s.first, s.ctx, s.total, s.q0, 256};
+    for (;;) {
+      if (rg.u >= rg.end) {
+        if (late == late_end) break;
+        rg.u = uni(late);
+        rg.end = uni(late_end);
+        late = late_end;
+      }
+      int keys, pieces;
+      const long long start = tile_of(rg.u, s, keys);
+      if (rg.take(start, keys, s.tb, s.te, s.slot, pieces)) {
+        if (s.slot == 2 * rg.me + 1 && threadIdx.x == 0)
+          cuts[rg.me] = CutRecord{pieces, s.b, s.h, s.first, s.ctx, s.total, s.q0, 256, s.blocks, s.slot0};
+        return s;
+      }
+    }
+    s.te = 0;
     return s;
   }
 };

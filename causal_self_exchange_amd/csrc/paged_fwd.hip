@@ -12,8 +12,9 @@
 // count term, output); otherwise it leaves a partial state, and join_kernel
 // finishes the row.
 //
-// Launches: plan (more than 256 requests only), the long chunks (paged_chunk.hip,
-// where there can be any), scan, join.
+// Launches: plan (more than kPlanInline requests only), the chunk kernel
+// (paged_chunk.hip, where a request can fill its tiles; the rest is left to the
+// scan), scan, join.
 #include "paged_device.h"
 
 namespace rel {
@@ -35,11 +36,11 @@ __device__ __forceinline__ void lds_barrier() {
   asm volatile("" ::: "memory");
 }
 
-__global__ __launch_bounds__(kThreads) void plan_kernel(PagedArgs a, int row_block, int chunk_min) {
+__global__ __launch_bounds__(kThreads) void plan_kernel(PagedArgs a, int row_block, int chunks) {
   __shared__ PlanScratch sc;
   Plan p = ws_plan(a);
-  if (chunk_min == 0) p.tile_sum = nullptr;
-  make_plan(a, row_block, chunk_min, sc, p);
+  if (!chunks) p.tile_sum = nullptr;
+  make_plan(a, row_block, chunks != 0, sc, p);
 }
 
 // ---- scan ---------------------------------------------------------------------
@@ -91,7 +92,7 @@ struct Geom {
 };
 
 template <typename Tin, int D, int NB>
-__global__ __launch_bounds__(kThreads, (Geom<Tin, D, NB>::kPerCu)) void scan_kernel(PagedArgs a, HeadParams hp, int chunk_min) {
+__global__ __launch_bounds__(kThreads, (Geom<Tin, D, NB>::kPerCu)) void scan_kernel(PagedArgs a, HeadParams hp, int chunks) {
   using C = Geom<Tin, D, NB>;
   constexpr bool kBf = C::kBf;
   constexpr int kRb = 16 * NB;
@@ -101,7 +102,7 @@ __global__ __launch_bounds__(kThreads, (Geom<Tin, D, NB>::kPerCu)) void scan_ker
   __shared__ float s_m[kWaves][16], s_l[kWaves][16];
   __shared__ PlanLds lds;
 
-  const Plan plan = load_plan(a, kRb, chunk_min, lds);
+  const Plan plan = load_plan(a, kRb, chunks != 0, lds);
   const States states = States::scan(a);
   const int G = a.H / a.H_kv;
   const int tid = threadIdx.x;
@@ -126,7 +127,7 @@ __global__ __launch_bounds__(kThreads, (Geom<Tin, D, NB>::kPerCu)) void scan_ker
     int b, kvh, first_tok, ctx, total, row0, rows, slot, first, nsteps;
     bool any;
   };
-  ScanSource source(a, plan, kRb, chunk_min);
+  ScanSource source(a, plan, kRb, chunks != 0);
   auto next_run = [&]() __attribute__((always_inline)) -> Run {
     const ScanSegment sg = source.next();
     const int k0 = uni(sg.k0), k1 = uni(sg.k1);
@@ -449,11 +450,14 @@ __device__ __forceinline__ void join_rows(const PagedArgs& a, const HeadParams& 
   const bool few = c.rows <= kWaves;
   const int i = few ? wave : first_row + (threadIdx.x >> 4);
   const int from = few ? lane >> 4 : 0, by = few ? 4 : 1;
-  // A tile's rows are positions of one head; a block's are tokens times the heads of a group.
+  // A tile's rows are blocks of 32 positions of the group's heads (Segment); a row
+  // block's are tokens times the heads of a group.
   const int G = a.H / a.H_kv;
-  const int tq = tile ? c.row0 + i - c.ctx : (c.row0 + i) / G;
-  const int h = tile ? c.head : c.head * G + (c.row0 + i) - tq * G;
-  const bool ok = i < c.rows && tq >= 0 && c.ctx + tq < c.total;
+  const int block = tile ? c.slot0 + (i >> 5) : 0;
+  const int x = tile ? block / c.blocks : 0;
+  const int tq = tile ? c.row0 + 32 * (block - x * c.blocks) + (i & 31) - c.ctx : (c.row0 + i) / G;
+  const int h = tile ? c.head + x : c.head * G + (c.row0 + i) - tq * G;
+  const bool ok = i < c.rows && tq >= 0 && c.ctx + tq < c.total && x < G;
   float M = kEmptyMax, L = 0.0f, z[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) z[e] = 0.0f;
@@ -495,15 +499,16 @@ hipError_t launch_rows(const PagedArgs& a, const HeadParams& hp, hipStream_t s) 
   int cu = 0;
   hipError_t e = device_cu_count(&cu);
   if (e != hipSuccess) return e;
-  // Long chunks: bf16, with a token stride whose 256 rows a 31-bit byte offset
-  // reaches.
-  const bool chunks = sizeof(Tin) == 2 && a.max_new >= kChunkMin && a.N >= kChunkMin && a.ld1 < (1 << 22);
-  const int chunk_min = chunks ? kChunkMin : 0;
+  // The chunk kernel: bf16, where a request can fill a query tile (the workspace
+  // counts on no more tokens than the batch has), with a token stride whose 256
+  // rows a 31-bit byte offset reaches.
+  const bool chunks = sizeof(Tin) == 2 && paged_chunks_possible(a.max_new < a.N ? a.max_new : a.N, a.H / a.H_kv) &&
+                      a.ld1 < (1 << 22);
   const int chunk_groups = chunks ? (cu < kChunkGroups ? cu : kChunkGroups) : 0;
   int scan_groups = cu * Geom<Tin, D, NB>::kPerCu;
   scan_groups = scan_groups * NB < kScanGroups ? scan_groups : kScanGroups / NB;
   if (a.S > kPlanInline) {
-    hipLaunchKernelGGL(plan_kernel, dim3(1), dim3(kThreads), 0, s, a, 16 * NB, chunk_min);
+    hipLaunchKernelGGL(plan_kernel, dim3(1), dim3(kThreads), 0, s, a, 16 * NB, (int)chunks);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
@@ -511,7 +516,7 @@ hipError_t launch_rows(const PagedArgs& a, const HeadParams& hp, hipStream_t s) 
     e = launch_paged_chunk(a, hp, chunk_groups, s);
     if (e != hipSuccess) return e;
   }
-  hipLaunchKernelGGL((scan_kernel<Tin, D, NB>), dim3(scan_groups), dim3(kThreads), 0, s, a, hp, chunk_min);
+  hipLaunchKernelGGL((scan_kernel<Tin, D, NB>), dim3(scan_groups), dim3(kThreads), 0, s, a, hp, (int)chunks);
   e = hipGetLastError();
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL((join_kernel<Tin, D>), dim3(scan_groups * NB + 16 * chunk_groups), dim3(kThreads), 0, s, a, hp,

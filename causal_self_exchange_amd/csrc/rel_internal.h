@@ -175,26 +175,31 @@ struct PagedArgs {
 };
 
 // Workspace of relation_paged_fwd (paged_device.h): the work sums of batches of
-// more than kPlanInline requests (two 64-bit ones), a 32-byte record per
+// more than kPlanInline requests (two 64-bit ones), a 40-byte record per
 // work-group and the partial states (m, l) and z[d_h] of the scan kernel's row
-// blocks, and the same of the long-chunk kernel's query tiles of 256 rows (bf16,
-// requests with at least kChunkMin new tokens). A work-group leaves at most two
-// partial states.
+// blocks, and the same of the chunk kernel's query tiles of 256 rows (bf16, where a
+// request can fill kChunkRows of one). A work-group leaves at most two partial
+// states.
 constexpr int kPlanInline = 128;
 constexpr int kScanGroups = 1024;         // at most, with 16 rows each; 512 with 32
 constexpr int kScanStateRows = 2 * kScanGroups * 16;
-constexpr int kChunkMin = 128;
+constexpr int kChunkRows = 128;
 constexpr int kChunkGroups = 256;
 constexpr int kChunkStateRows = 2 * kChunkGroups * 256;
-constexpr int64_t kCutBytes = 32;
+constexpr int64_t kCutBytes = 40;
 inline __host__ __device__ int64_t paged_sum_bytes(int64_t S) { return ((S + 1) * 8 + 255) / 256 * 256; }
 inline __host__ __device__ int64_t paged_scan_offset(int64_t S) { return 2 * paged_sum_bytes(S); }
 inline __host__ __device__ int64_t paged_chunk_offset(int64_t S, int d_h) {
   return paged_scan_offset(S) + kScanGroups * kCutBytes + (int64_t)kScanStateRows * (d_h + 2) * 4;
 }
-inline size_t paged_ws_bytes(int64_t N, int64_t S, int d_h) {
+// Whether a request with new_tokens tokens and G query heads per cached head can
+// fill a query tile far enough for the chunk kernel.
+inline bool paged_chunks_possible(int64_t new_tokens, int G) {
+  return new_tokens * (G < 8 ? G : 8) >= kChunkRows;
+}
+inline size_t paged_ws_bytes(int64_t N, int64_t S, int G, int d_h) {
   const int64_t chunk = kChunkGroups * kCutBytes + (int64_t)kChunkStateRows * (d_h + 2) * 4;
-  return static_cast<size_t>(paged_chunk_offset(S, d_h) + (N >= kChunkMin ? chunk : 0));
+  return static_cast<size_t>(paged_chunk_offset(S, d_h) + (paged_chunks_possible(N, G) ? chunk : 0));
 }
 
 // Launchers (return the hipError_t of the launch).

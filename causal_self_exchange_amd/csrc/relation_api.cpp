@@ -285,7 +285,7 @@ size_t relation_paged_workspace_bytes(int N, int S, int H, int H_kv, int d_h) {
   if (N < 1 || S < 1 || S > 65535 || H < 1 || H > REL_MAX_HEADS || H_kv < 1 || H % H_kv != 0 ||
       !fwd_head_dim_ok(d_h))
     return 0;
-  return rel::paged_ws_bytes(N, S, d_h);
+  return rel::paged_ws_bytes(N, S, H / H_kv, d_h);
 }
 
 rel_status relation_paged_fwd(const void* P1, int64_t ld1, const void* cache_P2, const void* cache_V,
