@@ -34,11 +34,16 @@ struct Req {
 };
 
 // The cut of the work (below): keys of a scan unit, units that a segment costs
-// beside its keys, the least that a cut leaves, units of the shortest range.
+// beside its keys, the least that a cut leaves, units of the shortest range of the
+// scan (fp32 products take 8 times as long per key: six chunks of up to 97 tokens
+// of 8 heads of 48, 27 us at 1 and 34 at 4; in bf16 single tokens lose 1 us at 1)
+// and of the chunks.
 constexpr int kScanUnit = 128;
 constexpr int kExtra = 2;
 constexpr int kSnap = 2;
 constexpr int kMinRange = 4;
+constexpr int kMinRangeF32 = 1;
+constexpr int kMinRangeChunk = 8;
 
 // Query tiles of a request's new tokens (chunk kernel): 256 rows, 32 for each of 8 waves.
 //   Full tiles: 256 positions of one head, from ctx rounded down to a multiple of
@@ -303,8 +308,8 @@ struct ScanSource {
     long long start;
     Req r;
   };
-  __device__ __forceinline__ ScanSource(const PagedArgs& args, const Plan& plan, int rows, bool with_chunks)
-      : a(args), p(plan), rg(plan.unit_sum[args.S], kMinRange, blockIdx.x, gridDim.x), row_block(rows),
+  __device__ __forceinline__ ScanSource(const PagedArgs& args, const Plan& plan, int rows, bool with_chunks, int least)
+      : a(args), p(plan), rg(plan.unit_sum[args.S], least, blockIdx.x, gridDim.x), row_block(rows),
         chunks(with_chunks), cuts(States::scan(args).cuts) {
     if (threadIdx.x == 0) cuts[rg.me].pieces = 0;
     if (rg.u < rg.end) {
@@ -375,7 +380,7 @@ struct ChunkSource {
   long long late = 0, late_end = 0;
   CutRecord* cuts;
   __device__ __forceinline__ ChunkSource(const PagedArgs& args, const Plan& plan)
-      : a(args), p(plan), rg(plan.tile_sum[args.S], 2 * kMinRange, blockIdx.x, gridDim.x), cuts(States::chunk(args).cuts) {
+      : a(args), p(plan), rg(plan.tile_sum[args.S], kMinRangeChunk, blockIdx.x, gridDim.x), cuts(States::chunk(args).cuts) {
     if (threadIdx.x == 0) cuts[rg.me].pieces = 0;
     if (rg.u < rg.end) {
       Segment s;

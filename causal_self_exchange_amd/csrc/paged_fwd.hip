@@ -127,7 +127,7 @@ __global__ __launch_bounds__(kThreads, (Geom<Tin, D, NB>::kPerCu)) void scan_ker
     int b, kvh, first_tok, ctx, total, row0, rows, slot, first, nsteps;
     bool any;
   };
-  ScanSource source(a, plan, kRb, chunks != 0);
+  ScanSource source(a, plan, kRb, chunks != 0, kBf ? kMinRange : kMinRangeF32);
   auto next_run = [&]() __attribute__((always_inline)) -> Run {
     const ScanSegment sg = source.next();
     const int k0 = uni(sg.k0), k1 = uni(sg.k1);

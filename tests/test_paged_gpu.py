@@ -224,6 +224,90 @@ def test_paged_fwd_long_chunks(d, page, H, Hkv, reqs):
     check_fwd(P.make("bf16", H, Hkv, d, page, reqs, seed=d + H, stride_pad=8, pad_rows=2), 0.5, "bf16")
 
 
+@pytest.mark.parametrize("d,page,H,Hkv,reqs", [
+    # Chunks whose rows share query tiles with those of the other heads: one block of 32 positions to eight, from
+    # positions at and off their multiples, groups that do not divide the eight waves, histories long enough to be cut.
+    (64, 16, 8, 1, [(0, 16), (16, 16), (17, 16), (40, 17), (3, 1), (64, 8)]),
+    (128, 16, 8, 2, [(0, 32), (32, 32), (33, 32), (95, 65), (7, 127), (5000, 100)]),
+    (128, 64, 12, 4, [(50, 50), (1, 192), (31, 224), (63, 255), (12000, 43)]),
+    (80, 32, 5, 1, [(20, 90), (70, 200), (0, 255), (3000, 26)]),
+    (48, 16, 24, 1, [(0, 8), (9, 6), (500, 33), (31, 2), (31, 5)]),
+    (32, 256, 9, 3, [(100, 60), (64, 43), (1000, 300)]),
+    (64, 128, 3, 3, [(0, 127), (1, 128), (31, 160), (700, 129)]),
+])
+def test_paged_fwd_shared_tiles(d, page, H, Hkv, reqs):
+    check_fwd(P.make("bf16", H, Hkv, d, page, reqs, seed=d + H, stride_pad=24, pad_rows=1), 0.5, "bf16")
+
+
+@pytest.mark.parametrize("dt,S,H,Hkv,d,ctx_hi,new_hi,every", [
+    ("bf16", 128, 4, 2, 64, 200, 1, 0), ("bf16", 129, 4, 2, 64, 200, 1, 0), ("bf16", 300, 2, 1, 64, 90, 4, 0),
+    ("bf16", 260, 4, 1, 128, 300, 2, 90), ("f32", 200, 2, 2, 48, 100, 3, 0), ("bf16", 700, 1, 1, 32, 40, 2, 200),
+])
+def test_paged_fwd_many_requests(dt, S, H, Hkv, d, ctx_hi, new_hi, every):
+    """Batches around and past the number of requests whose sums fit a work-group's memory; every so many a long chunk."""
+    rng = np.random.default_rng(S)
+    reqs = [(int(rng.integers(0, ctx_hi)), int(rng.integers(0 if new_hi > 1 else 1, new_hi + 1))) for _ in range(S)]
+    for b in range(every // 2, S, every or S):
+        if every:
+            reqs[b] = (reqs[b][0], 150 + b)
+    m = P.make(dt, H, Hkv, d, 16, reqs, seed=S, pad_rows=2)
+    m["total"][S // 3] = -1
+    check_fwd(m, 0.5, dt)
+
+
+def test_paged_fwd_many_heads():
+    check_fwd(P.make("bf16", 256, 256, 32, 16, [(5, 1), (40, 3)], seed=1), 0.5, "bf16")
+    check_fwd(P.make("bf16", 256, 2, 64, 16, [(5, 1), (700, 2), (20, 9)], seed=1), 0.5, "bf16")
+    check_fwd(P.make("f32", 256, 1, 32, 16, [(5, 1), (90, 2)], seed=1), 0.5, "f32")
+
+
+def test_paged_fwd_token_strides_past_the_chunk_tiles():
+    """A token stride whose 256 rows no 31-bit offset reaches."""
+    m = P.make("bf16", 2, 1, 64, 16, [(30, 140), (3, 1)], seed=3)
+    d = P.to_device(m)
+    wide = torch.empty((m["N"], 1 << 22), dtype=torch.bfloat16, device=DEV)
+    view = wide[:, :128].unflatten(1, (2, 64))
+    view.copy_(m["P1"])
+    y = R.paged_fwd(view, d["cP2"], d["cV"], d["table"], d["total"], d["cu"], m["tau"], 0.5, max_new=140)
+    torch.cuda.synchronize()
+    ref, spread = PO.paged_fwd(P.f64(m["P1"]), np.nan_to_num(P.f64(m["cP2"])), np.nan_to_num(P.f64(m["cV"])),
+                               m["table"].numpy(), m["total"].numpy(), m["cu"].numpy(), m["tau"], 0.5,
+                               np.zeros(tuple(m["P1"].shape)), 140, with_spread=True)
+    assert np.all(np.abs(P.f64(y) - ref) <= P.bound(ref, spread, "bf16", 1e-6))
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_caches_past_32_bit_offsets(dt):
+    """Pages on both sides of 2^31 and 2^32 elements: written by the append, read by single tokens and chunks."""
+    H, Hkv, d, page = 4, 2, 128, 256
+    per = Hkv * page * d
+    n_pages = (1 << 32) // per + 40
+    reqs = [(600, 1), (100, 160), (300, 5)]
+    m = P.make(dt, H, Hkv, d, page, reqs, seed=7)
+    held = int(m["cP2"].shape[0])
+    marks = [(1 << 31) // per, (1 << 32) // per]
+    where = np.array([0, n_pages - 1] + [k + j for k in marks for j in (-2, -1, 0, 1)] + list(range(50, 50 + held)))[:held]
+    big = [torch.empty((n_pages, Hkv, page, d), dtype=m["cP2"].dtype, device=DEV) for _ in range(2)]
+    at = torch.from_numpy(where).to(DEV)
+    for b, c in zip(big, (m["cP2"], m["cV"])):
+        b[at] = c.to(DEV)
+    small = m["table"].numpy()
+    table = torch.from_numpy(np.where(small >= 0, where[np.clip(small, 0, None)], P.BAD).astype(np.int32)).to(DEV)
+    dev = P.to_device(m)
+    want = R.paged_fwd(dev["P1"], dev["cP2"], dev["cV"], dev["table"], dev["total"], dev["cu"], m["tau"], 0.5, max_new=160)
+    got = R.paged_fwd(dev["P1"], *big, table, dev["total"], dev["cu"], m["tau"], 0.5, max_new=160)
+    assert torch.equal(got, want)
+    # The same rows appended: into the last row of each page that is used.
+    n = len(where)
+    x = torch.from_numpy(np.random.default_rng(1).standard_normal((n, 2 * Hkv, d))).to(m["cP2"].dtype).to(DEV)
+    slot = i32(where * page + page - 1)
+    R.paged_append(x[:, :Hkv], x[:, Hkv:], slot, *big)
+    torch.cuda.synchronize()
+    assert torch.equal(big[0][at][:, :, -1], x[:, :Hkv]) and torch.equal(big[1][at][:, :, -1], x[:, Hkv:])
+    for b, c in zip(big, (m["cP2"], m["cV"])):
+        np.testing.assert_array_equal(b[at][:, :, :-1].cpu().float().numpy(), c[:, :, :-1].float().numpy())
+
+
 @pytest.mark.parametrize("dt,reqs", [("bf16", RAGGED), ("bf16", CHUNKS), ("f32", RAGGED)])
 def test_paged_fwd_large_evidence(dt, reqs):
     """Evidence far beyond the exponent range of an unshifted exponential (|U| to some hundreds): the stabiliser moves.
