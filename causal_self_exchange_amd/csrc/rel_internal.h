@@ -183,7 +183,7 @@ struct PagedArgs {
 constexpr int kPlanInline = 128;
 constexpr int kScanGroups = 1024;         // at most, with 16 rows each; 512 with 32
 constexpr int kScanStateRows = 2 * kScanGroups * 16;
-constexpr int kChunkRows = 128;
+constexpr int kChunkRows = 65;
 constexpr int kChunkGroups = 256;
 constexpr int kChunkStateRows = 2 * kChunkGroups * 256;
 constexpr int64_t kCutBytes = 40;
