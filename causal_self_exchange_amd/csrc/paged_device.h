@@ -344,10 +344,15 @@ struct ScanSource {
     const ScanRows n(a, k.r, row_block);
     k.units = n.units;
     const long long v = u - p.unit_sum[k.b];
-    const int block = divide(v, n.units + kExtra);       // cached head, row block
-    k.start = p.unit_sum[k.b] + (long long)block * (n.units + kExtra);
-    k.kvh = block / n.blocks;
-    k.row0 = (block - k.kvh * n.blocks) * row_block;
+    const int item = divide(v, n.units + kExtra);
+    k.start = p.unit_sum[k.b] + (long long)item * (n.units + kExtra);
+    // Stripes of as many heads as a range has items, row block by row block.
+    const int most = min(a.H_kv, max(1, divide(rg.per, n.units + kExtra)));
+    const int first = item / (most * n.blocks) * most;   // the stripe's first head
+    const int width = min(most, a.H_kv - first);
+    const int rest = item - first * n.blocks, rb = rest / width;
+    k.kvh = first + rest - rb * width;
+    k.row0 = rb * row_block;
     k.rows = min(row_block, n.rows - k.row0);
     return k;
   }
