@@ -223,11 +223,12 @@ __device__ __forceinline__ int divide(long long v, long long n) {
 }
 
 // The row block or tile that the end of a work-group's range divides, for the
-// join: pieces = 0 when there is none. Piece 0 is the last segment of the range,
-// the others the first segments of the ranges after it.
+// join: pieces = 0 when there is none. Piece 0 is the last segment of the range
+// `owner`, piece p the first segment of the p-th range after it.
 struct CutRecord {
-  int pieces, b, head, first, ctx, total, row0, rows;
+  int pieces, owner, b, head, first, ctx, total, row0, rows;
   int blocks, slot0;      // of a query tile
+  int pad;
 };
 static_assert(sizeof(CutRecord) == kCutBytes, "workspace layout");
 
@@ -289,9 +290,10 @@ struct Range {
     return u < end;
   }
   // The part of an item of n units at `start` that begins at u: units [k0, k1) of
-  // its keys, in the partial state `slot` (-1: all of them). false: the item
-  // belongs to the next range.
-  __device__ __forceinline__ bool take(long long start, int n, int& k0, int& k1, int& slot, int& pieces) {
+  // its keys, in the partial state `slot` (-1: all of them); where the range's end
+  // divides it, pieces and owner as in CutRecord. false: the item belongs to the
+  // next range.
+  __device__ __forceinline__ bool take(long long start, int n, int& k0, int& k1, int& slot, int& pieces, int& owner) {
     const long long stop = start + kExtra + n;
     const bool inside = u > start;
     k0 = inside ? (int)(u - start - kExtra) : 0;
@@ -303,7 +305,9 @@ struct Range {
       if (k < kSnap) return false;
       if (n - k >= kSnap) {
         k1 = (int)k;
-        pieces = 2 + (int)((stop - kSnap - end) / per);     // the cuts from here on that stay in it, and one
+        // The range of the first cut that stays in the item; the cuts after it, and one.
+        owner = inside ? (int)((start + kExtra + kSnap + per - 1) / per) - 1 : me;
+        pieces = 2 + (int)((stop - kSnap - (owner + 1) * per) / per);
       }
     }
     slot = inside ? 2 * me : (pieces ? 2 * me + 1 : -1);
@@ -359,11 +363,11 @@ struct ScanSource {
   __device__ __forceinline__ ScanSegment next() {
     ScanSegment s{};
     Block k;
-    int u0, u1, pieces;
+    int u0, u1, pieces, owner;
     do {
       if (!rg.more()) return s;
       k = block_of(rg.u);
-    } while (!rg.take(k.start, k.units, u0, u1, s.slot, pieces));
+    } while (!rg.take(k.start, k.units, u0, u1, s.slot, pieces, owner));
     s.any = 1;
     s.b = k.b;
     s.kvh = k.kvh;
@@ -376,8 +380,8 @@ struct ScanSource {
     const int last = s.ctx + (s.row0 + s.rows - 1) / (a.H / a.H_kv);
     s.k0 = u0 * kScanUnit;
     s.k1 = (int)min((long long)last, (long long)u1 * kScanUnit);
-    if (s.slot == 2 * rg.me + 1 && threadIdx.x == 0)
-      cuts[rg.me] = CutRecord{pieces, s.b, s.kvh, s.first, s.ctx, s.total, s.row0, s.rows, 0, 0};
+    if (pieces > 0 && threadIdx.x == 0)
+      cuts[rg.me] = CutRecord{pieces, owner, s.b, s.kvh, s.first, s.ctx, s.total, s.row0, s.rows, 0, 0, 0};
     return s;
   }
 };
@@ -450,11 +454,11 @@ struct ChunkSource {
   __device__ __forceinline__ Segment next() {
     Segment s{};
     while (rg.more()) {
-      int keys, pieces;
+      int keys, pieces, owner;
       const long long start = tile_of(rg.u, s, keys);
-      if (rg.take(start, keys, s.tb, s.te, s.slot, pieces)) {
-        if (s.slot == 2 * rg.me + 1 && threadIdx.x == 0)
-          cuts[rg.me] = CutRecord{pieces, s.b, s.h, s.first, s.ctx, s.total, s.q0, 256, s.blocks, s.slot0};
+      if (rg.take(start, keys, s.tb, s.te, s.slot, pieces, owner)) {
+        if (pieces > 0 && threadIdx.x == 0)
+          cuts[rg.me] = CutRecord{pieces, owner, s.b, s.h, s.first, s.ctx, s.total, s.q0, 256, s.blocks, s.slot0, 0};
         return s;
       }
     }
@@ -528,6 +532,16 @@ __device__ __forceinline__ void finish_row(const PagedArgs& a, const HeadParams&
   store8(static_cast<Tin*>(a.Y) + ((size_t)t * a.H + h) * D + col, y);
 }
 
+// The state (m, l, zp) joined to (M, L, z).
+__device__ __forceinline__ void merge(float& M, float& L, float (&z)[8], float m, float l, const float (&zp)[8]) {
+  const float Mn = fmaxf(M, m);
+  const float f = __builtin_amdgcn_exp2f(M - Mn), fp = __builtin_amdgcn_exp2f(m - Mn);
+  M = Mn;
+  L = L * f + l * fp;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) z[e] = z[e] * f + zp[e] * fp;
+}
+
 // A partial state at row `at` of st joined to (M, L, z), 16 lanes of 8 columns.
 template <int D>
 __device__ __forceinline__ void join_state(const States& st, int64_t at, int sl, float& M, float& L, float (&z)[8]) {
@@ -537,15 +551,13 @@ __device__ __forceinline__ void join_state(const States& st, int64_t at, int sl,
     x = reinterpret_cast<const f32x4*>(st.z + at * D + 8 * sl)[0];
     y = reinterpret_cast<const f32x4*>(st.z + at * D + 8 * sl)[1];
   }
-  const float Mn = fmaxf(M, ml.x);
-  const float fo = __builtin_amdgcn_exp2f(M - Mn), fn = __builtin_amdgcn_exp2f(ml.x - Mn);
-  M = Mn;
-  L = L * fo + ml.y * fn;
+  float zp[8];
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
-    z[e] = z[e] * fo + x[e] * fn;
-    z[4 + e] = z[4 + e] * fo + y[e] * fn;
+    zp[e] = x[e];
+    zp[4 + e] = y[e];
   }
+  merge(M, L, z, ml.x, ml.y, zp);
 }
 
 }  // namespace paged

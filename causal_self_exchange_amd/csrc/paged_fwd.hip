@@ -438,18 +438,25 @@ __global__ __launch_bounds__(kThreads, (Geom<Tin, D, NB>::kPerCu)) void scan_ker
 
 // ---- join ---------------------------------------------------------------------
 
-// Rows of the row block or query tile that the end of range k divides: 16 rows per
-// work-group, 16 lanes per row; up to 4 rows take a wave each, with every fourth
-// piece to a group of 16 lanes.
+// Rows of the row block or query tile that the end of range k divides, by the
+// share'th of its `shares` work-groups. A block in n pieces has n - 1 ranges that it
+// ends, so shares * (n - 1) work-groups: as they suffice, each takes one row (every
+// 16th piece to a group of 16 lanes), 4 (a wave each, every 4th piece) or 16. One
+// token of 16 heads over 131,072 rows of one cached head leaves 256 pieces of 16
+// rows: 66 us with one work-group for all of them, 33 us so.
 template <typename Tin, int D>
-__device__ __forceinline__ void join_rows(const PagedArgs& a, const HeadParams& hp, const States& st, int k, int first_row,
-                                          int state_rows, bool tile) {
+__device__ __forceinline__ void join_rows(const PagedArgs& a, const HeadParams& hp, const States& st, int k, int share,
+                                          int shares, int state_rows, bool tile) {
+  __shared__ float s_state[kWaves - 1][16][10];
   const CutRecord c = st.cuts[k];
-  if (c.pieces == 0 || first_row >= c.rows) return;
+  if (c.pieces == 0) return;
+  const int groups = shares * (c.pieces - 1);
+  const int per = c.rows <= groups ? 1 : (c.rows <= 4 * groups ? 4 : 16);
+  const int first_row = per * (shares * (k - c.owner) + share);
+  if (first_row >= c.rows) return;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, sl = lane & 15;
-  const bool few = c.rows <= kWaves;
-  const int i = few ? wave : first_row + (threadIdx.x >> 4);
-  const int from = few ? lane >> 4 : 0, by = few ? 4 : 1;
+  const int i = first_row + (per == 1 ? 0 : (per == 4 ? wave : (int)threadIdx.x >> 4));
+  const int from = per == 1 ? (int)threadIdx.x >> 4 : (per == 4 ? lane >> 4 : 0), by = 16 / per;
   // A tile's rows are blocks of 32 positions of the group's heads (Segment); a row
   // block's are tokens times the heads of a group.
   const int G = a.H / a.H_kv;
@@ -464,33 +471,50 @@ __device__ __forceinline__ void join_rows(const PagedArgs& a, const HeadParams& 
   if (i < c.rows) {
 #pragma unroll 4
     for (int p = from; p < c.pieces; p += by)
-      join_state<D>(st, (int64_t)(p == 0 ? 2 * k + 1 : 2 * (k + p)) * state_rows + i, sl, M, L, z);
+      join_state<D>(st, (int64_t)(p == 0 ? 2 * c.owner + 1 : 2 * (c.owner + p)) * state_rows + i, sl, M, L, z);
   }
-  if (few) {
+  if (per < 16) {
 #pragma unroll
     for (int o = 16; o < 64; o <<= 1) {
-      const float Mo = __shfl_xor(M, o), Mn = fmaxf(M, Mo);
-      const float f = __builtin_amdgcn_exp2f(M - Mn), fo = __builtin_amdgcn_exp2f(Mo - Mn);
-      L = L * f + __shfl_xor(L, o) * fo;
+      float zo[8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) z[e] = z[e] * f + __shfl_xor(z[e], o) * fo;
-      M = Mn;
+      for (int e = 0; e < 8; ++e) zo[e] = __shfl_xor(z[e], o);
+      merge(M, L, z, __shfl_xor(M, o), __shfl_xor(L, o), zo);
+    }
+  }
+  if (per == 1) {
+    if (wave > 0 && lane < 16) {
+      float* s = s_state[wave - 1][sl];
+      s[0] = M;
+      s[1] = L;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) s[2 + e] = z[e];
+    }
+    __syncthreads();
+    if (wave > 0) return;
+#pragma unroll
+    for (int w = 0; w < kWaves - 1; ++w) {
+      const float* s = s_state[w][sl];
+      float zo[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) zo[e] = s[2 + e];
+      merge(M, L, z, s[0], s[1], zo);
     }
   }
   finish_row<Tin, D>(a, hp, c.b, ok ? c.first + tq : 0, ok ? h : 0, ok ? c.ctx + tq : 0, sl, M, L, z, ok && from == 0);
 }
 
 // The first scan_groups * row_block / 16 work-groups join the scan's row blocks,
-// the others 16 rows each of the long chunks' tiles.
+// the others, 16 per range, the query tiles.
 template <typename Tin, int D>
 __global__ __launch_bounds__(kThreads) void join_kernel(PagedArgs a, HeadParams hp, int scan_groups, int row_block) {
   const int blocks = row_block / 16;
   int i = (int)blockIdx.x;
   if (i < scan_groups * blocks) {
-    join_rows<Tin, D>(a, hp, States::scan(a), i / blocks, 16 * (i % blocks), row_block, false);
+    join_rows<Tin, D>(a, hp, States::scan(a), i / blocks, i % blocks, blocks, row_block, false);
   } else if constexpr (sizeof(Tin) == 2) {
     i -= scan_groups * blocks;
-    join_rows<Tin, D>(a, hp, States::chunk(a), i / 16, 16 * (i % 16), 256, true);
+    join_rows<Tin, D>(a, hp, States::chunk(a), i / 16, i % 16, 16, 256, true);
   }
 }
 

@@ -175,7 +175,7 @@ struct PagedArgs {
 };
 
 // Workspace of relation_paged_fwd (paged_device.h): the work sums of batches of
-// more than kPlanInline requests (two 64-bit ones), a 40-byte record per
+// more than kPlanInline requests (two 64-bit ones), a 48-byte record per
 // work-group and the partial states (m, l) and z[d_h] of the scan kernel's row
 // blocks, and the same of the chunk kernel's query tiles of 256 rows (bf16, where a
 // request can fill kChunkRows of one). A work-group leaves at most two partial
@@ -186,7 +186,7 @@ constexpr int kScanStateRows = 2 * kScanGroups * 16;
 constexpr int kChunkRows = 65;
 constexpr int kChunkGroups = 256;
 constexpr int kChunkStateRows = 2 * kChunkGroups * 256;
-constexpr int64_t kCutBytes = 40;
+constexpr int64_t kCutBytes = 48;
 inline __host__ __device__ int64_t paged_sum_bytes(int64_t S) { return ((S + 1) * 8 + 255) / 256 * 256; }
 inline __host__ __device__ int64_t paged_scan_offset(int64_t S) { return 2 * paged_sum_bytes(S); }
 inline __host__ __device__ int64_t paged_chunk_offset(int64_t S, int d_h) {

@@ -255,6 +255,16 @@ def test_paged_fwd_many_requests(dt, S, H, Hkv, d, ctx_hi, new_hi, every):
     check_fwd(m, 0.5, dt)
 
 
+@pytest.mark.parametrize("dt,H,Hkv,d,reqs", [
+    ("bf16", 1, 1, 128, [(40000, 1)]), ("bf16", 16, 1, 64, [(50000, 1)]), ("bf16", 8, 1, 128, [(9000, 4), (30000, 3)]),
+    ("bf16", 4, 1, 64, [(20000, 64)]), ("bf16", 2, 2, 80, [(15000, 1), (0, 1), (20, 2)]), ("f32", 16, 1, 32, [(9000, 2)]),
+    ("f32", 1, 1, 48, [(12000, 1)]),
+])
+def test_paged_fwd_many_pieces(dt, H, Hkv, d, reqs):
+    """Few rows whose histories lie in many ranges: one, four or sixteen rows to a work-group that joins them."""
+    check_fwd(P.make(dt, H, Hkv, d, 16, reqs, seed=d + H), 0.5, dt)
+
+
 def test_paged_fwd_many_heads():
     check_fwd(P.make("bf16", 256, 256, 32, 16, [(5, 1), (40, 3)], seed=1), 0.5, "bf16")
     check_fwd(P.make("bf16", 256, 2, 64, 16, [(5, 1), (700, 2), (20, 9)], seed=1), 0.5, "bf16")
