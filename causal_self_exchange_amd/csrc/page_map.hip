@@ -9,12 +9,14 @@
 //   and the second needs the whole first one. Pages are moved one per thread,
 //   whichever request they belong to (found by bisection in the sums, in LDS): a
 //   request of 2000 tokens returns 125 pages, which one thread would move in 25 us.
+//   A thread has four in flight: 1024 prompts, which move 10,000 pages, 19.0 us one
+//   by one, 14.7 so. Up to 256 requests and 512 tokens take 4 waves instead of 16,
+//   whose barriers and sums are shorter: 256 requests of one token 8.3 us by 16
+//   waves, 5.3 by 4.
 // page_slots: one thread per packed token finds its request by bisection in
-//   the offsets and its page in the table. Up to kSlotsInline tokens page_map
-//   does it itself.
-// The call moves a few KB: it is bound by the latency of its dependent steps
-// (256 requests of one token 9 us before the offsets were kept in LDS and the
-// sums taken together, 1024 prompts 37 us).
+//   the offsets and its page in the table (60,000 tokens 4 us). Up to kSlotsInline
+//   tokens page_map does it itself.
+// The call moves a few KB: it is bound by the latency of its dependent steps.
 #include "rel_internal.h"
 #include "rel_device.h"
 
@@ -23,12 +25,14 @@ namespace rel {
 namespace {
 
 constexpr int kMapThreads = 1024;
-constexpr int kMapWaves = kMapThreads / 64;
+constexpr int kMapFew = 256;              // threads for as many requests
+constexpr int kAtOnce = 4;                // pages that a thread moves together
 constexpr int kSlotThreads = 256;
 constexpr int kSlotsInline = 4096;
 constexpr int kSlotsLds = 4096;           // requests whose offsets page_slots keeps in LDS
 
-// Inclusive sum over the work-group, and the work-group's total.
+// Inclusive sum over a work-group of T threads, and its total.
+template <int T>
 __device__ __forceinline__ long long block_sum(long long x, long long* red, long long* total) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
 #pragma unroll
@@ -40,7 +44,7 @@ __device__ __forceinline__ long long block_sum(long long x, long long* red, long
   __syncthreads();
   long long before = 0, all = 0;
 #pragma unroll 4
-  for (int w = 0; w < kMapWaves; ++w) {
+  for (int w = 0; w < T / 64; ++w) {
     const long long r = red[w];
     before += w < wave ? r : 0;
     all += r;
@@ -60,6 +64,16 @@ __device__ __forceinline__ int first_past(const Int* end, int n, Int i) {
     else lo = mid + 1;
   }
   return lo;
+}
+
+// The same for n = T, where there is one, in a fixed number of steps: several
+// searches run side by side.
+template <int T>
+__device__ __forceinline__ int first_past_of(const int* end, int i) {
+  int at = 0;
+#pragma unroll
+  for (int step = T / 2; step > 0; step >>= 1) at += end[at + step - 1] <= i ? step : 0;
+  return at;
 }
 
 __device__ __forceinline__ int pages_of(int rows, int shift) {
@@ -97,10 +111,12 @@ __device__ __forceinline__ void write_slot(const PageMapArgs& a, int t, int b, i
   a.pos[t] = pos;
 }
 
-__global__ __launch_bounds__(kMapThreads) void page_map_kernel(PageMapArgs a, int with_slots) {
-  __shared__ long long red[kMapWaves];
-  __shared__ int s_end[kMapThreads], s_held[kMapThreads], s_to[kMapThreads], s_ok[kMapThreads], s_taken;
+template <int T>
+__global__ __launch_bounds__(T) void page_map_kernel(PageMapArgs a, int with_slots) {
+  __shared__ long long red[T / 64];
+  __shared__ int s_end[T], s_held[T], s_to[T], s_ok[T], s_taken;
   const int tid = threadIdx.x;
+  const Request own(a, tid);
   long long all;
   if (tid == 0) s_taken = 0;
 
@@ -108,18 +124,25 @@ __global__ __launch_bounds__(kMapThreads) void page_map_kernel(PageMapArgs a, in
   int have = a.n_free[0];
   have = have < 0 ? 0 : (have > a.F ? a.F : have);
   long long back = 0;
-  for (int b0 = 0; b0 < a.S; b0 += kMapThreads) {
-    const Request r(a, b0 + tid);
+  for (int b0 = 0; b0 < a.S; b0 += T) {
+    const Request r = b0 == 0 ? own : Request(a, b0 + tid);
     const int held = r.gone ? pages_of(r.len, a.page_shift) : 0;
-    const long long sum = block_sum(held, red, &all);
+    const long long sum = block_sum<T>(held, red, &all);
     const long long room = a.F - have - back;             // entries left above the list
     const int n = (int)(all < room ? all : (room > 0 ? room : 0));
     s_end[tid] = (int)(sum < n ? sum : n);
     s_held[tid] = (int)(sum - held < n ? sum - held : n);
     __syncthreads();
-    for (int k = tid; k < n; k += kMapThreads) {
-      const int x = first_past(s_end, kMapThreads, k);
-      a.free_pages[have + back + k] = a.table[(size_t)(b0 + x) * a.max_pages + (k - s_held[x])];
+    for (int k0 = tid; k0 < n; k0 += kAtOnce * T) {
+      int page[kAtOnce];
+#pragma unroll
+      for (int j = 0; j < kAtOnce; ++j) {
+        const int k = min(k0 + j * T, n - 1), x = first_past_of<T>(s_end, k);
+        page[j] = a.table[(size_t)(b0 + x) * a.max_pages + (k - s_held[x])];
+      }
+#pragma unroll
+      for (int j = 0; j < kAtOnce; ++j)
+        if (k0 + j * T < n) a.free_pages[have + back + k0 + j * T] = page[j];
     }
     back += all;
     __syncthreads();                   // s_end is read; the last time, the list is whole too
@@ -129,15 +152,15 @@ __global__ __launch_bounds__(kMapThreads) void page_map_kernel(PageMapArgs a, in
   // Offsets, totals and pages for the new tokens.
   long long tokens = 0, needed = 0;
   constexpr long long kMost = 0x7fffffff;
-  for (int b0 = 0; b0 < a.S; b0 += kMapThreads) {
+  for (int b0 = 0; b0 < a.S; b0 += T) {
     const int b = b0 + tid;
-    const Request r(a, b);
-    const long long end = tokens + block_sum(r.q, red, &all);
+    const Request r = b0 == 0 ? own : Request(a, b);
+    const long long end = tokens + block_sum<T>(r.q, red, &all);
     tokens += all;
     const int held = pages_of(r.len, a.page_shift);
     bool ok = r.fits && end <= a.N;
     const int need = ok ? pages_of(r.len + r.q, a.page_shift) - held : 0;
-    const long long upto = needed + block_sum(need, red, &all);
+    const long long upto = needed + block_sum<T>(need, red, &all);
     ok = ok && (need == 0 || upto <= top);
     if (b < a.S) {
       a.cu[b + 1] = (int)(end < kMost ? end : kMost);
@@ -152,13 +175,22 @@ __global__ __launch_bounds__(kMapThreads) void page_map_kernel(PageMapArgs a, in
     s_held[tid] = need;
     __syncthreads();
     const int taken = s_taken, before = (int)(needed < top ? needed : top);
-    for (int k = before + tid; k < taken; k += kMapThreads) {
-      const int x = first_past(s_end, kMapThreads, k);
-      a.table[(size_t)(b0 + x) * a.max_pages + s_to[x] + (k - (s_end[x] - s_held[x]))] = a.free_pages[top - 1 - k];
+    for (int k0 = before + tid; k0 < taken; k0 += kAtOnce * T) {
+      int page[kAtOnce];
+      size_t to[kAtOnce];
+#pragma unroll
+      for (int j = 0; j < kAtOnce; ++j) {
+        const int k = min(k0 + j * T, taken - 1), x = first_past_of<T>(s_end, k);
+        page[j] = a.free_pages[top - 1 - k];
+        to[j] = (size_t)(b0 + x) * a.max_pages + s_to[x] + (k - (s_end[x] - s_held[x]));
+      }
+#pragma unroll
+      for (int j = 0; j < kAtOnce; ++j)
+        if (k0 + j * T < taken) a.table[to[j]] = page[j];
     }
     needed += all;
     __syncthreads();                   // the lists are read, the pages are in the table
-    if (with_slots && a.S <= kMapThreads) {
+    if (with_slots && a.S <= T) {
       s_end[tid] = b < a.S ? (int)(end < kMost ? end : kMost) : (int)kMost;
       s_to[tid] = r.len;
       s_held[tid] = (int)(end - r.q < kMost ? end - r.q : kMost);
@@ -171,7 +203,7 @@ __global__ __launch_bounds__(kMapThreads) void page_map_kernel(PageMapArgs a, in
   }
   if (!with_slots) return;
   __syncthreads();
-  for (int t = tid; t < a.N; t += kMapThreads) {
+  for (int t = tid; t < a.N; t += T) {
     const int x = first_past(s_end, a.S, t);
     const bool in = x < a.S;
     write_slot(a, t, in ? x : 0, s_held[in ? x : 0], s_to[in ? x : 0], in && s_ok[x]);
@@ -197,7 +229,11 @@ __global__ __launch_bounds__(kSlotThreads) void page_slots_kernel(PageMapArgs a)
 
 hipError_t launch_page_map(const PageMapArgs& a, hipStream_t s) {
   const int with_slots = a.N <= kSlotsInline && a.S <= kMapThreads;
-  hipLaunchKernelGGL(page_map_kernel, dim3(1), dim3(kMapThreads), 0, s, a, with_slots);
+  if (a.S <= kMapFew && a.N <= 2 * kMapFew) {
+    hipLaunchKernelGGL(page_map_kernel<kMapFew>, dim3(1), dim3(kMapFew), 0, s, a, with_slots);
+  } else {
+    hipLaunchKernelGGL(page_map_kernel<kMapThreads>, dim3(1), dim3(kMapThreads), 0, s, a, with_slots);
+  }
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || with_slots) return e;
   const unsigned blocks = (unsigned)(((long long)a.N + kSlotThreads - 1) / kSlotThreads);
