@@ -46,10 +46,10 @@ __device__ __forceinline__ void store8(Tin* p, const float (&x)[8]) {
 }
 
 template <typename Tin, int D>
-__global__ __launch_bounds__(kThreads) void paged_append_kernel(PagedAppendArgs a, PrestepParams pp) {
+__global__ __launch_bounds__(kThreads) void paged_append_kernel(PagedAppendArgs a, PrestepParams pp, int first) {
   constexpr int kGroups = D / 16;
   __shared__ float s_cos[D / 2], s_sin[D / 2];
-  const int t = blockIdx.x;
+  const int t = first + (int)blockIdx.x;
   const int slot = a.slot[t];
   if (slot < 0 || (slot >> a.page_shift) >= a.n_pages) return;   // uniform for the work-group
   const int tid = threadIdx.x;
@@ -142,8 +142,15 @@ __global__ __launch_bounds__(kThreads) void paged_append_kernel(PagedAppendArgs 
 
 template <typename Tin, int D>
 hipError_t launch_typed(const PagedAppendArgs& a, const PrestepParams& pp, hipStream_t s) {
-  hipLaunchKernelGGL((paged_append_kernel<Tin, D>), dim3((unsigned)a.N), dim3(kThreads), 0, s, a, pp);
-  return hipGetLastError();
+  // A launch has fewer than 2^32 threads.
+  constexpr int kMost = 1 << 23;
+  for (int64_t first = 0; first < a.N; first += kMost) {
+    const unsigned n = (unsigned)(a.N - first < kMost ? a.N - first : kMost);
+    hipLaunchKernelGGL((paged_append_kernel<Tin, D>), dim3(n), dim3(kThreads), 0, s, a, pp, (int)first);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 }  // namespace

@@ -137,9 +137,10 @@ void fill_prestep_params(rel::PrestepParams& pp, float rope_base, const float* t
   for (int k = 0; k < 64; ++k)
     pp.inv_freq[k] = k < d_h / 2 ? std::pow(static_cast<double>(rope_base), -2.0 * k / d_h) : 0.0;
   for (int k = 0; k < 128; ++k) {
-    const double t = (theta && k < H / 2) ? static_cast<double>(theta[k]) : 0.0;
-    pp.cos_theta[k] = static_cast<float>(std::cos(t));
-    pp.sin_theta[k] = static_cast<float>(std::sin(t));
+    const bool mixes = theta && k < H / 2;
+    const double t = mixes ? static_cast<double>(theta[k]) : 0.0;
+    pp.cos_theta[k] = mixes ? static_cast<float>(std::cos(t)) : 1.0f;
+    pp.sin_theta[k] = mixes ? static_cast<float>(std::sin(t)) : 0.0f;
   }
 }
 
@@ -201,9 +202,10 @@ int page_shift_of(int page_size) {
   return -1;
 }
 
-// Rows and table widths are counted in 32 bits on the device.
+// Rows and table widths are counted in 32 bits on the device, with room for the
+// tiles that run past a request's end.
 bool page_counts_ok(int64_t n_pages, int page_size) {
-  return n_pages >= 1 && page_shift_of(page_size) >= 0 && n_pages * page_size < (int64_t(1) << 31);
+  return n_pages >= 1 && page_shift_of(page_size) >= 0 && n_pages * page_size <= (int64_t(1) << 31) - 65536;
 }
 
 bool stride_ok(int64_t ld, int64_t heads, int d_h, size_t es) {

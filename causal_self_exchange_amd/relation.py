@@ -7,6 +7,7 @@ missing or a call fails, an exception is raised.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -509,6 +510,19 @@ def _run_on(fn, dev, stream, args):
         raise RelationError(fn, st)
 
 
+def _on(stream):
+    """Where a call allocates: its stream's memory, which later work of other
+    streams does not reuse before the call has run."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
+def _count(name: str, x) -> int:
+    x = int(x)
+    if not -2**31 <= x < 2**31:
+        raise ValueError(f"{name} = {x} does not fit 32 bits")
+    return x
+
+
 def _host_floats(x, n: int):
     """Host float[n] from a float or n of them."""
     if isinstance(x, (list, tuple)) and len(x) == n:
@@ -532,6 +546,7 @@ def _tokens(fn, name, t):
 def _table(fn, t):
     if not isinstance(t, torch.Tensor) or t.dim() != 2:
         raise ValueError(f"{fn}: block_table must be an [S, max_pages] tensor")
+    _count("max_pages", t.shape[1])
     return t.shape
 
 
@@ -551,7 +566,8 @@ def page_map(lens, n_new, block_table, free_pages, n_free, N: int, page_size: in
     S, width = _table(fn, block_table)
     if not isinstance(free_pages, torch.Tensor) or free_pages.dim() != 1:
         raise ValueError("page_map: free_pages must be a 1-d tensor")
-    N, F = int(N), free_pages.shape[0]
+    N, F = _count("N", N), _count("F", free_pages.shape[0])
+    page_size, n_pages = _count("page_size", page_size), _count("n_pages", n_pages)
     specs = [("block_table", block_table, (S, width), _I32, True), ("free_pages", free_pages, (F,), _I32, True),
              ("lens", lens, (S,), _I32, True), ("n_new", n_new, (S,), _I32, True), ("n_free", n_free, (1,), _I32, True)]
     if out is not None:
@@ -562,12 +578,13 @@ def page_map(lens, n_new, block_table, free_pages, n_free, N: int, page_size: in
                   ("pos", pos, (N,), _I32, True), ("n_free_out", n_free_out, (1,), _I32, True)]
     dev = _check_tensors(fn, specs)
     if out is None:
-        out = tuple(torch.empty(max(n, 0), dtype=_I32, device=dev) for n in (S + 1, S, N, N, 1))
+        with _on(stream):
+            out = tuple(torch.empty(max(n, 0), dtype=_I32, device=dev) for n in (S + 1, S, N, N, 1))
         cu, total, slot, pos, n_free_out = out
     _run_on("relation_page_map", dev, stream,
             (lens.data_ptr(), n_new.data_ptr(), block_table.data_ptr(), free_pages.data_ptr(), n_free.data_ptr(),
              n_free_out.data_ptr(), cu.data_ptr(), total.data_ptr(), slot.data_ptr(), pos.data_ptr(), S, N, F, width,
-             int(page_size), int(n_pages)))
+             page_size, n_pages))
     return out
 
 
@@ -595,10 +612,11 @@ def paged_append(P2, I, slot, cache_P2, cache_V, P1=None, pos=None, rope="none",
     elif out is not None:
         raise ValueError("paged_append: out is given without P1")
     dev = _check_tensors(fn, specs)
-    if P1 is not None and out is None:
-        out = torch.zeros((N, H, D), dtype=dt, device=dev)
     if theta is not None and len(theta) != Hkv // 2:
         raise ValueError(f"theta needs H_kv/2 = {Hkv // 2} angles")
+    if P1 is not None and out is None:
+        with _on(stream):
+            out = torch.zeros((N, H, D), dtype=dt, device=dev)
     _run_on("relation_paged_append", dev, stream,
             (_ptr(P1), P2.data_ptr(), I.data_ptr(), 0 if P1 is None else _ld(P1), _ld(P2), _ld(I), slot.data_ptr(),
              _ptr(pos), ROPE[rope], float(rope_base), None if theta is None else _host_floats(theta, Hkv // 2),
@@ -635,13 +653,16 @@ def paged_fwd(P1, cache_P2, cache_V, block_table, total, cu, tau, lam: float = 0
         if workspace.numel() < need:
             raise ValueError(f"paged_fwd: workspace holds {workspace.numel()} bytes, {need} needed")
         specs.append(("workspace", workspace, workspace.shape, torch.uint8, True))
+    max_new = N if max_new is None else _count("max_new", max_new)
     dev = _check_tensors(fn, specs)
-    if out is None:
-        out = torch.zeros((N, H, D), dtype=dt, device=dev)
-    if workspace is None:
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
+    if out is None or workspace is None:
+        with _on(stream):
+            if out is None:
+                out = torch.zeros((N, H, D), dtype=dt, device=dev)
+            if workspace is None:
+                workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
     _run_on("relation_paged_fwd", dev, stream,
             (P1.data_ptr(), _ld(P1), cache_P2.data_ptr(), cache_V.data_ptr(), block_table.data_ptr(), total.data_ptr(),
              cu.data_ptr(), _host_floats(tau, H), float(lam), out.data_ptr(), N, S, H, Hkv, D, n_pages, ps, width,
-             N if max_new is None else int(max_new), _dtype_code(P1), workspace.data_ptr(), workspace.numel()))
+             max_new, _dtype_code(P1), workspace.data_ptr(), workspace.numel()))
     return out

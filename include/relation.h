@@ -371,7 +371,8 @@ rel_status relation_cache_append(void* cache_P2, void* cache_V, int32_t* len,
  * are padding). The H query heads form groups of H / H_kv consecutive heads that
  * share one cached head (query head h reads cached head h / (H / H_kv)).
  * One serving step: relation_page_map, relation_paged_append, relation_paged_fwd.
- * Limits: S <= 65535; N * H, n_pages * page_size and max_pages * page_size < 2^31.
+ * Limits: S <= 65535; N * H < 2^31; n_pages * page_size and max_pages * page_size
+ * at most 2^31 - 65536.
  * A request whose device-side numbers are not valid is skipped as each call
  * describes, and a page number outside [0, n_pages) is never followed: its rows
  * read as zeros and are not written. Slots must be distinct: of tokens that
@@ -427,7 +428,8 @@ rel_status relation_page_map(const int32_t* len, const int32_t* n_new,
  *   ld1, ld2, ldi : elements between consecutive tokens of P1, P2, I (a token's
  *                 heads are contiguous), a multiple of 16 bytes, at least
  *                 heads * d_h: slices of one fused projection go in as they are
- *   slot, pos   : in,  device int32[N]; pos may be NULL for REL_ROPE_NONE
+ *   slot, pos   : in,  device int32[N]; pos may be NULL for REL_ROPE_NONE. Of
+ *                 tokens with the same slot either's values may stay
  *   rope, rope_base, theta, pairing : as in relation_prestep, theta (host, may
  *                 be NULL) with H_kv / 2 angles for the H_kv information heads
  *   P1o         : out, device contiguous [N, H, d_h]; may be P1 if ld1 = H * d_h
@@ -466,7 +468,7 @@ size_t relation_paged_workspace_bytes(int N, int S, int H, int H_kv, int d_h);
  *                 (a multiple of 16 bytes, at least H * d_h)
  *   total       : in,  device int32[S], cached rows per request, the new ones
  *                 included (relation_page_map's)
- *   cu          : in,  device int32[S+1]
+ *   cu          : in,  device int32[S+1], not decreasing
  *   max_new     : no request has more new tokens (1 for a decode step)
  *   tau_s, lambda : as in relation_fwd_ex, tau_s host float[H]
  *   Y           : out, device contiguous [N, H, d_h]
@@ -477,7 +479,10 @@ size_t relation_paged_workspace_bytes(int N, int S, int H, int H_kv, int d_h);
  * Rows at or past total[b] may hold anything and are not used; a row that is
  * used may not hold NaN or infinities (they reach other rows of its request,
  * never another request's).
- * Numerics: as relation_fwd_ex; the same call gives the same bits.
+ * Numerics: as the output of relation_fwd_lse (evidence scaled in fp32, in bf16
+ * one rounding of the weights for the transport), but that where several rows
+ * share a tile the row sum may be of the rounded weights; the same call gives the
+ * same bits.
  */
 rel_status relation_paged_fwd(const void* P1, int64_t ld1, const void* cache_P2,
                               const void* cache_V, const int32_t* block_table,

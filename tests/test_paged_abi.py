@@ -96,6 +96,7 @@ def fwd(**kw):
     (dict(Hkv=0), E_SHAPE), (dict(max_new=0), E_SHAPE), (dict(Hkv=3), E_GROUP), (dict(Hkv=16), E_GROUP), (dict(dt=-1), E_DTYPE),
     (dict(d=16), E_HEADDIM), (dict(page=20), E_PAGE), (dict(n_pages=0), E_PAGE), (dict(max_pages=0), E_PAGE),
     (dict(max_pages=1 << 28), E_PAGE), (dict(n_pages=1 << 26, page=256), E_PAGE),
+    (dict(max_pages=(1 << 27) - 4095), E_PAGE), (dict(n_pages=(1 << 23) - 255, page=256), E_PAGE),
     (dict(tau=(1.0,) * 7 + (0.0,)), E_TAU), (dict(tau=(float("nan"),) * 8), E_TAU), (dict(lam=float("inf")), E_LAMBDA),
     (dict(ld1=504), E_STRIDE), (dict(ld1=514), E_STRIDE), (dict(ws=None), E_WS), (dict(nb=0), E_WS),
     (dict(P1=at(0) + 4), E_ALIGN), (dict(Y=at(6) + 8), E_ALIGN), (dict(ws=at(7) + 4), E_ALIGN), (dict(table=at(3) + 2), E_ALIGN),
@@ -167,6 +168,8 @@ def b_fwd(**kw):
     (b_fwd(P1=z(7, 8, 32)), ValueError, "P1 has shape"), (b_fwd(cache_V=z(20, 2, 16, 64, dtype=torch.float32)), TypeError, "cache_V has dtype"),
     (b_fwd(out=z(7, 8, 63)), ValueError, "out has shape"), (b_fwd(workspace=z(4, dtype=torch.uint8)), ValueError, "workspace holds"),
     (b_fwd(cu=z(4, dtype=torch.int64)), TypeError, "cu has dtype"), (b_fwd(), ValueError, "device tensor"),
+    (b_map(N=2**32 + 7), ValueError, "32 bits"), (b_map(page_size=2**32 + 16), ValueError, "32 bits"),
+    (b_map(n_pages=2**31), ValueError, "32 bits"), (b_fwd(max_new=2**32 + 1), ValueError, "32 bits"),
 ])
 def test_binding_checks(call, exc, words):
     with pytest.raises(exc, match=words):

@@ -133,6 +133,18 @@ def test_paged_append(dt, N, H, Hkv, d, page, rope, mix, pairing, fused):
         assert np.all(P.f64(c).transpose(0, 2, 1, 3)[rest] == 5.0)
 
 
+def test_paged_append_of_more_tokens_than_one_launch_takes():
+    N = (1 << 23) + 5
+    n_pages = -(-N // 256)
+    x = torch.randn((N, 2, 32), device=DEV).to(torch.bfloat16)
+    slot = torch.arange(N - 1, -1, -1, dtype=torch.int32, device=DEV)
+    c = [torch.zeros((n_pages, 1, 256, 32), dtype=torch.bfloat16, device=DEV) for _ in range(2)]
+    R.paged_append(x[:, :1], x[:, 1:], slot, *c)
+    torch.cuda.synchronize()
+    for k in range(2):
+        assert torch.equal(c[k].view(-1, 32)[:N].flip(0), x[:, k])
+
+
 @pytest.mark.parametrize("dt,N,H,d,rope,pairing", [("bf16", 50, 4, 128, "half", "A"), ("f32", 21, 6, 48, "interleaved", "B"),
                                                    ("bf16", 9, 2, 80, "interleaved", "A"), ("f32", 64, 8, 64, "half", "B")])
 def test_paged_append_equals_prestep(dt, N, H, d, rope, pairing):
@@ -522,6 +534,32 @@ def test_paged_calls_replay_in_a_graph():
         torch.cuda.synchronize()
         for k, (a, b) in enumerate(zip(got, want)):
             assert torch.equal(a, b), k
+
+
+def test_paged_calls_allocate_on_the_stream_they_are_given():
+    """What a call allocates for a stream other than the current one is not taken by the current one's next tensors."""
+    m = P.make("bf16", 8, 2, 128, 16, [(20000, 1), (300, 9), (0, 400)], seed=1, pad_rows=3)
+    want = run_fwd(m, 0.5, None, fill=0.0)
+    d = P.to_device(m)
+    n = R.paged_workspace_bytes(m["N"], 3, 8, 2, 128)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(3):
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(20_000_000)
+        y = R.paged_fwd(d["P1"], d["cP2"], d["cV"], d["table"], d["total"], d["cu"], m["tau"], 0.5, max_new=m["max_new"],
+                        stream=side)
+        others = [torch.zeros(n, dtype=torch.uint8, device=DEV), torch.ones_like(y)]
+        torch.cuda.synchronize()
+        assert torch.equal(y, want) and float(others[1].min()) == 1.0
+        x = torch.randn((m["N"], 4, 128), device=DEV, dtype=torch.bfloat16)
+        slot, c = i32(np.arange(m["N"])), [torch.zeros_like(d["cP2"]) for _ in range(2)]
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(20_000_000)
+        q = R.paged_append(x[:, :2], x[:, 2:], slot, *c, P1=x, stream=side)
+        torch.cuda.synchronize()
+        assert torch.equal(q, x)
 
 
 def test_paged_calls_on_two_streams():
