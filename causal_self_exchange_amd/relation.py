@@ -486,8 +486,9 @@ def _check_tensors(fn, specs):
     dev = specs[0][1].device
     if dev.type != "cuda":
         raise ValueError(f"{fn}: {specs[0][0]} must be a device tensor")
+    index = specs[0][1].get_device()
     for name, t, _, _, dense in specs:
-        if t.device != dev:
+        if t.get_device() != index:           # -1 on the CPU; cheaper than comparing devices
             raise ValueError(f"{fn}: {name} is on {t.device}, the inputs on {dev}")
         if dense and not t.is_contiguous():
             raise ValueError(f"{fn}: {name} must be contiguous")
