@@ -475,21 +475,24 @@ struct ChunkSource {
 
 // ---- rows ---------------------------------------------------------------------
 
+// Eight elements as they lie in memory.
 template <typename Tin>
-__device__ __forceinline__ void load8(const Tin* p, float (&x)[8]) {
-  if constexpr (sizeof(Tin) == 2) {
-    const bf16x8 v = *reinterpret_cast<const bf16x8*>(p);
+struct Raw8 {
+  static constexpr int kWords = sizeof(Tin) / 2;
+  u32x4 w[kWords];
+  __device__ __forceinline__ void zero() {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = (float)v[e];
-  } else {
-    const f32x4 v = reinterpret_cast<const f32x4*>(p)[0], w = reinterpret_cast<const f32x4*>(p)[1];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      x[e] = v[e];
-      x[4 + e] = w[e];
-    }
+    for (int i = 0; i < kWords; ++i) w[i] = u32x4{0u, 0u, 0u, 0u};
   }
-}
+  __device__ __forceinline__ void load(const Tin* p) {
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) w[i] = reinterpret_cast<const u32x4*>(p)[i];
+  }
+  __device__ __forceinline__ float operator[](int e) const {
+    if constexpr (sizeof(Tin) == 2) return (float)__builtin_bit_cast(bf16x8, w[0])[e];
+    else return __builtin_bit_cast(f32x4, w[e >> 2])[e & 3];
+  }
+};
 
 template <typename Tin>
 __device__ __forceinline__ void store8(Tin* p, const float (&x)[8]) {
@@ -502,40 +505,46 @@ __device__ __forceinline__ void store8(Tin* p, const float (&x)[8]) {
   }
 }
 
+// A row's own P1, P2 and V (zeros where it has none), by 16 lanes of 8 columns
+// each: loaded ahead of finish_row, behind whose table lookup they would wait.
+template <typename Tin, int D>
+struct OwnRow {
+  Raw8<Tin> q, k, v;
+  __device__ __forceinline__ void load(const PagedArgs& a, int b, int t, int h, int pos, int sl, bool row_ok) {
+    q.zero();
+    k.zero();
+    v.zero();
+    if (!row_ok || sl >= D / 8) return;
+    const int page = a.table[(size_t)b * a.max_pages + (pos >> a.page_shift)];
+    q.load(static_cast<const Tin*>(a.P1) + (size_t)t * a.ld1 + (size_t)h * D + 8 * sl);
+    if (page >= 0 && page < a.n_pages) {
+      const int kvh = h / (a.H / a.H_kv);
+      const size_t row =
+          ((((size_t)page * a.H_kv + kvh) << a.page_shift) + (pos & ((1 << a.page_shift) - 1))) * D + 8 * sl;
+      k.load(static_cast<const Tin*>(a.cP2) + row);
+      v.load(static_cast<const Tin*>(a.cV) + row);
+    }
+  }
+};
+
 // Output of one row from its history's state, by 16 lanes of 8 columns each:
 // z (sum of weights times V), m (log2 stabiliser) and l (sum of weights); the
 // Self evidence and V come from the row's own cached row.
 template <typename Tin, int D>
-__device__ __forceinline__ void finish_row(const PagedArgs& a, const HeadParams& hp, int b, int t, int h, int pos,
-                                           int sl, float m, float l, const float (&z)[8], bool row_ok) {
-  const bool live = row_ok && sl < D / 8;
-  const int col = live ? 8 * sl : 0;
-  const int kvh = h / (a.H / a.H_kv);
-  float q[8], k[8], v[8];
-#pragma unroll
-  for (int e = 0; e < 8; ++e) q[e] = k[e] = v[e] = 0.0f;
-  if (live) {
-    load8(static_cast<const Tin*>(a.P1) + (size_t)t * a.ld1 + (size_t)h * D + col, q);
-    const int page = a.table[(size_t)b * a.max_pages + (pos >> a.page_shift)];
-    if (page >= 0 && page < a.n_pages) {
-      const size_t row =
-          ((((size_t)page * a.H_kv + kvh) << a.page_shift) + (pos & ((1 << a.page_shift) - 1))) * D + col;
-      load8(static_cast<const Tin*>(a.cP2) + row, k);
-      load8(static_cast<const Tin*>(a.cV) + row, v);
-    }
-  }
+__device__ __forceinline__ void finish_row(const PagedArgs& a, const HeadParams& hp, const OwnRow<Tin, D>& own, int t,
+                                           int h, int pos, int sl, float m, float l, const float (&z)[8], bool row_ok) {
   float u = 0.0f;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) u = fmaf(q[e], k[e], u);
+  for (int e = 0; e < 8; ++e) u = fmaf(own.q[e], own.k[e], u);
 #pragma unroll
   for (int o = 8; o > 0; o >>= 1) u += __shfl_xor(u, o, 16);
-  if (!live) return;
+  if (!row_ok || sl >= D / 8) return;
   const float S = sigmoid_f32(u * hp.scale * hp.inv_tau[h]);
   const RowCombine c(S, m * kLn2, l, hp.lambda * logf((float)(pos + 1)));
   float y[8];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) y[e] = c.w_self * v[e] + c.w_hist * z[e];
-  store8(static_cast<Tin*>(a.Y) + ((size_t)t * a.H + h) * D + col, y);
+  for (int e = 0; e < 8; ++e) y[e] = c.w_self * own.v[e] + c.w_hist * z[e];
+  store8(static_cast<Tin*>(a.Y) + ((size_t)t * a.H + h) * D + 8 * sl, y);
 }
 
 // The state (m, l, zp) joined to (M, L, z).

@@ -388,6 +388,15 @@ __global__ __launch_bounds__(kThreads, (Geom<Tin, D, NB>::kPerCu)) void scan_ker
 #pragma unroll
       for (int w = 1; w < kWaves; ++w) M = fmaxf(M, s_m[w][li]);
       const float f = __builtin_amdgcn_exp2f(m2[nb] - M);
+      const int rr = tid >> 4, sl = tid & 15;
+      const int row = row0 + 16 * nb + rr;
+      const bool ok = 16 * nb + rr < rows;
+      const int tq = ok ? row / G : 0;
+      const int h = kvh * G + (ok ? row - tq * G : 0);
+      // The row's own entries, while the states meet (fp32: behind it, where the
+      // registers that it takes are free).
+      OwnRow<Tin, D> own;
+      if (kBf && cur.slot < 0) own.load(a, b, cur.first_tok + tq, h, ctx + tq, sl, ok);
       f32x4 share[C::kDb];
 #pragma unroll
       for (int db = 0; db < C::kDb; ++db)
@@ -403,9 +412,6 @@ __global__ __launch_bounds__(kThreads, (Geom<Tin, D, NB>::kPerCu)) void scan_ker
         }
         lds_barrier();
       }
-      const int rr = tid >> 4, sl = tid & 15;
-      const int row = row0 + 16 * nb + rr;
-      const bool ok = 16 * nb + rr < rows;
       float L = 0.0f, zs[8];
       M = s_m[0][rr];
 #pragma unroll
@@ -422,10 +428,9 @@ __global__ __launch_bounds__(kThreads, (Geom<Tin, D, NB>::kPerCu)) void scan_ker
         }
       }
       lds_barrier();                                // read before the next rows' states
-      const int tq = ok ? row / G : 0;
-      const int h = kvh * G + (ok ? row - tq * G : 0);
       if (cur.slot < 0) {
-        finish_row<Tin, D>(a, hp, b, cur.first_tok + tq, h, ctx + tq, sl, M, L, zs, ok);
+        if (!kBf) own.load(a, b, cur.first_tok + tq, h, ctx + tq, sl, ok);
+        finish_row<Tin, D>(a, hp, own, cur.first_tok + tq, h, ctx + tq, sl, M, L, zs, ok);
       } else if (ok) {
         const int64_t p = (int64_t)cur.slot * kRb + 16 * nb + rr;
         if (sl == 0) states.ml[p] = make_float2(M, L);
@@ -470,6 +475,8 @@ __device__ __forceinline__ void join_rows(const PagedArgs& a, const HeadParams& 
   const int tq = tile ? c.row0 + 32 * (block - x * c.blocks) + (i & 31) - c.ctx : (c.row0 + i) / G;
   const int h = tile ? c.head + x : c.head * G + (c.row0 + i) - tq * G;
   const bool ok = i < c.rows && tq >= 0 && c.ctx + tq < c.total && x < G;
+  OwnRow<Tin, D> own;
+  own.load(a, c.b, c.first + tq, h, c.ctx + tq, sl, ok && from == 0);
   float M = kEmptyMax, L = 0.0f, z[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) z[e] = 0.0f;
@@ -506,7 +513,7 @@ __device__ __forceinline__ void join_rows(const PagedArgs& a, const HeadParams& 
       merge(M, L, z, s[0], s[1], zo);
     }
   }
-  finish_row<Tin, D>(a, hp, c.b, ok ? c.first + tq : 0, ok ? h : 0, ok ? c.ctx + tq : 0, sl, M, L, z, ok && from == 0);
+  finish_row<Tin, D>(a, hp, own, c.first + tq, h, c.ctx + tq, sl, M, L, z, ok && from == 0);
 }
 
 // The first scan_groups * row_block / 16 work-groups join the scan's row blocks,
