@@ -22,7 +22,8 @@ using namespace paged;
 template <int D, int DR>
 __global__ __launch_bounds__(kThreads, 1) void paged_chunk_kernel(PagedArgs a, HeadParams hp) {
   __shared__ PlanLds lds;
-  const Plan plan = load_plan(a, 0, true, lds);
+  bool chunks = true;
+  const Plan plan = load_plan(a, 0, chunks, lds);
   const FwdArgs none{};
   const RopeParams no_rope{};
   fwd_body<D, DR, true, false, true>(none, hp, no_rope, a, plan);

@@ -45,6 +45,15 @@ constexpr int kMinRange = 4;
 constexpr int kMinRangeF32 = 1;
 constexpr int kMinRangeChunk = 4;
 
+// The least work on query tiles, in units of the scan (32 rows by 128 keys, kExtra
+// more a row block): a batch with less leaves it to the scan, whose fixed costs are
+// 15 us lower, while the tiles are up to 1.4 times as fast. 32 heads of 128 in 8,
+// scan and tiles: a prompt of 300 tokens (1,800 units) 26 and 33 us, 16 chunks of 32
+// tokens over 1000 rows (5,600) 37 and 57, 64 of 32 over 100 (8,200) 59 and 43, a prompt
+// of 1024 (10,200) 55 and 46, 8 chunks of 127 over 2000 (19,500) 83 and 97, 32 of 32 over
+// 4000 (34,800) 171 and 134.
+constexpr int kChunkWork = 8000;
+
 // Query tiles of a request's new tokens (chunk kernel): 256 rows, 32 for each of 8 waves.
 //   Full tiles: 256 positions of one head, from ctx rounded down to a multiple of
 //   64 (64-key tiles then never straddle a tile's first position, and its own keys
@@ -55,9 +64,7 @@ constexpr int kMinRangeChunk = 4;
 //   one, leaves few waves idle. Where the tiles would hold fewer than kChunkRows
 //   rows each, two row blocks of the scan kernel, which read the keys together, are
 //   faster: the tokens left (rest) go there. 32 chunks over 4000 rows, 8 cached
-//   heads: 64 rows 110 us by the scan, 128 on tiles; 80 rows 200 and 131. (A batch
-//   too small to fill the card would do better with the scan up to 128 rows: 8 such
-//   chunks of 80 rows over 1000, 26 us and 39.)
+//   heads: 64 rows 110 us by the scan, 128 on tiles; 80 rows 200 and 131.
 struct ChunkTiles {
   int base64, full;            // first position / 64, full tiles
   int start, blocks, tiles, keys;   // shared tiles: first position, blocks of a head, per cached head, key tiles each
@@ -126,12 +133,31 @@ struct ScanRows {
 
 struct PlanScratch { long long red[4][2]; };
 
+// What a request's rows on query tiles would be in the scan.
+__device__ __forceinline__ long long tile_work(const PagedArgs& a, const Req& r) {
+  if (r.q == 0) return 0;
+  Req t = r;
+  t.q -= ChunkTiles(r.total - r.q, r.total, a.H / a.H_kv).rest;
+  const ScanRows n(a, t, 32);
+  return (long long)n.blocks * a.H_kv * (n.units + kExtra);
+}
+
 // Fills the sums whose arrays p has, by the work-group's first 256 threads; every
 // thread calls. row_block: rows per scan item; chunks: whether the chunk kernel
-// runs.
-__device__ __forceinline__ void make_plan(const PagedArgs& a, int row_block, bool chunks, PlanScratch& sc, const Plan& p) {
+// is launched. Returns whether there is work for it.
+__device__ __forceinline__ bool make_plan(const PagedArgs& a, int row_block, bool chunks, PlanScratch& sc, const Plan& p) {
   const int G = a.H / a.H_kv;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  if (chunks) {
+    long long work = 0;
+    for (int b = tid; b < a.S && tid < 256; b += 256) work += tile_work(a, Req(a, b));
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) work += __shfl_xor(work, o, 64);
+    if (lane == 0 && wave < 4) sc.red[wave][0] = work;
+    __syncthreads();
+    chunks = sc.red[0][0] + sc.red[1][0] + sc.red[2][0] + sc.red[3][0] >= kChunkWork;
+    __syncthreads();
+  }
   long long done[2] = {0, 0};
   for (int b0 = 0; b0 < a.S; b0 += 256) {
     const int b = b0 + tid;
@@ -146,7 +172,7 @@ __device__ __forceinline__ void make_plan(const PagedArgs& a, int row_block, boo
         const ScanRows n(a, s, row_block);
         own[0] = (long long)n.blocks * a.H_kv * (n.units + kExtra);
       }
-      if (p.tile_sum && r.q > 0) own[1] = ChunkTiles(r.total - r.q, r.total, G).units(a.H, a.H_kv);
+      if (p.tile_sum && chunks && r.q > 0) own[1] = ChunkTiles(r.total - r.q, r.total, G).units(a.H, a.H_kv);
     }
     long long x[2] = {own[0], own[1]};
 #pragma unroll
@@ -181,6 +207,7 @@ __device__ __forceinline__ void make_plan(const PagedArgs& a, int row_block, boo
     if (p.unit_sum) p.unit_sum[a.S] = done[0];
     if (p.tile_sum) p.tile_sum[a.S] = done[1];
   }
+  return chunks;
 }
 
 // The sums that plan_kernel left in the workspace (more than kPlanInline requests).
@@ -191,16 +218,21 @@ __device__ __forceinline__ Plan ws_plan(const PagedArgs& a) {
 
 // A kernel's sums: formed in LDS by each work-group for up to kPlanInline
 // requests (a launch of its own and the wait for it take 5 us), else read from
-// the workspace.
+// the workspace. chunks: in, whether the chunk kernel is launched; out, whether there
+// is work for it.
 struct PlanLds {
   PlanScratch sc;
   long long sum[kPlanInline + 1];
   Req part[kPlanInline];
 };
-__device__ __forceinline__ Plan load_plan(const PagedArgs& a, int row_block, bool chunks, PlanLds& lds) {
-  if (a.S > kPlanInline) return ws_plan(a);
+__device__ __forceinline__ Plan load_plan(const PagedArgs& a, int row_block, bool& chunks, PlanLds& lds) {
+  if (a.S > kPlanInline) {
+    const Plan w = ws_plan(a);
+    chunks = chunks && w.tile_sum[a.S] > 0;
+    return w;
+  }
   const Plan p = row_block > 0 ? Plan{lds.sum, nullptr, lds.part} : Plan{nullptr, lds.sum, lds.part};
-  make_plan(a, row_block, chunks, lds.sc, p);
+  chunks = make_plan(a, row_block, chunks, lds.sc, p);
   __syncthreads();
   return p;
 }

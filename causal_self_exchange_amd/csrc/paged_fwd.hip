@@ -97,7 +97,7 @@ struct Geom {
 };
 
 template <typename Tin, int D, int NB>
-__global__ __launch_bounds__(kThreads, (Geom<Tin, D, NB>::kPerCu)) void scan_kernel(PagedArgs a, HeadParams hp, int chunks) {
+__global__ __launch_bounds__(kThreads, (Geom<Tin, D, NB>::kPerCu)) void scan_kernel(PagedArgs a, HeadParams hp, int with_chunks) {
   using C = Geom<Tin, D, NB>;
   constexpr bool kBf = C::kBf;
   constexpr int kRb = 16 * NB;
@@ -107,7 +107,8 @@ __global__ __launch_bounds__(kThreads, (Geom<Tin, D, NB>::kPerCu)) void scan_ker
   __shared__ float s_m[kWaves][16], s_l[kWaves][16];
   __shared__ PlanLds lds;
 
-  const Plan plan = load_plan(a, kRb, chunks != 0, lds);
+  bool chunks = with_chunks != 0;
+  const Plan plan = load_plan(a, kRb, chunks, lds);
   const States states = States::scan(a);
   const int G = a.H / a.H_kv;
   const int tid = threadIdx.x;
@@ -132,7 +133,7 @@ __global__ __launch_bounds__(kThreads, (Geom<Tin, D, NB>::kPerCu)) void scan_ker
     int b, kvh, first_tok, ctx, total, row0, rows, slot, first, nsteps;
     bool any;
   };
-  ScanSource source(a, plan, kRb, chunks != 0, kBf ? kMinRange : kMinRangeF32);
+  ScanSource source(a, plan, kRb, chunks, kBf ? kMinRange : kMinRangeF32);
   auto next_run = [&]() __attribute__((always_inline)) -> Run {
     const ScanSegment sg = source.next();
     const int k0 = uni(sg.k0), k1 = uni(sg.k1);

@@ -179,17 +179,31 @@ def run_fwd(m, lam, dt, ws=None, fill=3.0, max_new=None):
     return Y
 
 
-def check_fwd(m, lam, dt, du=1e-6, fill=3.0, max_new=None):
+def check_fwd(m, lam, dt, du=1e-6, fill=3.0, max_new=None, skip=None):
+    """Y against the plain evaluation, but for the rows of request skip."""
     Y = run_fwd(m, lam, dt, fill=fill, max_new=max_new)
     y0 = np.full(tuple(m["P1"].shape), fill)
+    total, cu = m["total"].numpy().copy(), m["cu"].numpy()
+    if skip is not None:
+        total[skip] = -1
     ref, spread = PO.paged_fwd(P.f64(m["P1"]), np.nan_to_num(P.f64(m["cP2"])), np.nan_to_num(P.f64(m["cV"])),
-                               m["table"].numpy(), m["total"].numpy(), m["cu"].numpy(), m["tau"], lam, y0,
+                               m["table"].numpy(), total, cu, m["tau"], lam, y0,
                                m["max_new"] if max_new is None else max_new, with_spread=True)
     err = np.abs(P.f64(Y) - ref)
+    if skip is not None:
+        rows = slice(cu[skip], cu[skip + 1])
+        assert np.all(np.isfinite(err[rows])) and np.any(err[rows] > 0)
+        err[rows] = 0.0
     lim = np.where(spread > 0, P.bound(ref, spread, dt, du), 0.0)      # rows nobody writes stay exactly
     worst = np.unravel_index(np.argmax(err - lim), err.shape)
     assert np.all(err <= lim), (worst, err[worst], lim[worst], float(np.max(err / (lim + 1e-30))))
     return Y
+
+
+def filler(H):
+    """A request with enough work to put the batch's chunks on query tiles (8,000 units of 32 rows by 128 keys, two more a
+    row block): 75 row blocks and more over 16,000 rows. Its own rows are not looked at (check_fwd's skip)."""
+    return (16000, 75 * 32 // H + 1)
 
 
 DECODE = [(0, 1), (1, 1), (15, 1), (16, 1), (17, 1), (31, 1), (63, 1), (64, 1), (65, 1), (255, 1), (700, 1)]
@@ -232,8 +246,11 @@ def test_paged_fwd_long_history(dt, d):
     (32, 128, 3, 3, [(10, 1500)]), (128, 32, 16, 4, [(129, 190), (2, 5), (500, 140), (0, 127)]),
 ])
 def test_paged_fwd_long_chunks(d, page, H, Hkv, reqs):
-    """Chunks of 128 tokens and more, at and around the tile sizes, mixed with short ones; few and many pieces per tile."""
+    """Chunks of 128 tokens and more, at and around the tile sizes, mixed with short ones; few and many pieces per tile.
+    Alone (in the scan), and next to as much work as puts them on tiles."""
     check_fwd(P.make("bf16", H, Hkv, d, page, reqs, seed=d + H, stride_pad=8, pad_rows=2), 0.5, "bf16")
+    check_fwd(P.make("bf16", H, Hkv, d, page, reqs + [filler(H)], seed=d + H, stride_pad=8, pad_rows=2), 0.5, "bf16",
+              skip=len(reqs))
 
 
 @pytest.mark.parametrize("d,page,H,Hkv,reqs", [
@@ -249,6 +266,8 @@ def test_paged_fwd_long_chunks(d, page, H, Hkv, reqs):
 ])
 def test_paged_fwd_shared_tiles(d, page, H, Hkv, reqs):
     check_fwd(P.make("bf16", H, Hkv, d, page, reqs, seed=d + H, stride_pad=24, pad_rows=1), 0.5, "bf16")
+    check_fwd(P.make("bf16", H, Hkv, d, page, [filler(H)] + reqs, seed=d + H, stride_pad=24, pad_rows=1), 0.5, "bf16",
+              skip=0)
 
 
 @pytest.mark.parametrize("dt,S,H,Hkv,d,ctx_hi,new_hi,every", [
@@ -262,9 +281,11 @@ def test_paged_fwd_many_requests(dt, S, H, Hkv, d, ctx_hi, new_hi, every):
     for b in range(every // 2, S, every or S):
         if every:
             reqs[b] = (reqs[b][0], 150 + b)
+    if every:
+        reqs[S // 2] = filler(H)
     m = P.make(dt, H, Hkv, d, 16, reqs, seed=S, pad_rows=2)
     m["total"][S // 3] = -1
-    check_fwd(m, 0.5, dt)
+    check_fwd(m, 0.5, dt, skip=S // 2 if every else None)
 
 
 @pytest.mark.parametrize("dt,H,Hkv,d,reqs", [
