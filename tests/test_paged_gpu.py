@@ -410,7 +410,8 @@ def test_paged_fwd_equals_one_pass_rows(dt):
 def test_paged_fwd_same_call_same_bits_and_shared_workspace():
     """Calls of different shapes on one stream through one workspace, twice each."""
     ms = [P.make("bf16", 8, 2, 128, 16, [(9000, 1), (300, 1), (5000, 4)], seed=1),
-          P.make("bf16", 8, 8, 64, 16, CHUNKS, seed=2), P.make("f32", 4, 1, 48, 32, RAGGED, seed=3)]
+          P.make("bf16", 8, 8, 64, 16, CHUNKS, seed=2), P.make("f32", 4, 1, 48, 32, RAGGED, seed=3),
+          P.make("bf16", 8, 2, 128, 32, CHUNKS + [filler(8)], seed=4)]
     need = max(R.paged_workspace_bytes(m["N"], len(m["total"]), m["P1"].shape[1], m["cP2"].shape[1], m["P1"].shape[2])
                for m in ms)
     ws = torch.full((need,), 255, dtype=torch.uint8, device=DEV)
@@ -500,17 +501,26 @@ def test_serving_loop(dt, tol):
     assert sorted(used + rest) == list(range(40))
 
 
-def test_paged_calls_replay_in_a_graph():
+@pytest.mark.parametrize("N,H,page,width,steps", [
+    (700, 8, 16, 60, (([0] * 6, [300, 1, 0, 30, 2, 129]), ([300, 0, 16, 800, 2, 129], [1] * 6),
+                      ([301, 5, 0, 1, 3, 700], [40, 1, 300, 1, 1, 1]), ([10, 9, 8, 7, 6, 5], [0] * 6))),
+    # Chunks on query tiles, single tokens, chunks in the scan, tiles again.
+    (1500, 16, 64, 60, (([2300, 0, 0, 0, 0, 0], [1200, 1, 0, 200, 2, 65]), ([3500, 1, 16, 800, 2, 129], [1] * 6),
+                        ([301, 5, 0, 1, 3, 700], [40, 1, 300, 1, 1, 1]), ([2048, 9, 832, 7, 6, 5], [1000, 0, 400, 0, 0, 0]))),
+])
+def test_paged_calls_replay_in_a_graph(N, H, page, width, steps):
     """The three calls captured once and replayed with new lengths and inputs, against the eager calls. The captured
-    call's max_new covers every replay, and the batch is padded to its capacity."""
-    S, N, H, Hkv, d, page, n_pages = 6, 700, 8, 2, 64, 16, 200
+    call's max_new covers every replay, and the batch is padded to its capacity. Tables and free list name the same
+    pages; no step gives two tokens one slot (lengths of 2000 and 800 in the last one would, 48 of 1400: whose values
+    stay is then open, and eager and replay differ)."""
+    S, Hkv, d, n_pages = 6, 2, 64, 200
     rng = np.random.default_rng(2)
     lens, nn = torch.zeros(S, dtype=torch.int32, device=DEV), torch.zeros(S, dtype=torch.int32, device=DEV)
     base = rng.permutation(n_pages)
     x = torch.zeros((N, H + 2 * Hkv, d), dtype=torch.bfloat16, device=DEV)
     state = {}
     for name in ("graph", "eager"):
-        state[name] = dict(table=torch.zeros((S, 60), dtype=torch.int32, device=DEV), free=i32(base), n_free=i32([n_pages]),
+        state[name] = dict(table=torch.zeros((S, width), dtype=torch.int32, device=DEV), free=i32(base), n_free=i32([n_pages]),
                            cP2=torch.zeros((n_pages, Hkv, page, d), dtype=torch.bfloat16, device=DEV),
                            cV=torch.zeros((n_pages, Hkv, page, d), dtype=torch.bfloat16, device=DEV),
                            out=tuple(torch.zeros(k, dtype=torch.int32, device=DEV) for k in (S + 1, S, N, N, 1)),
@@ -535,21 +545,22 @@ def test_paged_calls_replay_in_a_graph():
     with torch.cuda.graph(graph):
         got = work(state["graph"])
     torch.cuda.synchronize()
-    for ln, n in (([0] * 6, [300, 1, 0, 30, 2, 129]), ([300, 0, 16, 800, 2, 129], [1] * 6), ([301, 5, 0, 1, 3, 700], [40, 1, 300, 1, 1, 1]),
-                  ([10, 9, 8, 7, 6, 5], [0] * 6)):
+    for ln, n in steps:
         lens.copy_(i32(ln))
         nn.copy_(i32(n))
         x.copy_(torch.from_numpy(rng.standard_normal(tuple(x.shape))).to(torch.bfloat16))
         for s in state.values():
             s["free"].copy_(i32(base))
             s["Y"].fill_(0.0)
-            s["table"].copy_(i32(np.arange(S * 60).reshape(S, 60) % n_pages))
+            s["table"].copy_(i32(np.arange(S * width).reshape(S, width) % n_pages))
         torch.cuda.synchronize()
         want = [t.clone() for t in work(state["eager"])]
         torch.cuda.synchronize()
+        slots = want[5][want[5] >= 0].cpu().numpy()
+        assert len(np.unique(slots)) == len(slots)
         for s in state.values():
             s["Y"].fill_(0.0)
-            s["table"].copy_(i32(np.arange(S * 60).reshape(S, 60) % n_pages))
+            s["table"].copy_(i32(np.arange(S * width).reshape(S, width) % n_pages))
         torch.cuda.synchronize()
         graph.replay()
         torch.cuda.synchronize()
@@ -583,9 +594,10 @@ def test_paged_calls_allocate_on_the_stream_they_are_given():
         assert torch.equal(q, x)
 
 
-def test_paged_calls_on_two_streams():
-    """Calls on two streams at once, a workspace each, against the same calls one after another."""
-    ms = [P.make("bf16", 8, 2, 128, 16, [(6000, 1), (300, 9), (0, 400)], seed=1), P.make("bf16", 4, 4, 64, 16, CHUNKS, seed=2)]
+def test_paged_calls_on_streams_at_once():
+    """Calls on three streams at once, a workspace each, against the same calls one after another."""
+    ms = [P.make("bf16", 8, 2, 128, 16, [(6000, 1), (300, 9), (0, 400)], seed=1), P.make("bf16", 4, 4, 64, 16, CHUNKS, seed=2),
+          P.make("bf16", 8, 2, 128, 16, CHUNKS + [filler(8)], seed=3)]
     want = [run_fwd(m, 0.5, None) for m in ms]
     ds = [P.to_device(m) for m in ms]
     streams = [torch.cuda.Stream() for _ in ms]
