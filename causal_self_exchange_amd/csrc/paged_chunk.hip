@@ -9,8 +9,8 @@
 // a segment's evidence overflows it, so joining a divided tile is mostly a sum.
 //
 // What bounds it: the weights on VALU next to the MFMA, as in the training forward.
-// 2048 tokens of 32 heads of 128 in 8 cached ones over 30,001 rows: 1198 us with the
-// join, 869 TFLOP/s (MfmaUtil 41%); five prompts of 500 to 6,000 tokens 996 us.
+// 2048 tokens of 32 heads of 128 in 8 cached ones over 30,001 rows: 1175 us with the
+// join, 886 TFLOP/s (MfmaUtil 41%); five prompts of 500 to 6,000 tokens 976 us.
 #include "fwd_body.h"
 
 namespace rel {

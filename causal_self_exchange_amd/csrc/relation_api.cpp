@@ -132,10 +132,11 @@ bool prestep_modes_ok(rel_rope rope, float rope_base, const float* theta, rel_pa
   return true;
 }
 
-// Rotary frequencies and Givens factors of H information heads.
-void fill_prestep_params(rel::PrestepParams& pp, float rope_base, const float* theta, int H, int d_h) {
+// Rotary frequencies (where there is a rotation) and Givens factors of H
+// information heads.
+void fill_prestep_params(rel::PrestepParams& pp, bool rotates, float rope_base, const float* theta, int H, int d_h) {
   for (int k = 0; k < 64; ++k)
-    pp.inv_freq[k] = k < d_h / 2 ? std::pow(static_cast<double>(rope_base), -2.0 * k / d_h) : 0.0;
+    pp.inv_freq[k] = rotates && k < d_h / 2 ? std::pow(static_cast<double>(rope_base), -2.0 * k / d_h) : 0.0;
   for (int k = 0; k < 128; ++k) {
     const bool mixes = theta && k < H / 2;
     const double t = mixes ? static_cast<double>(theta[k]) : 0.0;
@@ -173,7 +174,7 @@ rel_status prestep_setup(rel::PrestepArgs& a, rel::PrestepParams& pp, const void
   }
   a = rel::PrestepArgs{P1, P2, I, pos0, P1o, P2o, Io, B, H, T, d_h, static_cast<int>(rope),
                        pairing == REL_PAIRS_A ? 0 : 1, theta ? 1 : 0};
-  fill_prestep_params(pp, rope_base, theta, H, d_h);
+  fill_prestep_params(pp, true, rope_base, theta, H, d_h);
   return REL_OK;
 }
 
@@ -276,7 +277,7 @@ rel_status relation_paged_append(const void* P1, const void* P2, const void* I, 
   const Range outs[] = {{P1o, P1 ? static_cast<size_t>(N) * H * d_h * es : 0}, {cache_P2, cb}, {cache_V, cb}};
   if (any_alias(ins, outs)) return REL_E_ALIAS;
   rel::PrestepParams pp;
-  fill_prestep_params(pp, rope_base, theta, H_kv, d_h);
+  fill_prestep_params(pp, rope != REL_ROPE_NONE, rope_base, theta, H_kv, d_h);
   const rel::PagedAppendArgs a{P1, P2, I, ld1, ld2, ldi, slot, pos, P1o, cache_P2, cache_V, N, H, H_kv, d_h,
                                n_pages, page_shift_of(page_size), static_cast<int>(rope),
                                pairing == REL_PAIRS_A ? 0 : 1, theta ? 1 : 0};

@@ -470,10 +470,31 @@ def _raw_stream(index: int) -> int:
     return raw(index) if raw is not None else torch.cuda.current_stream(index).cuda_stream
 
 
+def _heads_contiguous(t, shape) -> bool:
+    st = t.stride()
+    return st[2] == 1 and (shape[1] <= 1 or st[1] == shape[2])
+
+
 def _check_tensors(fn, specs):
+    """Shapes, dtypes and token layouts of all tensors, their device and contiguity. dense
+    False: a packed token tensor [N, heads, d_h] whose tokens may be further apart (a slice of
+    a fused projection). Returns the device. One pass where nothing is wrong; what is
+    wrong is told by _refuse."""
+    first = specs[0][1]
+    if isinstance(first, torch.Tensor) and first.is_cuda:
+        index = first.get_device()
+        for _, t, shape, dtype, dense in specs:
+            if not (isinstance(t, torch.Tensor) and t.shape == shape and t.dtype is dtype and t.get_device() == index
+                    and (t.is_contiguous() if dense else _heads_contiguous(t, shape))):
+                break
+        else:
+            return first.device
+    return _refuse(fn, specs)
+
+
+def _refuse(fn, specs):
     """Shapes, dtypes and token layouts of all tensors first, whatever device they
-    are on; then device and contiguity. dense False: a packed token tensor [N, heads, d_h] whose
-    tokens may be further apart (a slice of a fused projection). Returns the device."""
+    are on; then device and contiguity."""
     for name, t, shape, dtype, dense in specs:
         if not isinstance(t, torch.Tensor):
             raise TypeError(f"{fn}: {name} must be a torch.Tensor")
@@ -481,18 +502,17 @@ def _check_tensors(fn, specs):
             raise ValueError(f"{fn}: {name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
         if t.dtype is not dtype:
             raise TypeError(f"{fn}: {name} has dtype {t.dtype}, expected {dtype}")
-        if not dense and (t.stride(2) != 1 or (shape[1] > 1 and t.stride(1) != shape[2])):
+        if not dense and not _heads_contiguous(t, shape):
             raise ValueError(f"{fn}: the heads of each token of {name} must be contiguous")
     dev = specs[0][1].device
     if dev.type != "cuda":
         raise ValueError(f"{fn}: {specs[0][0]} must be a device tensor")
-    index = specs[0][1].get_device()
     for name, t, _, _, dense in specs:
-        if t.get_device() != index:           # -1 on the CPU; cheaper than comparing devices
+        if t.device != dev:
             raise ValueError(f"{fn}: {name} is on {t.device}, the inputs on {dev}")
         if dense and not t.is_contiguous():
             raise ValueError(f"{fn}: {name} must be contiguous")
-    return dev
+    raise AssertionError(fn)
 
 
 def _run_on(fn, dev, stream, args):
@@ -528,6 +548,8 @@ def _host_floats(x, n: int):
     """Host float[n] from a float or n of them."""
     if isinstance(x, (list, tuple)) and len(x) == n:
         return (ctypes.c_float * n)(*x)
+    if isinstance(x, float):
+        return (ctypes.c_float * n)(*([x] * n))
     arr = np.ascontiguousarray(np.broadcast_to(np.asarray(x, dtype=np.float32), (n,)))
     return (ctypes.c_float * n).from_buffer_copy(arr)
 
