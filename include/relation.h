@@ -447,7 +447,8 @@ rel_status relation_paged_append(const void* P1, const void* P2, const void* I,
 
 /*
  * relation_paged_workspace_bytes - device workspace relation_paged_fwd needs
- * (the work plan and the partial states of split histories). 0 on invalid
+ * (the work plan and the partial states of split histories): about 132 KB times
+ * d_h, and 528 KB times d_h more where N * min(H / H_kv, 8) > 64. 0 on invalid
  * sizes. Calls that may run at the same time need a workspace each, calls on
  * one stream may share one; nothing is kept in it between calls.
  */
