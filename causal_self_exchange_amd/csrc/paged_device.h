@@ -33,14 +33,22 @@ struct Req {
   }
 };
 
-// The cut of the work (below): keys of a scan unit, units that a segment costs
-// beside its keys, the least that a cut leaves, units of the shortest range of the
-// scan (fp32 products take 8 times as long per key: six chunks of up to 97 tokens
-// of 8 heads of 48, 27 us at 1 and 34 at 4; in bf16 single tokens lose 1 us at 1)
-// and of the chunks (a prompt of 300 tokens of 32 heads 45 us at 8, 33 at 4).
+// The cut of the work (below):
+//   kScanUnit   keys of a unit of the scan.
+//   kExtra      units that a segment costs beside its keys, in the scan.
+//   kChunkExtra the same in the chunks: five prompts of 500 to 6,000 tokens 1000 us at
+//               2, 981 at 4, 1004 at 10.
+//   kSnap       the least units that a cut leaves; in fp32, where a unit takes longer,
+//               1: four chunks of 16 tokens over 1000 rows 24.5 us at 2, 21.9 at 1.
+//   kMinRange   units of the scan's shortest range (single tokens lose 1 us at 1); in
+//               fp32 1: six chunks of up to 97 tokens of 8 heads of 48 34 us at 4, 27 at 1.
+//   kMinRangeChunk the same of the chunks: a prompt of 300 tokens of 32 heads 45 us at
+//               8, 33 at 4.
 constexpr int kScanUnit = 128;
 constexpr int kExtra = 2;
+constexpr int kChunkExtra = 4;
 constexpr int kSnap = 2;
+constexpr int kSnapF32 = 1;
 constexpr int kMinRange = 4;
 constexpr int kMinRangeF32 = 1;
 constexpr int kMinRangeChunk = 4;
@@ -82,10 +90,10 @@ struct ChunkTiles {
   }
   // Key tiles and set-ups of the full tiles before k.
   __device__ __forceinline__ long long before(int k) const {
-    return (long long)k * (base64 + kExtra) + 2LL * k * (k + 1);
+    return (long long)k * (base64 + kChunkExtra) + 2LL * k * (k + 1);
   }
   __device__ __forceinline__ long long units(int H, int H_kv) const {
-    return before(full) * H + (long long)tiles * H_kv * (keys + kExtra);
+    return before(full) * H + (long long)tiles * H_kv * (keys + kChunkExtra);
   }
 };
 
@@ -107,7 +115,7 @@ __device__ __forceinline__ Req scan_part(Req r, bool chunks, int G) {
 // or one 64-key tile of one query tile (chunks). The units of all row blocks or
 // tiles form one line, request by request, which is cut into equal ranges, one per
 // work-group: one request or many, ragged or not, all have the same work. A row
-// block or tile counts kExtra units more than its keys: that is what a segment
+// block or tile counts kExtra (kChunkExtra) units more than its keys: what a segment
 // costs beside them (set-up, the waves' states meeting, the output: 3 to 5 us;
 // without it the work-group with the most short histories came last, 64 us
 // against a median of 43 on drafted tokens of 48 requests). A cut less than kSnap
@@ -294,20 +302,21 @@ struct States {
 struct Range {
   long long u, end, per, units;
   long long late = 0, late_end = 0;
-  int me;
-  __device__ __forceinline__ Range(long long all, int least, int group, int groups) : units(all) {
+  int me, extra, snap;
+  __device__ __forceinline__ Range(long long all, int least, int set_up, int shortest, int group, int groups)
+      : units(all), extra(set_up), snap(shortest) {
     me = groups % 8 == 0 ? (group & 7) * (groups >> 3) + (group >> 3) : group;
     per = (units + groups - 1) / groups;
     per = uni(per < least ? least : per);
     u = uni(me * per);
     end = uni(u + per < units ? u + per : units);
   }
-  // The first cut moves to its place: u is in the item [start, start + kExtra + n).
+  // The first cut moves to its place: u is in the item [start, start + extra + n).
   __device__ __forceinline__ void settle(long long start, int n) {
-    const long long k = u - start - kExtra, stop = start + kExtra + n;
-    if (k < kSnap) {
+    const long long k = u - start - extra, stop = start + extra + n;
+    if (k < snap) {
       u = uni(start);
-    } else if (n - k < kSnap) {
+    } else if (n - k < snap) {
       u = uni(stop);
     } else if (stop < end) {
       late = u;
@@ -329,20 +338,20 @@ struct Range {
   // divides it, pieces and owner as in CutRecord. false: the item belongs to the
   // next range.
   __device__ __forceinline__ bool take(long long start, int n, int& k0, int& k1, int& slot, int& pieces, int& owner) {
-    const long long stop = start + kExtra + n;
+    const long long stop = start + extra + n;
     const bool inside = u > start;
-    k0 = inside ? (int)(u - start - kExtra) : 0;
+    k0 = inside ? (int)(u - start - extra) : 0;
     k1 = n;
     pieces = 0;
     u = uni(stop);
     if (end < stop) {
-      const long long k = end - start - kExtra;
-      if (k < kSnap) return false;
-      if (n - k >= kSnap) {
+      const long long k = end - start - extra;
+      if (k < snap) return false;
+      if (n - k >= snap) {
         k1 = (int)k;
         // The range of the first cut that stays in the item; the cuts after it, and one.
-        owner = inside ? (int)((start + kExtra + kSnap + per - 1) / per) - 1 : me;
-        pieces = 2 + (int)((stop - kSnap - (owner + 1) * per) / per);
+        owner = inside ? (int)((start + extra + snap + per - 1) / per) - 1 : me;
+        pieces = 2 + (int)((stop - snap - (owner + 1) * per) / per);
       }
     }
     slot = inside ? 2 * me : (pieces ? 2 * me + 1 : -1);
@@ -367,8 +376,8 @@ struct ScanSource {
     long long start;
     Req r;
   };
-  __device__ __forceinline__ ScanSource(const PagedArgs& args, const Plan& plan, int rows, bool with_chunks, int least)
-      : a(args), p(plan), rg(plan.unit_sum[args.S], least, blockIdx.x, gridDim.x), row_block(rows),
+  __device__ __forceinline__ ScanSource(const PagedArgs& args, const Plan& plan, int rows, bool with_chunks, int least, int snap)
+      : a(args), p(plan), rg(plan.unit_sum[args.S], least, kExtra, snap, blockIdx.x, gridDim.x), row_block(rows),
         chunks(with_chunks), cuts(States::scan(args).cuts) {
     if (threadIdx.x == 0) cuts[rg.me].pieces = 0;
     if (rg.u < rg.end) {
@@ -445,7 +454,7 @@ struct ChunkSource {
   Range rg;
   CutRecord* cuts;
   __device__ __forceinline__ ChunkSource(const PagedArgs& args, const Plan& plan)
-      : a(args), p(plan), rg(plan.tile_sum[args.S], kMinRangeChunk, blockIdx.x, gridDim.x), cuts(States::chunk(args).cuts) {
+      : a(args), p(plan), rg(plan.tile_sum[args.S], kMinRangeChunk, kChunkExtra, kSnap, blockIdx.x, gridDim.x), cuts(States::chunk(args).cuts) {
     if (threadIdx.x == 0) cuts[rg.me].pieces = 0;
     if (rg.u < rg.end) {
       Segment s;
@@ -480,14 +489,14 @@ struct ChunkSource {
       keys = t.base64 + 4 * (lo + 1);
       return u - (w - t.before(lo));
     }
-    const int item = divide(v - all_full, t.keys + kExtra);   // cached head, tile
+    const int item = divide(v - all_full, t.keys + kChunkExtra);   // cached head, tile
     s.kvh = item / t.tiles;
     s.h = s.kvh * G;
     s.q0 = t.start;
     s.blocks = t.blocks;
     s.slot0 = 8 * (item - s.kvh * t.tiles);
     keys = t.keys;
-    return p.tile_sum[s.b] + all_full + (long long)item * (t.keys + kExtra);
+    return p.tile_sum[s.b] + all_full + (long long)item * (t.keys + kChunkExtra);
   }
   __device__ __forceinline__ Segment next() {
     Segment s{};

@@ -133,7 +133,8 @@ __global__ __launch_bounds__(kThreads, (Geom<Tin, D, NB>::kPerCu)) void scan_ker
     int b, kvh, first_tok, ctx, total, row0, rows, slot, first, nsteps;
     bool any;
   };
-  ScanSource source(a, plan, kRb, chunks, kBf ? kMinRange : kMinRangeF32);
+  ScanSource source(a, plan, kRb, chunks, kBf ? kMinRange : kMinRangeF32,
+                    kBf ? kSnap : kSnapF32);
   auto next_run = [&]() __attribute__((always_inline)) -> Run {
     const ScanSegment sg = source.next();
     const int k0 = uni(sg.k0), k1 = uni(sg.k1);
