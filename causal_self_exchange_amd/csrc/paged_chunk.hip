@@ -9,8 +9,9 @@
 // a segment's evidence overflows it, so joining a divided tile is mostly a sum.
 //
 // What bounds it: the weights on VALU next to the MFMA, as in the training forward.
-// 2048 tokens of 32 heads of 128 in 8 cached ones over 30,001 rows: 1175 us with the
-// join, 886 TFLOP/s (MfmaUtil 41%); five prompts of 500 to 6,000 tokens 976 us.
+// 2048 tokens of 32 heads of 128 in 8 cached ones over 30,001 rows: 1175 to 1209 us
+// with the join, 861 to 886 TFLOP/s (MfmaUtil 41%); five prompts of 500 to 6,000 tokens
+// 976 to 990 us.
 #include "fwd_body.h"
 
 namespace rel {
