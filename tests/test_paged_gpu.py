@@ -263,6 +263,7 @@ def test_paged_fwd_long_chunks(d, page, H, Hkv, reqs):
     (48, 16, 24, 1, [(0, 8), (9, 6), (500, 33), (31, 2), (31, 5)]),
     (32, 256, 9, 3, [(100, 60), (64, 43), (1000, 300)]),
     (64, 128, 3, 3, [(0, 127), (1, 128), (31, 160), (700, 129)]),
+    (32, 16, 256, 2, [(0, 9), (31, 10), (200, 33), (5, 1)]),
 ])
 def test_paged_fwd_shared_tiles(d, page, H, Hkv, reqs):
     check_fwd(P.make("bf16", H, Hkv, d, page, reqs, seed=d + H, stride_pad=24, pad_rows=1), 0.5, "bf16")
