@@ -56,7 +56,7 @@ constexpr int kMinRangeChunk = 4;
 // The least work on query tiles, in units of the scan (32 rows by 128 keys, kExtra
 // more a row block): a batch with less leaves it to the scan, whose fixed costs are
 // 15 us lower, while the tiles are up to 1.4 times as fast. 32 heads of 128 in 8,
-// scan and tiles: a prompt of 300 tokens (1,800 units) 26 and 33 us, 16 chunks of 32
+// scan (with the launch of a chunk kernel that finds no work, 5 us) and tiles: a prompt of 300 tokens (1,800 units) 26 and 33 us, 16 chunks of 32
 // tokens over 1000 rows (5,600) 37 and 57, 64 of 32 over 100 (8,200) 59 and 43, a prompt
 // of 1024 (10,200) 55 and 46, 8 chunks of 127 over 2000 (19,500) 83 and 97, 32 of 32 over
 // 4000 (34,800) 171 and 134.
