@@ -15,11 +15,11 @@
 // What bounds it: single tokens, the reads of the cache (64 tokens over 1,024 to
 // 4,096 rows of 32 heads of 128: 454 us, 5.9 TB/s, every byte read once; 64 over 4000
 // rows of 8 heads of 32 to 128: 5.2 to 5.8 TB/s); short calls, the latency of the
-// first loads, the meeting and the join (one token over 300 rows: 9.7 and 2.4 us).
+// first loads and the meeting (one token over 300 rows: 9.8 us).
 //
 // Launches: plan (more than kPlanInline requests only), the chunk kernel
 // (paged_chunk.hip, where a request can fill its tiles; the rest is left to the
-// scan), scan, join.
+// scan), scan, join (where a row block can have been divided).
 #include "paged_device.h"
 
 namespace rel {
@@ -97,7 +97,7 @@ struct Geom {
 };
 
 template <typename Tin, int D, int NB>
-__global__ __launch_bounds__(kThreads, (Geom<Tin, D, NB>::kPerCu)) void scan_kernel(PagedArgs a, HeadParams hp, int with_chunks) {
+__global__ __launch_bounds__(kThreads, (Geom<Tin, D, NB>::kPerCu)) void scan_kernel(PagedArgs a, HeadParams hp, int with_chunks, int whole) {
   using C = Geom<Tin, D, NB>;
   constexpr bool kBf = C::kBf;
   constexpr int kRb = 16 * NB;
@@ -134,7 +134,7 @@ __global__ __launch_bounds__(kThreads, (Geom<Tin, D, NB>::kPerCu)) void scan_ker
     bool any;
   };
   ScanSource source(a, plan, kRb, chunks, kBf ? kMinRange : kMinRangeF32,
-                    kBf ? kSnap : kSnapF32);
+                    whole ? kWhole : (kBf ? kSnap : kSnapF32));
   auto next_run = [&]() __attribute__((always_inline)) -> Run {
     const ScanSegment sg = source.next();
     const int k0 = uni(sg.k0), k1 = uni(sg.k1);
@@ -557,9 +557,12 @@ hipError_t launch_rows(const PagedArgs& a, const HeadParams& hp, hipStream_t s) 
     e = launch_paged_chunk(a, hp, chunk_groups, s);
     if (e != hipSuccess) return e;
   }
-  hipLaunchKernelGGL((scan_kernel<Tin, D, NB>), dim3(scan_groups), dim3(kThreads), 0, s, a, hp, (int)chunks);
+  // Few short row blocks stay whole, one per work-group at most, and need no join.
+  const bool whole = !chunks && keys <= (sizeof(Tin) == 2 ? kWholeUnits : kWholeUnitsF32) + 1 + kExtra &&
+                     ((int64_t)a.N * a.H / (16 * NB) + (int64_t)a.S * a.H_kv) <= scan_groups;
+  hipLaunchKernelGGL((scan_kernel<Tin, D, NB>), dim3(scan_groups), dim3(kThreads), 0, s, a, hp, (int)chunks, (int)whole);
   e = hipGetLastError();
-  if (e != hipSuccess) return e;
+  if (e != hipSuccess || whole) return e;
   hipLaunchKernelGGL((join_kernel<Tin, D>), dim3(scan_groups * NB + 16 * chunk_groups), dim3(kThreads), 0, s, a, hp,
                      scan_groups, 16 * NB);
   return hipGetLastError();
