@@ -8,6 +8,10 @@
 // ones keep every compute unit busy to the end. The scan's stabiliser is 0 unless
 // a segment's evidence overflows it, so joining a divided tile is mostly a sum.
 //
+// The weights are rounded to bf16 once for the transport, and summed rounded, as in
+// the inference forward. Two bf16 terms a weight, as in the scan, took five prompts from
+// 951 to 1215 us and 2048 tokens over 30,001 rows from 1160 to 1544.
+//
 // What bounds it: the weights on VALU next to the MFMA, as in the training forward.
 // 2048 tokens of 32 heads of 128 in 8 cached ones over 30,001 rows: 1175 to 1209 us
 // with the join, 861 to 886 TFLOP/s (MfmaUtil 41%); five prompts of 500 to 6,000 tokens

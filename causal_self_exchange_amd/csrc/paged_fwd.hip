@@ -319,18 +319,30 @@ __global__ __launch_bounds__(kThreads, (Geom<Tin, D, NB>::kPerCu)) void scan_ker
         }
       }
       if constexpr (kBf) {
-        // The transport's operand: weights rounded to bf16, like the other bf16 forwards.
-        u32x4 wf[NB];
+        // The transport's operand: each weight as two bf16 terms, itself rounded and what that
+        // leaves (an fp32 difference, exact), so at most 2^-16 of a weight is lost, where one
+        // term loses 2^-8 and single tokens would be less exact than relation_decode's. One
+        // and two terms: single tokens (decode_batch of 64 over 1,024 to 4,096 rows of 32
+        // heads) 455 and 455 us, 32 requests of 8 tokens of 64 heads in 8 of 128 over 4,096
+        // rows 112 and 116, 64 of 6 tokens of 32 heads in 4 of 64 over 4000 70 and 75.
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb)
-          wf[nb] = u32x4{pack_bf16(w[nb][0][0], w[nb][0][1]), pack_bf16(w[nb][0][2], w[nb][0][3]),
-                         pack_bf16(w[nb][1][0], w[nb][1][1]), pack_bf16(w[nb][1][2], w[nb][1][3])};
+        for (int nb = 0; nb < NB; ++nb) {
+          u32x4 hi, lo;
 #pragma unroll
-        for (int db = 0; db < C::kDb; ++db)
+          for (int k = 0; k < 4; ++k) {
+            const float x = w[nb][k >> 1][2 * (k & 1)], y = w[nb][k >> 1][2 * (k & 1) + 1];
+            hi[k] = pack_bf16(x, y);
+            lo[k] = pack_bf16(x - __builtin_bit_cast(float, hi[k] << 16), y - __builtin_bit_cast(float, hi[k] & 0xffff0000u));
+          }
 #pragma unroll
-          for (int nb = 0; nb < NB; ++nb)
+          for (int db = 0; db < C::kDb; ++db)
             acc[nb][db] =
-                __builtin_amdgcn_mfma_f32_16x16x32_bf16(vb[db], __builtin_bit_cast(bf16x8, wf[nb]), acc[nb][db], 0, 0, 0);
+                __builtin_amdgcn_mfma_f32_16x16x32_bf16(vb[db], __builtin_bit_cast(bf16x8, hi), acc[nb][db], 0, 0, 0);
+#pragma unroll
+          for (int db = 0; db < C::kDb; ++db)
+            acc[nb][db] =
+                __builtin_amdgcn_mfma_f32_16x16x32_bf16(vb[db], __builtin_bit_cast(bf16x8, lo), acc[nb][db], 0, 0, 0);
+        }
       } else {
 #pragma unroll
         for (int rr = 0; rr < 4; ++rr)

@@ -480,10 +480,12 @@ size_t relation_paged_workspace_bytes(int N, int S, int H, int H_kv, int d_h);
  * Rows at or past total[b] may hold anything and are not used; a row that is
  * used may not hold NaN or infinities (they reach other rows of its request,
  * never another request's).
- * Numerics: as the output of relation_fwd_lse (evidence scaled in fp32, in bf16
- * one rounding of the weights for the transport), but that where several rows
- * share a tile the row sum may be of the rounded weights; the same call gives the
- * same bits.
+ * Numerics: evidence scaled in fp32, row sums and states in fp32; the same call
+ * gives the same bits. In bf16 each weight enters the transport as two bf16
+ * terms, at most 2^-16 of it off, so a single token is as exact as
+ * relation_decode's (which has fp32 weights). Batches with much work put
+ * requests with many rows (max_new * H / H_kv > 64) on query tiles, with
+ * relation_fwd's weights: rounded to bf16 once (2^-8 of each), as is their sum.
  */
 rel_status relation_paged_fwd(const void* P1, int64_t ld1, const void* cache_P2,
                               const void* cache_V, const int32_t* block_table,
