@@ -30,7 +30,10 @@ using namespace paged;
 
 constexpr int kWaves = 4;
 constexpr int kThreads = 64 * kWaves;
-constexpr float kLazy = 32.0f;            // log2 slack before the stabiliser moves
+// log2 slack before the stabiliser moves, as in decode.hip: n keys' weights times V then
+// stay below n 2^8 max |V|. 2^32 overflowed for V from 2^96 on, where the outputs are
+// finite (decode_batch and decode_long 455 and 219 us at either).
+constexpr float kLazy = 8.0f;
 
 // A work-group barrier for LDS data alone: outstanding vector memory operations
 // (the next segment's loads) are not waited for.
@@ -294,7 +297,7 @@ __global__ __launch_bounds__(kThreads, (Geom<Tin, D, NB>::kPerCu)) void scan_ker
               e2[hb][rr] = key0 + 16 * hb + 4 * lj + rr < pos[nb] ? e2[hb][rr] : -INFINITY;
         }
         // The stabiliser starts at 0 (SiLU >= -0.2785, so no weight is small) and
-        // moves only when a score passes it by 2^32.
+        // moves only when a score passes it by 2^kLazy.
         float mx = -INFINITY;
 #pragma unroll
         for (int hb = 0; hb < C::kHalves; ++hb)
