@@ -87,6 +87,7 @@ constexpr int kThreads = kWaves * 64;
 constexpr int kKSlots = 4;        // LDS ring depth of P2 (tile t in slot t % 4)
 constexpr int kVSlots = 4;        // LDS ring depth of V (tile t in slot t % 4)
 constexpr float kFinite = 0x1p100f;   // largest row sum the fixed offset accepts
+constexpr float kPartFinite = 0x1p119f;   // O of a part of a query tile (paged form)
 
 // P2 tiles are kept in the row layout (evidence operands), V tiles in the
 // transposed layout (transport operands).
@@ -728,14 +729,16 @@ __device__ __forceinline__ void fwd_body(const FwdArgs& a, const HeadParams& hp,
     // before the ring is reused.
     wait_vm_lgkm<0, 15>();
 
-    // Exactness of the fixed offset: every row sum below 2^100 and O finite.
+    // Exactness of the fixed offset: every row sum below 2^100 and O finite. A part of a
+    // query tile (paged) stays below 2^119, so that its at most 256 parts (one to a range)
+    // sum to 2^127 at most.
     const float lrow = kLse && !kPaged ? lane_pair_sum(lsum) : l16[0];
     float omax = 0.0f;
 #pragma unroll
     for (int db = 0; db < C::kDb; ++db)
 #pragma unroll
       for (int r = 0; r < 16; ++r) omax = fmaxf(omax, fabsf(o[db][r]));
-    const bool ok = lrow <= kFinite && omax < INFINITY;
+    const bool ok = lrow <= kFinite && omax < (kPaged && sg.slot >= 0 ? kPartFinite : INFINITY);
     const bool wave_bad = __any(!ok);
     if (lane_now() == 0) flags[wave] = wave_bad ? 1 : 0;
     __syncthreads();
