@@ -552,13 +552,13 @@ hipError_t launch_rows(const PagedArgs& a, const HeadParams& hp, hipStream_t s) 
   int cu = 0;
   hipError_t e = device_cu_count(&cu);
   if (e != hipSuccess) return e;
-  // The chunk kernel: bf16, where a request can fill a query tile (the workspace
+  // The chunk kernel: bf16 unless the scan is selected, where a request can fill a query tile (the workspace
   // counts on no more tokens than the batch has), with a token stride whose 256
   // rows a 31-bit byte offset reaches, and where the lengths can add up to its least
   // work (its launch without any takes 5 us).
   const int64_t keys = ((int64_t)a.max_pages << a.page_shift) / kScanUnit + 1 + kExtra;
   const int64_t most = ((int64_t)a.N * a.H / 32 + (int64_t)a.S * a.H_kv + 1) * keys;
-  const bool chunks = sizeof(Tin) == 2 && paged_chunks_possible(a.max_new < a.N ? a.max_new : a.N, a.H / a.H_kv) &&
+  const bool chunks = sizeof(Tin) == 2 && a.tiles && paged_chunks_possible(a.max_new < a.N ? a.max_new : a.N, a.H / a.H_kv) &&
                       a.ld1 < (1 << 22) && most >= kChunkWork;
   const int chunk_groups = chunks ? (cu < kChunkGroups ? cu : kChunkGroups) : 0;
   int scan_groups = cu * Geom<Tin, D, NB>::kPerCu;

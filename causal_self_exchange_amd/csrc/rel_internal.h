@@ -172,6 +172,7 @@ struct PagedArgs {
   void* Y;
   void* ws;
   int N, S, H, H_kv, d_h, n_pages, page_shift, max_pages, max_new;
+  int tiles;            // whether chunks may go to query tiles
 };
 
 // Workspace of relation_paged_fwd (paged_device.h): the work sums of batches of

@@ -76,12 +76,15 @@ void read_kernel_env() {
   });
 }
 
+bool fwd_scan_selected() {
+  read_kernel_env();
+  return g_fwd_kernel.load(std::memory_order_relaxed) == REL_KERNEL_SCAN;
+}
+
 // Which forward kernel runs: the MFMA kernel for bf16 where it exists, else
 // the row-scan kernel (always, once REL_KERNEL_SCAN is selected).
 bool use_mfma(rel_dtype dt, int d_h, int T) {
-  if (dt != REL_BF16 || !rel::fwd_mfma_supported(d_h, T)) return false;
-  read_kernel_env();
-  return g_fwd_kernel.load(std::memory_order_relaxed) != REL_KERNEL_SCAN;
+  return dt == REL_BF16 && rel::fwd_mfma_supported(d_h, T) && !fwd_scan_selected();
 }
 
 // Forward with an optional row log-normaliser output (lse may be null).
@@ -323,7 +326,8 @@ rel_status relation_paged_fwd(const void* P1, int64_t ld1, const void* cache_P2,
   const Range outs[] = {{Y, static_cast<size_t>(ny) * es}, {workspace, need}};
   if (any_alias(ins, outs)) return REL_E_ALIAS;
   const rel::PagedArgs a{P1, ld1, cache_P2, cache_V, block_table, total, cu, Y, workspace, N, S, H, H_kv, d_h,
-                         n_pages, page_shift_of(page_size), max_pages, max_new};
+                         n_pages, page_shift_of(page_size), max_pages, max_new,
+                         dt == REL_BF16 && !fwd_scan_selected()};
   return rel::launch_paged(a, hp, dt == REL_BF16, stream) == hipSuccess ? REL_OK : REL_E_LAUNCH;
 }
 

@@ -99,7 +99,8 @@ KERNELS = {"auto": 0, "scan": 1}
 
 def select_kernels(fwd: str = "auto", bwd: str = "auto"):
     """Process-wide choice of the bf16 forward / backward kernels: "auto"
-    (the MFMA kernels wherever they apply) or "scan" (the row-scan kernels)."""
+    (the MFMA kernels wherever they apply) or "scan" (the row-scan kernels;
+    paged_fwd: no query tiles, whose weights are rounded to bf16)."""
     _check("relation_select_kernels", lib().relation_select_kernels(KERNELS[fwd], KERNELS[bwd]))
 
 

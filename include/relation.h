@@ -484,8 +484,9 @@ size_t relation_paged_workspace_bytes(int N, int S, int H, int H_kv, int d_h);
  * gives the same bits. In bf16 each weight enters the transport as two bf16
  * terms, at most 2^-16 of it off, so a single token is as exact as
  * relation_decode's (which has fp32 weights). Batches with much work put
- * requests with many rows (max_new * H / H_kv > 64) on query tiles, with
- * relation_fwd's weights: rounded to bf16 once (2^-8 of each), as is their sum.
+ * requests with many rows on query tiles, with relation_fwd's weights: rounded to
+ * bf16 once (2^-8 of each), and summed so. relation_select_kernels with
+ * REL_KERNEL_SCAN for the forward keeps all rows off the tiles.
  */
 rel_status relation_paged_fwd(const void* P1, int64_t ld1, const void* cache_P2,
                               const void* cache_V, const int32_t* block_table,
@@ -508,7 +509,8 @@ typedef enum {
 /*
  * relation_select_kernels - which kernels the bf16 forward family
  * (relation_fwd, relation_fwd_ex, relation_fwd_lse, relation_fwd_model) and
- * relation_bwd run. The selection is process-wide; calls made after this
+ * relation_bwd run; relation_paged_fwd under the forward's REL_KERNEL_SCAN
+ * takes no query tiles, so that every row has the scan's weights. The selection is process-wide; calls made after this
  * one returns use it. Before any call to it, the selection comes from the
  * environment variables RELATION_FWD_KERNEL and RELATION_BWD_KERNEL (the
  * value "scan" selects REL_KERNEL_SCAN), read once, the first time a
