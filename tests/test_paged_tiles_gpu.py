@@ -1,4 +1,6 @@
-"""Chunks on query tiles of the paged forward, next to the same calls in the scan."""
+"""Chunks on query tiles of the paged forward, next to the same calls in the scan: the selection of kernels, and what the
+scan's small batches do not reach of the tiles."""
+import numpy as np
 import pytest
 import torch
 
@@ -62,3 +64,84 @@ def test_rows_of_the_scan_keep_their_weights_in_prompts():
     n = int(m["total"][0]) // 4 + 300
     PR.check_rows(m, call(m, "scan"), 0, [0, 5, 100, m["max_new"] - 1], [0, 3, 7], 0.5,
                   lambda r, s: PR.weights_bound(r, s, n, du, e_max))
+
+
+@pytest.mark.parametrize("d,page,H,Hkv", [(128, 16, 4, 2), (64, 64, 2, 2), (80, 32, 3, 1), (48, 16, 2, 1), (32, 128, 2, 2)])
+def test_chunks(d, page, H, Hkv):
+    reqs = T.CHUNKS + [T.filler(H)]
+    m = P.make("bf16", H, Hkv, d, page, reqs, seed=d + H, stride_pad=32, pad_rows=5)
+    T.check_fwd(m, 0.5, "bf16", skip=len(T.CHUNKS))
+    check_tiles(m, len(T.CHUNKS))
+
+
+@pytest.mark.parametrize("reqs", [T.CHUNKS, T.RAGGED + [(500, 300)]])
+def test_large_evidence(reqs):
+    """Evidence far beyond the exponent range of an unshifted exponential: the tiles' second pass, and joins of states with
+    a stabiliser of their own. du as in test_paged_fwd_large_evidence (scale 5, d = 64)."""
+    m = P.make("bf16", 4, 2, 64, 16, reqs + [T.filler(4)], seed=5, scale=5.0)
+    T.check_fwd(m, 0.5, "bf16", du=2e-3, skip=len(reqs))
+    check_tiles(m, len(reqs), du=2e-3)
+
+
+def test_pages_outside_the_cache_read_as_zeros():
+    m = P.make("bf16", 4, 2, 64, 16, T.CHUNKS + [T.filler(4)], seed=8)
+    bad = [P.BAD, m["cP2"].shape[0], 2**31 - 1]
+    for b in range(len(T.CHUNKS)):
+        m["table"][b, 0] = bad[b % 3]
+    for k, p in enumerate((0, 7, 8, 63, 64, 130, 400, 401, 402, 403, 999)):
+        m["table"][len(T.CHUNKS), p] = bad[k % 3]
+    T.check_fwd(m, 0.5, "bf16", skip=len(T.CHUNKS))
+    check_tiles(m, len(T.CHUNKS))
+
+
+def test_shared_pages():
+    m = P.make("bf16", 8, 2, 128, 16, [(64, 170), T.filler(8), (64, 150)], seed=4)
+    for b in (0, 2):
+        m["table"][b, :4] = m["table"][1, :4]
+    T.check_fwd(m, 0.5, "bf16", skip=1)
+    check_tiles(m, 1)
+
+
+def test_other_rows_stay():
+    """Refused, empty, oversized and inconsistent requests next to tiles."""
+    m = P.make("bf16", 4, 2, 64, 16, [(10, 150), (0, 0), (40, 300), (7, 1), (30, 900), (5, 200), (2, 130), T.filler(4)], seed=3,
+               pad_rows=40)
+    m["total"][2] = -1
+    m["total"][3] = 0
+    m["total"][5] = m["table"].shape[1] * 16 + 1
+    T.check_fwd(m, 0.5, "bf16", max_new=700, skip=7)      # request 4 has more than 700 new tokens
+    check_tiles(m, 7, max_new=700)
+    m["cu"][0] = -2
+    T.check_fwd(m, 0.5, "bf16", max_new=1000, skip=7)
+
+
+def test_caches_past_32_bit_offsets():
+    """Tiles over pages on both sides of 2^31 and 2^32 elements, against the same pages in a small cache."""
+    H, Hkv, d, page = 4, 2, 128, 256
+    per = Hkv * page * d
+    n_pages = (1 << 32) // per + 40
+    m = P.make("bf16", H, Hkv, d, page, [(100, 160), T.filler(4)], seed=7)
+    held = int(m["cP2"].shape[0])
+    marks = [(1 << 31) // per, (1 << 32) // per]
+    where = np.array([0, n_pages - 1] + [k + j for k in marks for j in range(-15, 15)] + list(range(50, 50 + held)))[:held]
+    assert len(set(where)) == held
+    big = [torch.empty((n_pages, Hkv, page, d), dtype=torch.bfloat16, device=DEV) for _ in range(2)]
+    at = torch.from_numpy(where).to(DEV)
+    for b, c in zip(big, (m["cP2"], m["cV"])):
+        b[at] = c.to(DEV)
+    small = m["table"].numpy()
+    table = torch.from_numpy(np.where(small >= 0, where[np.clip(small, 0, None)], P.BAD).astype(np.int32)).to(DEV)
+    Y, S = check_tiles(m, 1)
+    assert torch.equal(call(m, caches=big, table=table), Y)
+    assert torch.equal(call(m, "scan", caches=big, table=table), S)
+
+
+def test_serving_loop_on_tiles():
+    """A prompt and its continuation on tiles (10,000 and 11,700 units of work), single tokens and a
+    chunk in the scan: the rows of one forward. The bar of test_serving_loop."""
+    s = T.Server("bf16", 8, 2, 64, 16, 300, 3, 250, seed=5)
+    s.step([2100, 0, 70], 2200)
+    s.step([1500, 300, 1], 1801)
+    s.step([1, 2, 1], 5)
+    s.step([300, 1, 0], 301)
+    s.check(3e-2)
