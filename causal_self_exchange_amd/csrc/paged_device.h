@@ -33,30 +33,20 @@ struct Req {
   }
 };
 
-// The cut of the work (below):
-//   kScanUnit   keys of a unit of the scan.
-//   kExtra      units that a segment costs beside its keys, in the scan.
-//   kChunkExtra the same in the chunks: five prompts of 500 to 6,000 tokens 1000 us at
+// The cut of the work (below; kScanUnit, kExtra and whole row blocks in rel_internal.h):
+//   kChunkExtra kExtra of the chunks: five prompts of 500 to 6,000 tokens 1000 us at
 //               2, 981 at 4, 1004 at 10.
 //   kSnap       the least units that a cut leaves; in fp32, where a unit takes longer,
 //               1: four chunks of 16 tokens over 1000 rows 24.5 us at 2, 21.9 at 1.
-//   kWhole      in its place, where no row block can have more than kWholeUnits units
-//               and each can have a work-group of its own: nothing is divided, and
-//               the join is not launched (one token over 300 rows of 8 heads 17 and 14
-//               us; 16 over 1000 rows 22.8 and 21.7, over 2000 27 and 31; in fp32 4 over
-//               500 rows 17.4 and 15.6, over 1000 19 and 23).
+//   kWhole      in its place, where row blocks stay whole.
 //   kMinRange   units of the scan's shortest range (single tokens lose 1 us at 1); in
 //               fp32 1: six chunks of up to 97 tokens of 8 heads of 48 34 us at 4, 27 at 1.
 //   kMinRangeChunk the same of the chunks: a prompt of 300 tokens of 32 heads 45 us at
 //               8, 33 at 4.
-constexpr int kScanUnit = 128;
-constexpr int kExtra = 2;
 constexpr int kChunkExtra = 4;
 constexpr int kSnap = 2;
 constexpr int kSnapF32 = 1;
 constexpr int kWhole = 1 << 30;
-constexpr int kWholeUnits = 8;
-constexpr int kWholeUnitsF32 = 4;
 constexpr int kMinRange = 4;
 constexpr int kMinRangeF32 = 1;
 constexpr int kMinRangeChunk = 4;
@@ -143,7 +133,7 @@ struct ScanRows {
   __device__ __forceinline__ ScanRows(const PagedArgs& a, const Req& r, int row_block) {
     rows = r.q * (a.H / a.H_kv);
     blocks = (rows + row_block - 1) / row_block;
-    units = max(1, (r.total - 1 + kScanUnit - 1) / kScanUnit);
+    units = paged_scan_units(r.total);
   }
 };
 

@@ -556,8 +556,8 @@ hipError_t launch_rows(const PagedArgs& a, const HeadParams& hp, hipStream_t s) 
   // counts on no more tokens than the batch has), with a token stride whose 256
   // rows a 31-bit byte offset reaches, and where the lengths can add up to its least
   // work (its launch without any takes 5 us).
-  const int64_t keys = ((int64_t)a.max_pages << a.page_shift) / kScanUnit + 1 + kExtra;
-  const int64_t most = ((int64_t)a.N * a.H / 32 + (int64_t)a.S * a.H_kv + 1) * keys;
+  const int table_rows = a.max_pages << a.page_shift;
+  const int64_t most = ((int64_t)a.N * a.H / 32 + (int64_t)a.S * a.H_kv + 1) * (paged_scan_units(table_rows) + kExtra);
   const bool chunks = sizeof(Tin) == 2 && a.tiles && paged_chunks_possible(a.max_new < a.N ? a.max_new : a.N, a.H / a.H_kv) &&
                       a.ld1 < (1 << 22) && most >= kChunkWork;
   const int chunk_groups = chunks ? (cu < kChunkGroups ? cu : kChunkGroups) : 0;
@@ -573,8 +573,8 @@ hipError_t launch_rows(const PagedArgs& a, const HeadParams& hp, hipStream_t s) 
     if (e != hipSuccess) return e;
   }
   // Few short row blocks stay whole, one per work-group at most, and need no join.
-  const bool whole = !chunks && keys <= (sizeof(Tin) == 2 ? kWholeUnits : kWholeUnitsF32) + 1 + kExtra &&
-                     ((int64_t)a.N * a.H / (16 * NB) + (int64_t)a.S * a.H_kv) <= scan_groups;
+  const bool whole = !chunks && paged_whole(table_rows, (int64_t)a.N * a.H / (16 * NB) + (int64_t)a.S * a.H_kv,
+                                            scan_groups, sizeof(Tin) == 2);
   hipLaunchKernelGGL((scan_kernel<Tin, D, NB>), dim3(scan_groups), dim3(kThreads), 0, s, a, hp, (int)chunks, (int)whole);
   e = hipGetLastError();
   if (e != hipSuccess || whole) return e;

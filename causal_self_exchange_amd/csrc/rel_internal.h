@@ -203,6 +203,28 @@ inline size_t paged_ws_bytes(int64_t N, int64_t S, int G, int d_h) {
   return static_cast<size_t>(paged_chunk_offset(S, d_h) + (paged_chunks_possible(N, G) ? chunk : 0));
 }
 
+// The scan's cut (paged_device.h has the rest of its numbers):
+//   kScanUnit   keys of a unit of the scan.
+//   kExtra      units that a segment costs beside its keys, in the scan.
+//   kWholeUnits where no row block can have more units than that and each can have a
+//               work-group of its own, nothing is divided and the join is not launched.
+//               Divided and whole: one token over 300 rows of 8 heads of 64 17 and 14 us,
+//               over 1060 (9 units) 16.8 and 14.6; 16 of 16 heads in 4 of 128 over 1060
+//               23.0 and 20.2, over 2000 27 and 31; in fp32 4 over 550 rows (5 units)
+//               16.4 and 16.3, over 1000 19 and 23.
+constexpr int kScanUnit = 128;
+constexpr int kExtra = 2;
+constexpr int kWholeUnits = 9;
+constexpr int kWholeUnitsF32 = 5;
+// Units of a row block of a request of `total` rows (a row sees those before its own).
+inline __host__ __device__ int paged_scan_units(int total) {
+  return total > kScanUnit ? (total - 1 + kScanUnit - 1) / kScanUnit : 1;
+}
+// table_rows: rows that a table row can hold, the most that a request can have.
+inline bool paged_whole(int table_rows, int64_t row_blocks, int groups, bool bf16) {
+  return paged_scan_units(table_rows) <= (bf16 ? kWholeUnits : kWholeUnitsF32) && row_blocks <= groups;
+}
+
 // Launchers (return the hipError_t of the launch).
 hipError_t launch_fwd_scan(const FwdArgs& a, const HeadParams& hp, bool bf16, hipStream_t s);
 // Compute units of the current device (queried once per device, then cached:
