@@ -41,15 +41,15 @@ struct Req {
 //   kWhole      in its place, where row blocks stay whole.
 //   kMinRange   units of the scan's shortest range (single tokens lose 1 us at 1); in
 //               fp32 1: six chunks of up to 97 tokens of 8 heads of 48 34 us at 4, 27 at 1.
-//   kMinRangeChunk the same of the chunks: a prompt of 300 tokens of 32 heads 45 us at
-//               8, 33 at 4.
+//               The chunks need none: kChunkWork units of the scan are more than 1,000
+//               of theirs (a query tile takes the place of 8 row blocks at most), 4 and
+//               more to a work-group.
 constexpr int kChunkExtra = 4;
 constexpr int kSnap = 2;
 constexpr int kSnapF32 = 1;
 constexpr int kWhole = 1 << 30;
 constexpr int kMinRange = 4;
 constexpr int kMinRangeF32 = 1;
-constexpr int kMinRangeChunk = 4;
 
 // The least work on query tiles, in units of the scan (32 rows by 128 keys, kExtra
 // more a row block): a batch with less leaves it to the scan, whose fixed costs are
@@ -452,7 +452,8 @@ struct ChunkSource {
   Range rg;
   CutRecord* cuts;
   __device__ __forceinline__ ChunkSource(const PagedArgs& args, const Plan& plan)
-      : a(args), p(plan), rg(plan.tile_sum[args.S], kMinRangeChunk, kChunkExtra, kSnap, blockIdx.x, gridDim.x), cuts(States::chunk(args).cuts) {
+      : a(args), p(plan), rg(plan.tile_sum[args.S], 1, kChunkExtra, kSnap, blockIdx.x, gridDim.x),
+        cuts(States::chunk(args).cuts) {
     if (threadIdx.x == 0) cuts[rg.me].pieces = 0;
     if (rg.u < rg.end) {
       Segment s;
