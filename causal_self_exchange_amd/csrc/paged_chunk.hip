@@ -15,7 +15,7 @@
 // What bounds it: the weights on VALU next to the MFMA, as in the training forward.
 // 2048 tokens of 32 heads of 128 in 8 cached ones over 30,001 rows: 1175 to 1209 us
 // with the join, 861 to 886 TFLOP/s (MfmaUtil 41%); five prompts of 500 to 6,000 tokens
-// 950 to 990 us.
+// 950 to 1007 us.
 #include "fwd_body.h"
 
 namespace rel {

@@ -53,11 +53,13 @@ constexpr int kMinRangeF32 = 1;
 
 // The least work on query tiles, in units of the scan (32 rows by 128 keys, kExtra
 // more a row block): a batch with less leaves it to the scan, whose fixed costs are
-// 15 us lower, while the tiles are up to 1.4 times as fast. 32 heads of 128 in 8,
-// scan (with the launch of a chunk kernel that finds no work, 5 us) and tiles: a prompt of 300 tokens (1,800 units) 26 and 33 us, 16 chunks of 32
-// tokens over 1000 rows (5,600) 37 and 57, 64 of 32 over 100 (8,200) 59 and 43, a prompt
-// of 1024 (10,200) 55 and 46, 8 chunks of 127 over 2000 (19,500) 83 and 97, 32 of 32 over
-// 4000 (34,800) 171 and 134.
+// lower. 32 heads of 128 in 8, scan (by selection, without a chunk kernel's launch) and
+// tiles: a prompt of 300 tokens (1,800 units) 19 and 33 us, 16 chunks of 32 tokens over
+// 1000 rows (5,600) 35 and 58, 64 of 32 over 100 (8,200) 55 and 44, a prompt of 1024
+// (10,200) 52 and 49, 8 chunks of 127 over 2000 (19,500) 88 and 96, 32 of 32 over 4000
+// (34,800) 174 and 130. The work alone does not part the two: it leaves out into how many
+// parts the tiles are cut (the 8 chunks: 32 tiles to 256 work-groups), and between 8,000
+// and 30,000 either may be up to a quarter faster than the one that runs.
 constexpr int kChunkWork = 8000;
 
 // Query tiles of a request's new tokens (chunk kernel): 256 rows, 32 for each of 8 waves.
@@ -70,7 +72,7 @@ constexpr int kChunkWork = 8000;
 //   one, leaves few waves idle. Where the tiles would hold fewer than kChunkRows
 //   rows each, two row blocks of the scan kernel, which read the keys together, are
 //   faster: the tokens left (rest) go there. 32 chunks over 4000 rows, 8 cached
-//   heads: 64 rows 110 us by the scan, 128 on tiles; 80 rows 200 and 131.
+//   heads: 64 rows 113 us by the scan, 128 on tiles; 80 rows 200 and 126.
 struct ChunkTiles {
   int base64, full;            // first position / 64, full tiles
   int start, blocks, tiles, keys;   // shared tiles: first position, blocks of a head, per cached head, key tiles each
@@ -112,7 +114,12 @@ __device__ __forceinline__ Req scan_part(Req r, bool chunks, int G) {
 // is 128 keys of one row block (scan: row_block rows of a request and cached head)
 // or one 64-key tile of one query tile (chunks). The units of all row blocks or
 // tiles form one line, request by request, which is cut into equal ranges, one per
-// work-group: one request or many, ragged or not, all have the same work. A row
+// work-group: one request or many, ragged or not. Every row block of a request counts
+// the units of its last one, so in a prompt that the scan takes, where a row block ends
+// at its own position, the ranges of early row blocks have less to do than those of late
+// ones, up to half the work being no keys. Units of a row block's own took fp32 prompts
+// of 2,000 tokens from 85 to 78 us, but 3 chunks of 600 over 100 rows from 70 to 94, as
+// a segment costs more than two units there. A row
 // block or tile counts kExtra (kChunkExtra) units more than its keys: what a segment
 // costs beside them (set-up, the waves' states meeting, the output: 3 to 5 us;
 // without it the work-group with the most short histories came last, 64 us
@@ -139,7 +146,8 @@ struct ScanRows {
 
 struct PlanScratch { long long red[4][2]; };
 
-// What a request's rows on query tiles would be in the scan.
+// What a request's rows on query tiles would be in the scan (units as ScanRows counts
+// them: of a prompt about twice its keys).
 __device__ __forceinline__ long long tile_work(const PagedArgs& a, const Req& r) {
   if (r.q == 0) return 0;
   Req t = r;

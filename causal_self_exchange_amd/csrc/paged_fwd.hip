@@ -85,8 +85,12 @@ struct Geom {
   static constexpr int kDb = D / 16;                         // 16-row blocks of O^T
   static constexpr int kZStride = D + 4;
   static constexpr int kZBytes = 16 * kZStride * 4;          // 16 rows where the waves' states meet
-  // Work-groups per compute unit (as many as the registers and the LDS admit) and
-  // slots per wave: together about 128 KB of loads in flight on a compute unit.
+  // Work-groups per compute unit and slots per wave: together about 128 KB of loads in
+  // flight on a compute unit. The registers admit them but in two fp32 kernels: d = 128
+  // with two row blocks keeps 43 in scratch, most of them addresses of operand reads that
+  // each step loads again (8 chunks of 64 tokens over 2000 rows of 8 heads in 2: 81 us, 53
+  // TFLOP/s; d = 64, without any, 42 us and 51), d = 64 with one row block 4, outside its
+  // key loop.
   static constexpr int kPerCu = NB == 1 && D <= 64 ? 4 : 2;
   static constexpr int kSlots = NB == 2 && kSlot <= 8192 ? 2 : 1;
   static constexpr int kRing = kWaves * kSlots * kSlot;
