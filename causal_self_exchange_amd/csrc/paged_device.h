@@ -58,7 +58,7 @@ constexpr int kMinRangeF32 = 1;
 // 1000 rows (5,600) 35 and 58, 64 of 32 over 100 (8,200) 55 and 44, a prompt of 1024
 // (10,200) 52 and 49, 8 chunks of 127 over 2000 (19,500) 88 and 96, 32 of 32 over 4000
 // (34,800) 174 and 130. The work alone does not part the two: it leaves out into how many
-// parts the tiles are cut (the 8 chunks: 32 tiles to 256 work-groups), and between 8,000
+// parts the tiles are cut (the 8 chunks: 192 tiles to 256 work-groups), and between 8,000
 // and 30,000 either may be up to a quarter faster than the one that runs.
 constexpr int kChunkWork = 8000;
 

@@ -556,10 +556,10 @@ hipError_t launch_rows(const PagedArgs& a, const HeadParams& hp, hipStream_t s) 
   int cu = 0;
   hipError_t e = device_cu_count(&cu);
   if (e != hipSuccess) return e;
-  // The chunk kernel: bf16 unless the scan is selected, where a request can fill a query tile (the workspace
-  // counts on no more tokens than the batch has), with a token stride whose 256
-  // rows a 31-bit byte offset reaches, and where the lengths can add up to its least
-  // work (its launch without any takes 5 us).
+  // The chunk kernel: bf16 unless the scan is selected, where a request can fill a query
+  // tile (the workspace counts on no more tokens than the batch has), with a token stride
+  // whose 256 rows a 31-bit byte offset reaches, and where the lengths can add up to its
+  // least work (its launch without any takes 5 us).
   const int table_rows = a.max_pages << a.page_shift;
   const int64_t most = ((int64_t)a.N * a.H / 32 + (int64_t)a.S * a.H_kv + 1) * (paged_scan_units(table_rows) + kExtra);
   const bool chunks = sizeof(Tin) == 2 && a.tiles && paged_chunks_possible(a.max_new < a.N ? a.max_new : a.N, a.H / a.H_kv) &&
