@@ -146,6 +146,12 @@ __device__ __forceinline__ void dma16_nt(const u32x4& r, const char* lds, int vo
   asm volatile("s_nop 4\n\tbuffer_load_dwordx4 %0, %1, 0 offen nt lds" : : "v"(voffset), "s"(r), "{m0}"(m0) : "memory");
 }
 
+// The same with 4 bytes a lane: to LDS byte address lds + 4 l.
+__device__ __forceinline__ void dma4(const u32x4& r, const char* lds, int voffset) {
+  const unsigned m0 = (unsigned)(size_t)(const __attribute__((address_space(3))) char*)lds;
+  asm volatile("s_nop 4\n\tbuffer_load_dword %0, %1, 0 offen lds" : : "v"(voffset), "s"(r), "{m0}"(m0) : "memory");
+}
+
 // Cache-policy operand of the buffer store builtins: non-temporal (gfx950).
 constexpr int kCachePolicyNT = 2;
 

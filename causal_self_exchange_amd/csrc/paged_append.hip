@@ -50,6 +50,29 @@ __device__ __forceinline__ void store8(Tin* p, const float (&x)[8]) {
   }
 }
 
+// The 8 rotary pairs of a group, by their cosines and sines: x and y are the group's 16
+// elements in order (interleaved pairs) or its 8 of either half (half split).
+__device__ __forceinline__ void turn(int rope, const float* cs, const float* sn, float (&x)[8], float (&y)[8]) {
+  if (rope == 1) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float c0 = cs[e], n0 = sn[e], c1 = cs[4 + e], n1 = sn[4 + e];
+      const float p = x[2 * e], q = x[2 * e + 1], r = y[2 * e], w = y[2 * e + 1];
+      x[2 * e] = fmaf(p, c0, -q * n0);
+      x[2 * e + 1] = fmaf(p, n0, q * c0);
+      y[2 * e] = fmaf(r, c1, -w * n1);
+      y[2 * e + 1] = fmaf(r, n1, w * c1);
+    }
+  } else if (rope == 2) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float c0 = cs[e], n0 = sn[e], p = x[e], q = y[e];
+      x[e] = fmaf(p, c0, -q * n0);
+      y[e] = fmaf(p, n0, q * c0);
+    }
+  }
+}
+
 template <typename Tin, int D>
 __global__ __launch_bounds__(kThreads) void paged_append_kernel(PagedAppendArgs a, PrestepParams pp, int first) {
   constexpr int kGroups = D / 16;
@@ -90,24 +113,7 @@ __global__ __launch_bounds__(kThreads) void paged_append_kernel(PagedAppendArgs 
       float x[8], y[8];
       load8(src + oa, x);
       load8(src + ob, y);
-      if (a.rope == 1) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float c0 = s_cos[8 * g + e], n0 = s_sin[8 * g + e], c1 = s_cos[8 * g + 4 + e], n1 = s_sin[8 * g + 4 + e];
-          const float p = x[2 * e], q = x[2 * e + 1], r = y[2 * e], w = y[2 * e + 1];
-          x[2 * e] = fmaf(p, c0, -q * n0);
-          x[2 * e + 1] = fmaf(p, n0, q * c0);
-          y[2 * e] = fmaf(r, c1, -w * n1);
-          y[2 * e + 1] = fmaf(r, n1, w * c1);
-        }
-      } else if (a.rope == 2) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float c0 = s_cos[8 * g + e], n0 = s_sin[8 * g + e], p = x[e], q = y[e];
-          x[e] = fmaf(p, c0, -q * n0);
-          y[e] = fmaf(p, n0, q * c0);
-        }
-      }
+      turn(a.rope, s_cos + 8 * g, s_sin + 8 * g, x, y);
       store8(dst + oa, x);
       store8(dst + ob, y);
     } else {
@@ -145,6 +151,146 @@ __global__ __launch_bounds__(kThreads) void paged_append_kernel(PagedAppendArgs 
   }
 }
 
+// ---- 8-bit pages ------------------------------------------------------------------
+//
+// A row x of P2 or of the information state is stored as e4m3 values q and one exponent
+// k, x = q 2^k: k is the least with max |x| <= 448 2^k. A power of two loses nothing
+// against a finer scale, as e4m3 rounds relative to each value (2^-4 of it, down to 2^-6
+// 2^k, below which steps are 2^-9 2^k), and it costs a byte and no multiplication where
+// the forward turns the values back into bf16. The row is rounded once, from the fp32 of
+// its rotation or mixing. Lanes of a power of two share a row (16 elements each), so that
+// its maximum is a few exchanges between lanes.
+constexpr int kLowScale = -100, kHighScale = 119;
+constexpr float kMostE4m3 = 448.0f;
+
+// k from a row's maximum (of its finite elements); 2^-k is a normal fp32 number.
+__device__ __forceinline__ int scale_exponent(float most) {
+  const unsigned b = __float_as_uint(most);
+  const int k = (int)(b >> 23) - 127 - 8 + ((b & 0x7fffffu) > 0x600000u ? 1 : 0);   // 448 = 1.75 2^8
+  return min(max(k, kLowScale), kHighScale);
+}
+
+__device__ __forceinline__ float finite_max(const float (&x)[8], const float (&y)[8]) {
+  float m = 0.0f;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const float p = fabsf(x[e]), q = fabsf(y[e]);
+    m = fmaxf(m, fmaxf(p <= 3.4028234e38f ? p : 0.0f, q <= 3.4028234e38f ? q : 0.0f));
+  }
+  return m;
+}
+
+// Eight elements as e4m3, to nearest even; what is past the largest scale saturates,
+// NaN and infinities become NaN.
+__device__ __forceinline__ uint2 quantise8(const float (&x)[8], float inv) {
+  float y[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e)
+    y[e] = fabsf(x[e]) <= 3.4028234e38f ? __builtin_amdgcn_fmed3f(x[e] * inv, -kMostE4m3, kMostE4m3) : x[e];
+  int lo = __builtin_amdgcn_cvt_pk_fp8_f32(y[0], y[1], 0, false);
+  lo = __builtin_amdgcn_cvt_pk_fp8_f32(y[2], y[3], lo, true);
+  int hi = __builtin_amdgcn_cvt_pk_fp8_f32(y[4], y[5], 0, false);
+  hi = __builtin_amdgcn_cvt_pk_fp8_f32(y[6], y[7], hi, true);
+  return make_uint2((unsigned)lo, (unsigned)hi);
+}
+
+// One work-group per token, as above: the rows that are quantised first, then P1.
+template <int D>
+__global__ __launch_bounds__(kThreads) void paged_append_q8_kernel(PagedAppendArgs a, uint8_t* scale, PrestepParams pp, int first) {
+  constexpr int kGroups = D / 16;
+  constexpr int kLanes = kGroups <= 2 ? 2 : (kGroups <= 4 ? 4 : 8);   // of a row
+  __shared__ float s_cos[D / 2], s_sin[D / 2];
+  const int t = first + (int)blockIdx.x;
+  const int slot = a.slot[t];
+  if (slot < 0 || (slot >> a.page_shift) >= a.n_pages) return;   // uniform for the work-group
+  const int tid = threadIdx.x;
+  if (a.rope != 0 && tid < D / 2) {
+    float sn, cs;
+    sincos_of((double)a.pos[t] * pp.inv_freq[tid], &sn, &cs);
+    s_cos[tid] = cs;
+    s_sin[tid] = sn;
+  }
+  __syncthreads();
+  const int page = slot >> a.page_shift, off = slot & ((1 << a.page_shift) - 1);
+  // Quantises the row of head h that the lanes hold 16 elements of each, 8 of them at
+  // column oa and 8 at ob (nothing where the lane has none).
+  auto store_row = [&](int part, int h, int g, int oa, int ob, const float (&x)[8], const float (&y)[8]) {
+    float most = g < kGroups ? finite_max(x, y) : 0.0f;
+#pragma unroll
+    for (int o = 1; o < kLanes; o <<= 1) most = fmaxf(most, __shfl_xor(most, o, 64));
+    if (g >= kGroups) return;
+    const int k = scale_exponent(most);
+    const float inv = __uint_as_float((unsigned)(127 - k) << 23);
+    const size_t head = (size_t)page * a.H_kv + h;
+    uint8_t* const row = static_cast<uint8_t*>(part ? a.cV : a.cP2) + ((head << a.page_shift) + off) * D;
+    const uint2 p = quantise8(x, inv), q = quantise8(y, inv);
+    if (ob == oa + 8) {
+      *reinterpret_cast<uint4*>(row + oa) = make_uint4(p.x, p.y, q.x, q.y);
+    } else {
+      *reinterpret_cast<uint2*>(row + oa) = p;
+      *reinterpret_cast<uint2*>(row + ob) = q;
+    }
+    if (g == 0) scale[(((head << 1) + part) << a.page_shift) + off] = (uint8_t)(k + 127);
+  };
+  const int keys = a.H_kv * kLanes;
+  const int info = (a.mix ? a.H_kv / 2 : a.H_kv) * kLanes;
+  const int all = keys + info + a.H * kGroups;
+  for (int u = tid; u < all; u += kThreads) {
+    float x[2][8], y[2][8];
+    if (u < keys) {
+      const int h = u / kLanes, g = u % kLanes;
+      const int oa = a.rope == 2 ? 8 * g : 16 * g, ob = a.rope == 2 ? D / 2 + 8 * g : 16 * g + 8;
+      if (g < kGroups) {
+        const __bf16* src = static_cast<const __bf16*>(a.P2) + (size_t)t * a.ld2 + (size_t)h * D;
+        load8(src + oa, x[0]);
+        load8(src + ob, x[1]);
+        turn(a.rope, s_cos + 8 * g, s_sin + 8 * g, x[0], x[1]);
+      }
+      store_row(0, h, g, oa, ob, x[0], x[1]);
+    } else if (u < keys + info) {
+      const int k = (u - keys) / kLanes, g = (u - keys) % kLanes;
+      const __bf16* src = static_cast<const __bf16*>(a.I) + (size_t)t * a.ldi + 16 * g;
+      if (a.mix) {
+        const int ha = a.pairing == 0 ? 2 * k : 2 * k + 1, hb = (ha + 1) % a.H_kv;
+        if (g < kGroups) {
+          const float c = pp.cos_theta[k], s = pp.sin_theta[k];
+#pragma unroll
+          for (int w = 0; w < 2; ++w) {
+            load8(src + (size_t)ha * D + 8 * w, x[w]);
+            load8(src + (size_t)hb * D + 8 * w, y[w]);
+          }
+#pragma unroll
+          for (int w = 0; w < 2; ++w)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const float p = x[w][e], q = y[w][e];
+              x[w][e] = fmaf(c, p, -s * q);
+              y[w][e] = fmaf(s, p, c * q);
+            }
+        }
+        store_row(1, ha, g, 16 * g, 16 * g + 8, x[0], x[1]);
+        store_row(1, hb, g, 16 * g, 16 * g + 8, y[0], y[1]);
+      } else {
+        if (g < kGroups) {
+          load8(src + (size_t)k * D, x[0]);
+          load8(src + (size_t)k * D + 8, x[1]);
+        }
+        store_row(1, k, g, 16 * g, 16 * g + 8, x[0], x[1]);
+      }
+    } else {
+      const int v = u - keys - info, h = v / kGroups, g = v % kGroups;
+      const int oa = a.rope == 2 ? 8 * g : 16 * g, ob = a.rope == 2 ? D / 2 + 8 * g : 16 * g + 8;
+      const __bf16* src = static_cast<const __bf16*>(a.P1) + (size_t)t * a.ld1 + (size_t)h * D;
+      __bf16* dst = static_cast<__bf16*>(a.P1o) + ((size_t)t * a.H + h) * D;
+      load8(src + oa, x[0]);
+      load8(src + ob, x[1]);
+      turn(a.rope, s_cos + 8 * g, s_sin + 8 * g, x[0], x[1]);
+      store8(dst + oa, x[0]);
+      store8(dst + ob, x[1]);
+    }
+  }
+}
+
 template <typename Tin, int D>
 hipError_t launch_typed(const PagedAppendArgs& a, const PrestepParams& pp, hipStream_t s) {
   // A launch has fewer than 2^32 threads.
@@ -158,7 +304,30 @@ hipError_t launch_typed(const PagedAppendArgs& a, const PrestepParams& pp, hipSt
   return hipSuccess;
 }
 
+template <int D>
+hipError_t launch_q8(const PagedAppendArgs& a, uint8_t* scale, const PrestepParams& pp, hipStream_t s) {
+  constexpr int kMost = 1 << 23;
+  for (int64_t first = 0; first < a.N; first += kMost) {
+    const unsigned n = (unsigned)(a.N - first < kMost ? a.N - first : kMost);
+    hipLaunchKernelGGL(paged_append_q8_kernel<D>, dim3(n), dim3(kThreads), 0, s, a, scale, pp, (int)first);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
 }  // namespace
+
+hipError_t launch_paged_append_q8(const PagedAppendArgs& a, uint8_t* scale, const PrestepParams& pp, hipStream_t s) {
+  switch (a.d_h) {
+    case 32: return launch_q8<32>(a, scale, pp, s);
+    case 48: return launch_q8<48>(a, scale, pp, s);
+    case 64: return launch_q8<64>(a, scale, pp, s);
+    case 80: return launch_q8<80>(a, scale, pp, s);
+    case 128: return launch_q8<128>(a, scale, pp, s);
+    default: return hipErrorInvalidValue;
+  }
+}
 
 hipError_t launch_paged_append(const PagedAppendArgs& a, const PrestepParams& pp, bool bf16, hipStream_t s) {
   switch (a.d_h) {

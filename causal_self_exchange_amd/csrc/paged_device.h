@@ -2,6 +2,8 @@
 // the workspace, the requests' numbers, and the last step of a row.
 #pragma once
 
+#include <type_traits>
+
 #include "mfma_tile.h"
 #include "rel_internal.h"
 #include "rel_device.h"
@@ -18,6 +20,10 @@ __device__ __forceinline__ int uni(int x) { return __builtin_amdgcn_readfirstlan
 __device__ __forceinline__ long long uni(long long x) {
   return (long long)((unsigned long long)(unsigned)uni((int)(x >> 32)) << 32 | (unsigned)uni((int)x));
 }
+
+// The arguments of the kernels for pages of type Tc and tokens of type Tin.
+template <typename Tin, typename Tc, bool kTree>
+using ScanArgs = typename std::conditional<kTree || !std::is_same<Tin, Tc>::value, PagedExArgs, PagedArgs>::type;
 
 // What the device-side numbers say of request b; q = 0 for one that is skipped.
 struct Req {
@@ -521,6 +527,54 @@ struct ChunkSource {
   }
 };
 
+// ---- 8-bit rows -----------------------------------------------------------------
+
+// The value of a scale byte: 2^(e - 127). 255, which is none, reads as 2^127, so that a
+// masked row's weight of 0 stays 0 whatever its page holds; 0 reads as 0.
+__device__ __forceinline__ float scale_of(unsigned e) { return __uint_as_float(min(e, 254u) << 23); }
+
+// Eight e4m3 values times a power of two, as bf16: exact where the product is a normal
+// bf16 number.
+__device__ __forceinline__ u32x4 e4m3_to_bf16(u32x2 x, float scale) {
+  return u32x4{__builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(x[0], scale, false)),
+               __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(x[0], scale, true)),
+               __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(x[1], scale, false)),
+               __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(x[1], scale, true))};
+}
+
+// Lane i of a group of 16 receives byte i % 8 of the 8-byte rows that the group's lanes
+// i / 8 + 2 k address, k = 0 .. 7.
+__device__ __forceinline__ u32x2 lds_tr8_read(const char* p) {
+  typedef int i32x2 __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr8_b64_v2i32((__attribute__((address_space(3))) i32x2*)(p)));
+}
+
+// ---- trees ----------------------------------------------------------------------
+
+// Which of the new tokens o .. o + 3 of its request the packed token t sees, in bits 0 to
+// 3: its ancestors, and all rows that were cached before (o < 0). Bits at and past its own
+// place are the caller's to mask.
+__device__ __forceinline__ unsigned tree_bits(const PagedExArgs& a, int t, int o) {
+  const uint32_t* const row = a.tree + (size_t)t * a.words;
+  const int w = o >> 5;
+  const unsigned lo = w < 0 ? ~0u : (w < a.words ? row[w] : 0u);
+  const unsigned hi = w + 1 < 0 ? ~0u : (w + 1 < a.words ? row[w + 1] : 0u);
+  return (unsigned)(((unsigned long long)hi << 32 | lo) >> (o & 31)) & 15u;
+}
+
+// How many new tokens the packed token t, the tq'th of its request, sees, by 16 lanes.
+__device__ __forceinline__ int ancestors(const PagedExArgs& a, int t, int tq, int sl) {
+  int n = 0;
+  for (int w = sl; 32 * w < tq; w += 16) {
+    const uint32_t x = a.tree[(size_t)t * a.words + w];
+    const int left = tq - 32 * w;
+    n += __popc(left < 32 ? x & ((1u << left) - 1) : x);
+  }
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) n += __shfl_xor(n, o, 16);
+  return n;
+}
+
 // ---- rows ---------------------------------------------------------------------
 
 // Eight elements as they lie in memory.
@@ -554,11 +608,12 @@ __device__ __forceinline__ void store8(Tin* p, const float (&x)[8]) {
 }
 
 // A row's own P1, P2 and V (zeros where it has none), by 16 lanes of 8 columns
-// each: loaded ahead of finish_row, behind whose table lookup they would wait.
-template <typename Tin, int D>
+// each: loaded ahead of finish_row, behind whose table lookup they would wait. 8-bit rows
+// become bf16 here, exactly.
+template <typename Tin, int D, typename Tc>
 struct OwnRow {
   Raw8<Tin> q, k, v;
-  __device__ __forceinline__ void load(const PagedArgs& a, int b, int t, int h, int pos, int sl, bool row_ok) {
+  __device__ __forceinline__ void load(const ScanArgs<Tin, Tc, false>& a, int b, int t, int h, int pos, int sl, bool row_ok) {
     q.zero();
     k.zero();
     v.zero();
@@ -566,11 +621,17 @@ struct OwnRow {
     const int page = a.table[(size_t)b * a.max_pages + (pos >> a.page_shift)];
     q.load(static_cast<const Tin*>(a.P1) + (size_t)t * a.ld1 + (size_t)h * D + 8 * sl);
     if (page >= 0 && page < a.n_pages) {
-      const int kvh = h / (a.H / a.H_kv);
-      const size_t row =
-          ((((size_t)page * a.H_kv + kvh) << a.page_shift) + (pos & ((1 << a.page_shift) - 1))) * D + 8 * sl;
-      k.load(static_cast<const Tin*>(a.cP2) + row);
-      v.load(static_cast<const Tin*>(a.cV) + row);
+      const int kvh = h / (a.H / a.H_kv), off = pos & ((1 << a.page_shift) - 1);
+      const size_t head = (size_t)page * a.H_kv + kvh, row = ((head << a.page_shift) + off) * D + 8 * sl;
+      if constexpr (sizeof(Tc) == 1) {
+        const uint8_t* const sc = a.scale + (head << (a.page_shift + 1)) + off;
+        k.w[0] = e4m3_to_bf16(*reinterpret_cast<const u32x2*>(static_cast<const uint8_t*>(a.cP2) + row), scale_of(sc[0]));
+        v.w[0] = e4m3_to_bf16(*reinterpret_cast<const u32x2*>(static_cast<const uint8_t*>(a.cV) + row),
+                              scale_of(sc[1 << a.page_shift]));
+      } else {
+        k.load(static_cast<const Tin*>(a.cP2) + row);
+        v.load(static_cast<const Tin*>(a.cV) + row);
+      }
     }
   }
 };
@@ -578,9 +639,10 @@ struct OwnRow {
 // Output of one row from its history's state, by 16 lanes of 8 columns each:
 // z (sum of weights times V), m (log2 stabiliser) and l (sum of weights); the
 // Self evidence and V come from the row's own cached row.
-template <typename Tin, int D>
-__device__ __forceinline__ void finish_row(const PagedArgs& a, const HeadParams& hp, const OwnRow<Tin, D>& own, int t,
-                                           int h, int pos, int sl, float m, float l, const float (&z)[8], bool row_ok) {
+// seen: the rows before its own that it sees.
+template <typename Tin, int D, typename Tc>
+__device__ __forceinline__ void finish_row(const PagedArgs& a, const HeadParams& hp, const OwnRow<Tin, D, Tc>& own, int t,
+                                           int h, int seen, int sl, float m, float l, const float (&z)[8], bool row_ok) {
   float u = 0.0f;
 #pragma unroll
   for (int e = 0; e < 8; ++e) u = fmaf(own.q[e], own.k[e], u);
@@ -588,7 +650,7 @@ __device__ __forceinline__ void finish_row(const PagedArgs& a, const HeadParams&
   for (int o = 8; o > 0; o >>= 1) u += __shfl_xor(u, o, 16);
   if (!row_ok || sl >= D / 8) return;
   const float S = sigmoid_f32(u * hp.scale * hp.inv_tau[h]);
-  const RowCombine c(S, m * kLn2, l, hp.lambda * logf((float)(pos + 1)));
+  const RowCombine c(S, m * kLn2, l, hp.lambda * logf((float)(seen + 1)));
   float y[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) y[e] = c.w_self * own.v[e] + c.w_hist * z[e];

@@ -1,0 +1,28 @@
+// The paged Relation Cache's forward of trees of drafted tokens over pages of the tokens'
+// own type (relation_paged_fwd_ex): the scan of paged_scan.h with a row of ancestor bits
+// per token. Only the steps that hold new tokens look at them.
+#include "paged_scan.h"
+
+namespace rel {
+
+namespace {
+
+template <typename Tin, int D>
+hipError_t launch_typed(const PagedExArgs& a, const HeadParams& hp, hipStream_t s) {
+  return launch_scan<Tin, D, Tin, true>(a, hp, s);
+}
+
+}  // namespace
+
+hipError_t launch_paged_tree(const PagedExArgs& a, const HeadParams& hp, bool bf16, hipStream_t s) {
+  switch (a.d_h) {
+    case 32: return bf16 ? launch_typed<__bf16, 32>(a, hp, s) : launch_typed<float, 32>(a, hp, s);
+    case 48: return bf16 ? launch_typed<__bf16, 48>(a, hp, s) : launch_typed<float, 48>(a, hp, s);
+    case 64: return bf16 ? launch_typed<__bf16, 64>(a, hp, s) : launch_typed<float, 64>(a, hp, s);
+    case 80: return bf16 ? launch_typed<__bf16, 80>(a, hp, s) : launch_typed<float, 80>(a, hp, s);
+    case 128: return bf16 ? launch_typed<__bf16, 128>(a, hp, s) : launch_typed<float, 128>(a, hp, s);
+    default: return hipErrorInvalidValue;
+  }
+}
+
+}  // namespace rel

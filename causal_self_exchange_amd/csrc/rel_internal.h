@@ -175,6 +175,40 @@ struct PagedArgs {
   int tiles;            // whether chunks may go to query tiles
 };
 
+// An element of an 8-bit page (OCP e4m3, finite and NaN).
+struct e4m3 { uint8_t bits; };
+
+struct PagedExArgs : PagedArgs {
+  const uint8_t* scale;   // [n_pages][H_kv][2][page]: exponents of the P2 and V rows (8-bit pages)
+  const uint32_t* tree;   // [N][words] ancestor bits, or null
+  int words;
+};
+
+struct TreePlanArgs {
+  const int32_t* parent;  // [N]
+  const int32_t* total;
+  const int32_t* cu;
+  uint32_t* tree;         // [N][words]
+  int32_t* pos;           // [N]
+  int N, S, words;
+};
+
+struct PagedKeepArgs {
+  void* cP2;
+  void* cV;
+  uint8_t* scale;         // 8-bit pages, else null
+  const int32_t* table;
+  const int32_t* total;
+  const int32_t* cu;
+  const int32_t* keep;    // [N]
+  const int32_t* n_keep;  // [S]
+  int32_t* lens;          // [S]
+  int32_t* free_pages;    // [F]
+  const int32_t* n_free;
+  int32_t* n_free_out;
+  int N, S, H_kv, row_bytes, n_pages, page_shift, max_pages, F;
+};
+
 // Workspace of relation_paged_fwd (paged_device.h): the work sums of batches of
 // more than kPlanInline requests (two 64-bit ones), a 48-byte record per
 // work-group and the partial states (m, l) and z[d_h] of the scan kernel's row
@@ -268,7 +302,13 @@ hipError_t launch_cache_append(void* cP2, void* cV, int32_t* len, const void* p2
                                int B, int H, int L_cap, int d_h, bool bf16, hipStream_t s);
 hipError_t launch_page_map(const PageMapArgs& a, hipStream_t s);
 hipError_t launch_paged_append(const PagedAppendArgs& a, const PrestepParams& pp, bool bf16, hipStream_t s);
+hipError_t launch_paged_append_q8(const PagedAppendArgs& a, uint8_t* scale, const PrestepParams& pp, hipStream_t s);
+hipError_t launch_tree_plan(const TreePlanArgs& a, hipStream_t s);
+hipError_t launch_paged_keep(const PagedKeepArgs& a, hipStream_t s);
 hipError_t launch_paged(const PagedArgs& a, const HeadParams& hp, bool bf16, hipStream_t s);
+// The same with a tree, and over 8-bit pages (tokens in bf16, tree optional).
+hipError_t launch_paged_tree(const PagedExArgs& a, const HeadParams& hp, bool bf16, hipStream_t s);
+hipError_t launch_paged_q8(const PagedExArgs& a, const HeadParams& hp, hipStream_t s);
 // The chunks of the batch that fill query tiles (bf16), without the joining of
 // divided tiles.
 hipError_t launch_paged_chunk(const PagedArgs& a, const HeadParams& hp, int groups, hipStream_t s);

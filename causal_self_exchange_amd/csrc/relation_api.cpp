@@ -249,12 +249,20 @@ rel_status relation_page_map(const int32_t* len, const int32_t* n_new, int32_t* 
   return rel::launch_page_map(a, stream) == hipSuccess ? REL_OK : REL_E_LAUNCH;
 }
 
-rel_status relation_paged_append(const void* P1, const void* P2, const void* I, int64_t ld1, int64_t ld2,
-                                 int64_t ldi, const int32_t* slot, const int32_t* pos, rel_rope rope,
-                                 float rope_base, const float* theta, rel_pairing pairing, void* P1o,
-                                 void* cache_P2, void* cache_V, int N, int H, int H_kv, int d_h, int n_pages,
-                                 int page_size, rel_dtype dt, hipStream_t stream) {
-  if (!P2 || !I || !slot || !cache_P2 || !cache_V || !P1 != !P1o || (!pos && rope != REL_ROPE_NONE))
+}  // extern "C"
+
+namespace {
+
+// Bytes of the scales of an 8-bit cache of nc elements.
+size_t scale_bytes(int64_t nc, int d_h) { return static_cast<size_t>(nc / d_h) * 2; }
+
+// relation_paged_append (scale null, q8 false) and relation_paged_append_q8.
+rel_status append_impl(const void* P1, const void* P2, const void* I, int64_t ld1, int64_t ld2,
+                       int64_t ldi, const int32_t* slot, const int32_t* pos, rel_rope rope,
+                       float rope_base, const float* theta, rel_pairing pairing, void* P1o,
+                       void* cache_P2, void* cache_V, void* scale, bool q8, int N, int H, int H_kv, int d_h,
+                       int n_pages, int page_size, rel_dtype dt, hipStream_t stream) {
+  if (!P2 || !I || !slot || !cache_P2 || !cache_V || (q8 && !scale) || !P1 != !P1o || (!pos && rope != REL_ROPE_NONE))
     return REL_E_NULL;
   if (!P1) H = 0;
   int64_t nc = 0;
@@ -269,22 +277,47 @@ rel_status relation_paged_append(const void* P1, const void* P2, const void* I, 
     return REL_E_STRIDE;
   if (!prestep_modes_ok(rope, rope_base, theta, pairing, H_kv)) return REL_E_PRESTEP;
   if (!aligned16(P1) || !aligned16(P2) || !aligned16(I) || !aligned16(P1o) || !aligned16(cache_P2) ||
-      !aligned16(cache_V) || !aligned4(slot) || !aligned4(pos))
+      !aligned16(cache_V) || !aligned16(scale) || !aligned4(slot) || !aligned4(pos))
     return REL_E_ALIGN;
   const bool in_place = P1 && P1o == P1 && ld1 == static_cast<int64_t>(H) * d_h;
-  const size_t nb = static_cast<size_t>(N) * 4, cb = static_cast<size_t>(nc) * es;
+  const size_t nb = static_cast<size_t>(N) * 4, cb = static_cast<size_t>(nc) * (q8 ? 1 : es);
   const Range ins[] = {{P1, P1 && !in_place ? strided_bytes(N, ld1, H, d_h, es) : 0},
                        {P2, strided_bytes(N, ld2, H_kv, d_h, es)},
                        {I, strided_bytes(N, ldi, H_kv, d_h, es)},
                        {slot, nb}, {pos, pos ? nb : 0}};
-  const Range outs[] = {{P1o, P1 ? static_cast<size_t>(N) * H * d_h * es : 0}, {cache_P2, cb}, {cache_V, cb}};
+  const Range outs[] = {{P1o, P1 ? static_cast<size_t>(N) * H * d_h * es : 0}, {cache_P2, cb}, {cache_V, cb},
+                        {scale, q8 ? scale_bytes(nc, d_h) : 0}};
   if (any_alias(ins, outs)) return REL_E_ALIAS;
   rel::PrestepParams pp;
   fill_prestep_params(pp, rope != REL_ROPE_NONE, rope_base, theta, H_kv, d_h);
   const rel::PagedAppendArgs a{P1, P2, I, ld1, ld2, ldi, slot, pos, P1o, cache_P2, cache_V, N, H, H_kv, d_h,
                                n_pages, page_shift_of(page_size), static_cast<int>(rope),
                                pairing == REL_PAIRS_A ? 0 : 1, theta ? 1 : 0};
-  return rel::launch_paged_append(a, pp, dt == REL_BF16, stream) == hipSuccess ? REL_OK : REL_E_LAUNCH;
+  const hipError_t e = q8 ? rel::launch_paged_append_q8(a, static_cast<uint8_t*>(scale), pp, stream)
+                          : rel::launch_paged_append(a, pp, dt == REL_BF16, stream);
+  return e == hipSuccess ? REL_OK : REL_E_LAUNCH;
+}
+
+}  // namespace
+
+extern "C" {
+
+rel_status relation_paged_append(const void* P1, const void* P2, const void* I, int64_t ld1, int64_t ld2,
+                                 int64_t ldi, const int32_t* slot, const int32_t* pos, rel_rope rope,
+                                 float rope_base, const float* theta, rel_pairing pairing, void* P1o,
+                                 void* cache_P2, void* cache_V, int N, int H, int H_kv, int d_h, int n_pages,
+                                 int page_size, rel_dtype dt, hipStream_t stream) {
+  return append_impl(P1, P2, I, ld1, ld2, ldi, slot, pos, rope, rope_base, theta, pairing, P1o, cache_P2, cache_V,
+                     nullptr, false, N, H, H_kv, d_h, n_pages, page_size, dt, stream);
+}
+
+rel_status relation_paged_append_q8(const void* P1, const void* P2, const void* I, int64_t ld1, int64_t ld2,
+                                    int64_t ldi, const int32_t* slot, const int32_t* pos, rel_rope rope,
+                                    float rope_base, const float* theta, rel_pairing pairing, void* P1o,
+                                    void* cache_P2, void* cache_V, void* cache_scale, int N, int H, int H_kv,
+                                    int d_h, int n_pages, int page_size, hipStream_t stream) {
+  return append_impl(P1, P2, I, ld1, ld2, ldi, slot, pos, rope, rope_base, theta, pairing, P1o, cache_P2, cache_V,
+                     cache_scale, true, N, H, H_kv, d_h, n_pages, page_size, REL_BF16, stream);
 }
 
 size_t relation_paged_workspace_bytes(int N, int S, int H, int H_kv, int d_h) {
@@ -294,16 +327,25 @@ size_t relation_paged_workspace_bytes(int N, int S, int H, int H_kv, int d_h) {
   return rel::paged_ws_bytes(N, S, H / H_kv, d_h);
 }
 
-rel_status relation_paged_fwd(const void* P1, int64_t ld1, const void* cache_P2, const void* cache_V,
-                              const int32_t* block_table, const int32_t* total, const int32_t* cu,
-                              const float* tau_s, float lambda, void* Y, int N, int S, int H, int H_kv,
-                              int d_h, int n_pages, int page_size, int max_pages, int max_new, rel_dtype dt,
-                              void* workspace, size_t ws_bytes, hipStream_t stream) {
+}  // extern "C"
+
+namespace {
+
+// relation_paged_fwd (ex false, no scales, no tree) and relation_paged_fwd_ex.
+rel_status paged_fwd_impl(const void* P1, int64_t ld1, const void* cache_P2, const void* cache_V, const void* scale,
+                          const int32_t* block_table, const int32_t* total, const int32_t* cu, const int32_t* tree,
+                          int words, const float* tau_s, float lambda, void* Y, int N, int S, int H, int H_kv,
+                          int d_h, int n_pages, int page_size, int max_pages, int max_new, rel_dtype dt, bool ex,
+                          void* workspace, size_t ws_bytes, hipStream_t stream) {
   if (!P1 || !cache_P2 || !cache_V || !block_table || !total || !cu || !tau_s || !Y) return REL_E_NULL;
   int64_t nc = 0, ny = 0, nt = 0;
   if (N < 1 || S < 1 || S > 65535 || H < 1 || H > REL_MAX_HEADS || H_kv < 1 || max_new < 1) return REL_E_SHAPE;
   if (H % H_kv != 0) return REL_E_GROUP;
-  if (!dtype_ok(dt)) return REL_E_DTYPE;
+  const bool q8 = dt == REL_E4M3;
+  if (!(ex && q8) && !dtype_ok(dt)) return REL_E_DTYPE;
+  if (q8 && !scale) return REL_E_NULL;
+  if (!q8 && scale) return REL_E_DTYPE;
+  if (tree ? words < 1 || words > REL_MAX_TREE_WORDS : words != 0) return REL_E_SHAPE;
   if (!fwd_head_dim_ok(d_h)) return REL_E_HEADDIM;
   if (!page_counts_ok(n_pages, page_size) || !page_counts_ok(max_pages, page_size)) return REL_E_PAGE;
   if (!count(nc, {n_pages, H_kv, page_size, d_h}) || !count(ny, {N, H, d_h}) || !count(nt, {S, max_pages}) ||
@@ -312,23 +354,99 @@ rel_status relation_paged_fwd(const void* P1, int64_t ld1, const void* cache_P2,
   HeadParams hp;
   const rel_status st = pack_heads(hp, tau_s, H, d_h, lambda);
   if (st != REL_OK) return st;
-  const size_t es = elem_size(dt);
+  const size_t es = q8 ? 2 : elem_size(dt);
   if (!stride_ok(ld1, H, d_h, es)) return REL_E_STRIDE;
   const size_t need = relation_paged_workspace_bytes(N, S, H, H_kv, d_h);
   if (!workspace || ws_bytes < need) return REL_E_WORKSPACE;
   if (!aligned16(P1) || !aligned16(cache_P2) || !aligned16(cache_V) || !aligned16(Y) || !aligned16(workspace) ||
-      !aligned4(block_table) || !aligned4(total) || !aligned4(cu))
+      !aligned16(scale) || !aligned4(tree) || !aligned4(block_table) || !aligned4(total) || !aligned4(cu))
     return REL_E_ALIGN;
-  const size_t cb = static_cast<size_t>(nc) * es;
+  const size_t cb = static_cast<size_t>(nc) * (q8 ? 1 : es);
   const Range ins[] = {{P1, strided_bytes(N, ld1, H, d_h, es)}, {cache_P2, cb}, {cache_V, cb},
                        {block_table, static_cast<size_t>(nt) * 4}, {total, static_cast<size_t>(S) * 4},
-                       {cu, static_cast<size_t>(S) * 4 + 4}};
+                       {cu, static_cast<size_t>(S) * 4 + 4}, {scale, q8 ? scale_bytes(nc, d_h) : 0},
+                       {tree, static_cast<size_t>(N) * words * 4}};
   const Range outs[] = {{Y, static_cast<size_t>(ny) * es}, {workspace, need}};
   if (any_alias(ins, outs)) return REL_E_ALIAS;
-  const rel::PagedArgs a{P1, ld1, cache_P2, cache_V, block_table, total, cu, Y, workspace, N, S, H, H_kv, d_h,
-                         n_pages, page_shift_of(page_size), max_pages, max_new,
-                         dt == REL_BF16 && !fwd_scan_selected()};
-  return rel::launch_paged(a, hp, dt == REL_BF16, stream) == hipSuccess ? REL_OK : REL_E_LAUNCH;
+  const rel::PagedExArgs a{{P1, ld1, cache_P2, cache_V, block_table, total, cu, Y, workspace, N, S, H, H_kv, d_h,
+                            n_pages, page_shift_of(page_size), max_pages, max_new,
+                            dt == REL_BF16 && !fwd_scan_selected()},
+                           static_cast<const uint8_t*>(scale), reinterpret_cast<const uint32_t*>(tree), words};
+  const hipError_t e = q8     ? rel::launch_paged_q8(a, hp, stream)
+                       : tree ? rel::launch_paged_tree(a, hp, dt == REL_BF16, stream)
+                              : rel::launch_paged(a, hp, dt == REL_BF16, stream);
+  return e == hipSuccess ? REL_OK : REL_E_LAUNCH;
+}
+
+}  // namespace
+
+extern "C" {
+
+rel_status relation_paged_fwd(const void* P1, int64_t ld1, const void* cache_P2, const void* cache_V,
+                              const int32_t* block_table, const int32_t* total, const int32_t* cu,
+                              const float* tau_s, float lambda, void* Y, int N, int S, int H, int H_kv,
+                              int d_h, int n_pages, int page_size, int max_pages, int max_new, rel_dtype dt,
+                              void* workspace, size_t ws_bytes, hipStream_t stream) {
+  return paged_fwd_impl(P1, ld1, cache_P2, cache_V, nullptr, block_table, total, cu, nullptr, 0, tau_s, lambda, Y, N, S,
+                        H, H_kv, d_h, n_pages, page_size, max_pages, max_new, dt, false, workspace, ws_bytes, stream);
+}
+
+rel_status relation_paged_fwd_ex(const void* P1, int64_t ld1, const void* cache_P2, const void* cache_V,
+                                 const void* cache_scale, const int32_t* block_table, const int32_t* total,
+                                 const int32_t* cu, const int32_t* tree, int tree_words, const float* tau_s,
+                                 float lambda, void* Y, int N, int S, int H, int H_kv, int d_h, int n_pages,
+                                 int page_size, int max_pages, int max_new, rel_dtype pages, void* workspace,
+                                 size_t ws_bytes, hipStream_t stream) {
+  return paged_fwd_impl(P1, ld1, cache_P2, cache_V, cache_scale, block_table, total, cu, tree, tree_words, tau_s, lambda,
+                        Y, N, S, H, H_kv, d_h, n_pages, page_size, max_pages, max_new, pages, true, workspace, ws_bytes,
+                        stream);
+}
+
+rel_status relation_tree_plan(const int32_t* parent, const int32_t* total, const int32_t* cu, int32_t* tree,
+                              int32_t* pos, int N, int S, int tree_words, hipStream_t stream) {
+  if (!parent || !total || !cu || !tree || !pos) return REL_E_NULL;
+  if (N < 1 || S < 1 || S > 65535 || tree_words < 1 || tree_words > REL_MAX_TREE_WORDS) return REL_E_SHAPE;
+  const void* all[] = {parent, total, cu, tree, pos};
+  for (const void* p : all)
+    if (!aligned4(p)) return REL_E_ALIGN;
+  const size_t nb = static_cast<size_t>(N) * 4, sb = static_cast<size_t>(S) * 4;
+  const Range ins[] = {{parent, nb}, {total, sb}, {cu, sb + 4}};
+  const Range outs[] = {{tree, nb * tree_words}, {pos, nb}};
+  if (any_alias(ins, outs)) return REL_E_ALIAS;
+  const rel::TreePlanArgs a{parent, total, cu, reinterpret_cast<uint32_t*>(tree), pos, N, S, tree_words};
+  return rel::launch_tree_plan(a, stream) == hipSuccess ? REL_OK : REL_E_LAUNCH;
+}
+
+rel_status relation_paged_keep(void* cache_P2, void* cache_V, void* cache_scale, const int32_t* block_table,
+                               const int32_t* total, const int32_t* cu, const int32_t* keep, const int32_t* n_keep,
+                               int32_t* len, int32_t* free_pages, const int32_t* n_free, int32_t* n_free_out, int N,
+                               int S, int F, int H_kv, int d_h, int n_pages, int page_size, int max_pages,
+                               rel_dtype pages, hipStream_t stream) {
+  const bool q8 = pages == REL_E4M3;
+  if (!cache_P2 || !cache_V || (q8 && !cache_scale) || !block_table || !total || !cu || !keep || !n_keep || !len ||
+      !free_pages || !n_free || !n_free_out)
+    return REL_E_NULL;
+  int64_t nc = 0, nt = 0;
+  if (N < 1 || S < 1 || S > 65535 || F < 1 || H_kv < 1 || H_kv > REL_MAX_HEADS) return REL_E_SHAPE;
+  if ((!q8 && !dtype_ok(pages)) || (!q8 && cache_scale)) return REL_E_DTYPE;
+  if (!fwd_head_dim_ok(d_h)) return REL_E_HEADDIM;
+  if (!page_counts_ok(n_pages, page_size) || !page_counts_ok(max_pages, page_size)) return REL_E_PAGE;
+  if (!count(nc, {n_pages, H_kv, page_size, d_h}) || !count(nt, {S, max_pages})) return REL_E_SHAPE;
+  if (!aligned16(cache_P2) || !aligned16(cache_V) || !aligned16(cache_scale)) return REL_E_ALIGN;
+  const void* words[] = {block_table, total, cu, keep, n_keep, len, free_pages, n_free, n_free_out};
+  for (const void* p : words)
+    if (!aligned4(p)) return REL_E_ALIGN;
+  const size_t es = q8 ? 1 : elem_size(pages), cb = static_cast<size_t>(nc) * es, sb = static_cast<size_t>(S) * 4;
+  // n_free_out may be n_free (in place).
+  const Range ins[] = {{block_table, static_cast<size_t>(nt) * 4}, {total, sb}, {cu, sb + 4},
+                       {keep, static_cast<size_t>(N) * 4}, {n_keep, sb}, {n_free, n_free_out == n_free ? 0u : 4u}};
+  const Range outs[] = {{cache_P2, cb}, {cache_V, cb}, {cache_scale, q8 ? scale_bytes(nc, d_h) : 0}, {len, sb},
+                        {free_pages, static_cast<size_t>(F) * 4}, {n_free_out, 4}};
+  if (any_alias(ins, outs)) return REL_E_ALIAS;
+  const rel::PagedKeepArgs a{cache_P2, cache_V, static_cast<uint8_t*>(cache_scale), block_table, total, cu, keep, n_keep,
+                             len, free_pages, n_free, n_free_out, N, S, H_kv, static_cast<int>(d_h * es), n_pages,
+                             page_shift_of(page_size), max_pages, F};
+  return rel::launch_paged_keep(a, stream) == hipSuccess ? REL_OK : REL_E_LAUNCH;
 }
 
 const char* relation_status_str(rel_status s) {

@@ -17,7 +17,7 @@ import torch
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "librelation.so")
 
-REL_F32, REL_BF16 = 0, 1
+REL_F32, REL_BF16, REL_E4M3 = 0, 1, 2
 _DT = {torch.float32: REL_F32, torch.bfloat16: REL_BF16}
 
 _lib = None
@@ -79,6 +79,15 @@ def lib() -> ctypes.CDLL:
         L.relation_paged_fwd.argtypes = [vp, l64, vp, vp, vp, vp, vp, fp, f, vp, i, i, i, i, i, i, i, i, i, i,
                                          vp, sz, vp]
         L.relation_paged_fwd.restype = i
+        L.relation_paged_append_q8.argtypes = [vp, vp, vp, l64, l64, l64, vp, vp, i, f, fp, i, vp, vp, vp, vp,
+                                               i, i, i, i, i, i, vp]
+        L.relation_paged_append_q8.restype = i
+        L.relation_tree_plan.argtypes = [vp] * 5 + [i] * 3 + [vp]
+        L.relation_tree_plan.restype = i
+        L.relation_paged_fwd_ex.argtypes = [vp, l64, vp, vp, vp, vp, vp, vp, vp, i, fp, f, vp] + [i] * 10 + [vp, sz, vp]
+        L.relation_paged_fwd_ex.restype = i
+        L.relation_paged_keep.argtypes = [vp] * 12 + [i] * 9 + [vp]
+        L.relation_paged_keep.restype = i
         L.relation_status_str.argtypes = [i]
         L.relation_status_str.restype = ctypes.c_char_p
         L.relation_select_kernels.argtypes = [i, i]
@@ -92,7 +101,8 @@ EXPORTS = ("relation_fwd", "relation_fwd_ex", "relation_fwd_lse", "relation_bwd_
            "relation_fwd_model", "relation_linear_workspace_bytes", "relation_linear_fwd",
            "relation_decode_workspace_bytes", "relation_decode", "relation_decode_noalloc",
            "relation_cache_append", "relation_page_map", "relation_paged_append",
-           "relation_paged_workspace_bytes", "relation_paged_fwd", "relation_status_str", "relation_select_kernels")
+           "relation_paged_workspace_bytes", "relation_paged_fwd", "relation_paged_append_q8", "relation_tree_plan",
+           "relation_paged_fwd_ex", "relation_paged_keep", "relation_status_str", "relation_select_kernels")
 
 KERNELS = {"auto": 0, "scan": 1}
 
@@ -574,6 +584,16 @@ def _table(fn, t):
     return t.shape
 
 
+def _token_dtype(fn, specs, cdt, shp, scale):
+    """The tokens' type for pages of type cdt; 8-bit pages have scales, which join specs."""
+    if cdt is torch.float8_e4m3fn:
+        specs.append(("scale", scale, (shp[0], shp[1], 2, shp[2]), torch.float8_e8m0fnu, True))
+        return torch.bfloat16
+    if scale is not None:
+        raise TypeError(f"{fn}: scale belongs to float8_e4m3fn pages, these are {cdt}")
+    return cdt
+
+
 def _ld(t) -> int:
     """Elements between consecutive tokens of a packed [N, heads, d_h] tensor."""
     return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
@@ -613,19 +633,24 @@ def page_map(lens, n_new, block_table, free_pages, n_free, N: int, page_size: in
 
 
 def paged_append(P2, I, slot, cache_P2, cache_V, P1=None, pos=None, rope="none", rope_base: float = 1e4, theta=None,
-                 pairing="A", out=None, stream=None):
+                 pairing="A", out=None, stream=None, scale=None):
     """Pre-steps of a packed batch with P2 and the mixed I stored into the pages:
     P2, I [N, H_kv, d_h] and optionally P1 [N, H, d_h] (tokens may be slices of a
-    fused projection), slot and pos int32[N] (page_map), caches [n_pages, H_kv,
-    page_size, d_h]. Returns the rotated P1 ([N, H, d_h]; out, which may be P1
+    fused projection), slot and pos int32[N] (page_map, tree_plan), caches [n_pages,
+    H_kv, page_size, d_h]. Returns the rotated P1 ([N, H, d_h]; out, which may be P1
     itself if contiguous) or None. Rows of tokens without a slot are not written
-    (zero in a P1 that the call allocates)."""
+    (zero in a P1 that the call allocates).
+
+    8-bit pages: float8_e4m3fn caches with scale, float8_e8m0fnu [n_pages, H_kv, 2,
+    page_size] (of the P2 and the V rows), and bfloat16 tokens, quantised as they are
+    stored."""
     fn = "paged_append"
     n_pages, Hkv, ps, D = shp = _pages(fn, cache_P2)
     N = _tokens(fn, "P2", P2)[0]
-    dt, H = cache_P2.dtype, 0
-    specs = [("cache_P2", cache_P2, shp, dt, True), ("cache_V", cache_V, shp, dt, True),
-             ("P2", P2, (N, Hkv, D), dt, False), ("I", I, (N, Hkv, D), dt, False), ("slot", slot, (N,), _I32, True)]
+    cdt, H = cache_P2.dtype, 0
+    specs = [("cache_P2", cache_P2, shp, cdt, True), ("cache_V", cache_V, shp, cdt, True)]
+    dt = _token_dtype(fn, specs, cdt, shp, scale)
+    specs += [("P2", P2, (N, Hkv, D), dt, False), ("I", I, (N, Hkv, D), dt, False), ("slot", slot, (N,), _I32, True)]
     if pos is not None:
         specs.append(("pos", pos, (N,), _I32, True))
     if P1 is not None:
@@ -641,11 +666,12 @@ def paged_append(P2, I, slot, cache_P2, cache_V, P1=None, pos=None, rope="none",
     if P1 is not None and out is None:
         with _on(stream):
             out = torch.zeros((N, H, D), dtype=dt, device=dev)
-    _run_on("relation_paged_append", dev, stream,
+    name, pages = ("relation_paged_append", ()) if scale is None else ("relation_paged_append_q8", (scale.data_ptr(),))
+    _run_on(name, dev, stream,
             (_ptr(P1), P2.data_ptr(), I.data_ptr(), 0 if P1 is None else _ld(P1), _ld(P2), _ld(I), slot.data_ptr(),
              _ptr(pos), ROPE[rope], float(rope_base), None if theta is None else _host_floats(theta, Hkv // 2),
-             PAIRS[pairing], _ptr(out), cache_P2.data_ptr(), cache_V.data_ptr(), N, H, Hkv, D, n_pages, ps,
-             _dtype_code(cache_P2)))
+             PAIRS[pairing], _ptr(out), cache_P2.data_ptr(), cache_V.data_ptr(), *pages, N, H, Hkv, D, n_pages, ps,
+             *(() if pages else (_dtype_code(cache_P2),))))
     return out
 
 
@@ -654,20 +680,30 @@ def paged_workspace_bytes(N: int, S: int, H: int, H_kv: int, d_h: int) -> int:
 
 
 def paged_fwd(P1, cache_P2, cache_V, block_table, total, cu, tau, lam: float = 0.0, max_new=None, out=None,
-              workspace=None, stream=None):
+              workspace=None, stream=None, scale=None, tree=None):
     """Y [N, H, d_h] of a packed batch of new tokens whose own rows are in the
     pages already: P1 [N, H, d_h] (rotated), caches [n_pages, H_kv, page_size,
     d_h], block_table int32[S, max_pages], total int32[S], cu int32[S+1]
     (page_map). max_new: the most new tokens of one request (default N). Rows that
-    no request owns are not written (zero in a Y that the call allocates)."""
+    no request owns are not written (zero in a Y that the call allocates).
+
+    8-bit pages: float8_e4m3fn caches with scale (paged_append) and a bfloat16 P1.
+    tree: int32[N, words] ancestor bits (tree_plan): a token of a request of at most
+    32 * words new tokens sees, of those, its ancestors and itself alone."""
     fn = "paged_fwd"
     n_pages, Hkv, ps, D = shp = _pages(fn, cache_P2)
     N, H = _tokens(fn, "P1", P1)[:2]
     S, width = _table(fn, block_table)
-    dt = cache_P2.dtype
-    specs = [("cache_P2", cache_P2, shp, dt, True), ("cache_V", cache_V, shp, dt, True), ("P1", P1, (N, H, D), dt, False),
-             ("block_table", block_table, (S, width), _I32, True), ("total", total, (S,), _I32, True),
-             ("cu", cu, (S + 1,), _I32, True)]
+    cdt = cache_P2.dtype
+    specs = [("cache_P2", cache_P2, shp, cdt, True), ("cache_V", cache_V, shp, cdt, True)]
+    dt = _token_dtype(fn, specs, cdt, shp, scale)
+    specs += [("P1", P1, (N, H, D), dt, False),
+              ("block_table", block_table, (S, width), _I32, True), ("total", total, (S,), _I32, True),
+              ("cu", cu, (S + 1,), _I32, True)]
+    words = 0
+    if tree is not None:
+        words = _tree_words(fn, tree)
+        specs.append(("tree", tree, (N, words), _I32, True))
     if out is not None:
         specs.append(("out", out, (N, H, D), dt, True))
     need = paged_workspace_bytes(N, S, H, Hkv, D)
@@ -685,8 +721,89 @@ def paged_fwd(P1, cache_P2, cache_V, block_table, total, cu, tau, lam: float = 0
                 out = torch.zeros((N, H, D), dtype=dt, device=dev)
             if workspace is None:
                 workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
-    _run_on("relation_paged_fwd", dev, stream,
-            (P1.data_ptr(), _ld(P1), cache_P2.data_ptr(), cache_V.data_ptr(), block_table.data_ptr(), total.data_ptr(),
-             cu.data_ptr(), _host_floats(tau, H), float(lam), out.data_ptr(), N, S, H, Hkv, D, n_pages, ps, width,
-             max_new, _dtype_code(P1), workspace.data_ptr(), workspace.numel()))
+    args = (block_table.data_ptr(), total.data_ptr(), cu.data_ptr())
+    if scale is None and tree is None:
+        fn, args, pages = "relation_paged_fwd", args, _dtype_code(P1)
+    else:
+        fn, args = "relation_paged_fwd_ex", (_ptr(scale), *args, _ptr(tree), words)
+        pages = REL_E4M3 if scale is not None else _dtype_code(P1)
+    _run_on(fn, dev, stream,
+            (P1.data_ptr(), _ld(P1), cache_P2.data_ptr(), cache_V.data_ptr(), *args, _host_floats(tau, H), float(lam),
+             out.data_ptr(), N, S, H, Hkv, D, n_pages, ps, width, max_new, pages, workspace.data_ptr(),
+             workspace.numel()))
     return out
+
+
+# ---- trees of drafted tokens -------------------------------------------------------
+
+MAX_TREE_WORDS = 32
+
+
+def _tree_words(fn, tree) -> int:
+    if not isinstance(tree, torch.Tensor) or tree.dim() != 2 or not 1 <= tree.shape[1] <= MAX_TREE_WORDS:
+        raise ValueError(f"{fn}: tree must be an [N, words] tensor of 1 to {MAX_TREE_WORDS} words")
+    return tree.shape[1]
+
+
+def tree_plan(parent, total, cu, words: int, out=None, stream=None):
+    """Ancestor bits and positions of packed trees of drafted tokens: parent int32[N],
+    each token's parent as its place among its request's new tokens (outside [0, own
+    place): a root), total int32[S], cu int32[S+1] (page_map). Requests of more than
+    32 * words new tokens are chunks, each token seeing all before it. Returns (tree
+    [N, words], pos [N]) int32; out: the two tensors. Rows of tree that no tree's token
+    owns are not written (zero in a tree that the call allocates)."""
+    fn = "tree_plan"
+    for name, t in (("parent", parent), ("total", total)):
+        if not isinstance(t, torch.Tensor) or t.dim() != 1:
+            raise ValueError(f"{fn}: {name} must be a 1-d tensor")
+    N, S, words = _count("N", parent.shape[0]), total.shape[0], int(words)
+    if not 1 <= words <= MAX_TREE_WORDS:
+        raise ValueError(f"{fn}: words must be 1 to {MAX_TREE_WORDS}, not {words}")
+    specs = [("parent", parent, (N,), _I32, True), ("total", total, (S,), _I32, True), ("cu", cu, (S + 1,), _I32, True)]
+    if out is not None:
+        if len(out) != 2:
+            raise ValueError(f"{fn}: out must be (tree, pos)")
+        specs += [("tree", out[0], (N, words), _I32, True), ("pos", out[1], (N,), _I32, True)]
+    dev = _check_tensors(fn, specs)
+    if out is None:
+        with _on(stream):
+            out = (torch.zeros((N, words), dtype=_I32, device=dev), torch.empty(N, dtype=_I32, device=dev))
+    _run_on("relation_tree_plan", dev, stream,
+            (parent.data_ptr(), total.data_ptr(), cu.data_ptr(), out[0].data_ptr(), out[1].data_ptr(), N, S, words))
+    return out
+
+
+def paged_keep(cache_P2, cache_V, block_table, total, cu, keep, n_keep, lens, free_pages, n_free, n_free_out=None,
+               scale=None, stream=None):
+    """Cuts each request back to the new tokens that it keeps: request b keeps n_keep[b]
+    (int32[S]), whose places among its new tokens keep[cu[b]:] (int32[N]) names in
+    growing order. Their rows move to the front of the new ones (caches, and scale for
+    float8_e4m3fn ones, in place), lens int32[S] becomes the cached rows, and the pages
+    behind them go back to free_pages int32[F] (n_free int32[1] entries). Returns the
+    list's new count, int32[1] (n_free_out, which may be n_free)."""
+    fn = "paged_keep"
+    n_pages, Hkv, ps, D = shp = _pages(fn, cache_P2)
+    S, width = _table(fn, block_table)
+    for name, t in (("keep", keep), ("free_pages", free_pages)):
+        if not isinstance(t, torch.Tensor) or t.dim() != 1:
+            raise ValueError(f"{fn}: {name} must be a 1-d tensor")
+    N, F = _count("N", keep.shape[0]), _count("F", free_pages.shape[0])
+    cdt = cache_P2.dtype
+    specs = [("cache_P2", cache_P2, shp, cdt, True), ("cache_V", cache_V, shp, cdt, True)]
+    _token_dtype(fn, specs, cdt, shp, scale)
+    specs += [("block_table", block_table, (S, width), _I32, True), ("total", total, (S,), _I32, True),
+              ("cu", cu, (S + 1,), _I32, True), ("keep", keep, (N,), _I32, True), ("n_keep", n_keep, (S,), _I32, True),
+              ("lens", lens, (S,), _I32, True), ("free_pages", free_pages, (F,), _I32, True),
+              ("n_free", n_free, (1,), _I32, True)]
+    if n_free_out is not None:
+        specs.append(("n_free_out", n_free_out, (1,), _I32, True))
+    pages = REL_E4M3 if cdt is torch.float8_e4m3fn else _dtype_code(cache_P2)
+    dev = _check_tensors(fn, specs)
+    if n_free_out is None:
+        with _on(stream):
+            n_free_out = torch.empty(1, dtype=_I32, device=dev)
+    _run_on("relation_paged_keep", dev, stream,
+            (cache_P2.data_ptr(), cache_V.data_ptr(), _ptr(scale), block_table.data_ptr(), total.data_ptr(), cu.data_ptr(),
+             keep.data_ptr(), n_keep.data_ptr(), lens.data_ptr(), free_pages.data_ptr(), n_free.data_ptr(),
+             n_free_out.data_ptr(), N, S, F, Hkv, D, n_pages, ps, width, pages))
+    return n_free_out

@@ -80,7 +80,11 @@ typedef enum {
   REL_E_STRIDE = 15    /* a token stride is too small or not 16-byte sized   */
 } rel_status;
 
-typedef enum { REL_F32 = 0, REL_BF16 = 1 } rel_dtype;
+typedef enum {
+  REL_F32 = 0,
+  REL_BF16 = 1,
+  REL_E4M3 = 2   /* 8-bit pages of the paged Relation Cache only (with bf16 tokens) */
+} rel_dtype;
 
 /* Rotary pair convention of the pre-step: pair k turns by pos * base^(-2k/d_h). */
 typedef enum {
@@ -496,6 +500,126 @@ rel_status relation_paged_fwd(const void* P1, int64_t ld1, const void* cache_P2,
                               int page_size, int max_pages, int max_new,
                               rel_dtype dt, void* workspace, size_t ws_bytes,
                               hipStream_t stream);
+
+/*
+ * ---- 8-bit pages, trees of drafted tokens -------------------------------------
+ *
+ * REL_E4M3 pages: cache_P2 and cache_V hold OCP e4m3 values (8 bits, finite and NaN)
+ * in the layout above, and cache_scale, device uint8[n_pages, H_kv, 2, page_size],
+ * the exponents e of each row's scales 2^(e - 127), of its P2 at [.., 0, r] and of
+ * its V at [.., 1, r]. A row stands for its values times its scale. Tokens (P1, P2,
+ * I, Y) are bf16.
+ *
+ * A tree of drafted tokens: the new tokens of a request in an order in which each
+ * comes after its parent. tree is device uint32[N, tree_words] (as int32): bit a % 32
+ * of word a / 32 in the row of the request's token k says that token k sees token a,
+ * one of its ancestors; bits at and past k are ignored. A request with more than
+ * 32 * tree_words new tokens has no tree (its rows of tree are not read): each of
+ * its tokens sees all before it, so chunks of prompts and trees share a batch.
+ * One serving step: relation_page_map, relation_tree_plan, relation_paged_append(_q8)
+ * with the plan's positions, relation_paged_fwd_ex, then, once the tokens to accept
+ * are chosen, relation_paged_keep.
+ */
+#define REL_MAX_TREE_WORDS 32
+
+/*
+ * relation_paged_append_q8 - relation_paged_append of bf16 tokens into 8-bit pages:
+ * the rotated P2 and the mixed I~ of a token are rounded once, from their fp32
+ * values x, to e4m3 values of x / 2^k (nearest even), k the least exponent with
+ * max |x| <= 448 * 2^k over the row's finite elements, kept in [-100, 119] (what
+ * is larger saturates at 448 * 2^119). NaN and infinities are stored as NaN. P1o is
+ * bf16, as there.
+ *
+ *   cache_scale : out, as above; written for the rows that are
+ * Other arguments as in relation_paged_append.
+ */
+rel_status relation_paged_append_q8(const void* P1, const void* P2, const void* I,
+                                    int64_t ld1, int64_t ld2, int64_t ldi,
+                                    const int32_t* slot, const int32_t* pos,
+                                    rel_rope rope, float rope_base,
+                                    const float* theta, rel_pairing pairing,
+                                    void* P1o, void* cache_P2, void* cache_V,
+                                    void* cache_scale, int N, int H, int H_kv,
+                                    int d_h, int n_pages, int page_size,
+                                    hipStream_t stream);
+
+/*
+ * relation_tree_plan - ancestor bits and positions of packed trees.
+ *   parent : in,  device int32[N], the parent of each packed token as its place among
+ *            its request's new tokens; a value outside [0, k) for the k'th makes it a
+ *            root, which sees only the rows that were cached before
+ *   total, cu : in, as relation_page_map leaves them
+ *   tree   : out, device uint32[N, tree_words] (as int32): the bits of each token's
+ *            ancestors, whole rows, for requests of at most 32 * tree_words new tokens;
+ *            other rows are left as they were
+ *   pos    : out, device int32[N]: cached rows plus ancestors (a chunk's tokens: plus
+ *            their place), the position at which the token is rotated and would stay
+ *            if its path were kept; -1 for padding and for tokens of refused requests.
+ *            Requests with cu outside [0, N] are skipped.
+ * 1 <= tree_words <= REL_MAX_TREE_WORDS.
+ */
+rel_status relation_tree_plan(const int32_t* parent, const int32_t* total,
+                              const int32_t* cu, int32_t* tree, int32_t* pos,
+                              int N, int S, int tree_words, hipStream_t stream);
+
+/*
+ * relation_paged_fwd_ex - relation_paged_fwd over pages of any type, with or without
+ * trees. Token k of a request with a tree, whose own row is row p = total[b] -
+ * (cu[b+1] - cu[b]) + k as before, sees the A rows cached before the new tokens,
+ * its ancestors' rows and its own:
+ *   R_p = sigmoid(U_p / tau_h),  R_j = SiLU(U_j) - lambda log(n + 1) for the others,
+ * n their number (A plus the ancestors).
+ *
+ *   cache_scale : REL_E4M3 pages: their scales; else NULL
+ *   tree, tree_words : as above; NULL and 0 for none
+ *   pages       : type of the pages; P1 and Y are of that type, bf16 for REL_E4M3
+ * Other arguments, what is skipped, and the workspace as in relation_paged_fwd, which
+ * this equals, bit for bit, for REL_F32 and REL_BF16 pages without a tree.
+ * Numerics: as there, on the values that 8-bit rows stand for (exact in bf16 where
+ * scale times value is a normal bf16 number; a scale exponent of 0 reads as 0, and
+ * 255, which is no scale, as 254). Weights enter the transport as two bf16 terms in
+ * every row of 8-bit pages and of trees: no query tiles.
+ */
+rel_status relation_paged_fwd_ex(const void* P1, int64_t ld1, const void* cache_P2,
+                                 const void* cache_V, const void* cache_scale,
+                                 const int32_t* block_table, const int32_t* total,
+                                 const int32_t* cu, const int32_t* tree,
+                                 int tree_words, const float* tau_s, float lambda,
+                                 void* Y, int N, int S, int H, int H_kv, int d_h,
+                                 int n_pages, int page_size, int max_pages,
+                                 int max_new, rel_dtype pages, void* workspace,
+                                 size_t ws_bytes, hipStream_t stream);
+
+/*
+ * relation_paged_keep - cuts each request back to the new tokens that it keeps (the
+ * accepted path of a tree, or the accepted first ones of a draft). With A rows cached
+ * before its new tokens, request b keeps n_keep[b] of them, those whose places
+ * keep[cu[b]], keep[cu[b] + 1], ... name in growing order: their rows move to rows
+ * A, A + 1, ... of the request, len[b] becomes A + n_keep[b], and its pages behind
+ * ceil(len[b] / page_size), up to ceil(total[b] / page_size), go on top of the free
+ * list in request order, page order within a request (their table entries stay as
+ * they are). A request whose n_keep is outside [0, its new tokens], or whose places are
+ * not growing and among its new tokens, keeps none; one whose cu or total is not valid
+ * (relation_paged_fwd's conditions, max_new aside; no new tokens are valid) is left
+ * alone, len too. Rows behind the kept ones may hold anything afterwards.
+ *
+ *   cache_P2, cache_V, cache_scale : in/out, pages and scales (NULL unless REL_E4M3)
+ *   keep, n_keep : in, device int32[N], int32[S]
+ *   len          : out, device int32[S], the lengths for the next relation_page_map
+ *   free_pages   : in/out, device int32[F]; entries at and above *n_free are
+ *                  overwritten by returned pages (those past F are dropped)
+ *   n_free       : in, device int32[1], clamped into [0, F]
+ *   n_free_out   : out, device int32[1]; may be n_free
+ * No two requests may hold the same page among those that their new tokens reach.
+ */
+rel_status relation_paged_keep(void* cache_P2, void* cache_V, void* cache_scale,
+                               const int32_t* block_table, const int32_t* total,
+                               const int32_t* cu, const int32_t* keep,
+                               const int32_t* n_keep, int32_t* len,
+                               int32_t* free_pages, const int32_t* n_free,
+                               int32_t* n_free_out, int N, int S, int F, int H_kv,
+                               int d_h, int n_pages, int page_size, int max_pages,
+                               rel_dtype pages, hipStream_t stream);
 
 /* Human-readable name of a status code (static string, never NULL). */
 const char* relation_status_str(rel_status s);
