@@ -562,7 +562,17 @@ __device__ __forceinline__ unsigned tree_bits(const PagedExArgs& a, int t, int o
   return (unsigned)(((unsigned long long)hi << 32 | lo) >> (o & 31)) & 15u;
 }
 
-// How many new tokens the packed token t, the tq'th of its request, sees, by 16 lanes.
+// How many new tokens the packed token t, the tq'th of its request, sees; below, the same
+// by 16 lanes.
+__device__ __forceinline__ int ancestors_of(const PagedExArgs& a, int t, int tq) {
+  int n = 0;
+  for (int w = 0; 32 * w < tq; ++w) {
+    const uint32_t x = a.tree[(size_t)t * a.words + w];
+    const int left = tq - 32 * w;
+    n += __popc(left < 32 ? x & ((1u << left) - 1) : x);
+  }
+  return n;
+}
 __device__ __forceinline__ int ancestors(const PagedExArgs& a, int t, int tq, int sl) {
   int n = 0;
   for (int w = sl; 32 * w < tq; w += 16) {

@@ -2,6 +2,7 @@
 // of paged_scan.h with e4m3 rows, without and with trees of drafted tokens. Every batch
 // goes through the scan, prompts too.
 #include "paged_scan.h"
+#include "paged_tile.h"
 
 namespace rel {
 
@@ -9,6 +10,9 @@ namespace {
 
 template <int D>
 hipError_t launch_typed(const PagedExArgs& a, const HeadParams& hp, hipStream_t s) {
+  constexpr int kCols = D <= 64 ? 64 : 128;
+  if (tiles_wanted(a))
+    return a.tree ? launch_tiles<kCols, D, e4m3, true>(a, hp, s) : launch_tiles<kCols, D, e4m3, false>(a, hp, s);
   return a.tree ? launch_scan<__bf16, D, e4m3, true>(a, hp, s) : launch_scan<__bf16, D, e4m3, false>(a, hp, s);
 }
 

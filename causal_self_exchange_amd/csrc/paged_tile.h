@@ -1,0 +1,840 @@
+// Query tiles for the paged Relation Cache's rows over 8-bit pages and of trees
+// (relation_paged_fwd_ex): where a request has many rows to a cached head, the keys are
+// brought into LDS once for 256 of them.
+//
+// A work-group of eight waves takes 256 rows (whole tokens of a request, times the query
+// heads of a cached head), 32 to a wave, and goes through its keys in tiles of 64. A
+// tile's rows are loaded into registers while the tile before is computed, become bf16
+// there (8-bit rows times their scales, exactly), and are stored to LDS in the two layouts
+// of mfma_tile.h; two buffers, one barrier a tile. The products are the 32x32x16 ones of
+// the forward: a lane holds one query row's scores and weights, and no state of a row is
+// divided between waves.
+//
+// The keys of all row blocks are cut into equal ranges as in the scan (paged_device.h);
+// here a row block counts its own keys, so early blocks of a prompt take less of a range
+// than late ones.
+#pragma once
+
+#include "paged_device.h"
+
+namespace rel {
+
+namespace {
+
+using namespace paged;
+
+constexpr int kTileRowsQ = 256;           // query rows of a work-group
+constexpr int kTileWaves = 8;
+constexpr int kTileThreads = 64 * kTileWaves;
+constexpr int kTileExtra = 8;             // units (64 keys of a row block) that a segment costs beside its keys
+constexpr int kTileSnap = 2;
+constexpr int kTileMin = 4;               // units of the shortest range
+
+// Row blocks of a request: `tokens` of its new ones each.
+// A tile of up to 128 rows, one wave to a SIMD, takes 3,240 cycles, of more 4,450: 12 to 16.
+struct RowBlocks {
+  int tokens, blocks, ctx, weight;
+  __device__ __forceinline__ RowBlocks(const PagedArgs& a, const Req& r) {
+    tokens = kTileRowsQ / (a.H / a.H_kv);
+    blocks = (r.q + tokens - 1) / tokens;
+    ctx = r.total - r.q;
+    weight = (long long)r.q * (a.H / a.H_kv) <= kTileRowsQ / 2 ? 12 : 16;
+  }
+  // Units of the row blocks before k of one cached head: each has ctx and the tokens up to
+  // its own last one, in 64ths times the weight, rounded over the sum, and one for what that
+  // leaves.
+  __device__ __forceinline__ long long before(int k) const {
+    return (long long)k * (kTileExtra + 1) + ((((long long)k * ctx + (long long)tokens * k * (k + 1) / 2) * weight) >> 10);
+  }
+  __device__ __forceinline__ int size(int k) const { return (int)(before(k + 1) - before(k)); }
+};
+
+struct TilePlanLds {
+  long long red[kTileWaves];
+  long long sum[kPlanInline + 1];
+  Req part[kPlanInline];
+};
+
+// Exclusive sums of the requests' units in sum[0 .. S], by a whole work-group.
+__device__ __forceinline__ void tile_plan(const PagedArgs& a, long long* sum, Req* part, long long* red) {
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  long long done = 0;
+  for (int b0 = 0; b0 < a.S; b0 += kTileThreads) {
+    const int b = b0 + tid;
+    long long own = 0;
+    if (b < a.S) {
+      const Req r(a, b);
+      if (part) part[b] = r;
+      if (r.q > 0) {
+        const RowBlocks n(a, r);
+        own = n.before(n.blocks) * a.H_kv;
+      }
+    }
+    long long x = own;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+      const long long y = __shfl_up(x, o, 64);
+      if (lane >= o) x += y;
+    }
+    if (lane == 63) red[wave] = x;
+    __syncthreads();
+    long long all = 0;
+#pragma unroll
+    for (int w = 0; w < kTileWaves; ++w) {
+      x += w < wave ? red[w] : 0;
+      all += red[w];
+    }
+    if (b < a.S) sum[b] = done + x - own;
+    done += all;
+    __syncthreads();
+  }
+  if (tid == 0) sum[a.S] = done;
+}
+
+__global__ __launch_bounds__(kTileThreads) void tile_plan_kernel(PagedArgs a) {
+  __shared__ long long red[kTileWaves];
+  tile_plan(a, ws_plan(a).unit_sum, nullptr, red);
+}
+
+// States of divided row blocks: the scan's records, room for two of every work-group's in
+// the chunks' part of the workspace (which is there: paged_chunks_possible).
+constexpr int kTileGroups = kChunkStateRows / (2 * kTileRowsQ);
+static_assert(kTileGroups <= kScanGroups, "a record for each");
+__device__ __forceinline__ States tile_states(const PagedArgs& a) {
+  States s = States::chunk(a);
+  s.cuts = States::scan(a).cuts;
+  return s;
+}
+
+struct TileSource {
+  const PagedArgs& a;
+  const long long* sum;
+  const Req* part;
+  Range rg;
+  CutRecord* cuts;
+  struct Block {
+    int b, kvh, rb, units;
+    long long start;
+    Req r;
+  };
+  __device__ __forceinline__ TileSource(const PagedArgs& args, const long long* s, const Req* p)
+      : a(args), sum(s), part(p), rg(s[args.S], kTileMin, kTileExtra, kTileSnap, blockIdx.x, gridDim.x),
+        cuts(tile_states(args).cuts) {
+    if (threadIdx.x == 0) cuts[rg.me].pieces = 0;
+    if (rg.u < rg.end) {
+      const Block k = block_of(rg.u);
+      rg.settle(k.start, k.units);
+    }
+  }
+  // Stripes of as many heads as a range has items, row block by row block (ScanSource).
+  __device__ __forceinline__ Block block_of(long long u) const {
+    Block k;
+    k.b = find_request(sum, a.S, u);
+    k.r = part ? part[k.b] : Req(a, k.b);
+    const RowBlocks n(a, k.r);
+    const long long head = n.before(n.blocks);
+    long long v = u - sum[k.b];
+    const int most = min(a.H_kv, max(1, divide(rg.per * n.blocks, head)));
+    const int first = divide(v, head * most) * most;      // the stripe's first head
+    const int width = min(most, a.H_kv - first);
+    v -= head * first;
+    int lo = 0, hi = n.blocks - 1;                        // the last row block that starts at or before v
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (width * n.before(mid) <= v) lo = mid;
+      else hi = mid - 1;
+    }
+    const int size = n.size(lo);
+    v -= width * n.before(lo);
+    const int x = divide(v, size);
+    k.kvh = first + x;
+    k.rb = lo;
+    k.units = size - kTileExtra;
+    k.start = u - (v - (long long)x * size);
+    return k;
+  }
+  __device__ __forceinline__ ScanSegment next() {
+    ScanSegment s{};
+    Block k;
+    int u0, u1, pieces, owner;
+    do {
+      if (!rg.more()) return s;
+      k = block_of(rg.u);
+    } while (!rg.take(k.start, k.units, u0, u1, s.slot, pieces, owner));
+    const RowBlocks n(a, k.r);
+    const int G = a.H / a.H_kv;
+    const int tokens = min(n.tokens, k.r.q - k.rb * n.tokens);
+    s.any = 1;
+    s.b = k.b;
+    s.kvh = k.kvh;
+    s.row0 = k.rb * n.tokens * G;
+    s.rows = tokens * G;
+    s.first = k.r.first;
+    s.ctx = n.ctx;
+    s.total = k.r.total;
+    // Keys below the block's last row's position, by whole tiles. Units cover them, and up to
+    // two more.
+    const int last = n.ctx + k.rb * n.tokens + tokens - 1;
+    auto key_of = [&](int u) __attribute__((always_inline)) -> long long {
+      return 64 * ((n.weight == 16 ? u : ((long long)u * 16 + 11) / 12));
+    };
+    s.k0 = (int)min((long long)((last + 63) & ~63), key_of(u0));
+    s.k1 = u1 == k.units ? last : (int)min((long long)last, key_of(u1));
+    if (pieces > 0 && threadIdx.x == 0)
+      cuts[rg.me] = CutRecord{pieces, owner, s.b, s.kvh, s.first, s.ctx, s.total, s.row0, s.rows, 0, 0, 0};
+    return s;
+  }
+};
+
+// A tile of 64 rows in LDS, blocks of 8 rows by 8 chunks of 16 bytes: P2's block has its
+// chunks 144 bytes apart, rows of a chunk next to each other; V's is the transposed layout
+// of mfma_tile.h. Operand reads are a lane base and an immediate, without bank conflicts.
+// So are the stores of a row's pieces, by lanes that hold neighbouring ones (an 8-bit piece
+// is two chunks, so a store has every other chunk of a row; the second eight chunks are
+// 128 bytes further on, in the other half of the banks).
+template <int D>
+struct QTile {
+  using L = TileLayout<D>;
+  static constexpr int kKBlock = 1152, kChunk = 144, kPad = 128;
+  static constexpr int kHalves = D / 64;
+  static constexpr int kKHalf = 8 * kKBlock + kPad, kVHalf = 8 * L::kVBlock + kPad;
+  static constexpr int kVOff = kHalves * kKHalf;
+  static constexpr int kBuf = kVOff + kHalves * kVHalf;
+  static constexpr int k_imm(int kb, int ds) { return kKHalf * (ds / 4) + 4 * kKBlock * kb + 2 * kChunk * (ds % 4); }
+  // Rows 8 half .. of the transport operand (kb, ks, db).
+  static constexpr int v_imm(int kb, int ks, int db, int half) { return kVHalf * (db >> 1) + L::kVBlock * (4 * kb + 2 * ks + half); }
+  __device__ static int k_base(int lq, int hf) { return kKBlock * (lq >> 3) + 16 * (lq & 7) + kChunk * hf; }
+  __device__ static int k_at(int row, int cc) { return kKHalf * (cc >> 3) + kKBlock * (row >> 3) + 16 * (row & 7) + kChunk * (cc & 7); }
+  __device__ static int v_at(int row, int cc) {
+    const int rr = row & 7;
+    return kVOff + kVHalf * (cc >> 3) + L::kVBlock * (row >> 3) + 16 * (8 * rr + ((cc & 7) ^ (4 * ((rr >> 1) & 1))));
+  }
+  __device__ static bf16x8 v_operand(const VBase& vb, int kb, int ks, int db) {
+    const char* const p = (db & 1) ? vb.odd : vb.even;
+    bf16x8 v;
+    v.lo = lds_tr_read(p + v_imm(kb, ks, db, 0));
+    v.hi = lds_tr_read(p + v_imm(kb, ks, db, 1));
+    return v;
+  }
+};
+
+// A work-group barrier for LDS data alone: the next tiles' loads are not waited for.
+__device__ __forceinline__ void tile_barrier() {
+  asm volatile("" ::: "memory");
+  wait_vm_lgkm<63, 0>();
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
+// What a block step does with the weights.
+enum : int { kNoWeights = 0, kAllSeen = 1, kMasked = 2 };
+
+// D: the layout's columns (64, 128), DR those of a row in memory.
+template <int D, int DR, typename Tc, bool kTree>
+__global__ __launch_bounds__(kTileThreads, 2) void tile_kernel(ScanArgs<__bf16, Tc, kTree> a, HeadParams hp) {
+  using L = TileLayout<D>;
+  using Q = QTile<D>;
+  constexpr bool k8 = sizeof(Tc) == 1;
+  constexpr int kEs = (int)sizeof(Tc);
+  constexpr int kPiece = 16 / kEs;                        // elements of a 16-byte piece of a row
+  constexpr int kPieces = D / kPiece;                     // of a row in the layout
+  constexpr int kWaveRows = 64 / kPieces;                 // rows of a wave's piece, within one page
+  // Where four waves hold a tile of P2, the others take V's.
+  constexpr bool kSplit = kWaveRows * kTileWaves > 64;
+  static_assert(!kSplit || k8, "16-bit rows have two pieces a lane");
+  constexpr int kMovers = kSplit ? kTileWaves / 2 : kTileWaves;
+  constexpr int kStepRows = kMovers * kWaveRows;          // rows between a thread's pieces
+  constexpr int kUnits = 64 / kStepRows;                  // pieces of a tile (of P2, of V) per thread
+  constexpr int kYStride = 2 * D + 16;                    // bytes of a row of Y on its way out
+  // 8-bit tiles wait in LDS, each lane's pieces where it alone reads them: kAhead tiles of
+  // a wave's P2 and V pieces and of their scales.
+  constexpr int kAhead = k8 ? 4 : 0;
+  constexpr int kParts = kSplit ? 1 : 2;
+  constexpr int kRaw = kParts * 1024 + 256;
+  constexpr int kTileLoads = kParts + 1;                  // direct loads of a wave and tile
+  constexpr int kRing = 2 * Q::kBuf;
+  constexpr int kScan = kRing + kTileWaves * kAhead * kRaw;
+  constexpr int kBytes = kScan > kTileRowsQ * kYStride ? kScan : kTileRowsQ * kYStride;
+  constexpr int kNS = 2 * L::kDs, kSc = 16 / kNS;         // MFMA steps of a block, weights formed per step
+  constexpr float kFinite = 0x1p100f, kPartFinite = 0x1p119f;
+  __shared__ __attribute__((aligned(16))) char smem[kBytes];
+  __shared__ int s_bad[kTileWaves];
+  __shared__ TilePlanLds lds;
+
+  const long long* sum = ws_plan(a).unit_sum;
+  if (a.S <= kPlanInline) {
+    tile_plan(a, lds.sum, lds.part, lds.red);
+    __syncthreads();
+    sum = lds.sum;
+  }
+  const States states = tile_states(a);
+  const int G = a.H / a.H_kv;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int lq = lane & 31, hf = lane >> 5;
+  const float k2 = hp.scale * kLog2e;
+  const int pmask = (1 << a.page_shift) - 1;
+
+  // A operand of the row-sum product (16x16x32, the weights as B operand): with ones where
+  // lane bits 2 and 4 agree, lane l's results are the sum of its own row l % 32.
+  bf16x8 sel;
+  {
+    const __bf16 v = (((lane >> 2) ^ (lane >> 4)) & 1) ? (__bf16)0.0f : (__bf16)1.0f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) sel[e] = v;
+  }
+
+  // This thread's pieces of a tile: rows prow + kStepRows i, piece pc.
+  const int wrow = lane / kPieces, pc = lane % kPieces;
+  const int mover = wave % kMovers;
+  const int prow = kWaveRows * mover + wrow;
+  const int src = pc * kPiece < DR ? wrow * DR * kEs + 16 * pc : kOutOfRange;
+  struct Pieces { u32x4 x[kUnits]; };
+
+  // Token of a row block that its row x belongs to, x / G (0.5 / G from an integer, far more
+  // than the product is off for x, G <= 256).
+  const float per_head = 1.0f / (float)G;
+  auto token = [&](int x) __attribute__((always_inline)) -> int { return (int)(((float)x + 0.5f) * per_head); };
+
+  const int koff = Q::k_base(lq, hf), te = L::tr_base(lane, false), to = L::tr_base(lane, true);
+  TileSource source(a, sum, a.S <= kPlanInline ? lds.part : nullptr);
+  ScanSegment cur = source.next();
+  while (cur.any) {
+    const int b = uni(cur.b), kvh = uni(cur.kvh), first = uni(cur.first), ctx = uni(cur.ctx), total = uni(cur.total);
+    const int row0 = uni(cur.row0), rows = uni(cur.rows), slot = uni(cur.slot), k0 = uni(cur.k0), k1 = uni(cur.k1);
+    const int t0 = k0 >> 6, J = max(((k1 + 63) >> 6) - t0, 0);   // key tiles t0 .. t0 + J - 1, counted from 0 below
+    bool tree = false;
+    if constexpr (kTree) tree = total - ctx <= 32 * a.words;
+
+    // Page of the wave's rows of each piece: lane x holds the entry of tile win0 + x
+    // (checked when it is used). P2 is loaded a tile ahead of V.
+    int win[kUnits], win0 = 0;
+    auto load_window = [&](int t) __attribute__((always_inline)) {
+      win0 = max(t - 32, 0);
+#pragma unroll
+      for (int i = 0; i < kUnits; ++i) {
+        const int key = 64 * (t0 + win0 + lane) + kStepRows * i + kWaveRows * mover;
+        win[i] = win0 + lane < J && key < total ? a.table[(size_t)b * a.max_pages + (key >> a.page_shift)] : -1;
+      }
+    };
+    load_window(0);
+    // Rows at and past the request's end, tiles past the segment and pages outside the
+    // cache are zeros.
+    struct Rows { size_t head; int off, left; };          // cached head's page, row in it, rows
+    auto rows_of = [&](int t, int i) __attribute__((always_inline)) -> Rows {
+      const int key = 64 * (t0 + t) + kStepRows * i + kWaveRows * mover;
+      const int page = __builtin_amdgcn_readlane(win[i], (t - win0) & 63);
+      const bool in = t < J && page >= 0 && page < a.n_pages;
+      return Rows{(size_t)(in ? page : 0) * a.H_kv + kvh, key & pmask, in ? min(total - key, kWaveRows) : 0};
+    };
+    auto base_of = [&](int part, const Rows& r) __attribute__((always_inline)) -> const char* {
+      return static_cast<const char*>(part ? a.cV : a.cP2) + ((r.head << a.page_shift) + r.off) * (DR * kEs);
+    };
+    auto put = [&](int part, int t, int row, int cc, const u32x4& x) __attribute__((always_inline)) {
+      *reinterpret_cast<u32x4*>(smem + (t & 1) * Q::kBuf + (part ? Q::v_at(row, cc) : Q::k_at(row, cc))) = x;
+    };
+    // 16-bit pages: a tile's pieces in registers.
+    auto load = [&](int part, int t, Pieces& p) __attribute__((always_inline)) {
+#pragma unroll
+      for (int i = 0; i < kUnits; ++i) {
+        const Rows r = rows_of(t, i);
+        p.x[i] = __builtin_amdgcn_raw_buffer_load_b128(rsrc(base_of(part, r), r.left * DR * kEs), src, 0, 0);
+      }
+    };
+    auto store = [&](int part, int t, const Pieces& p) __attribute__((always_inline)) {
+#pragma unroll
+      for (int i = 0; i < kUnits; ++i) put(part, t, prow + kStepRows * i, pc, p.x[i]);
+    };
+    // 8-bit pages: direct loads of tile t into its place in LDS (its window is there), and
+    // from there as bf16. No branches: they would part a block step's products from its
+    // weights.
+    char* const raw = smem + kRing + wave * (kAhead * kRaw);
+    const int second = kSplit ? wave >= kMovers : 0;      // the part that a wave with one moves
+    auto fetch = [&](int t) __attribute__((always_inline)) {
+      const Rows r = rows_of(t, 0);
+      char* const at = raw + (t & 3) * kRaw;
+      auto words = [&](const void* base, int bytes) __attribute__((always_inline)) -> u32x4 {
+        u32x4 w = rsrc_words(base, bytes);
+#pragma unroll
+        for (int x = 0; x < 3; ++x) w[x] = (unsigned)uni((int)w[x]);
+        return w;
+      };
+#pragma unroll
+      for (int i = 0; i < kParts; ++i) dma16(words(base_of(kSplit ? second : i, r), r.left * DR), at + 1024 * i, src);
+      // Scales: dwords of four rows, of P2 by the first lanes, of V (its rows lie a page's
+      // rows further on) by the next; one of the two where the wave moves one.
+      constexpr int kDw = kWaveRows / 4;
+      const int ps = 1 << a.page_shift;
+      const u32x4 sc = words(a.scale + (r.head << (a.page_shift + 1)) + r.off, r.left > 0 ? 2 * ps - r.off : 0);
+      dma4(sc, at + 1024 * kParts, lane < kDw ? 4 * lane + second * ps : (!kSplit && lane < 2 * kDw ? ps + 4 * (lane - kDw) : kOutOfRange));
+    };
+    // Where this lane's piece of an even tile goes, of P2 or of V; odd tiles kBuf further on.
+    const int kput = Q::k_at(prow, 2 * pc), vput = Q::v_at(prow, 2 * pc);
+    const int vput1 = Q::v_at(prow, 2 * pc + 1) - vput;
+    struct Wide { u32x4 x; int e; };
+    auto peek = [&](int part, int t) __attribute__((always_inline)) -> Wide {
+      const char* const at = raw + (t & 3) * kRaw;
+      return Wide{*reinterpret_cast<const u32x4*>(at + (kSplit ? 0 : 1024 * part) + 16 * lane),
+                  reinterpret_cast<const uint8_t*>(at + 1024 * kParts)[(kSplit ? 0 : kWaveRows * part) + wrow]};
+    };
+    auto widen = [&](int part, int t, const Wide& w) __attribute__((always_inline)) {
+      const float f = scale_of((unsigned)w.e);
+      char* const to = smem + (t & 1) * Q::kBuf + (part ? vput : kput);
+      *reinterpret_cast<u32x4*>(to) = e4m3_to_bf16(u32x2{w.x[0], w.x[1]}, f);
+      *reinterpret_cast<u32x4*>(to + (part ? vput1 : Q::kChunk)) = e4m3_to_bf16(u32x2{w.x[2], w.x[3]}, f);
+    };
+    // Tile tk of P2 and tv of V, by the waves that move them.
+    auto widen_both = [&](int tk, int tv) __attribute__((always_inline)) {
+      if constexpr (kSplit) {
+        widen(second, second ? tv : tk, peek(0, second ? tv : tk));
+      } else {
+        widen(0, tk, peek(0, tk));
+        widen(1, tv, peek(1, tv));
+      }
+    };
+
+    if constexpr (k8) {
+      if (J > 0) {
+#pragma unroll
+        for (int t = 0; t < kAhead; ++t) fetch(t);
+      }
+    }
+
+    // The wave's rows as B operands: row 32 wave + lq, columns 16 ds + 8 hf.
+    const bool active = 32 * wave < rows;                 // waves without rows only move tiles
+    const int mine = 32 * wave + lq;
+    const bool ok = mine < rows;
+    const int tok0 = row0 / G;
+    const int tq = tok0 + (ok ? token(mine) : 0);
+    const int pos = ok ? ctx + tq : 0;                    // no key is below 0
+    const int tok = first + tq;
+    bf16x8 q[L::kDs];
+    {
+      const int h = kvh * G + (ok ? mine - token(mine) * G : 0);
+      const __bf16* const p = static_cast<const __bf16*>(a.P1) + (size_t)tok * a.ld1 + (size_t)h * DR + 8 * hf;
+#pragma unroll
+      for (int ds = 0; ds < L::kDs; ++ds) {
+        u32x4 x = {0u, 0u, 0u, 0u};
+        if (ok && 16 * ds < DR) x = *reinterpret_cast<const u32x4*>(p + 16 * ds);
+        q[ds] = __builtin_bit_cast(bf16x8, x);
+      }
+    }
+    const ScanSegment nxt = source.next();                // while the first tiles are on their way
+    // Blocks of 32 keys, counted from the segment's first, that all of the wave's rows see.
+    const int seen_all = (tree ? ctx : ctx + tok0 + uni(token(32 * wave))) / 32 - 2 * t0;
+    // Which of the lane's 16 keys of block x its row sees.
+    auto sees = [&](int x) -> unsigned {
+      unsigned v = 0;
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const int key = 64 * t0 + 32 * x + 8 * g + 4 * hf;
+        unsigned s = (1u << min(max(pos - key, 0), 4)) - 1;
+        if constexpr (kTree)
+          if (tree) s &= tree_bits(a, tok, key - ctx);
+        v |= s << (4 * g);
+      }
+      return v;
+    };
+
+    f32x16 o[L::kDb];
+    f32x4 l16 = {0.0f, 0.0f, 0.0f, 0.0f};
+    float m2 = 0.0f, l = 0.0f;
+#pragma unroll
+    for (int db = 0; db < L::kDb; ++db) o[db] = f32x16{};
+
+    // ---- the scan: one block step forms the evidence of one block (E), the weights of the
+    // block before (W) and the transport of the one before that (T), the products one by one
+    // beside parts of the weights; the offset is 0 (see below).
+    auto kslot = [&](int t) -> const char* { return smem + (t & 1) * Q::kBuf + koff; };
+    auto vslot = [&](int t) -> VBase {
+      const char* const v = smem + (t & 1) * Q::kBuf + Q::kVOff;
+      return VBase{v + te, v + to};
+    };
+    bf16x8 ring[4];                                       // step i reads ring[i % 4]
+    auto operand = [&](int i, const char* kt, int kbE, const VBase& vt, int kbT) __attribute__((always_inline)) -> bf16x8 {
+      if ((i & 1) == 0) return *reinterpret_cast<const bf16x8*>(kt + Q::k_imm(kbE, i >> 1));
+      return Q::v_operand(vt, kbT, (i >> 1) / L::kDb, (i >> 1) % L::kDb);
+    };
+    auto step = [&](auto doE, auto doW, auto doT, f32x16& sE, const f32x16& sW, u32x4 (&pW)[2], const u32x4 (&pT)[2],
+                    const char* kt, int kbE, const VBase& vt, int kbT, int blockW, auto beside) __attribute__((always_inline)) {
+      constexpr bool E = decltype(doE)::value, T = decltype(doT)::value;
+      constexpr int W = decltype(doW)::value;
+      float xv[16], tv[16];
+      unsigned vis = 0;
+      if constexpr (W == kMasked) vis = sees(blockW);
+      // Weight of score n in two stages: tv = 1 / (1 + 2^-x), then w = 2^(x tv).
+      auto front = [&](int n) __attribute__((always_inline)) {
+        xv[n] = sW[n] * k2;
+        tv[n] = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-xv[n]));
+      };
+      auto back = [&](int n) __attribute__((always_inline)) {
+        float w = __builtin_amdgcn_exp2f(xv[n] * tv[n]);
+        if constexpr (W == kMasked) w = vis >> n & 1u ? w : 0.0f;
+        if (n & 1) pW[n >> 3][(n & 7) >> 1] = pack_bf16(tv[n - 1], w);
+        else tv[n] = w;
+      };
+      auto reads = [&](int i) __attribute__((always_inline)) {
+        if (i < kNS && ((i & 1) == 0 ? E : T)) ring[i & 3] = operand(i, kt, kbE, vt, kbT);
+      };
+      reads(0);
+      reads(1);
+#pragma unroll
+      for (int i = 0; i < kNS; ++i) {
+        reads(i + 2);
+        if ((i & 1) == 0) {
+          if constexpr (E) {
+            const int ds = i >> 1;
+            if (ds == 0) {
+              const f32x16 zero = {};
+              sE = __builtin_amdgcn_mfma_f32_32x32x16_bf16(ring[i & 3], q[0], zero, 0, 0, 0);
+            } else {
+              sE = __builtin_amdgcn_mfma_f32_32x32x16_bf16(ring[i & 3], q[ds], sE, 0, 0, 0);
+            }
+          }
+        } else if constexpr (T) {
+          const int k = i >> 1, ks = k / L::kDb, db = k % L::kDb;
+          const bf16x8 w = __builtin_bit_cast(bf16x8, pT[ks]);
+          o[db] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(ring[i & 3], w, o[db], 0, 0, 0);
+          if (db == L::kDb - 1) l16 = __builtin_amdgcn_mfma_f32_16x16x32_bf16(sel, w, l16, 0, 0, 0);
+        }
+        beside(i);
+        if constexpr (W != kNoWeights) {
+          if (i >= 1) {
+#pragma unroll
+            for (int n = (i - 1) * kSc; n < i * kSc; ++n) back(n);
+          }
+#pragma unroll
+          for (int n = i * kSc; n < (i + 1) * kSc; ++n) front(n);
+          if (i == kNS - 1) {
+#pragma unroll
+            for (int n = i * kSc; n < 16; ++n) back(n);
+          }
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    };
+    using On = std::true_type;
+    using Off = std::false_type;
+    using None = std::integral_constant<int, kNoWeights>;
+    using All = std::integral_constant<int, kAllSeen>;
+    using Some = std::integral_constant<int, kMasked>;
+
+    auto nothing = [](int) __attribute__((always_inline)) {};
+    Pieces rk, rv;
+    Wide wk, wv;
+    f32x16 sA = {}, sB = {};
+    u32x4 pA[2] = {}, pB[2] = {};
+    if (J > 0) {
+      if constexpr (k8) {
+        wait_vm_lgkm<2 * kTileLoads, 15>();
+        asm volatile("" ::: "memory");
+        widen_both(0, 0);
+        if (!kSplit || !second) widen(0, 1, peek(0, 1));
+      } else {
+        Pieces k1st, v1st, k2nd;
+        load(0, 0, k1st);
+        load(1, 0, v1st);
+        load(0, 1, k2nd);
+        load(0, 2, rk);
+        load(1, 1, rv);
+        store(0, 0, k1st);
+        store(1, 0, v1st);
+        store(0, 1, k2nd);
+      }
+      tile_barrier();
+      if (active) {
+        const char* const kt = kslot(0);
+        const VBase none = vslot(0);
+        step(On{}, None{}, Off{}, sA, sB, pB, pA, kt, 0, none, 0, 0, nothing);
+        if (seen_all > 0) step(On{}, All{}, Off{}, sB, sA, pB, pA, kt, 1, none, 0, 0, nothing);
+        else step(On{}, Some{}, Off{}, sB, sA, pB, pA, kt, 1, none, 0, 0, nothing);
+      }
+      tile_barrier();
+    }
+    // Tile j's blocks are transported in iteration j, whose evidence is of tile j + 1. Its
+    // stores go where tile j of P2 and tile j - 1 of V were, last read in iteration j - 1.
+    // One loop for the iterations whose weights all rows see, one for the others, and the
+    // last one by itself: as branches in one loop they cost 100 registers.
+    // What iteration j moves, in the kNS parts of its first block step.
+    auto move = [&](int j, int i) __attribute__((always_inline)) {
+      if constexpr (k8) {
+        static_assert(kNS >= 8, "parts of a step");
+        if (i == 0) {
+          // Tile j + 2 has landed (vector memory operations complete in order; tile j + 3's
+          // may be on their way).
+          asm volatile("" ::: "memory");
+          wait_vm_lgkm<kTileLoads, 15>();
+          asm volatile("" ::: "memory");
+          if constexpr (kSplit) {
+            wk = peek(0, second ? j + 1 : j + 2);
+          } else {
+            wk = peek(0, j + 2);
+            wv = peek(1, j + 1);
+          }
+        }
+        if (i == kNS / 4) {
+          if constexpr (kSplit) widen(second, second ? j + 1 : j + 2, wk);
+          else widen(0, j + 2, wk);
+        }
+        if (i == kNS / 2 && !kSplit) widen(1, j + 1, wv);
+        if (i == 3 * kNS / 4) {
+          asm volatile("" ::: "memory");
+          fetch(j + 4);                                   // where tile j was
+          asm volatile("" ::: "memory");
+        }
+      } else {
+        if (i == 0) store(0, j + 2, rk);
+        if (i == kNS / 4) store(1, j + 1, rv);
+        if (i == kNS / 2) load(0, j + 3, rk);
+        if (i == 3 * kNS / 4) load(1, j + 2, rv);
+      }
+    };
+    auto window = [&](int j) __attribute__((always_inline)) {
+      if (j + 4 >= win0 + 64) load_window(j + 4);
+    };
+    if (active) {
+      const int steady = min((seen_all - 1) >> 1, J - 1);   // 2 j + 2 < seen_all
+      int j = 0;
+#pragma nounroll
+      for (; j < steady; ++j) {
+        window(j);
+        const char* const kt = kslot(j + 1);
+        const VBase vt = vslot(j);
+        step(On{}, All{}, On{}, sA, sB, pA, pB, kt, 0, vt, 0, 0, [&](int i) __attribute__((always_inline)) { move(j, i); });
+        step(On{}, All{}, On{}, sB, sA, pB, pA, kt, 1, vt, 1, 0, nothing);
+        tile_barrier();
+      }
+#pragma nounroll
+      for (; j < J - 1; ++j) {
+        window(j);
+        const char* const kt = kslot(j + 1);
+        const VBase vt = vslot(j);
+        step(On{}, Some{}, On{}, sA, sB, pA, pB, kt, 0, vt, 0, 2 * j + 1, [&](int i) __attribute__((always_inline)) { move(j, i); });
+        step(On{}, Some{}, On{}, sB, sA, pB, pA, kt, 1, vt, 1, 2 * j + 2, nothing);
+        tile_barrier();
+      }
+      if (J > 0) {
+        const VBase vt = vslot(j);
+        step(Off{}, Some{}, On{}, sA, sB, pA, pB, nullptr, 0, vt, 0, 2 * j + 1, nothing);
+        step(Off{}, None{}, On{}, sB, sA, pB, pA, nullptr, 1, vt, 1, 0, nothing);
+        tile_barrier();
+      }
+    } else {
+#pragma nounroll
+      for (int j = 0; j < J; ++j) {
+        window(j);
+#pragma unroll
+        for (int i = 0; i < kNS; ++i) move(j, i);
+        tile_barrier();
+      }
+    }
+    // The compiler has left out wait states between a product and what reads it behind a
+    // branch.
+    asm volatile("s_nop 15\n\ts_nop 3\n\ts_waitcnt vmcnt(0)" ::: "memory");   // and the last direct loads
+    l = l16[0];
+
+    // The offset 0 is exact where nothing overflows: SiLU >= -0.2785, so no weight is small.
+    // Row sums up to 2^100 and, in parts (at most 256 to a row block), results up to 2^119
+    // pass; else the segment is scanned again with a stabiliser that follows the scores.
+    float omax = 0.0f;
+#pragma unroll
+    for (int db = 0; db < L::kDb; ++db)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) omax = fmaxf(omax, fabsf(o[db][r]));
+    const bool fine = l <= kFinite && omax < (slot >= 0 ? kPartFinite : INFINITY);
+    const bool bad = __any(ok && !fine);
+    if (lane == 0) s_bad[wave] = bad ? 1 : 0;
+    __syncthreads();
+    int redo = 0;
+#pragma unroll
+    for (int w = 0; w < kTileWaves; ++w) redo |= s_bad[w];
+    redo = __builtin_amdgcn_readfirstlane(redo);
+    __syncthreads();
+    if (redo) {
+#pragma unroll
+      for (int db = 0; db < L::kDb; ++db) o[db] = f32x16{};
+      l = 0.0f;
+#pragma nounroll
+      for (int t = 0; t < J; ++t) {
+        if (t < win0 || t >= win0 + 64) load_window(t);
+        if constexpr (k8) {
+          fetch(t);
+          wait_vm_lgkm<0, 15>();
+          asm volatile("" ::: "memory");
+          widen_both(t, t);
+        } else {
+          load(0, t, rk);
+          load(1, t, rv);
+          store(0, t, rk);
+          store(1, t, rv);
+        }
+        __syncthreads();
+#pragma nounroll
+        for (int kb = 0; kb < 2; ++kb) {
+          f32x16 s = {};
+#pragma unroll
+          for (int ds = 0; ds < L::kDs; ++ds) {
+            const bf16x8 x = *reinterpret_cast<const bf16x8*>(kslot(t) + (kb ? Q::k_imm(1, 0) : 0) + Q::k_imm(0, ds));
+            s = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x, q[ds], s, 0, 0, 0);
+          }
+          const unsigned vis = sees(2 * t + kb);
+          float mx = -INFINITY;
+#pragma unroll
+          for (int r = 0; r < 16; ++r) {
+            const float x = s[r] * k2;
+            s[r] = vis >> r & 1u ? x * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-x)) : -INFINITY;
+            mx = fmaxf(mx, s[r]);
+          }
+          const float top = fmaxf(m2, lane_pair_max(mx)), f = __builtin_amdgcn_exp2f(m2 - top);
+          m2 = top;
+          l *= f;
+#pragma unroll
+          for (int db = 0; db < L::kDb; ++db)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) o[db][r] *= f;
+          u32x4 w[2];
+#pragma unroll
+          for (int r = 0; r < 16; r += 2) {
+            const float x = __builtin_amdgcn_exp2f(s[r] - m2), y = __builtin_amdgcn_exp2f(s[r + 1] - m2);
+            l += x + y;
+            w[r >> 3][(r >> 1) & 3] = pack_bf16(x, y);
+          }
+          const VBase vt = vslot(t);
+          const VBase vb{vt.even + 4 * L::kVBlock * kb, vt.odd + 4 * L::kVBlock * kb};
+#pragma unroll
+          for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+            for (int db = 0; db < L::kDb; ++db)
+              o[db] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(Q::v_operand(vb, 0, ks, db), __builtin_bit_cast(bf16x8, w[ks]),
+                                                              o[db], 0, 0, 0);
+        }
+        __syncthreads();
+      }
+      asm volatile("s_nop 15\n\ts_nop 3" ::: "memory");
+      l = lane_pair_sum(l);
+    }
+
+    if (slot < 0) {
+      // Self evidence of the lane's row from its own cached row, the columns that the lane
+      // holds of P1; then its V, in the columns that it holds of the result. Y passes through
+      // LDS (the wave's own part), so that each store writes whole rows.
+      const int page = ok ? a.table[(size_t)b * a.max_pages + (pos >> a.page_shift)] : -1;
+      const bool has = page >= 0 && page < a.n_pages;
+      const size_t head = (size_t)(has ? page : 0) * a.H_kv + kvh;
+      const size_t at = ((head << a.page_shift) + (pos & pmask)) * DR;
+      const char* const kp = static_cast<const char*>(a.cP2) + (at + 8 * hf) * kEs;
+      const char* const vp = static_cast<const char*>(a.cV) + (at + 4 * hf) * kEs;
+      typedef unsigned words8 __attribute__((ext_vector_type(2 * kEs)));
+      typedef unsigned words4 __attribute__((ext_vector_type(kEs)));
+      words8 ko[DR / 16];
+      words4 vo[DR / 8];
+      float ks = 1.0f, vs = 1.0f;
+#pragma unroll
+      for (int ds = 0; ds < DR / 16; ++ds) ko[ds] = has ? *reinterpret_cast<const words8*>(kp + 16 * ds * kEs) : words8{};
+#pragma unroll
+      for (int c = 0; c < DR / 8; ++c) vo[c] = has ? *reinterpret_cast<const words4*>(vp + 8 * c * kEs) : words4{};
+      if constexpr (k8) {
+        const uint8_t* const sc = a.scale + (head << (a.page_shift + 1)) + (pos & pmask);
+        ks = has ? scale_of(sc[0]) : 0.0f;
+        vs = has ? scale_of(sc[1 << a.page_shift]) : 0.0f;
+      }
+      int seen = tq;
+      if constexpr (kTree)
+        if (tree) seen = ancestors_of(a, tok, tq);
+      float u = 0.0f;
+#pragma unroll
+      for (int ds = 0; ds < DR / 16; ++ds) {
+        bf16x8 x;
+        if constexpr (k8) x = __builtin_bit_cast(bf16x8, e4m3_to_bf16(u32x2{ko[ds][0], ko[ds][1]}, ks));
+        else x = __builtin_bit_cast(bf16x8, ko[ds]);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) u = fmaf((float)q[ds][e], (float)x[e], u);
+      }
+      u = lane_pair_sum(u);
+      const int h = kvh * G + (ok ? mine - token(mine) * G : 0);
+      const float S = sigmoid_f32(u * hp.scale * hp.inv_tau[h]);
+      const RowCombine c(S, m2 * kLn2, l, hp.lambda * logf((float)(ctx + seen + 1)));
+      char* const y = smem + wave * (32 * kYStride);
+#pragma unroll
+      for (int db = 0; db < L::kDb; ++db)
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          if (32 * db + 8 * g >= DR) continue;            // the layout's other columns
+          bf16x4 v, out;
+          if constexpr (k8) {
+            const u32x4 w = e4m3_to_bf16(u32x2{vo[4 * db + g][0], 0u}, vs);
+            v = __builtin_bit_cast(bf16x4, u32x2{w[0], w[1]});
+          } else {
+            v = __builtin_bit_cast(bf16x4, vo[4 * db + g]);
+          }
+#pragma unroll
+          for (int e = 0; e < 4; ++e) out[e] = (__bf16)(c.w_self * (float)v[e] + c.w_hist * o[db][4 * g + e]);
+          *reinterpret_cast<bf16x4*>(y + lq * kYStride + 2 * (32 * db + 8 * g + 4 * hf)) = out;
+        }
+      tile_barrier();
+      constexpr int kC = D / 8, kStoreRows = 64 / kC;     // 16-byte chunks of a row, rows of a store
+      const int ch = lane % kC;
+#pragma unroll
+      for (int i = 0; i < 32 / kStoreRows; ++i) {
+        const int r = i * kStoreRows + lane / kC, row = 32 * wave + r;
+        if (row >= rows || ch >= DR / 8) continue;
+        const int x = token(row);
+        *reinterpret_cast<u32x4*>(static_cast<__bf16*>(a.Y) +
+                                  ((size_t)(first + tok0 + x) * a.H + kvh * G + row - x * G) * DR + 8 * ch) =
+            *reinterpret_cast<const u32x4*>(y + r * kYStride + 16 * ch);
+      }
+    } else if (ok) {
+      const int64_t at = (int64_t)slot * kTileRowsQ + mine;
+      if (hf == 0) states.ml[at] = make_float2(m2, l);
+      float* const zp = states.z + at * DR + 4 * hf;
+#pragma unroll
+      for (int db = 0; db < L::kDb; ++db)
+#pragma unroll
+        for (int g = 0; g < 4; ++g)
+          if (32 * db + 8 * g < DR)
+            *reinterpret_cast<f32x4*>(zp + 32 * db + 8 * g) =
+                f32x4{o[db][4 * g], o[db][4 * g + 1], o[db][4 * g + 2], o[db][4 * g + 3]};
+    }
+    tile_barrier();                        // read before the next segment's keys
+    cur = nxt;
+  }
+}
+
+// Joins of the row blocks that ranges divide, kTileRowsQ / 16 work-groups to a range.
+template <int DR, typename Tc, bool kTree>
+__global__ __launch_bounds__(kTileThreads) void tile_join_kernel(ScanArgs<__bf16, Tc, kTree> a, HeadParams hp) {
+  constexpr int kShares = kTileRowsQ / 16;
+  join_rows<__bf16, DR, Tc, kTree>(a, hp, tile_states(a), (int)blockIdx.x / kShares, (int)blockIdx.x % kShares, kShares,
+                                   kTileRowsQ, false);
+}
+
+// Whether the batch goes to query tiles: where a request can have more rows to a cached
+// head than two row blocks of the scan (and the workspace has the chunks' part).
+constexpr int kTileRowsLeast = 128;
+inline bool tiles_wanted(const PagedArgs& a) {
+  const int G = a.H / a.H_kv;
+  const int64_t most = a.max_new < a.N ? a.max_new : a.N;
+  return a.tiles && G <= kTileRowsQ && most * G > kTileRowsLeast && paged_chunks_possible(most, G);
+}
+
+template <int D, int DR, typename Tc, bool kTree>
+hipError_t launch_tiles(const ScanArgs<__bf16, Tc, kTree>& a, const HeadParams& hp, hipStream_t s) {
+  int cu = 0;
+  hipError_t e = device_cu_count(&cu);
+  if (e != hipSuccess) return e;
+  const int groups = cu < kTileGroups ? cu : kTileGroups;
+  if (a.S > kPlanInline) {
+    hipLaunchKernelGGL(tile_plan_kernel, dim3(1), dim3(kTileThreads), 0, s, (const PagedArgs&)a);
+    e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  hipLaunchKernelGGL((tile_kernel<D, DR, Tc, kTree>), dim3(groups), dim3(kTileThreads), 0, s, a, hp);
+  e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL((tile_join_kernel<DR, Tc, kTree>), dim3(groups * (kTileRowsQ / 16)), dim3(kTileThreads), 0, s, a, hp);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+}  // namespace rel

@@ -2,6 +2,7 @@
 // own type (relation_paged_fwd_ex): the scan of paged_scan.h with a row of ancestor bits
 // per token. Only the steps that hold new tokens look at them.
 #include "paged_scan.h"
+#include "paged_tile.h"
 
 namespace rel {
 
@@ -9,6 +10,8 @@ namespace {
 
 template <typename Tin, int D>
 hipError_t launch_typed(const PagedExArgs& a, const HeadParams& hp, hipStream_t s) {
+  if constexpr (sizeof(Tin) == 2)
+    if (tiles_wanted(a)) return launch_tiles<(D <= 64 ? 64 : 128), D, __bf16, true>(a, hp, s);
   return launch_scan<Tin, D, Tin, true>(a, hp, s);
 }
 

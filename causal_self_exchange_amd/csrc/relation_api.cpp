@@ -370,7 +370,7 @@ rel_status paged_fwd_impl(const void* P1, int64_t ld1, const void* cache_P2, con
   if (any_alias(ins, outs)) return REL_E_ALIAS;
   const rel::PagedExArgs a{{P1, ld1, cache_P2, cache_V, block_table, total, cu, Y, workspace, N, S, H, H_kv, d_h,
                             n_pages, page_shift_of(page_size), max_pages, max_new,
-                            dt == REL_BF16 && !fwd_scan_selected()},
+                            dt != REL_F32 && !fwd_scan_selected()},
                            static_cast<const uint8_t*>(scale), reinterpret_cast<const uint32_t*>(tree), words};
   const hipError_t e = q8     ? rel::launch_paged_q8(a, hp, stream)
                        : tree ? rel::launch_paged_tree(a, hp, dt == REL_BF16, stream)

@@ -166,6 +166,14 @@ def run_ex(m, lam, ws=None, fill=3.0, max_new=None):
     return Y
 
 
+def on_tiles(m, max_new=None):
+    """Whether a batch of 8-bit pages or 16-bit trees goes to query tiles: requests may have more than 128 rows to a cached
+    head, and a batch of that many tokens has the workspace's part for them."""
+    G = m["P1"].shape[1] // m["cP2"].shape[1]
+    most = min(m["max_new"] if max_new is None else max_new, m["N"])
+    return most * G > 128 and most * min(G, 8) >= 65 and (m.get("tree") is not None or "k64" in m)
+
+
 def check_ex(m, lam, fill=3.0, max_new=None, du=None):
     Y = run_ex(m, lam, fill=fill, max_new=max_new)
     y0 = np.full(tuple(m["P1"].shape), fill)
@@ -175,6 +183,10 @@ def check_ex(m, lam, fill=3.0, max_new=None, du=None):
                                m["max_new"] if max_new is None else max_new, tree=tree)
     if m["P1"].dtype == torch.float32:
         lim = P.bound(ref, spread, "f32", 1e-6 if du is None else du)
+    elif on_tiles(m, max_new):
+        # Rows on query tiles: weights rounded to bf16 once (relation.h), the bound of the forward's tiles.
+        at_most, e_max = PW.evidence_error(m["P1"], torch.from_numpy(k))
+        lim = P.bound(ref, spread, "bf16", at_most + 8 * e_max * 2.0**-24)
     else:
         at_most, e_max = PW.evidence_error(m["P1"], torch.from_numpy(k))
         lim = PW.weights_bound(ref, spread, int(m["total"].max()), at_most, e_max)
@@ -489,10 +501,13 @@ def test_speculative_serving_loop(pages):
         k64, v64 = (P.f64(c) * (2.0**exps(sc)[:, :, j, :, None] if sc is not None else 1.0) for j, c in enumerate(caches))
         ref, spread = XO.paged_fwd(P.f64(q), k64, v64, table.cpu().numpy(), tot, at, tau, 0.5, np.zeros((N, H, d)), max(count),
                                    tree=tree.cpu().numpy())
+        at_most, e_max = PW.evidence_error(q, torch.from_numpy(k64))
         if tdt == torch.float32:
             lim = P.bound(ref, spread, "f32", 1e-6)
+        elif on_tiles(dict(P1=q, cP2=caches[0], max_new=max(count), N=N, tree=tree)):
+            lim = P.bound(ref, spread, "bf16", at_most + 8 * e_max * 2.0**-24)
         else:
-            lim = PW.weights_bound(ref, spread, int(tot.max()), *PW.evidence_error(q, torch.from_numpy(k64)))
+            lim = PW.weights_bound(ref, spread, int(tot.max()), at_most, e_max)
         assert np.all(np.abs(P.f64(Y) - ref) <= lim)
         # Keep a path of each tree (prompts: all of it).
         keep, n_keep, rows = np.zeros(N, dtype=np.int64), [], [held_rows(b, int(tot[b])) for b in range(S)]
