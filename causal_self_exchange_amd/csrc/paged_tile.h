@@ -23,9 +23,6 @@ namespace {
 
 using namespace paged;
 
-constexpr int kTileRowsQ = 256;           // query rows of a work-group
-constexpr int kTileWaves = 8;
-constexpr int kTileThreads = 64 * kTileWaves;
 constexpr int kTileExtra = 8;             // units (64 keys of a row block) that a segment costs beside its keys
 constexpr int kTileSnap = 2;
 constexpr int kTileMin = 4;               // units of the shortest range
@@ -34,11 +31,11 @@ constexpr int kTileMin = 4;               // units of the shortest range
 // A tile of up to 128 rows, one wave to a SIMD, takes 3,240 cycles, of more 4,450: 12 to 16.
 struct RowBlocks {
   int tokens, blocks, ctx, weight;
-  __device__ __forceinline__ RowBlocks(const PagedArgs& a, const Req& r) {
-    tokens = kTileRowsQ / (a.H / a.H_kv);
+  __device__ __forceinline__ RowBlocks(const PagedArgs& a, const Req& r, int rows) {
+    tokens = rows / (a.H / a.H_kv);
     blocks = (r.q + tokens - 1) / tokens;
     ctx = r.total - r.q;
-    weight = (long long)r.q * (a.H / a.H_kv) <= kTileRowsQ / 2 ? 12 : 16;
+    weight = rows == 256 && (long long)r.q * (a.H / a.H_kv) <= 128 ? 12 : 16;
   }
   // Units of the row blocks before k of one cached head: each has ctx and the tokens up to
   // its own last one, in 64ths times the weight, rounded over the sum, and one for what that
@@ -50,23 +47,24 @@ struct RowBlocks {
 };
 
 struct TilePlanLds {
-  long long red[kTileWaves];
+  long long red[8];
   long long sum[kPlanInline + 1];
   Req part[kPlanInline];
 };
 
-// Exclusive sums of the requests' units in sum[0 .. S], by a whole work-group.
-__device__ __forceinline__ void tile_plan(const PagedArgs& a, long long* sum, Req* part, long long* red) {
+// Exclusive sums of the requests' units in sum[0 .. S], by a whole work-group of W waves.
+template <int W>
+__device__ __forceinline__ void tile_plan(const PagedArgs& a, int rows, long long* sum, Req* part, long long* red) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   long long done = 0;
-  for (int b0 = 0; b0 < a.S; b0 += kTileThreads) {
+  for (int b0 = 0; b0 < a.S; b0 += 64 * W) {
     const int b = b0 + tid;
     long long own = 0;
     if (b < a.S) {
       const Req r(a, b);
       if (part) part[b] = r;
       if (r.q > 0) {
-        const RowBlocks n(a, r);
+        const RowBlocks n(a, r, rows);
         own = n.before(n.blocks) * a.H_kv;
       }
     }
@@ -80,7 +78,7 @@ __device__ __forceinline__ void tile_plan(const PagedArgs& a, long long* sum, Re
     __syncthreads();
     long long all = 0;
 #pragma unroll
-    for (int w = 0; w < kTileWaves; ++w) {
+    for (int w = 0; w < W; ++w) {
       x += w < wave ? red[w] : 0;
       all += red[w];
     }
@@ -91,15 +89,15 @@ __device__ __forceinline__ void tile_plan(const PagedArgs& a, long long* sum, Re
   if (tid == 0) sum[a.S] = done;
 }
 
-__global__ __launch_bounds__(kTileThreads) void tile_plan_kernel(PagedArgs a) {
-  __shared__ long long red[kTileWaves];
-  tile_plan(a, ws_plan(a).unit_sum, nullptr, red);
+__global__ __launch_bounds__(256) void tile_plan_kernel(PagedArgs a, int rows) {
+  __shared__ long long red[4];
+  tile_plan<4>(a, rows, ws_plan(a).unit_sum, nullptr, red);
 }
 
 // States of divided row blocks: the scan's records, room for two of every work-group's in
 // the chunks' part of the workspace (which is there: paged_chunks_possible).
-constexpr int kTileGroups = kChunkStateRows / (2 * kTileRowsQ);
-static_assert(kTileGroups <= kScanGroups, "a record for each");
+constexpr int tile_groups(int rows) { return kChunkStateRows / (2 * rows); }
+static_assert(tile_groups(128) <= kScanGroups, "a record for each");
 __device__ __forceinline__ States tile_states(const PagedArgs& a) {
   States s = States::chunk(a);
   s.cuts = States::scan(a).cuts;
@@ -111,14 +109,15 @@ struct TileSource {
   const long long* sum;
   const Req* part;
   Range rg;
+  int rows;
   CutRecord* cuts;
   struct Block {
     int b, kvh, rb, units;
     long long start;
     Req r;
   };
-  __device__ __forceinline__ TileSource(const PagedArgs& args, const long long* s, const Req* p)
-      : a(args), sum(s), part(p), rg(s[args.S], kTileMin, kTileExtra, kTileSnap, blockIdx.x, gridDim.x),
+  __device__ __forceinline__ TileSource(const PagedArgs& args, int block_rows, const long long* s, const Req* p)
+      : a(args), sum(s), part(p), rg(s[args.S], kTileMin, kTileExtra, kTileSnap, blockIdx.x, gridDim.x), rows(block_rows),
         cuts(tile_states(args).cuts) {
     if (threadIdx.x == 0) cuts[rg.me].pieces = 0;
     if (rg.u < rg.end) {
@@ -131,7 +130,7 @@ struct TileSource {
     Block k;
     k.b = find_request(sum, a.S, u);
     k.r = part ? part[k.b] : Req(a, k.b);
-    const RowBlocks n(a, k.r);
+    const RowBlocks n(a, k.r, rows);
     const long long head = n.before(n.blocks);
     long long v = u - sum[k.b];
     const int most = min(a.H_kv, max(1, divide(rg.per * n.blocks, head)));
@@ -161,7 +160,7 @@ struct TileSource {
       if (!rg.more()) return s;
       k = block_of(rg.u);
     } while (!rg.take(k.start, k.units, u0, u1, s.slot, pieces, owner));
-    const RowBlocks n(a, k.r);
+    const RowBlocks n(a, k.r, rows);
     const int G = a.H / a.H_kv;
     const int tokens = min(n.tokens, k.r.q - k.rb * n.tokens);
     s.any = 1;
@@ -229,9 +228,10 @@ __device__ __forceinline__ void tile_barrier() {
 // What a block step does with the weights.
 enum : int { kNoWeights = 0, kAllSeen = 1, kMasked = 2 };
 
-// D: the layout's columns (64, 128), DR those of a row in memory.
-template <int D, int DR, typename Tc, bool kTree>
-__global__ __launch_bounds__(kTileThreads, 2) void tile_kernel(ScanArgs<__bf16, Tc, kTree> a, HeadParams hp) {
+// D: the layout's columns (64, 128), DR those of a row in memory; W: waves.
+template <int D, int DR, int W, typename Tc, bool kTree>
+__global__ __launch_bounds__(64 * W, 2) void tile_kernel(ScanArgs<__bf16, Tc, kTree> a, HeadParams hp) {
+  constexpr int kTileWaves = W, kTileRowsQ = 32 * W;
   using L = TileLayout<D>;
   using Q = QTile<D>;
   constexpr bool k8 = sizeof(Tc) == 1;
@@ -263,7 +263,7 @@ __global__ __launch_bounds__(kTileThreads, 2) void tile_kernel(ScanArgs<__bf16, 
 
   const long long* sum = ws_plan(a).unit_sum;
   if (a.S <= kPlanInline) {
-    tile_plan(a, lds.sum, lds.part, lds.red);
+    tile_plan<W>(a, kTileRowsQ, lds.sum, lds.part, lds.red);
     __syncthreads();
     sum = lds.sum;
   }
@@ -297,7 +297,7 @@ __global__ __launch_bounds__(kTileThreads, 2) void tile_kernel(ScanArgs<__bf16, 
   auto token = [&](int x) __attribute__((always_inline)) -> int { return (int)(((float)x + 0.5f) * per_head); };
 
   const int koff = Q::k_base(lq, hf), te = L::tr_base(lane, false), to = L::tr_base(lane, true);
-  TileSource source(a, sum, a.S <= kPlanInline ? lds.part : nullptr);
+  TileSource source(a, kTileRowsQ, sum, a.S <= kPlanInline ? lds.part : nullptr);
   ScanSegment cur = source.next();
   while (cur.any) {
     const int b = uni(cur.b), kvh = uni(cur.kvh), first = uni(cur.first), ctx = uni(cur.ctx), total = uni(cur.total);
@@ -458,10 +458,10 @@ __global__ __launch_bounds__(kTileThreads, 2) void tile_kernel(ScanArgs<__bf16, 
     auto step = [&](auto doE, auto doW, auto doT, f32x16& sE, const f32x16& sW, u32x4 (&pW)[2], const u32x4 (&pT)[2],
                     const char* kt, int kbE, const VBase& vt, int kbT, int blockW, auto beside) __attribute__((always_inline)) {
       constexpr bool E = decltype(doE)::value, T = decltype(doT)::value;
-      constexpr int W = decltype(doW)::value;
+      constexpr int kW = decltype(doW)::value;
       float xv[16], tv[16];
       unsigned vis = 0;
-      if constexpr (W == kMasked) vis = sees(blockW);
+      if constexpr (kW == kMasked) vis = sees(blockW);
       // Weight of score n in two stages: tv = 1 / (1 + 2^-x), then w = 2^(x tv).
       auto front = [&](int n) __attribute__((always_inline)) {
         xv[n] = sW[n] * k2;
@@ -469,7 +469,7 @@ __global__ __launch_bounds__(kTileThreads, 2) void tile_kernel(ScanArgs<__bf16, 
       };
       auto back = [&](int n) __attribute__((always_inline)) {
         float w = __builtin_amdgcn_exp2f(xv[n] * tv[n]);
-        if constexpr (W == kMasked) w = vis >> n & 1u ? w : 0.0f;
+        if constexpr (kW == kMasked) w = vis >> n & 1u ? w : 0.0f;
         if (n & 1) pW[n >> 3][(n & 7) >> 1] = pack_bf16(tv[n - 1], w);
         else tv[n] = w;
       };
@@ -498,7 +498,7 @@ __global__ __launch_bounds__(kTileThreads, 2) void tile_kernel(ScanArgs<__bf16, 
           if (db == L::kDb - 1) l16 = __builtin_amdgcn_mfma_f32_16x16x32_bf16(sel, w, l16, 0, 0, 0);
         }
         beside(i);
-        if constexpr (W != kNoWeights) {
+        if constexpr (kW != kNoWeights) {
           if (i >= 1) {
 #pragma unroll
             for (int n = (i - 1) * kSc; n < i * kSc; ++n) back(n);
@@ -802,37 +802,55 @@ __global__ __launch_bounds__(kTileThreads, 2) void tile_kernel(ScanArgs<__bf16, 
 
 // Joins of the row blocks that ranges divide, kTileRowsQ / 16 work-groups to a range.
 template <int DR, typename Tc, bool kTree>
-__global__ __launch_bounds__(kTileThreads) void tile_join_kernel(ScanArgs<__bf16, Tc, kTree> a, HeadParams hp) {
-  constexpr int kShares = kTileRowsQ / 16;
-  join_rows<__bf16, DR, Tc, kTree>(a, hp, tile_states(a), (int)blockIdx.x / kShares, (int)blockIdx.x % kShares, kShares,
-                                   kTileRowsQ, false);
+__global__ __launch_bounds__(kThreads) void tile_join_kernel(ScanArgs<__bf16, Tc, kTree> a, HeadParams hp, int rows) {
+  const int shares = rows / 16;
+  join_rows<__bf16, DR, Tc, kTree>(a, hp, tile_states(a), (int)blockIdx.x / shares, (int)blockIdx.x % shares, shares, rows, false);
 }
 
-// Whether the batch goes to query tiles: where a request can have more rows to a cached
-// head than two row blocks of the scan (and the workspace has the chunks' part).
-constexpr int kTileRowsLeast = 128;
+// Whether the batch goes to query tiles. Two row blocks of the scan, 64 rows, are faster:
+// 32 requests of 64 rows over 4,000 8-bit rows of 8 heads of 128 120 us by the scan, 153 on
+// tiles; of 96 rows 172 and 159, of 256 387 and 230. And the tiles' fixed costs have to be
+// worth their while, by the rows of all heads times the most keys that a request can have:
+// one request of 64 tokens of 32 heads over 4,000 (8 million) 37 and 43 us, two over 16,000
+// (66 million) 101 and 81, 16 over 1,000 (33 million) 74 and 77. The host knows the tables'
+// width, not the lengths: short requests in wide tables lose up to 15 us. And the workspace
+// has to have the chunks' part.
+constexpr int kTileRowsLeast = 64;
+constexpr int64_t kTileWork = 40000000;
 inline bool tiles_wanted(const PagedArgs& a) {
   const int G = a.H / a.H_kv;
-  const int64_t most = a.max_new < a.N ? a.max_new : a.N;
-  return a.tiles && G <= kTileRowsQ && most * G > kTileRowsLeast && paged_chunks_possible(most, G);
+  const int64_t most = a.max_new < a.N ? a.max_new : a.N, keys = (int64_t)a.max_pages << a.page_shift;
+  return a.tiles && G <= 128 && most * G > kTileRowsLeast && paged_chunks_possible(most, G) && (int64_t)a.N * a.H * keys >= kTileWork;
+}
+
+template <int D, int DR, int W, typename Tc, bool kTree>
+hipError_t launch_tiles_of(const ScanArgs<__bf16, Tc, kTree>& a, const HeadParams& hp, hipStream_t s) {
+  int cu = 0;
+  hipError_t e = device_cu_count(&cu);
+  if (e != hipSuccess) return e;
+  cu *= 8 / W;
+  const int groups = cu < tile_groups(32 * W) ? cu : tile_groups(32 * W);
+  if (a.S > kPlanInline) {
+    hipLaunchKernelGGL(tile_plan_kernel, dim3(1), dim3(256), 0, s, (const PagedArgs&)a, 32 * W);
+    e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  hipLaunchKernelGGL((tile_kernel<D, DR, W, Tc, kTree>), dim3(groups), dim3(64 * W), 0, s, a, hp);
+  e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL((tile_join_kernel<DR, Tc, kTree>), dim3(groups * 2 * W), dim3(kThreads), 0, s, a, hp, 32 * W);
+  return hipGetLastError();
 }
 
 template <int D, int DR, typename Tc, bool kTree>
 hipError_t launch_tiles(const ScanArgs<__bf16, Tc, kTree>& a, const HeadParams& hp, hipStream_t s) {
-  int cu = 0;
-  hipError_t e = device_cu_count(&cu);
-  if (e != hipSuccess) return e;
-  const int groups = cu < kTileGroups ? cu : kTileGroups;
-  if (a.S > kPlanInline) {
-    hipLaunchKernelGGL(tile_plan_kernel, dim3(1), dim3(kTileThreads), 0, s, (const PagedArgs&)a);
-    e = hipGetLastError();
-    if (e != hipSuccess) return e;
+  // Up to 128 rows to a cached head: work-groups of four waves, two to a compute unit, where
+  // the LDS holds both.
+  if constexpr (D == 64) {
+    const int64_t most = a.max_new < a.N ? a.max_new : a.N;
+    if (most * (a.H / a.H_kv) <= 128) return launch_tiles_of<D, DR, 4, Tc, kTree>(a, hp, s);
   }
-  hipLaunchKernelGGL((tile_kernel<D, DR, Tc, kTree>), dim3(groups), dim3(kTileThreads), 0, s, a, hp);
-  e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  hipLaunchKernelGGL((tile_join_kernel<DR, Tc, kTree>), dim3(groups * (kTileRowsQ / 16)), dim3(kTileThreads), 0, s, a, hp);
-  return hipGetLastError();
+  return launch_tiles_of<D, DR, 8, Tc, kTree>(a, hp, s);
 }
 
 }  // namespace

@@ -166,34 +166,48 @@ def run_ex(m, lam, ws=None, fill=3.0, max_new=None):
     return Y
 
 
-def on_tiles(m, max_new=None):
-    """Whether a batch of 8-bit pages or 16-bit trees goes to query tiles: requests may have more than 128 rows to a cached
-    head, and a batch of that many tokens has the workspace's part for them."""
-    G = m["P1"].shape[1] // m["cP2"].shape[1]
+def many_rows(m, max_new=None):
+    """Whether requests may have more than 64 rows to a cached head, in a batch of 8-bit pages or of 16-bit trees whose
+    workspace has the part for query tiles."""
+    H, Hkv = m["P1"].shape[1], m["cP2"].shape[1]
     most = min(m["max_new"] if max_new is None else max_new, m["N"])
-    return most * G > 128 and most * min(G, 8) >= 65 and (m.get("tree") is not None or "k64" in m)
+    return most * (H // Hkv) > 64 and most * min(H // Hkv, 8) >= 65 and (m.get("tree") is not None or "k64" in m)
+
+
+def on_tiles(m, max_new=None):
+    """Whether such a batch goes to query tiles: by its rows times the most keys that its table admits."""
+    return many_rows(m, max_new) and m["N"] * m["P1"].shape[1] * m["table"].shape[1] * m["cP2"].shape[2] >= 40000000
+
+
+def widened(m):
+    """The same batch with a table wide enough for query tiles."""
+    cols = -(-40000000 // (m["N"] * m["P1"].shape[1] * m["cP2"].shape[2])) + 1
+    return dict(m, table=torch.cat([m["table"], torch.full((m["table"].shape[0], cols), P.BAD, dtype=torch.int32)], 1))
+
+
+def limit(m, ref, spread, k, du=None, max_new=None):
+    """Bound of a batch's rows; on query tiles the weights are rounded to bf16 once (relation.h), elsewhere kept."""
+    if m["P1"].dtype == torch.float32:
+        return P.bound(ref, spread, "f32", 1e-6 if du is None else du)
+    at_most, e_max = PW.evidence_error(m["P1"], torch.from_numpy(k))
+    if on_tiles(m, max_new):
+        return P.bound(ref, spread, "bf16", at_most + 8 * e_max * 2.0**-24)
+    return PW.weights_bound(ref, spread, int(m["total"].max()), at_most, e_max)
 
 
 def check_ex(m, lam, fill=3.0, max_new=None, du=None):
-    Y = run_ex(m, lam, fill=fill, max_new=max_new)
+    """A batch against the plain evaluation; where it has the rows for query tiles, in a wide table too."""
     y0 = np.full(tuple(m["P1"].shape), fill)
     k, v = (m["k64"], m["v64"]) if "k64" in m else (np.nan_to_num(P.f64(m[c])) for c in ("cP2", "cV"))
     tree = m["tree"].numpy() if m.get("tree") is not None else None
     ref, spread = XO.paged_fwd(P.f64(m["P1"]), k, v, m["table"].numpy(), m["total"].numpy(), m["cu"].numpy(), m["tau"], lam, y0,
                                m["max_new"] if max_new is None else max_new, tree=tree)
-    if m["P1"].dtype == torch.float32:
-        lim = P.bound(ref, spread, "f32", 1e-6 if du is None else du)
-    elif on_tiles(m, max_new):
-        # Rows on query tiles: weights rounded to bf16 once (relation.h), the bound of the forward's tiles.
-        at_most, e_max = PW.evidence_error(m["P1"], torch.from_numpy(k))
-        lim = P.bound(ref, spread, "bf16", at_most + 8 * e_max * 2.0**-24)
-    else:
-        at_most, e_max = PW.evidence_error(m["P1"], torch.from_numpy(k))
-        lim = PW.weights_bound(ref, spread, int(m["total"].max()), at_most, e_max)
-    lim = np.where(spread > 0, lim, 0.0)                       # rows nobody writes stay exactly
-    err = np.abs(P.f64(Y) - ref)
-    worst = np.unravel_index(np.argmax(err - lim), err.shape)
-    assert np.all(err <= lim), (worst, err[worst], lim[worst], ref[worst])
+    for b in [m] + ([widened(m)] if many_rows(m, max_new) and m["P1"].dtype == torch.bfloat16 else []):
+        Y = run_ex(b, lam, fill=fill, max_new=max_new)
+        lim = np.where(spread > 0, limit(b, ref, spread, k, du, max_new), 0.0)     # rows nobody writes stay exactly
+        err = np.abs(P.f64(Y) - ref)
+        worst = np.unravel_index(np.argmax(err - lim), err.shape)
+        assert np.all(err <= lim), (on_tiles(b, max_new), worst, err[worst], lim[worst], ref[worst])
     return Y
 
 
@@ -271,6 +285,33 @@ def test_fwd_trees_long_and_mixed(pages, d, H, Hkv):
     check_ex(m, 0.5)
 
 
+@pytest.mark.parametrize("pages,d,H,Hkv,reqs", [
+    ("e4m3", 128, 2, 1, [(6000, 128), (31, 129), (0, 1)]), ("e4m3", 64, 8, 2, [(63, 255), (64, 256), (65, 257), (1, 511)]),
+    ("e4m3", 80, 5, 1, [(4097, 300), (20, 51), (20, 52)]), ("e4m3", 48, 8, 8, [(0, 256), (3, 1), (0, 64), (100, 900)]),
+    ("e4m3", 32, 3, 3, [(10, 1500)]), ("e4m3", 128, 24, 2, [(129, 30), (2, 5), (500, 140), (0, 21), (90, 22)]),
+    ("e4m3", 64, 128, 1, [(70, 3), (5, 1), (300, 2)]), ("e4m3", 128, 256, 2, [(70, 3), (5, 1), (300, 2)]),
+    ("bf16", 128, 7, 1, [(700, 60), (31, 37), (0, 9)]), ("bf16", 64, 4, 2, [(9000, 64), (64, 65), (63, 33)]),
+    ("bf16", 80, 16, 2, [(129, 100), (4000, 17), (0, 1)]),
+])
+def test_fwd_query_tiles(pages, d, H, Hkv, reqs):
+    """At and around the tiles' 128 and 256 rows, groups that do not divide them, histories in few and many pieces."""
+    m = make8(H, Hkv, d, 16, reqs, d + H, stride_pad=8, pad_rows=2) if pages == "e4m3" else P.make(pages, H, Hkv, d, 32, reqs, d + H)
+    words = min(32, -(-max(n for _, n in reqs) // 32))
+    if pages == "e4m3":
+        check_ex(m, 0.5)
+    check_ex(with_trees(m, reqs, words, d), 0.5)
+
+
+@pytest.mark.parametrize("S,H,Hkv,d,new_hi", [(128, 16, 2, 64, 12), (129, 16, 2, 64, 12), (140, 8, 2, 128, 40), (300, 4, 1, 32, 60)])
+def test_fwd_query_tiles_many_requests(S, H, Hkv, d, new_hi):
+    rng = np.random.default_rng(S)
+    reqs = [(int(rng.integers(0, 200)), int(rng.integers(0, new_hi + 1))) for _ in range(S)]
+    reqs[S // 2] = (reqs[S // 2][0], new_hi)
+    m = with_trees(make8(H, Hkv, d, 16, reqs, seed=S, pad_rows=2), reqs, 2, S)
+    m["total"][S // 3] = -1
+    check_ex(m, 0.5)
+
+
 @pytest.mark.parametrize("pages", ["e4m3", "bf16", "f32"])
 def test_fwd_tree_of_a_path_is_the_chunk(pages):
     """Trees that are one path, under any number of words, are the chunks' rows, bit for bit in the scan."""
@@ -295,17 +336,20 @@ def test_fwd_all_roots_see_the_cache_alone(pages):
     np.testing.assert_array_equal(P.f64(Y[:5]), own.repeat(2, axis=1))
 
 
-def test_fwd_8bit_leaves_other_rows():
-    m = make8(4, 2, 64, 16, [(10, 3), (0, 0), (40, 4), (7, 1), (30, 20), (5, 2), (2, 2)], seed=3, pad_rows=4)
-    m = with_trees(m, [(10, 3), (0, 0), (40, 4), (7, 1), (30, 20), (5, 2), (2, 2)], 1, 3)
-    m["total"][2], m["total"][3], m["total"][5] = -1, 0, m["table"].shape[1] * 16 + 1
+@pytest.mark.parametrize("new", [20, 200])
+def test_fwd_8bit_leaves_other_rows(new):
+    reqs = [(10, 3), (0, 0), (40, 4), (7, 1), (30, new), (5, 2), (2, 2), (9, 90)]
+    m = make8(4, 2, 64, 16, reqs, seed=3, pad_rows=4)
+    m = with_trees(m, reqs, 1, 3)
+    m["total"][2], m["total"][3], m["total"][5] = -1, 0, 2**31 - 1
     check_ex(m, 0.5, max_new=8)
+    check_ex(m, 0.5, max_new=100)
     for tree in (m["tree"], None):
         m["tree"] = tree
         for k, v in ((-1, m["N"] + 1), (0, -2)):
             cu = m["cu"].clone()
             m["cu"][k] = v
-            check_ex(m, 0.5, max_new=64)
+            check_ex(m, 0.5, max_new=300)
             m["cu"] = cu
 
 
@@ -324,6 +368,9 @@ def test_fwd_ex_large_evidence(pages, reqs):
     """Evidence to some hundreds: the stabiliser moves. fp32: du as for the forward without trees."""
     m = make8(4, 2, 64, 16, reqs, 5, spread=0, scale=5.0) if pages == "e4m3" else P.make(pages, 4, 2, 64, 16, reqs, 5, scale=5.0)
     check_ex(with_trees(m, reqs, 3, 5), 0.5, du=2e-3)
+    m["tree"] = None
+    if pages == "e4m3":
+        check_ex(m, 0.5)
 
 
 def test_fwd_8bit_far_scales():
@@ -501,13 +548,7 @@ def test_speculative_serving_loop(pages):
         k64, v64 = (P.f64(c) * (2.0**exps(sc)[:, :, j, :, None] if sc is not None else 1.0) for j, c in enumerate(caches))
         ref, spread = XO.paged_fwd(P.f64(q), k64, v64, table.cpu().numpy(), tot, at, tau, 0.5, np.zeros((N, H, d)), max(count),
                                    tree=tree.cpu().numpy())
-        at_most, e_max = PW.evidence_error(q, torch.from_numpy(k64))
-        if tdt == torch.float32:
-            lim = P.bound(ref, spread, "f32", 1e-6)
-        elif on_tiles(dict(P1=q, cP2=caches[0], max_new=max(count), N=N, tree=tree)):
-            lim = P.bound(ref, spread, "bf16", at_most + 8 * e_max * 2.0**-24)
-        else:
-            lim = PW.weights_bound(ref, spread, int(tot.max()), at_most, e_max)
+        lim = limit(dict(P1=q, cP2=caches[0], table=table, total=total, max_new=max(count), N=N, tree=tree), ref, spread, k64)
         assert np.all(np.abs(P.f64(Y) - ref) <= lim)
         # Keep a path of each tree (prompts: all of it).
         keep, n_keep, rows = np.zeros(N, dtype=np.int64), [], [held_rows(b, int(tot[b])) for b in range(S)]
@@ -536,14 +577,17 @@ def test_speculative_serving_loop(pages):
         assert sorted(used + free[:int(n_free)].tolist()) == list(range(n_pages))
 
 
+@pytest.mark.parametrize("width", [60, 1100])
 @pytest.mark.parametrize("pages", ["e4m3", "bf16"])
-def test_calls_replay_in_a_graph(pages):
-    """A whole step captured once and replayed with new lengths, trees and inputs, against the eager calls."""
-    S, N, H, Hkv, d, page, n_pages, width = 6, 300, 8, 2, 64, 16, 460, 60
+def test_calls_replay_in_a_graph(pages, width):
+    """A whole step captured once and replayed with new lengths, trees and inputs, against the eager calls: in the scan, and
+    in a table wide enough for query tiles."""
+    S, N, H, Hkv, d, page, n_pages, held = 6, 300, 8, 2, 64, 16, 460, 60
+    assert (N * H * width * page >= 40000000) == (width > held)
     rng = np.random.default_rng(2)
     lens0, nn, parent, keep, n_keep = (torch.zeros(k, dtype=torch.int32, device=DEV) for k in (S, S, N, N, S))
     base = rng.permutation(n_pages)
-    base = base[base >= S * width]                     # the table rows hold the others
+    base = base[base >= S * held]                     # the table rows hold the others
     x = torch.zeros((N, H + 2 * Hkv, d), dtype=torch.bfloat16, device=DEV)
     cdt = torch.float8_e4m3fn if pages == "e4m3" else torch.bfloat16
     state = {}
@@ -587,7 +631,8 @@ def test_calls_replay_in_a_graph(pages):
         keep.copy_(i32(kp))
         n_keep.copy_(i32(nk))
         x.copy_(torch.from_numpy(rng.standard_normal(tuple(x.shape))).to(torch.bfloat16))
-        own = i32(np.arange(S * width).reshape(S, width))
+        own = torch.full((S, width), P.BAD, dtype=torch.int32, device=DEV)
+        own[:, :held] = i32(np.arange(S * held).reshape(S, held))
         # Eager from the graph's state, then the replay from the same.
         for name in ("eager", "graph"):
             s = state[name]
@@ -614,19 +659,19 @@ def test_calls_replay_in_a_graph(pages):
 def test_calls_on_streams_at_once():
     """Forwards on three streams at once, a workspace each, and other calls of the kind beside them."""
     ms = [make8(8, 2, 128, 16, [(6000, 1), (300, 9), (0, 200)], 1), with_trees(make8(4, 4, 64, 16, TREES, 2), TREES, 2, 2),
-          with_trees(P.make("bf16", 8, 2, 128, 16, TREES, 3), TREES, 2, 3)]
+          widened(with_trees(P.make("bf16", 8, 2, 128, 16, TREES, 3), TREES, 2, 3)), widened(make8(8, 2, 128, 16, CHUNKS, 4))]
     want = [run_ex(m, 0.5) for m in ms]
     ds = [X.to_device(m) for m in ms]
     streams, outs = [torch.cuda.Stream() for _ in ms], [torch.full_like(y, 3.0) for y in want]
     wss = [torch.empty(R.paged_workspace_bytes(m["N"], len(m["total"]), *(m["P1"].shape[1], m["cP2"].shape[1], m["P1"].shape[2])),
                        dtype=torch.uint8, device=DEV) for m in ms]
-    plans = [R.tree_plan(i32(m["parent"]), d["total"], d["cu"], 2)[1].clone() for m, d in list(zip(ms, ds))[1:]]
+    plans = [R.tree_plan(i32(m["parent"]), d["total"], d["cu"], 2)[1].clone() for m, d in list(zip(ms, ds))[1:3]]
     torch.cuda.synchronize()
     for _ in range(5):
         for d, s, y, ws in zip(ds, streams, outs, wss):
             R.paged_fwd(d["P1"], d["cP2"], d["cV"], d["table"], d["total"], d["cu"], d["tau"], 0.5, max_new=d["max_new"], out=y,
                         stream=s, workspace=ws, scale=d.get("scale"), tree=d.get("tree"))
-        again = [R.tree_plan(i32(m["parent"]), d["total"], d["cu"], 2, stream=s)[1] for m, d, s in list(zip(ms, ds, streams))[1:]]
+        again = [R.tree_plan(i32(m["parent"]), d["total"], d["cu"], 2, stream=s)[1] for m, d, s in list(zip(ms, ds, streams))[1:3]]
     torch.cuda.synchronize()
     for y, w in zip(outs, want):
         assert torch.equal(y, w)
@@ -636,7 +681,8 @@ def test_calls_on_streams_at_once():
 
 def test_same_call_same_bits_through_one_workspace():
     ms = [make8(8, 2, 128, 16, [(9000, 1), (300, 1), (5000, 4)], 1), with_trees(make8(8, 8, 64, 16, TREES, 2), TREES, 2, 2),
-          with_trees(P.make("f32", 4, 1, 48, 32, TREES, 3), TREES, 2, 3)]
+          with_trees(P.make("f32", 4, 1, 48, 32, TREES, 3), TREES, 2, 3), widened(make8(8, 2, 128, 16, CHUNKS, 4)),
+          widened(with_trees(P.make("bf16", 8, 2, 64, 16, TREES, 5), TREES, 2, 5))]
     need = max(R.paged_workspace_bytes(m["N"], len(m["total"]), m["P1"].shape[1], m["cP2"].shape[1], m["P1"].shape[2]) for m in ms)
     ws = torch.full((need,), 255, dtype=torch.uint8, device=DEV)
     first = [run_ex(m, 0.5, ws=ws) for m in ms]
