@@ -3,12 +3,19 @@
 // brought into LDS once for 256 of them.
 //
 // A work-group of eight waves takes 256 rows (whole tokens of a request, times the query
-// heads of a cached head), 32 to a wave, and goes through its keys in tiles of 64. A
-// tile's rows are loaded into registers while the tile before is computed, become bf16
-// there (8-bit rows times their scales, exactly), and are stored to LDS in the two layouts
-// of mfma_tile.h; two buffers, one barrier a tile. The products are the 32x32x16 ones of
-// the forward: a lane holds one query row's scores and weights, and no state of a row is
-// divided between waves.
+// heads of a cached head), 32 to a wave, and goes through its keys in tiles of 64, which
+// pass through LDS as bf16 in the layouts of QTile: two buffers, one barrier a tile (of four
+// waves, two to a compute unit, for up to 128 rows of heads of up to 64). A tile of 16-bit
+// rows is loaded into registers while the one before is computed, an 8-bit tile straight
+// into a ring in LDS, four tiles ahead, and becomes bf16 on its way from there, its values
+// times their scale, exactly. The products are the 32x32x16 ones of the forward: a lane
+// holds one query row's scores and weights, and no state of a row is divided between waves.
+//
+// Bound by the loop's issue: a wave's tile is 36 products (1,090 cycles of the matrix unit),
+// 96 transcendentals and about 290 other instructions; a compute unit's takes 4,450 cycles
+// where the products alone would take 2,180 (with one wave to a SIMD 3,240, of 1,090). Two
+// chunks of 4,000 tokens of 32 heads of 128 in 4, over 0 and 4,000 8-bit rows, take 533 us,
+// 0.98 PFLOP/s (a large bf16 product by the library 1.32).
 //
 // The keys of all row blocks are cut into equal ranges as in the scan (paged_device.h);
 // here a row block counts its own keys, so early blocks of a prompt take less of a range
@@ -255,7 +262,7 @@ __global__ __launch_bounds__(64 * W, 2) void tile_kernel(ScanArgs<__bf16, Tc, kT
   constexpr int kRing = 2 * Q::kBuf;
   constexpr int kScan = kRing + kTileWaves * kAhead * kRaw;
   constexpr int kBytes = kScan > kTileRowsQ * kYStride ? kScan : kTileRowsQ * kYStride;
-  constexpr int kNS = 2 * L::kDs, kSc = 16 / kNS;         // MFMA steps of a block, weights formed per step
+  constexpr int kNS = 2 * L::kDs;                         // MFMA steps of a block
   constexpr float kFinite = 0x1p100f, kPartFinite = 0x1p119f;
   __shared__ __attribute__((aligned(16))) char smem[kBytes];
   __shared__ int s_bad[kTileWaves];
@@ -306,8 +313,8 @@ __global__ __launch_bounds__(64 * W, 2) void tile_kernel(ScanArgs<__bf16, Tc, kT
     bool tree = false;
     if constexpr (kTree) tree = total - ctx <= 32 * a.words;
 
-    // Page of the wave's rows of each piece: lane x holds the entry of tile win0 + x
-    // (checked when it is used). P2 is loaded a tile ahead of V.
+    // Page of the wave's rows of each piece: lane x holds the entry of tile win0 + x, -1 for
+    // tiles past the segment and for pages outside the cache. P2 is loaded a tile ahead of V.
     int win[kUnits], win0 = 0;
     auto load_window = [&](int t) __attribute__((always_inline)) {
       win0 = max(t - 32, 0);
@@ -315,6 +322,12 @@ __global__ __launch_bounds__(64 * W, 2) void tile_kernel(ScanArgs<__bf16, Tc, kT
       for (int i = 0; i < kUnits; ++i) {
         const int key = 64 * (t0 + win0 + lane) + kStepRows * i + kWaveRows * mover;
         win[i] = win0 + lane < J && key < total ? a.table[(size_t)b * a.max_pages + (key >> a.page_shift)] : -1;
+      }
+      // Waited for here, and not at the first use of each iteration.
+#pragma unroll
+      for (int i = 0; i < kUnits; ++i) {
+        win[i] = win[i] < a.n_pages ? win[i] : -1;
+        asm volatile("" : "+v"(win[i]));
       }
     };
     load_window(0);
@@ -324,7 +337,7 @@ __global__ __launch_bounds__(64 * W, 2) void tile_kernel(ScanArgs<__bf16, Tc, kT
     auto rows_of = [&](int t, int i) __attribute__((always_inline)) -> Rows {
       const int key = 64 * (t0 + t) + kStepRows * i + kWaveRows * mover;
       const int page = __builtin_amdgcn_readlane(win[i], (t - win0) & 63);
-      const bool in = t < J && page >= 0 && page < a.n_pages;
+      const bool in = page >= 0;
       return Rows{(size_t)(in ? page : 0) * a.H_kv + kvh, key & pmask, in ? min(total - key, kWaveRows) : 0};
     };
     auto base_of = [&](int part, const Rows& r) __attribute__((always_inline)) -> const char* {
@@ -462,25 +475,40 @@ __global__ __launch_bounds__(64 * W, 2) void tile_kernel(ScanArgs<__bf16, Tc, kT
       float xv[16], tv[16];
       unsigned vis = 0;
       if constexpr (kW == kMasked) vis = sees(blockW);
-      // Weight of score n in two stages: tv = 1 / (1 + 2^-x), then w = 2^(x tv).
-      auto front = [&](int n) __attribute__((always_inline)) {
-        xv[n] = sW[n] * k2;
-        tv[n] = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-xv[n]));
+      // Weight of score n in four parts, x log2 e and 2^-x, 1 / (1 + 2^-x), 2^(x / (1 + 2^-x))
+      // and the rounding, each in a later step than the transcendental that it needs: right
+      // behind it, every such pair cost a wait instruction (469 instructions a tile, now 424;
+      // 16 trees of 20 to 64 tokens over 2,000 to 30,000 rows of 64 heads of 64 in 8: 401 and
+      // 391 us, 32 of 128 in 8 356 and 342).
+      constexpr int kLast = kNS - 4;                      // step of the last first part
+      auto part = [&](int i) __attribute__((always_inline)) {
+#pragma unroll
+        for (int n = 0; n < 16; ++n) {
+          const int at = n * (kLast + 1) / 16;
+          if (i == at + 3) {
+            float w = tv[n];
+            if constexpr (kW == kMasked) w = __uint_as_float(__float_as_uint(w) & (unsigned)__builtin_amdgcn_sbfe((int)vis, n, 1));
+            if (n & 1) pW[n >> 3][(n & 7) >> 1] = pack_bf16(tv[n - 1], w);
+            else tv[n] = w;
+          }
+          if (i == at + 2) tv[n] = __builtin_amdgcn_exp2f(xv[n] * tv[n]);
+          if (i == at + 1) tv[n] = __builtin_amdgcn_rcpf(1.0f + tv[n]);
+          if (i == at) {
+            xv[n] = sW[n] * k2;
+            tv[n] = __builtin_amdgcn_exp2f(-xv[n]);
+          }
+        }
       };
-      auto back = [&](int n) __attribute__((always_inline)) {
-        float w = __builtin_amdgcn_exp2f(xv[n] * tv[n]);
-        if constexpr (kW == kMasked) w = vis >> n & 1u ? w : 0.0f;
-        if (n & 1) pW[n >> 3][(n & 7) >> 1] = pack_bf16(tv[n - 1], w);
-        else tv[n] = w;
-      };
+      // Two operands at a time, the second one's first: its wait is the first one's.
       auto reads = [&](int i) __attribute__((always_inline)) {
-        if (i < kNS && ((i & 1) == 0 ? E : T)) ring[i & 3] = operand(i, kt, kbE, vt, kbT);
+        if (i >= kNS) return;
+        if (T) ring[(i + 1) & 3] = operand(i + 1, kt, kbE, vt, kbT);
+        if (E) ring[i & 3] = operand(i, kt, kbE, vt, kbT);
       };
       reads(0);
-      reads(1);
 #pragma unroll
       for (int i = 0; i < kNS; ++i) {
-        reads(i + 2);
+        if ((i & 1) == 0) reads(i + 2);
         if ((i & 1) == 0) {
           if constexpr (E) {
             const int ds = i >> 1;
@@ -498,18 +526,7 @@ __global__ __launch_bounds__(64 * W, 2) void tile_kernel(ScanArgs<__bf16, Tc, kT
           if (db == L::kDb - 1) l16 = __builtin_amdgcn_mfma_f32_16x16x32_bf16(sel, w, l16, 0, 0, 0);
         }
         beside(i);
-        if constexpr (kW != kNoWeights) {
-          if (i >= 1) {
-#pragma unroll
-            for (int n = (i - 1) * kSc; n < i * kSc; ++n) back(n);
-          }
-#pragma unroll
-          for (int n = i * kSc; n < (i + 1) * kSc; ++n) front(n);
-          if (i == kNS - 1) {
-#pragma unroll
-            for (int n = i * kSc; n < 16; ++n) back(n);
-          }
-        }
+        if constexpr (kW != kNoWeights) part(i);
         __builtin_amdgcn_sched_barrier(0);
       }
     };
@@ -551,6 +568,10 @@ __global__ __launch_bounds__(64 * W, 2) void tile_kernel(ScanArgs<__bf16, Tc, kT
       }
       tile_barrier();
     }
+    // P1's loads have landed on every path: where one leaves that open, the compiler waits for
+    // all of a loop's own loads at the first product of each iteration.
+#pragma unroll
+    for (int ds = 0; ds < L::kDs; ++ds) asm volatile("" : "+v"(q[ds]));
     // Tile j's blocks are transported in iteration j, whose evidence is of tile j + 1. Its
     // stores go where tile j of P2 and tile j - 1 of V were, last read in iteration j - 1.
     // One loop for the iterations whose weights all rows see, one for the others, and the
