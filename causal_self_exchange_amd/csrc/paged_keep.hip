@@ -7,7 +7,10 @@
 // check the kept tokens for themselves, so that neither waits for the other. A round of
 // rows is loaded into registers before any of it is stored: a kept row's new place may be
 // another's old one, but never one that a later round reads, as places only grow.
-// Bound by latency: a table entry, a row, a barrier, a store.
+// Bound by latency, of a table entry, a row, a barrier and a store, and of the list's sums
+// and searches: 48 requests that keep up to 6 of 2 to 24 tokens of 4 heads 4.1 us, 512 that
+// keep up to 16 of 20 to 64 in 8-bit pages of 8 heads 15.7 (the rows alone 12.2, the list
+// alone 14.6; with four kept tokens' searches side by side the list took longer, 15.8).
 #include "page_list.h"
 #include "rel_internal.h"
 

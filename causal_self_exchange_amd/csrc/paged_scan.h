@@ -88,7 +88,10 @@ struct Geom {
   // with two row blocks keeps 43 in scratch, most of them addresses of operand reads that
   // each step loads again (8 chunks of 64 tokens over 2000 rows of 8 heads in 2: 81 us, 53
   // TFLOP/s; d = 64, without any, 42 us and 51), d = 64 with one row block 4, outside its
-  // key loop.
+  // key loop. 8-bit rows are half as long: one row block has three work-groups of one slot
+  // above d = 64, four below (64 tokens over 1,024 to 4,096 rows of 32 heads: d = 80 185 us,
+  // with two of two slots 211, d = 128 256 at either; d = 64 150 us, d = 32 100, with three
+  // of two slots 157 and 124).
   static constexpr int kPerCu = NB == 1 && D <= 64 ? 4 : (k8 && NB == 1 ? 3 : 2);
   static constexpr int kSlots = NB == 2 && kSlot <= (k8 ? 9000 : 8192) ? 2 : 1;
   static constexpr int kRing = kWaves * kSlots * kSlot;

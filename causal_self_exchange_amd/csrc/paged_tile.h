@@ -14,8 +14,8 @@
 // Bound by the loop's issue: a wave's tile is 36 products (1,090 cycles of the matrix unit),
 // 96 transcendentals and about 290 other instructions; a compute unit's takes 4,450 cycles
 // where the products alone would take 2,180 (with one wave to a SIMD 3,240, of 1,090). Two
-// chunks of 4,000 tokens of 32 heads of 128 in 4, over 0 and 4,000 8-bit rows, take 533 us,
-// 0.98 PFLOP/s (a large bf16 product by the library 1.32).
+// chunks of 4,000 tokens of 32 heads of 128 in 4, over up to 4,000 8-bit rows, take 540 us,
+// 0.84 PFLOP/s (a large bf16 product by the library 1.32).
 //
 // The keys of all row blocks are cut into equal ranges as in the scan (paged_device.h);
 // here a row block counts its own keys, so early blocks of a prompt take less of a range

@@ -577,8 +577,13 @@ rel_status relation_tree_plan(const int32_t* parent, const int32_t* total,
  * this equals, bit for bit, for REL_F32 and REL_BF16 pages without a tree.
  * Numerics: as there, on the values that 8-bit rows stand for (exact in bf16 where
  * scale times value is a normal bf16 number; a scale exponent of 0 reads as 0, and
- * 255, which is no scale, as 254). Weights enter the transport as two bf16 terms in
- * every row of 8-bit pages and of trees: no query tiles.
+ * 255, which is no scale, as 254); a row that is used may not hold NaN (they reach
+ * other rows of its request, of a tree's other branches too). Weights enter the
+ * transport as two bf16 terms, but that bf16 trees and 8-bit pages go to query tiles,
+ * with weights rounded to bf16 once (2^-8 of each) and summed so, as whole batches:
+ * where max_new (or N) times H / H_kv is past 64 and the batch's work (N H max_pages
+ * page_size) is large. relation_select_kernels with REL_KERNEL_SCAN for the forward
+ * keeps them off the tiles.
  */
 rel_status relation_paged_fwd_ex(const void* P1, int64_t ld1, const void* cache_P2,
                                  const void* cache_V, const void* cache_scale,
@@ -633,8 +638,9 @@ typedef enum {
 /*
  * relation_select_kernels - which kernels the bf16 forward family
  * (relation_fwd, relation_fwd_ex, relation_fwd_lse, relation_fwd_model) and
- * relation_bwd run; relation_paged_fwd under the forward's REL_KERNEL_SCAN
- * takes no query tiles, so that every row has the scan's weights. The selection is process-wide; calls made after this
+ * relation_bwd run; relation_paged_fwd and relation_paged_fwd_ex under the
+ * forward's REL_KERNEL_SCAN take no query tiles, so that every row has the
+ * scan's weights. The selection is process-wide; calls made after this
  * one returns use it. Before any call to it, the selection comes from the
  * environment variables RELATION_FWD_KERNEL and RELATION_BWD_KERNEL (the
  * value "scan" selects REL_KERNEL_SCAN), read once, the first time a
