@@ -373,6 +373,18 @@ def test_fwd_ex_large_evidence(pages, reqs):
         check_ex(m, 0.5)
 
 
+@pytest.mark.parametrize("pages,d", [("e4m3", 128), ("bf16", 64), ("e4m3", 48)])
+def test_fwd_query_tiles_large_evidence_over_long_history(pages, d):
+    """Row blocks that the tiles scan a second time, over more tiles than a wave holds table entries of, beside others."""
+    reqs = [(9000, 40), (6000, 64), (70, 30)]
+    m = make8(4, 1, d, 16, reqs, d, spread=0, scale=5.0) if pages == "e4m3" else P.make(pages, 4, 1, d, 16, reqs, d, scale=5.0)
+    m["P1"][m["cu"][1]:m["cu"][2]] *= 0.125
+    check_ex(with_trees(m, reqs, 2, d), 0.5)
+    m["tree"] = None
+    if pages == "e4m3":
+        check_ex(m, 0.5)
+
+
 def test_fwd_8bit_far_scales():
     """V rows of scales up to 2^90 and down to 2^-90 in one request: the bound is relative to what a row sums."""
     m = P.make("bf16", 2, 1, 64, 16, [(300, 1), (90, 40)], seed=2)
