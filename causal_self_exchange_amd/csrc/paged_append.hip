@@ -160,14 +160,14 @@ __global__ __launch_bounds__(kThreads) void paged_append_kernel(PagedAppendArgs 
 // forward turns the values back into bf16. Lanes of a power of two share a row (16
 // elements each), so that its maximum is a few exchanges between lanes.
 //
-// The row is rounded once, from the fp32 of its rotation or mixing, as above but for the
-// sines and cosines of P2, which are the fp64 ones rounded: a value within 2^-23 of the
-// middle between two steps may go to either, and both are as near to it. The rotation in
-// fp64 with a correct last rounding took 16,384 tokens of 32 + 8 heads of 128 from 75 to
-// 105 us.
+// The row is rounded once, from the fp32 of its rotation or mixing, as above but for P2's
+// sines and cosines, which are the fp64 ones rounded, and the factors of the mixing, from
+// fp64 angles in two parts: a value within 2^-23 of the middle between two steps may go to
+// either, and both are as near to it. The rotation in fp64 with a correct last rounding took
+// 16,384 tokens of 32 + 8 heads of 128 from 75 to 105 us.
 //
-// Bound by memory: those tokens read 201 MB and write 168 MB in 75 us, 4.9 TB/s (a copy of
-// 4 GB 4.7); 64 tokens of 32 + 32 heads take 6.3 us.
+// Bound by memory: those tokens read 201 MB and write 168 MB in 76 us, 4.8 TB/s (a copy of
+// 4 GB 4.7); 64 tokens of 32 + 32 heads take 6.4 us.
 constexpr int kLowScale = -100, kHighScale = 119;
 constexpr float kMostE4m3 = 448.0f;
 
@@ -234,7 +234,8 @@ __device__ __forceinline__ uint2 quantise8(const float (&x)[8], float inv) {
 
 // One work-group per token, as above: the rows that are quantised first, then P1.
 template <int D>
-__global__ __launch_bounds__(kThreads) void paged_append_q8_kernel(PagedAppendArgs a, uint8_t* scale, PrestepParams pp, int first) {
+__global__ __launch_bounds__(kThreads) void paged_append_q8_kernel(PagedAppendArgs a, uint8_t* scale, AppendQ8Params qp, int first) {
+  const PrestepParams& pp = qp.pre;
   constexpr int kGroups = D / 16;
   constexpr int kLanes = kGroups <= 2 ? 2 : (kGroups <= 4 ? 4 : 8);   // of a row
   __shared__ float s_cos[D / 2], s_sin[D / 2];
@@ -297,7 +298,7 @@ __global__ __launch_bounds__(kThreads) void paged_append_q8_kernel(PagedAppendAr
       if (a.mix) {
         const int ha = a.pairing == 0 ? 2 * k : 2 * k + 1, hb = (ha + 1) % a.H_kv;
         if (g < kGroups) {
-          const float c = pp.cos_theta[k], s = pp.sin_theta[k];
+          const float c = pp.cos_theta[k], s = pp.sin_theta[k], cr = qp.cos_rest[k], sr = qp.sin_rest[k];
 #pragma unroll
           for (int w = 0; w < 2; ++w) {
             load8(src + (size_t)ha * D + 8 * w, x[w]);
@@ -308,8 +309,10 @@ __global__ __launch_bounds__(kThreads) void paged_append_q8_kernel(PagedAppendAr
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
               const float p = x[w][e], q = y[w][e];
-              x[w][e] = fmaf(c, p, -s * q);
-              y[w][e] = fmaf(s, p, c * q);
+              // c, s times a bf16 number is exact: each sum is rounded once, and again with
+              // what the factors' rests give.
+              x[w][e] = fmaf(c, p, -s * q) + fmaf(cr, p, -sr * q);
+              y[w][e] = fmaf(s, p, c * q) + fmaf(sr, p, cr * q);
             }
         }
         store_row(1, ha, g, 16 * g, 16 * g + 8, x[0], x[1]);
@@ -349,11 +352,11 @@ hipError_t launch_typed(const PagedAppendArgs& a, const PrestepParams& pp, hipSt
 }
 
 template <int D>
-hipError_t launch_q8(const PagedAppendArgs& a, uint8_t* scale, const PrestepParams& pp, hipStream_t s) {
+hipError_t launch_q8(const PagedAppendArgs& a, uint8_t* scale, const AppendQ8Params& qp, hipStream_t s) {
   constexpr int kMost = 1 << 23;
   for (int64_t first = 0; first < a.N; first += kMost) {
     const unsigned n = (unsigned)(a.N - first < kMost ? a.N - first : kMost);
-    hipLaunchKernelGGL(paged_append_q8_kernel<D>, dim3(n), dim3(kThreads), 0, s, a, scale, pp, (int)first);
+    hipLaunchKernelGGL(paged_append_q8_kernel<D>, dim3(n), dim3(kThreads), 0, s, a, scale, qp, (int)first);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
@@ -362,13 +365,13 @@ hipError_t launch_q8(const PagedAppendArgs& a, uint8_t* scale, const PrestepPara
 
 }  // namespace
 
-hipError_t launch_paged_append_q8(const PagedAppendArgs& a, uint8_t* scale, const PrestepParams& pp, hipStream_t s) {
+hipError_t launch_paged_append_q8(const PagedAppendArgs& a, uint8_t* scale, const AppendQ8Params& qp, hipStream_t s) {
   switch (a.d_h) {
-    case 32: return launch_q8<32>(a, scale, pp, s);
-    case 48: return launch_q8<48>(a, scale, pp, s);
-    case 64: return launch_q8<64>(a, scale, pp, s);
-    case 80: return launch_q8<80>(a, scale, pp, s);
-    case 128: return launch_q8<128>(a, scale, pp, s);
+    case 32: return launch_q8<32>(a, scale, qp, s);
+    case 48: return launch_q8<48>(a, scale, qp, s);
+    case 64: return launch_q8<64>(a, scale, qp, s);
+    case 80: return launch_q8<80>(a, scale, qp, s);
+    case 128: return launch_q8<128>(a, scale, qp, s);
     default: return hipErrorInvalidValue;
   }
 }

@@ -106,6 +106,13 @@ struct PrestepParams {
   float sin_theta[128];
 };
 
+// Of the append into 8-bit pages: pre's Givens factors to 16 bits, and what these leave.
+struct AppendQ8Params {
+  PrestepParams pre;
+  float cos_rest[128];
+  float sin_rest[128];
+};
+
 // Linear Relation forward (chunk-parallel recurrence).
 constexpr int kLinChunk = 64;          // tokens per chunk
 struct LinArgs {
@@ -302,7 +309,7 @@ hipError_t launch_cache_append(void* cP2, void* cV, int32_t* len, const void* p2
                                int B, int H, int L_cap, int d_h, bool bf16, hipStream_t s);
 hipError_t launch_page_map(const PageMapArgs& a, hipStream_t s);
 hipError_t launch_paged_append(const PagedAppendArgs& a, const PrestepParams& pp, bool bf16, hipStream_t s);
-hipError_t launch_paged_append_q8(const PagedAppendArgs& a, uint8_t* scale, const PrestepParams& pp, hipStream_t s);
+hipError_t launch_paged_append_q8(const PagedAppendArgs& a, uint8_t* scale, const AppendQ8Params& qp, hipStream_t s);
 hipError_t launch_tree_plan(const TreePlanArgs& a, hipStream_t s);
 hipError_t launch_paged_keep(const PagedKeepArgs& a, hipStream_t s);
 hipError_t launch_paged(const PagedArgs& a, const HeadParams& hp, bool bf16, hipStream_t s);

@@ -9,6 +9,7 @@
 #include <cstdlib>
 #include <cstring>
 #include <mutex>
+#include <type_traits>
 
 #include "rel_internal.h"
 
@@ -125,7 +126,8 @@ bool use_bwd_mfma(rel_dtype dt, int d_h, int T) {
 
 size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
-bool prestep_modes_ok(rel_rope rope, float rope_base, const float* theta, rel_pairing pairing, int H) {
+template <typename Angle>
+bool prestep_modes_ok(rel_rope rope, float rope_base, const Angle* theta, rel_pairing pairing, int H) {
   if (rope != REL_ROPE_NONE && rope != REL_ROPE_INTERLEAVED && rope != REL_ROPE_HALF) return false;
   if (pairing != REL_PAIRS_A && pairing != REL_PAIRS_B) return false;
   if (rope != REL_ROPE_NONE && !(std::isfinite(rope_base) && rope_base > 1.0f)) return false;
@@ -137,7 +139,8 @@ bool prestep_modes_ok(rel_rope rope, float rope_base, const float* theta, rel_pa
 
 // Rotary frequencies (where there is a rotation) and Givens factors of H
 // information heads.
-void fill_prestep_params(rel::PrestepParams& pp, bool rotates, float rope_base, const float* theta, int H, int d_h) {
+template <typename Angle>
+void fill_prestep_params(rel::PrestepParams& pp, bool rotates, float rope_base, const Angle* theta, int H, int d_h) {
   for (int k = 0; k < 64; ++k)
     pp.inv_freq[k] = rotates && k < d_h / 2 ? std::pow(static_cast<double>(rope_base), -2.0 * k / d_h) : 0.0;
   for (int k = 0; k < 128; ++k) {
@@ -256,12 +259,32 @@ namespace {
 // Bytes of the scales of an 8-bit cache of nc elements.
 size_t scale_bytes(int64_t nc, int d_h) { return static_cast<size_t>(nc / d_h) * 2; }
 
-// relation_paged_append (scale null, q8 false) and relation_paged_append_q8.
+// The Givens factors in two parts: 16 bits, whose products with bf16 numbers are exact in
+// fp32, and what these leave.
+void split_factors(rel::AppendQ8Params& q, const double* theta, int pairs) {
+  auto split = [](double x, float& hi, float& rest) {
+    hi = static_cast<float>(x);
+    uint32_t b;
+    std::memcpy(&b, &hi, 4);
+    b &= 0xffffff00u;
+    std::memcpy(&hi, &b, 4);
+    rest = static_cast<float>(x - hi);
+  };
+  for (int k = 0; k < 128; ++k) {
+    const bool mixes = theta && k < pairs;
+    split(mixes ? std::cos(theta[k]) : 1.0, q.pre.cos_theta[k], q.cos_rest[k]);
+    split(mixes ? std::sin(theta[k]) : 0.0, q.pre.sin_theta[k], q.sin_rest[k]);
+  }
+}
+
+// relation_paged_append (angles in fp32, scale null) and relation_paged_append_q8 (in fp64).
+template <typename Angle>
 rel_status append_impl(const void* P1, const void* P2, const void* I, int64_t ld1, int64_t ld2,
                        int64_t ldi, const int32_t* slot, const int32_t* pos, rel_rope rope,
-                       float rope_base, const float* theta, rel_pairing pairing, void* P1o,
-                       void* cache_P2, void* cache_V, void* scale, bool q8, int N, int H, int H_kv, int d_h,
+                       float rope_base, const Angle* theta, rel_pairing pairing, void* P1o,
+                       void* cache_P2, void* cache_V, void* scale, int N, int H, int H_kv, int d_h,
                        int n_pages, int page_size, rel_dtype dt, hipStream_t stream) {
+  constexpr bool q8 = std::is_same<Angle, double>::value;
   if (!P2 || !I || !slot || !cache_P2 || !cache_V || (q8 && !scale) || !P1 != !P1o || (!pos && rope != REL_ROPE_NONE))
     return REL_E_NULL;
   if (!P1) H = 0;
@@ -288,13 +311,19 @@ rel_status append_impl(const void* P1, const void* P2, const void* I, int64_t ld
   const Range outs[] = {{P1o, P1 ? static_cast<size_t>(N) * H * d_h * es : 0}, {cache_P2, cb}, {cache_V, cb},
                         {scale, q8 ? scale_bytes(nc, d_h) : 0}};
   if (any_alias(ins, outs)) return REL_E_ALIAS;
-  rel::PrestepParams pp;
+  rel::AppendQ8Params qp;
+  rel::PrestepParams& pp = qp.pre;
   fill_prestep_params(pp, rope != REL_ROPE_NONE, rope_base, theta, H_kv, d_h);
   const rel::PagedAppendArgs a{P1, P2, I, ld1, ld2, ldi, slot, pos, P1o, cache_P2, cache_V, N, H, H_kv, d_h,
                                n_pages, page_shift_of(page_size), static_cast<int>(rope),
                                pairing == REL_PAIRS_A ? 0 : 1, theta ? 1 : 0};
-  const hipError_t e = q8 ? rel::launch_paged_append_q8(a, static_cast<uint8_t*>(scale), pp, stream)
-                          : rel::launch_paged_append(a, pp, dt == REL_BF16, stream);
+  hipError_t e;
+  if constexpr (q8) {
+    split_factors(qp, theta, H_kv / 2);
+    e = rel::launch_paged_append_q8(a, static_cast<uint8_t*>(scale), qp, stream);
+  } else {
+    e = rel::launch_paged_append(a, pp, dt == REL_BF16, stream);
+  }
   return e == hipSuccess ? REL_OK : REL_E_LAUNCH;
 }
 
@@ -308,16 +337,16 @@ rel_status relation_paged_append(const void* P1, const void* P2, const void* I, 
                                  void* cache_P2, void* cache_V, int N, int H, int H_kv, int d_h, int n_pages,
                                  int page_size, rel_dtype dt, hipStream_t stream) {
   return append_impl(P1, P2, I, ld1, ld2, ldi, slot, pos, rope, rope_base, theta, pairing, P1o, cache_P2, cache_V,
-                     nullptr, false, N, H, H_kv, d_h, n_pages, page_size, dt, stream);
+                     nullptr, N, H, H_kv, d_h, n_pages, page_size, dt, stream);
 }
 
 rel_status relation_paged_append_q8(const void* P1, const void* P2, const void* I, int64_t ld1, int64_t ld2,
                                     int64_t ldi, const int32_t* slot, const int32_t* pos, rel_rope rope,
-                                    float rope_base, const float* theta, rel_pairing pairing, void* P1o,
+                                    float rope_base, const double* theta, rel_pairing pairing, void* P1o,
                                     void* cache_P2, void* cache_V, void* cache_scale, int N, int H, int H_kv,
                                     int d_h, int n_pages, int page_size, hipStream_t stream) {
   return append_impl(P1, P2, I, ld1, ld2, ldi, slot, pos, rope, rope_base, theta, pairing, P1o, cache_P2, cache_V,
-                     cache_scale, true, N, H, H_kv, d_h, n_pages, page_size, REL_BF16, stream);
+                     cache_scale, N, H, H_kv, d_h, n_pages, page_size, REL_BF16, stream);
 }
 
 size_t relation_paged_workspace_bytes(int N, int S, int H, int H_kv, int d_h) {

@@ -79,8 +79,8 @@ def lib() -> ctypes.CDLL:
         L.relation_paged_fwd.argtypes = [vp, l64, vp, vp, vp, vp, vp, fp, f, vp, i, i, i, i, i, i, i, i, i, i,
                                          vp, sz, vp]
         L.relation_paged_fwd.restype = i
-        L.relation_paged_append_q8.argtypes = [vp, vp, vp, l64, l64, l64, vp, vp, i, f, fp, i, vp, vp, vp, vp,
-                                               i, i, i, i, i, i, vp]
+        L.relation_paged_append_q8.argtypes = [vp, vp, vp, l64, l64, l64, vp, vp, i, f, ctypes.POINTER(ctypes.c_double), i,
+                                               vp, vp, vp, vp, i, i, i, i, i, i, vp]
         L.relation_paged_append_q8.restype = i
         L.relation_tree_plan.argtypes = [vp] * 5 + [i] * 3 + [vp]
         L.relation_tree_plan.restype = i
@@ -555,14 +555,14 @@ def _count(name: str, x) -> int:
     return x
 
 
-def _host_floats(x, n: int):
-    """Host float[n] from a float or n of them."""
+def _host_floats(x, n: int, c_type=ctypes.c_float):
+    """Host float[n] (double[n]) from a float or n of them."""
     if isinstance(x, (list, tuple)) and len(x) == n:
-        return (ctypes.c_float * n)(*x)
+        return (c_type * n)(*x)
     if isinstance(x, float):
-        return (ctypes.c_float * n)(*([x] * n))
-    arr = np.ascontiguousarray(np.broadcast_to(np.asarray(x, dtype=np.float32), (n,)))
-    return (ctypes.c_float * n).from_buffer_copy(arr)
+        return (c_type * n)(*([x] * n))
+    arr = np.ascontiguousarray(np.broadcast_to(np.asarray(x, dtype=c_type), (n,)))
+    return (c_type * n).from_buffer_copy(arr)
 
 
 def _pages(fn, cache_P2):
@@ -666,10 +666,12 @@ def paged_append(P2, I, slot, cache_P2, cache_V, P1=None, pos=None, rope="none",
     if P1 is not None and out is None:
         with _on(stream):
             out = torch.zeros((N, H, D), dtype=dt, device=dev)
-    name, pages = ("relation_paged_append", ()) if scale is None else ("relation_paged_append_q8", (scale.data_ptr(),))
+    name, pages, angle = "relation_paged_append", (), ctypes.c_float
+    if scale is not None:
+        name, pages, angle = "relation_paged_append_q8", (scale.data_ptr(),), ctypes.c_double
     _run_on(name, dev, stream,
             (_ptr(P1), P2.data_ptr(), I.data_ptr(), 0 if P1 is None else _ld(P1), _ld(P2), _ld(I), slot.data_ptr(),
-             _ptr(pos), ROPE[rope], float(rope_base), None if theta is None else _host_floats(theta, Hkv // 2),
+             _ptr(pos), ROPE[rope], float(rope_base), None if theta is None else _host_floats(theta, Hkv // 2, angle),
              PAIRS[pairing], _ptr(out), cache_P2.data_ptr(), cache_V.data_ptr(), *pages, N, H, Hkv, D, n_pages, ps,
              *(() if pages else (_dtype_code(cache_P2),))))
     return out

@@ -30,7 +30,7 @@ hipError_t launch_cache_append(void*, void*, int32_t*, const void*, const void*,
 }
 hipError_t launch_page_map(const PageMapArgs&, hipStream_t) { return hipErrorLaunchFailure; }
 hipError_t launch_paged_append(const PagedAppendArgs&, const PrestepParams&, bool, hipStream_t) { return hipErrorLaunchFailure; }
-hipError_t launch_paged_append_q8(const PagedAppendArgs&, uint8_t*, const PrestepParams&, hipStream_t) { return hipErrorLaunchFailure; }
+hipError_t launch_paged_append_q8(const PagedAppendArgs&, uint8_t*, const AppendQ8Params&, hipStream_t) { return hipErrorLaunchFailure; }
 hipError_t launch_tree_plan(const TreePlanArgs&, hipStream_t) { return hipErrorLaunchFailure; }
 hipError_t launch_paged_keep(const PagedKeepArgs&, hipStream_t) { return hipErrorLaunchFailure; }
 hipError_t launch_paged_tree(const PagedExArgs&, const HeadParams&, bool, hipStream_t) { return hipErrorLaunchFailure; }

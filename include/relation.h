@@ -531,13 +531,15 @@ rel_status relation_paged_fwd(const void* P1, int64_t ld1, const void* cache_P2,
  * bf16, as there.
  *
  *   cache_scale : out, as above; written for the rows that are
+ *   theta       : host double[H_kv / 2]: an angle in fp32 is far enough from the one that
+ *                 is meant to store the farther of two e4m3 neighbours now and then
  * Other arguments as in relation_paged_append.
  */
 rel_status relation_paged_append_q8(const void* P1, const void* P2, const void* I,
                                     int64_t ld1, int64_t ld2, int64_t ldi,
                                     const int32_t* slot, const int32_t* pos,
                                     rel_rope rope, float rope_base,
-                                    const float* theta, rel_pairing pairing,
+                                    const double* theta, rel_pairing pairing,
                                     void* P1o, void* cache_P2, void* cache_V,
                                     void* cache_scale, int N, int H, int H_kv,
                                     int d_h, int n_pages, int page_size,

@@ -1,5 +1,6 @@
 """8-bit pages, trees and the cut to kept tokens without a GPU: refusals of the C ABI and
 of the binding, and pins of the plain evaluations."""
+import ctypes
 import os
 import shutil
 import subprocess
@@ -25,7 +26,7 @@ APP8 = {**dict(list(APP8.items())[:list(APP8).index("cV") + 1]), "scale": at(8),
 
 def append(**kw):
     m = {**APP8, **kw}
-    keep, th = fptr(m["theta"])
+    th = None if m["theta"] is None else (ctypes.c_double * len(m["theta"]))(*m["theta"])
     return R.lib().relation_paged_append_q8(*(th if k == "theta" else m[k] for k in APP8), None)
 
 

@@ -116,6 +116,28 @@ def test_paged_append_q8_equals_the_quantised_append():
         np.testing.assert_array_equal(P.f64(c[part])[slot // 16, :, slot % 16], q)
 
 
+def test_paged_append_q8_mixes_by_fp64_angles():
+    """Every stored value is one of the nearest to a number within 2^-23 of the exact one (fp32 sums of exact products,
+    rounded twice); angles rounded to fp32 put pairs that nearly cancel further off."""
+    N, Hkv, d, page = 2048, 8, 128, 16
+    rng = np.random.default_rng(5)
+    theta = rng.uniform(-3, 3, Hkv // 2)
+    x = torch.from_numpy(rng.standard_normal((N, Hkv, d))).to(torch.bfloat16)
+    c = [torch.zeros((N // page, Hkv, page, d), device=DEV).to(torch.float8_e4m3fn) for _ in range(2)]
+    sc = scales(N // page, Hkv, page)
+    R.paged_append(x.to(DEV), x.to(DEV), i32(np.arange(N)), *c, theta=list(theta), scale=sc)
+    torch.cuda.synchronize()
+    k = exps(sc)[:, :, 1].transpose(0, 2, 1).reshape(N, Hkv, 1)
+    q = P.f64(c[1]).transpose(0, 2, 1, 3).reshape(N, Hkv, d)
+    a, b = P.f64(x)[:, 0::2], P.f64(x)[:, 1::2]
+    cs, sn = np.cos(theta)[:, None], np.sin(theta)[:, None]
+    y = np.stack([cs * a - sn * b, sn * a + cs * b], 2).reshape(N, Hkv, d) / 2.0**k
+    top = np.abs(y).max(-1)
+    assert np.all(top <= 448 * (1 + 2.0**-22)) and np.all(top >= 224 * (1 - 2.0**-22))
+    half = 2.0 ** (np.maximum(np.floor(np.log2(np.maximum(np.abs(y), 2.0**-40))), -6) - 4)
+    assert np.all(np.abs(q - y) <= half + np.abs(y) * 2.0**-23)
+
+
 # ---- plan ----------------------------------------------------------------------------
 
 @pytest.mark.parametrize("S,n_hi,words,pad,seed", [(1, 1, 1, 0, 1), (3, 12, 1, 0, 2), (40, 32, 1, 7, 3), (17, 64, 2, 300, 4),
