@@ -1,6 +1,6 @@
 // The paged Relation Cache's forward over 8-bit pages (relation_paged_fwd_ex), without and
 // with trees of drafted tokens: the scan of paged_scan.h with e4m3 rows, or for batches
-// with many rows and much work (tiles_wanted) the query tiles of paged_tile.h.
+// with many rows and much work (tile_use) the query tiles of paged_tile.h.
 //
 // The scan is bound by memory: 64 tokens over 1,024 to 4,096 rows of 32 heads of 128 (1.35
 // GB) take 248 us, 5.4 TB/s, of 16-bit pages 451; one token over 300 rows of 8 heads of 64
@@ -16,8 +16,8 @@ namespace {
 template <int D>
 hipError_t launch_typed(const PagedExArgs& a, const HeadParams& hp, hipStream_t s) {
   constexpr int kCols = D <= 64 ? 64 : 128;
-  if (tiles_wanted(a))
-    return a.tree ? launch_tiles<kCols, D, e4m3, true>(a, hp, s) : launch_tiles<kCols, D, e4m3, false>(a, hp, s);
+  if (const TileUse use = tile_use(a); use != kToScan)
+    return a.tree ? launch_tiles<kCols, D, e4m3, true>(a, hp, use == kToBoth, s) : launch_tiles<kCols, D, e4m3, false>(a, hp, use == kToBoth, s);
   return a.tree ? launch_scan<__bf16, D, e4m3, true>(a, hp, s) : launch_scan<__bf16, D, e4m3, false>(a, hp, s);
 }
 

@@ -1,6 +1,6 @@
 // Query tiles for the paged Relation Cache's rows over 8-bit pages and of trees
 // (relation_paged_fwd_ex): where a request has many rows to a cached head, the keys are
-// brought into LDS once for 256 of them.
+// brought into LDS once for 256 of them. tile_use below says which requests come here.
 //
 // A work-group of eight waves takes 256 rows (whole tokens of a request, times the query
 // heads of a cached head), 32 to a wave, and goes through its keys in tiles of 64, which
@@ -22,7 +22,7 @@
 // than late ones.
 #pragma once
 
-#include "paged_device.h"
+#include "paged_scan.h"
 
 namespace rel {
 
@@ -60,8 +60,9 @@ struct TilePlanLds {
 };
 
 // Exclusive sums of the requests' units in sum[0 .. S], by a whole work-group of W waves.
+// Requests of up to `few` new tokens are the scan's.
 template <int W>
-__device__ __forceinline__ void tile_plan(const PagedArgs& a, int rows, long long* sum, Req* part, long long* red) {
+__device__ __forceinline__ void tile_plan(const PagedArgs& a, int rows, int few, long long* sum, Req* part, long long* red) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   long long done = 0;
   for (int b0 = 0; b0 < a.S; b0 += 64 * W) {
@@ -70,7 +71,7 @@ __device__ __forceinline__ void tile_plan(const PagedArgs& a, int rows, long lon
     if (b < a.S) {
       const Req r(a, b);
       if (part) part[b] = r;
-      if (r.q > 0) {
+      if (r.q > few) {
         const RowBlocks n(a, r, rows);
         own = n.before(n.blocks) * a.H_kv;
       }
@@ -96,18 +97,27 @@ __device__ __forceinline__ void tile_plan(const PagedArgs& a, int rows, long lon
   if (tid == 0) sum[a.S] = done;
 }
 
-__global__ __launch_bounds__(256) void tile_plan_kernel(PagedArgs a, int rows) {
+// The tiles' sums, and in the second work-group the scan's.
+__global__ __launch_bounds__(256) void tile_plan_kernel(PagedArgs a, int rows, int few) {
   __shared__ long long red[4];
-  tile_plan<4>(a, rows, ws_plan(a).unit_sum, nullptr, red);
+  __shared__ PlanScratch sc;
+  const Plan p = ws_plan(a);
+  if (blockIdx.x == 0) {
+    tile_plan<4>(a, rows, few, p.tile_sum, nullptr, red);
+  } else {
+    a.max_new = min(few, a.max_new);
+    make_plan(a, 32, false, sc, Plan{p.unit_sum, nullptr, nullptr});
+  }
 }
 
-// States of divided row blocks: the scan's records, room for two of every work-group's in
-// the chunks' part of the workspace (which is there: paged_chunks_possible).
+// States of divided row blocks: the second half of the scan's records (it has two row blocks
+// to an item here), room for two of every work-group's in the chunks' part of the workspace
+// (which is there: paged_chunks_possible).
 constexpr int tile_groups(int rows) { return kChunkStateRows / (2 * rows); }
-static_assert(tile_groups(128) <= kScanGroups, "a record for each");
+static_assert(tile_groups(128) <= kScanGroups / 2, "a record for each");
 __device__ __forceinline__ States tile_states(const PagedArgs& a) {
   States s = States::chunk(a);
-  s.cuts = States::scan(a).cuts;
+  s.cuts = States::scan(a).cuts + kScanGroups / 2;
   return s;
 }
 
@@ -237,7 +247,7 @@ enum : int { kNoWeights = 0, kAllSeen = 1, kMasked = 2 };
 
 // D: the layout's columns (64, 128), DR those of a row in memory; W: waves.
 template <int D, int DR, int W, typename Tc, bool kTree>
-__global__ __launch_bounds__(64 * W, 2) void tile_kernel(ScanArgs<__bf16, Tc, kTree> a, HeadParams hp) {
+__global__ __launch_bounds__(64 * W, 2) void tile_kernel(ScanArgs<__bf16, Tc, kTree> a, HeadParams hp, int few) {
   constexpr int kTileWaves = W, kTileRowsQ = 32 * W;
   using L = TileLayout<D>;
   using Q = QTile<D>;
@@ -268,9 +278,9 @@ __global__ __launch_bounds__(64 * W, 2) void tile_kernel(ScanArgs<__bf16, Tc, kT
   __shared__ int s_bad[kTileWaves];
   __shared__ TilePlanLds lds;
 
-  const long long* sum = ws_plan(a).unit_sum;
+  const long long* sum = ws_plan(a).tile_sum;
   if (a.S <= kPlanInline) {
-    tile_plan<W>(a, kTileRowsQ, lds.sum, lds.part, lds.red);
+    tile_plan<W>(a, kTileRowsQ, few, lds.sum, lds.part, lds.red);
     __syncthreads();
     sum = lds.sum;
   }
@@ -821,57 +831,88 @@ __global__ __launch_bounds__(64 * W, 2) void tile_kernel(ScanArgs<__bf16, Tc, kT
   }
 }
 
-// Joins of the row blocks that ranges divide, kTileRowsQ / 16 work-groups to a range.
+// Joins of the row blocks that ranges divide: of the tiles' ranges rows / 16 work-groups to
+// each, then of the scan's two.
 template <int DR, typename Tc, bool kTree>
-__global__ __launch_bounds__(kThreads) void tile_join_kernel(ScanArgs<__bf16, Tc, kTree> a, HeadParams hp, int rows) {
-  const int shares = rows / 16;
-  join_rows<__bf16, DR, Tc, kTree>(a, hp, tile_states(a), (int)blockIdx.x / shares, (int)blockIdx.x % shares, shares, rows, false);
+__global__ __launch_bounds__(kThreads) void tile_join_kernel(ScanArgs<__bf16, Tc, kTree> a, HeadParams hp, int rows, int groups) {
+  const int scan = (int)blockIdx.x - groups * (rows / 16), i = scan < 0 ? (int)blockIdx.x : scan, shares = scan < 0 ? rows / 16 : 2;
+  join_rows<__bf16, DR, Tc, kTree>(a, hp, scan < 0 ? tile_states(a) : States::scan(a), i / shares, i % shares, shares,
+                                   scan < 0 ? rows : 32, false);
 }
 
-// Whether the batch goes to query tiles. Two row blocks of the scan, 64 rows, are faster:
-// 32 requests of 64 rows over 4,000 8-bit rows of 8 heads of 128 120 us by the scan, 153 on
-// tiles; of 96 rows 172 and 159, of 256 387 and 230. And the tiles' fixed costs have to be
-// worth their while, by the rows of all heads times the most keys that a request can have:
-// one request of 64 tokens of 32 heads over 4,000 (8 million) 37 and 43 us, two over 16,000
-// (66 million) 101 and 81, 16 over 1,000 (33 million) 74 and 77. The host knows the tables'
-// width, not the lengths: short requests in wide tables lose up to 15 us. And the workspace
-// has to have the chunks' part.
+// Where a batch's requests go, by what the host knows: kToScan, kToTiles, or kToBoth (those of
+// up to kTileRowsLeast rows to a cached head to the scan).
+//   Two row blocks of the scan, 64 rows, are faster than a tile: 32 requests of 64 rows over
+//   4,000 8-bit rows of 8 heads of 128 120 us by the scan, 153 on tiles; of 96 rows 172 and
+//   159, of 256 387 and 230.
+//   The tiles' fixed costs have to be worth their while, by the rows of all heads times the
+//   most keys that a request can have, and 500 for what a row block costs beside them, scan
+//   and tiles: a prompt of 500 tokens of 8 heads (4 million) 19 and 29 us, a chunk of 64
+//   tokens of 32 heads over 4,000 rows (9) 35 and 37, 8 of 100 over none (16) 31 and 28, 16 of
+//   64 over 1,000 (49) 68 and 63, 65 trees of 60 over none (78) 84 and 35. The host knows the
+//   tables' width, not the lengths: short requests in wide tables lose up to 10 us.
+//   Where the requests have like numbers of tokens (kTileLike: the average is a quarter of the
+//   most), tiles for all are fastest, scan, both and tiles: 48 trees of 2 to 24 tokens of 16
+//   heads of 64 in 4 110, 98 and 85 us, 64 of 1 to 60 of 32 of 128 in 8 315, 232 and 220.
+//   Where few have many, tiles of few rows are slow, and those few alone are worth launches
+//   of their own from some 500 rows on. 62 tokens over 1,024 to 4,096 rows beside two chunks
+//   of 512, 32 heads of 128: 387, 357 and 707 us, in 8 cached heads 190, 177 and 216; 60
+//   beside four of 60, 16 heads in 4: 65, 88 and 98.
+// And the workspace has to have the chunks' part.
 constexpr int kTileRowsLeast = 64;
-constexpr int64_t kTileWork = 40000000;
-inline bool tiles_wanted(const PagedArgs& a) {
+constexpr int kTileRowsBeside = 512;
+constexpr int64_t kTileWork = 12000000;
+constexpr int kTileKeys = 500;
+constexpr int kTileLike = 4;
+enum TileUse { kToScan, kToTiles, kToBoth };
+inline TileUse tile_use(const PagedArgs& a) {
   const int G = a.H / a.H_kv;
-  const int64_t most = a.max_new < a.N ? a.max_new : a.N, keys = (int64_t)a.max_pages << a.page_shift;
-  return a.tiles && G <= 128 && most * G > kTileRowsLeast && paged_chunks_possible(most, G) && (int64_t)a.N * a.H * keys >= kTileWork;
+  const int64_t most = a.max_new < a.N ? a.max_new : a.N, keys = ((int64_t)a.max_pages << a.page_shift) + kTileKeys;
+  if (!a.tiles || G > 128 || most * G <= kTileRowsLeast || !paged_chunks_possible(most, G) || (int64_t)a.N * a.H * keys < kTileWork)
+    return kToScan;
+  if (kTileLike * (int64_t)a.N >= a.S * most) return kToTiles;
+  return most * G >= kTileRowsBeside ? kToBoth : kToScan;
 }
 
 template <int D, int DR, int W, typename Tc, bool kTree>
-hipError_t launch_tiles_of(const ScanArgs<__bf16, Tc, kTree>& a, const HeadParams& hp, hipStream_t s) {
+hipError_t launch_tiles_of(const ScanArgs<__bf16, Tc, kTree>& a, const HeadParams& hp, bool both, hipStream_t s) {
   int cu = 0;
   hipError_t e = device_cu_count(&cu);
   if (e != hipSuccess) return e;
-  cu *= 8 / W;
-  const int groups = cu < tile_groups(32 * W) ? cu : tile_groups(32 * W);
+  const int groups = cu * 8 / W < tile_groups(32 * W) ? cu * 8 / W : tile_groups(32 * W);
+  // The scan takes requests of up to `few` tokens (none where one token has more rows).
+  ScanArgs<__bf16, Tc, kTree> small = a;
+  const int few = both ? kTileRowsLeast / (a.H / a.H_kv) : 0;
+  small.max_new = few < a.max_new ? few : a.max_new;
+  int scan_groups = cu * Geom<Tc, DR, 2>::kPerCu;
+  scan_groups = few == 0 ? 0 : (scan_groups < kScanGroups / 2 ? scan_groups : kScanGroups / 2);
   if (a.S > kPlanInline) {
-    hipLaunchKernelGGL(tile_plan_kernel, dim3(1), dim3(256), 0, s, (const PagedArgs&)a, 32 * W);
+    hipLaunchKernelGGL(tile_plan_kernel, dim3(few == 0 ? 1 : 2), dim3(256), 0, s, (const PagedArgs&)a, 32 * W, few);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  hipLaunchKernelGGL((tile_kernel<D, DR, W, Tc, kTree>), dim3(groups), dim3(64 * W), 0, s, a, hp);
+  hipLaunchKernelGGL((tile_kernel<D, DR, W, Tc, kTree>), dim3(groups), dim3(64 * W), 0, s, a, hp, few);
   e = hipGetLastError();
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL((tile_join_kernel<DR, Tc, kTree>), dim3(groups * 2 * W), dim3(kThreads), 0, s, a, hp, 32 * W);
+  if (few > 0) {
+    hipLaunchKernelGGL((scan_kernel<__bf16, DR, 2, Tc, kTree>), dim3(scan_groups), dim3(kThreads), 0, s, small, hp, 0, 0);
+    e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  hipLaunchKernelGGL((tile_join_kernel<DR, Tc, kTree>), dim3(groups * 2 * W + scan_groups * 2), dim3(kThreads), 0, s, a, hp, 32 * W,
+                     groups);
   return hipGetLastError();
 }
 
 template <int D, int DR, typename Tc, bool kTree>
-hipError_t launch_tiles(const ScanArgs<__bf16, Tc, kTree>& a, const HeadParams& hp, hipStream_t s) {
+hipError_t launch_tiles(const ScanArgs<__bf16, Tc, kTree>& a, const HeadParams& hp, bool both, hipStream_t s) {
   // Up to 128 rows to a cached head: work-groups of four waves, two to a compute unit, where
   // the LDS holds both.
   if constexpr (D == 64) {
     const int64_t most = a.max_new < a.N ? a.max_new : a.N;
-    if (most * (a.H / a.H_kv) <= 128) return launch_tiles_of<D, DR, 4, Tc, kTree>(a, hp, s);
+    if (most * (a.H / a.H_kv) <= 128) return launch_tiles_of<D, DR, 4, Tc, kTree>(a, hp, false, s);
   }
-  return launch_tiles_of<D, DR, 8, Tc, kTree>(a, hp, s);
+  return launch_tiles_of<D, DR, 8, Tc, kTree>(a, hp, both, s);
 }
 
 }  // namespace

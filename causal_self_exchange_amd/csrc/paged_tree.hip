@@ -1,6 +1,6 @@
 // The paged Relation Cache's forward of trees of drafted tokens over pages of the tokens'
 // own type (relation_paged_fwd_ex): the scan of paged_scan.h with a row of ancestor bits
-// per token, or for bf16 batches with many rows and much work (tiles_wanted) the query tiles
+// per token, or for bf16 batches with many rows and much work (tile_use) the query tiles
 // of paged_tile.h. Only the steps that hold new tokens look at the bits.
 //
 // 48 trees of 2 to 24 tokens over 200 to 9,000 rows of 16 heads of 64 in 4 take 106 us by
@@ -16,7 +16,8 @@ namespace {
 template <typename Tin, int D>
 hipError_t launch_typed(const PagedExArgs& a, const HeadParams& hp, hipStream_t s) {
   if constexpr (sizeof(Tin) == 2)
-    if (tiles_wanted(a)) return launch_tiles<(D <= 64 ? 64 : 128), D, __bf16, true>(a, hp, s);
+    if (const TileUse use = tile_use(a); use != kToScan)
+      return launch_tiles<(D <= 64 ? 64 : 128), D, __bf16, true>(a, hp, use == kToBoth, s);
   return launch_scan<Tin, D, Tin, true>(a, hp, s);
 }
 

@@ -196,14 +196,21 @@ def many_rows(m, max_new=None):
     return most * (H // Hkv) > 64 and most * min(H // Hkv, 8) >= 65 and (m.get("tree") is not None or "k64" in m)
 
 
-def on_tiles(m, max_new=None):
-    """Whether such a batch goes to query tiles: by its rows times the most keys that its table admits."""
-    return many_rows(m, max_new) and m["N"] * m["P1"].shape[1] * m["table"].shape[1] * m["cP2"].shape[2] >= 40000000
+def tile_rows(m, max_new=None):
+    """The most rows to a cached head of requests that stay with the scan: by the batch's rows times the most keys that its
+    table admits (and 500), and by how like its requests are."""
+    H, Hkv = m["P1"].shape[1], m["cP2"].shape[1]
+    most = min(m["max_new"] if max_new is None else max_new, m["N"])
+    if not many_rows(m, max_new) or H // Hkv > 128 or m["N"] * H * (m["table"].shape[1] * m["cP2"].shape[2] + 500) < 12000000:
+        return 2**31
+    if 4 * m["N"] >= m["total"].shape[0] * most:
+        return 0
+    return 64 if most * (H // Hkv) >= 512 else 2**31
 
 
 def widened(m):
     """The same batch with a table wide enough for query tiles."""
-    cols = -(-40000000 // (m["N"] * m["P1"].shape[1] * m["cP2"].shape[2])) + 1
+    cols = -(-12000000 // (m["N"] * m["P1"].shape[1] * m["cP2"].shape[2])) + 1
     return dict(m, table=torch.cat([m["table"], torch.full((m["table"].shape[0], cols), P.BAD, dtype=torch.int32)], 1))
 
 
@@ -212,9 +219,15 @@ def limit(m, ref, spread, k, du=None, max_new=None):
     if m["P1"].dtype == torch.float32:
         return P.bound(ref, spread, "f32", 1e-6 if du is None else du)
     at_most, e_max = PW.evidence_error(m["P1"], torch.from_numpy(k))
-    if on_tiles(m, max_new):
-        return P.bound(ref, spread, "bf16", at_most + 8 * e_max * 2.0**-24)
-    return PW.weights_bound(ref, spread, int(m["total"].max()), at_most, e_max)
+    kept = PW.weights_bound(ref, spread, int(m["total"].max()), at_most, e_max)
+    least = tile_rows(m, max_new)
+    if least == 2**31:
+        return kept
+    G, tiled = m["P1"].shape[1] // m["cP2"].shape[1], np.zeros((m["N"], 1, 1), bool)
+    for a, b in zip(m["cu"].tolist(), m["cu"].tolist()[1:]):
+        if 0 <= a < b <= m["N"] and (b - a) * G > least:
+            tiled[a:b] = True
+    return np.where(tiled, P.bound(ref, spread, "bf16", at_most + 8 * e_max * 2.0**-24), kept)
 
 
 def check_ex(m, lam, fill=3.0, max_new=None, du=None):
@@ -229,7 +242,7 @@ def check_ex(m, lam, fill=3.0, max_new=None, du=None):
         lim = np.where(spread > 0, limit(b, ref, spread, k, du, max_new), 0.0)     # rows nobody writes stay exactly
         err = np.abs(P.f64(Y) - ref)
         worst = np.unravel_index(np.argmax(err - lim), err.shape)
-        assert np.all(err <= lim), (on_tiles(b, max_new), worst, err[worst], lim[worst], ref[worst])
+        assert np.all(err <= lim), (tile_rows(b, max_new), worst, err[worst], lim[worst], ref[worst])
     return Y
 
 
@@ -334,6 +347,22 @@ def test_fwd_query_tiles_many_requests(S, H, Hkv, d, new_hi):
     check_ex(m, 0.5)
 
 
+@pytest.mark.parametrize("pages,S,H,Hkv,d", [("e4m3", 40, 8, 2, 128), ("bf16", 40, 8, 8, 64), ("e4m3", 150, 4, 4, 48), ("bf16", 150, 16, 2, 80)])
+def test_fwd_single_tokens_beside_chunks(pages, S, H, Hkv, d):
+    """Requests for the scan and for query tiles in one call, both with histories that are divided."""
+    rng = np.random.default_rng(S + d)
+    reqs = [(int(rng.integers(0, 2500)), int(rng.integers(0, 3))) for _ in range(S)]
+    reqs[3], reqs[S // 2], reqs[S - 1] = (3000, 512 // (H // Hkv) + 3), (9000, 1), (70, 64 // (H // Hkv) + 1)
+    reqs[5] = (100, 64 // (H // Hkv))
+    m = widened(make8(H, Hkv, d, 32, reqs, S) if pages == "e4m3" else P.make(pages, H, Hkv, d, 32, reqs, S))
+    if pages == "e4m3":
+        assert tile_rows(m) == 64
+        check_ex(m, 0.5)
+    m = with_trees(m, reqs, 3, S)
+    assert tile_rows(m) == 64
+    check_ex(m, 0.5)
+
+
 @pytest.mark.parametrize("pages", ["e4m3", "bf16", "f32"])
 def test_fwd_tree_of_a_path_is_the_chunk(pages):
     """Trees that are one path, under any number of words, are the chunks' rows, bit for bit in the scan."""
@@ -433,10 +462,13 @@ def test_fwd_8bit_past_32_bit_offsets():
     sc = sc.view(torch.float8_e8m0fnu)
     small = m["table"].numpy()
     table = i32(np.where(small >= 0, where[np.clip(small, 0, None)], P.BAD))
-    for tree in (None, dev["tree"]):
+    wide = torch.full((len(reqs), 100), P.BAD, dtype=torch.int32, device=DEV)
+    for tree, cols in ((None, 0), (dev["tree"], 0), (None, 100), (dev["tree"], 100)):
         kw = dict(max_new=160, tree=tree)
-        want = R.paged_fwd(dev["P1"], dev["cP2"], dev["cV"], dev["table"], dev["total"], dev["cu"], m["tau"], 0.5, scale=dev["scale"], **kw)
-        got = R.paged_fwd(dev["P1"], *big, table, dev["total"], dev["cu"], m["tau"], 0.5, scale=sc, **kw)
+        assert (tile_rows(dict(m, table=torch.cat([m["table"], wide.cpu()[:, :cols]], 1))) == 0) == (cols > 0)
+        want = R.paged_fwd(dev["P1"], dev["cP2"], dev["cV"], torch.cat([dev["table"], wide[:, :cols]], 1), dev["total"], dev["cu"], m["tau"],
+                           0.5, scale=dev["scale"], **kw)
+        got = R.paged_fwd(dev["P1"], *big, torch.cat([table, wide[:, :cols]], 1), dev["total"], dev["cu"], m["tau"], 0.5, scale=sc, **kw)
         assert torch.equal(got, want)
     n = len(where)
     x = torch.from_numpy(np.random.default_rng(1).standard_normal((n, 2 * Hkv, d))).to(torch.bfloat16).to(DEV)
@@ -617,7 +649,7 @@ def test_calls_replay_in_a_graph(pages, width):
     """A whole step captured once and replayed with new lengths, trees and inputs, against the eager calls: in the scan, and
     in a table wide enough for query tiles."""
     S, N, H, Hkv, d, page, n_pages, held = 6, 300, 8, 2, 64, 16, 460, 60
-    assert (N * H * width * page >= 40000000) == (width > held)
+    assert (N * H * (width * page + 500) >= 12000000) == (width > held)
     rng = np.random.default_rng(2)
     lens0, nn, parent, keep, n_keep = (torch.zeros(k, dtype=torch.int32, device=DEV) for k in (S, S, N, N, S))
     base = rng.permutation(n_pages)
