@@ -162,12 +162,14 @@ __global__ __launch_bounds__(kThreads) void paged_append_kernel(PagedAppendArgs 
 //
 // The row is rounded once, from the fp32 of its rotation or mixing, as above but for P2's
 // sines and cosines, which are the fp64 ones rounded, and the factors of the mixing, from
-// fp64 angles in two parts: a value within 2^-23 of the middle between two steps may go to
-// either, and both are as near to it. The rotation in fp64 with a correct last rounding took
-// 16,384 tokens of 32 + 8 heads of 128 from 75 to 105 us.
+// fp64 angles in two parts. A value of P2 within 2^-23 of the middle between two steps may
+// go to either, and both are as near to it; a mixed one that is near there (one in 60,000)
+// is formed again in fp64. The rotation and mixing of all in fp64 took 16,384 tokens of 32 + 8
+// heads of 128 from 75 to 105 us.
 //
-// Bound by memory: those tokens read 201 MB and write 168 MB in 76 us, 4.8 TB/s (a copy of
-// 4 GB 4.7); 64 tokens of 32 + 32 heads take 6.4 us.
+// Bound by memory: those tokens read 201 MB and write 168 MB in 81 us, 4.6 TB/s (a copy of
+// 4 GB 4.7; without the check of the mixed values 77 us); 64 tokens of 32 + 32 heads take 7.0
+// us.
 constexpr int kLowScale = -100, kHighScale = 119;
 constexpr float kMostE4m3 = 448.0f;
 
@@ -230,6 +232,18 @@ __device__ __forceinline__ uint2 quantise8(const float (&x)[8], float inv) {
   int hi = __builtin_amdgcn_cvt_pk_fp8_f32(y[4], y[5], 0, false);
   hi = __builtin_amdgcn_cvt_pk_fp8_f32(y[6], y[7], hi, true);
   return make_uint2((unsigned)lo, (unsigned)hi);
+}
+
+// Whether x is within 8 steps of fp32 of the middle between two e4m3 values (of 2^-6 and
+// more over the row's scale, where these have four bits, whatever the scale).
+__device__ __forceinline__ bool near_tie(float x) { return (__float_as_uint(x) & 0xfffffu) - 0x7fff8u <= 16u; }
+
+// x in fp32, but not in the middle unless it is there.
+__device__ __forceinline__ float beside_tie(double x) {
+  const float f = (float)x;
+  unsigned b = __float_as_uint(f);
+  if ((b & 0xfffffu) == 0x80000u && (double)f != x) b += fabs(x) > fabs((double)f) ? 1u : -1u;
+  return __uint_as_float(b);
 }
 
 // One work-group per token, as above: the rows that are quantised first, then P1.
@@ -298,6 +312,7 @@ __global__ __launch_bounds__(kThreads) void paged_append_q8_kernel(PagedAppendAr
       if (a.mix) {
         const int ha = a.pairing == 0 ? 2 * k : 2 * k + 1, hb = (ha + 1) % a.H_kv;
         if (g < kGroups) {
+          constexpr int kTogether = 4;                     // with 8 the registers cost two work-groups: 96 us
           const float c = pp.cos_theta[k], s = pp.sin_theta[k], cr = qp.cos_rest[k], sr = qp.sin_rest[k];
 #pragma unroll
           for (int w = 0; w < 2; ++w) {
@@ -305,15 +320,29 @@ __global__ __launch_bounds__(kThreads) void paged_append_q8_kernel(PagedAppendAr
             load8(src + (size_t)hb * D + 8 * w, y[w]);
           }
 #pragma unroll
-          for (int w = 0; w < 2; ++w)
+          for (int e0 = 0; e0 < 16; e0 += kTogether) {
+            float p[kTogether], q[kTogether];
+            bool near = false;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const float p = x[w][e], q = y[w][e];
+            for (int e = 0; e < kTogether; ++e) {
+              float &u = x[(e0 + e) >> 3][(e0 + e) & 7], &v = y[(e0 + e) >> 3][(e0 + e) & 7];
+              p[e] = u;
+              q[e] = v;
               // c, s times a bf16 number is exact: each sum is rounded once, and again with
               // what the factors' rests give.
-              x[w][e] = fmaf(c, p, -s * q) + fmaf(cr, p, -sr * q);
-              y[w][e] = fmaf(s, p, c * q) + fmaf(sr, p, cr * q);
+              u = fmaf(c, p[e], -s * q[e]) + fmaf(cr, p[e], -sr * q[e]);
+              v = fmaf(s, p[e], c * q[e]) + fmaf(sr, p[e], cr * q[e]);
+              near |= near_tie(u) | near_tie(v);
             }
+            if (near) {
+              const double cd = (double)c + cr, sd = (double)s + sr;
+#pragma unroll
+              for (int e = 0; e < kTogether; ++e) {
+                x[(e0 + e) >> 3][(e0 + e) & 7] = beside_tie(cd * p[e] - sd * q[e]);
+                y[(e0 + e) >> 3][(e0 + e) & 7] = beside_tie(sd * p[e] + cd * q[e]);
+              }
+            }
+          }
         }
         store_row(1, ha, g, 16 * g, 16 * g + 8, x[0], x[1]);
         store_row(1, hb, g, 16 * g, 16 * g + 8, y[0], y[1]);

@@ -686,8 +686,9 @@ def paged_fwd(P1, cache_P2, cache_V, block_table, total, cu, tau, lam: float = 0
     """Y [N, H, d_h] of a packed batch of new tokens whose own rows are in the
     pages already: P1 [N, H, d_h] (rotated), caches [n_pages, H_kv, page_size,
     d_h], block_table int32[S, max_pages], total int32[S], cu int32[S+1]
-    (page_map). max_new: the most new tokens of one request (default N). Rows that
-    no request owns are not written (zero in a Y that the call allocates).
+    (page_map). max_new: the most new tokens of one request (default N; the closer,
+    the better the choice of kernels). Rows that no request owns are not written (zero
+    in a Y that the call allocates).
 
     8-bit pages: float8_e4m3fn caches with scale (paged_append) and a bfloat16 P1.
     tree: int32[N, words] ancestor bits (tree_plan): a token of a request of at most

@@ -532,7 +532,8 @@ rel_status relation_paged_fwd(const void* P1, int64_t ld1, const void* cache_P2,
  *
  *   cache_scale : out, as above; written for the rows that are
  *   theta       : host double[H_kv / 2]: an angle in fp32 is far enough from the one that
- *                 is meant to store the farther of two e4m3 neighbours now and then
+ *                 is meant to store the farther of two e4m3 neighbours now and then (I~
+ *                 is formed in fp64 where fp32 leaves open which is the nearer one)
  * Other arguments as in relation_paged_append.
  */
 rel_status relation_paged_append_q8(const void* P1, const void* P2, const void* I,
