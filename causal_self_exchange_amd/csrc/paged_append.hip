@@ -160,16 +160,13 @@ __global__ __launch_bounds__(kThreads) void paged_append_kernel(PagedAppendArgs 
 // forward turns the values back into bf16. Lanes of a power of two share a row (16
 // elements each), so that its maximum is a few exchanges between lanes.
 //
-// The row is rounded once, from the fp32 of its rotation or mixing, as above but for P2's
-// sines and cosines, which are the fp64 ones rounded, and the factors of the mixing, from
-// fp64 angles in two parts. A value of P2 within 2^-23 of the middle between two steps may
-// go to either, and both are as near to it; a mixed one that is near there (one in 60,000)
-// is formed again in fp64. The rotation and mixing of all in fp64 took 16,384 tokens of 32 + 8
-// heads of 128 from 75 to 105 us.
+// The row is rounded once, from the fp32 of its rotation or mixing, as above but for the
+// cosines and sines, which are fp64 ones in two parts (the mixing's from fp64 angles). A value that is near the middle between two steps then (one in
+// 60,000) is formed again in fp64, so that the nearest is stored. All rotations and mixings in
+// fp64 took 16,384 tokens of 32 + 8 heads of 128 from 75 to 105 us.
 //
-// Bound by memory: those tokens read 201 MB and write 168 MB in 81 us, 4.6 TB/s (a copy of
-// 4 GB 4.7; without the check of the mixed values 77 us); 64 tokens of 32 + 32 heads take 7.0
-// us.
+// Bound by memory: those tokens read 201 MB and write 168 MB in 85 us, 4.3 TB/s (a copy of
+// 4 GB 4.7; without the values formed again 77 us); 64 tokens of 32 + 32 heads take 7.5 us.
 constexpr int kLowScale = -100, kHighScale = 119;
 constexpr float kMostE4m3 = 448.0f;
 
@@ -246,6 +243,50 @@ __device__ __forceinline__ float beside_tie(double x) {
   return __uint_as_float(b);
 }
 
+// Values that are looked at together: with 8 the registers cost two work-groups (of the
+// mixing: 96 us).
+constexpr int kTogether = 4;
+
+// A number in two parts: 16 bits, whose products with bf16 numbers are exact in fp32, and
+// what they leave, to 2^-39.
+__device__ __forceinline__ float2 split(double x) {
+  const float hi = __uint_as_float(__float_as_uint((float)x) & 0xffffff00u);
+  return make_float2(hi, (float)(x - hi));
+}
+
+// turn for a row that is quantised, by split cosines and sines: each sum of exact products is
+// rounded once, and again with what the rests give, so that its error is a few steps of the
+// result also where a pair nearly cancels.
+template <int kRope>
+__device__ __forceinline__ void turn_q8(const float2* cs, const float2* sn, float (&x)[8], float (&y)[8]) {
+#pragma unroll
+  for (int e0 = 0; e0 < 8; e0 += kTogether) {
+    float p[kTogether], q[kTogether];
+    bool near = false;
+#pragma unroll
+    for (int e = 0; e < kTogether; ++e) {
+      const int k = e0 + e;
+      float &u = kRope == 2 ? x[k] : (k < 4 ? x[2 * k] : y[2 * k - 8]), &v = kRope == 2 ? y[k] : (k < 4 ? x[2 * k + 1] : y[2 * k - 7]);
+      p[e] = u;
+      q[e] = v;
+      const float2 c = cs[k], n = sn[k];
+      u = fmaf(c.x, p[e], -n.x * q[e]) + fmaf(c.y, p[e], -n.y * q[e]);
+      v = fmaf(n.x, p[e], c.x * q[e]) + fmaf(n.y, p[e], c.y * q[e]);
+      near |= near_tie(u) | near_tie(v);
+    }
+    if (near) {
+#pragma unroll
+      for (int e = 0; e < kTogether; ++e) {
+        const int k = e0 + e;
+        float &u = kRope == 2 ? x[k] : (k < 4 ? x[2 * k] : y[2 * k - 8]), &v = kRope == 2 ? y[k] : (k < 4 ? x[2 * k + 1] : y[2 * k - 7]);
+        const double c = (double)cs[k].x + cs[k].y, n = (double)sn[k].x + sn[k].y;
+        u = beside_tie(c * p[e] - n * q[e]);
+        v = beside_tie(n * p[e] + c * q[e]);
+      }
+    }
+  }
+}
+
 // One work-group per token, as above: the rows that are quantised first, then P1.
 template <int D>
 __global__ __launch_bounds__(kThreads) void paged_append_q8_kernel(PagedAppendArgs a, uint8_t* scale, AppendQ8Params qp, int first) {
@@ -253,7 +294,7 @@ __global__ __launch_bounds__(kThreads) void paged_append_q8_kernel(PagedAppendAr
   constexpr int kGroups = D / 16;
   constexpr int kLanes = kGroups <= 2 ? 2 : (kGroups <= 4 ? 4 : 8);   // of a row
   __shared__ float s_cos[D / 2], s_sin[D / 2];
-  __shared__ float s_cos2[D / 2], s_sin2[D / 2];          // P2's
+  __shared__ float2 s_cos2[D / 2], s_sin2[D / 2];         // P2's, split
   const int t = first + (int)blockIdx.x;
   const int slot = a.slot[t];
   if (slot < 0 || (slot >> a.page_shift) >= a.n_pages) return;   // uniform for the work-group
@@ -266,8 +307,8 @@ __global__ __launch_bounds__(kThreads) void paged_append_q8_kernel(PagedAppendAr
     s_sin[tid] = sn;
     double sn2, cs2;
     sincos_f64(ang, &sn2, &cs2);
-    s_cos2[tid] = (float)cs2;
-    s_sin2[tid] = (float)sn2;
+    s_cos2[tid] = split(cs2);
+    s_sin2[tid] = split(sn2);
   }
   __syncthreads();
   const int page = slot >> a.page_shift, off = slot & ((1 << a.page_shift) - 1);
@@ -303,7 +344,8 @@ __global__ __launch_bounds__(kThreads) void paged_append_q8_kernel(PagedAppendAr
         const __bf16* src = static_cast<const __bf16*>(a.P2) + (size_t)t * a.ld2 + (size_t)h * D;
         load8(src + oa, x[0]);
         load8(src + ob, x[1]);
-        turn(a.rope, s_cos2 + 8 * g, s_sin2 + 8 * g, x[0], x[1]);
+        if (a.rope == 1) turn_q8<1>(s_cos2 + 8 * g, s_sin2 + 8 * g, x[0], x[1]);
+        else if (a.rope == 2) turn_q8<2>(s_cos2 + 8 * g, s_sin2 + 8 * g, x[0], x[1]);
       }
       store_row(0, h, g, oa, ob, x[0], x[1]);
     } else if (u < keys + info) {
@@ -312,7 +354,6 @@ __global__ __launch_bounds__(kThreads) void paged_append_q8_kernel(PagedAppendAr
       if (a.mix) {
         const int ha = a.pairing == 0 ? 2 * k : 2 * k + 1, hb = (ha + 1) % a.H_kv;
         if (g < kGroups) {
-          constexpr int kTogether = 4;                     // with 8 the registers cost two work-groups: 96 us
           const float c = pp.cos_theta[k], s = pp.sin_theta[k], cr = qp.cos_rest[k], sr = qp.sin_rest[k];
 #pragma unroll
           for (int w = 0; w < 2; ++w) {
@@ -328,8 +369,7 @@ __global__ __launch_bounds__(kThreads) void paged_append_q8_kernel(PagedAppendAr
               float &u = x[(e0 + e) >> 3][(e0 + e) & 7], &v = y[(e0 + e) >> 3][(e0 + e) & 7];
               p[e] = u;
               q[e] = v;
-              // c, s times a bf16 number is exact: each sum is rounded once, and again with
-              // what the factors' rests give.
+              // As in turn_q8.
               u = fmaf(c, p[e], -s * q[e]) + fmaf(cr, p[e], -sr * q[e]);
               v = fmaf(s, p[e], c * q[e]) + fmaf(sr, p[e], cr * q[e]);
               near |= near_tie(u) | near_tie(v);

@@ -525,15 +525,15 @@ rel_status relation_paged_fwd(const void* P1, int64_t ld1, const void* cache_P2,
 /*
  * relation_paged_append_q8 - relation_paged_append of bf16 tokens into 8-bit pages:
  * the rotated P2 and the mixed I~ of a token are rounded once, from their fp32
- * values x, to e4m3 values of x / 2^k (nearest even), k the least exponent with
+ * values x (from fp64 where fp32 leaves two neighbours as near, 2^-6 and more over
+ * the scale), to e4m3 values of x / 2^k (nearest even), k the least exponent with
  * max |x| <= 448 * 2^k over the row's finite elements, kept in [-100, 119] (what
  * is larger saturates at 448 * 2^119). NaN and infinities are stored as NaN. P1o is
  * bf16, as there.
  *
  *   cache_scale : out, as above; written for the rows that are
  *   theta       : host double[H_kv / 2]: an angle in fp32 is far enough from the one that
- *                 is meant to store the farther of two e4m3 neighbours now and then (I~
- *                 is formed in fp64 where fp32 leaves open which is the nearer one)
+ *                 is meant to store the farther of two e4m3 neighbours now and then
  * Other arguments as in relation_paged_append.
  */
 rel_status relation_paged_append_q8(const void* P1, const void* P2, const void* I,

@@ -141,6 +141,33 @@ def test_paged_append_q8_mixes_by_fp64_angles():
     assert np.all(np.abs(q - y) <= half + off)
 
 
+@pytest.mark.parametrize("rope", ["interleaved", "half"])
+def test_paged_append_q8_rotates_to_the_nearest(rope):
+    """As above, of P2. The angles are below 2^15, so those in fp64 (and the frequencies' last bit) are within 2^-37."""
+    N, Hkv, d, page = 2048, 8, 128, 16
+    rng = np.random.default_rng(6)
+    x = torch.from_numpy(rng.standard_normal((N, Hkv, d))).to(torch.bfloat16)
+    pos = rng.integers(0, 20000, N)
+    c = [torch.zeros((N // page, Hkv, page, d), device=DEV).to(torch.float8_e4m3fn) for _ in range(2)]
+    sc = scales(N // page, Hkv, page)
+    R.paged_append(x.to(DEV), x.to(DEV), i32(np.arange(N)), *c, pos=i32(pos), rope=rope, scale=sc)
+    torch.cuda.synchronize()
+    k = exps(sc)[:, :, 0].transpose(0, 2, 1).reshape(N, Hkv, 1)
+    q = P.f64(c[0]).transpose(0, 2, 1, 3).reshape(N, Hkv, d)
+    ang = pos[:, None, None] * 10000.0 ** (-2.0 * np.arange(d // 2) / d)
+    half = rope == "half"
+    a, b = (P.f64(x)[..., :d // 2], P.f64(x)[..., d // 2:]) if half else (P.f64(x)[..., 0::2], P.f64(x)[..., 1::2])
+    both = [np.cos(ang) * a - np.sin(ang) * b, np.sin(ang) * a + np.cos(ang) * b]
+    mag = np.abs(a) + np.abs(b)
+    y, mag = (np.concatenate(both, -1), np.concatenate([mag, mag], -1)) if half else (
+        np.stack(both, -1).reshape(N, Hkv, d), np.repeat(mag, 2, -1))
+    y, mag = y / 2.0**k, mag / 2.0**k
+    step = 2.0 ** (np.maximum(np.floor(np.log2(np.maximum(np.abs(y), 2.0**-40))), -6) - 4)
+    # Below four bits, fp32: two roundings of the sum, and those of the split factors (2^-39 each).
+    off = np.where(np.abs(y) >= 2.0**-6, 0.0, np.abs(y) * 2.0**-22) + mag * 2.0**-36
+    assert np.all(np.abs(q - y) <= step + off)
+
+
 # ---- plan ----------------------------------------------------------------------------
 
 @pytest.mark.parametrize("S,n_hi,words,pad,seed", [(1, 1, 1, 0, 1), (3, 12, 1, 0, 2), (40, 32, 1, 7, 3), (17, 64, 2, 300, 4),
