@@ -666,12 +666,14 @@ __global__ __launch_bounds__(64 * W, 2) void tile_kernel(ScanArgs<__bf16, Tc, kT
 
     // The offset 0 is exact where nothing overflows: SiLU >= -0.2785, so no weight is small.
     // Row sums up to 2^100 and, in parts (at most 256 to a row block), results up to 2^119
-    // pass; else the segment is scanned again with a stabiliser that follows the scores.
+    // pass; else the segment is scanned again with a stabiliser that follows the scores. The
+    // maximum keeps a NaN (products of both signs past the range leave nothing else), which
+    // is below no limit.
     float omax = 0.0f;
 #pragma unroll
     for (int db = 0; db < L::kDb; ++db)
 #pragma unroll
-      for (int r = 0; r < 16; ++r) omax = fmaxf(omax, fabsf(o[db][r]));
+      for (int r = 0; r < 16; ++r) omax = __builtin_elementwise_maximum(omax, fabsf(o[db][r]));
     const bool fine = l <= kFinite && omax < (slot >= 0 ? kPartFinite : INFINITY);
     const bool bad = __any(ok && !fine);
     if (lane == 0) s_bad[wave] = bad ? 1 : 0;
