@@ -731,13 +731,14 @@ __device__ __forceinline__ void fwd_body(const FwdArgs& a, const HeadParams& hp,
 
     // Exactness of the fixed offset: every row sum below 2^100 and O finite. A part of a
     // query tile (paged) stays below 2^119, so that its at most 256 parts (one to a range)
-    // sum to 2^127 at most.
+    // sum to 2^127 at most. The maximum keeps a NaN (products of both signs past the range
+    // leave nothing else), which is below no limit.
     const float lrow = kLse && !kPaged ? lane_pair_sum(lsum) : l16[0];
     float omax = 0.0f;
 #pragma unroll
     for (int db = 0; db < C::kDb; ++db)
 #pragma unroll
-      for (int r = 0; r < 16; ++r) omax = fmaxf(omax, fabsf(o[db][r]));
+      for (int r = 0; r < 16; ++r) omax = __builtin_elementwise_maximum(omax, fabsf(o[db][r]));
     const bool ok = lrow <= kFinite && omax < (kPaged && sg.slot >= 0 ? kPartFinite : INFINITY);
     const bool wave_bad = __any(!ok);
     if (lane_now() == 0) flags[wave] = wave_bad ? 1 : 0;
