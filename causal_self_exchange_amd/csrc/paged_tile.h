@@ -273,7 +273,8 @@ __global__ __launch_bounds__(64 * W, 2) void tile_kernel(ScanArgs<__bf16, Tc, kT
   constexpr int kScan = kRing + kTileWaves * kAhead * kRaw;
   constexpr int kBytes = kScan > kTileRowsQ * kYStride ? kScan : kTileRowsQ * kYStride;
   constexpr int kNS = 2 * L::kDs;                         // MFMA steps of a block
-  constexpr float kFinite = 0x1p100f, kPartFinite = 0x1p119f;
+  constexpr float kFinite = 0x1p100f;
+  constexpr float kPartFinite = 0x1p127f / tile_groups(kTileRowsQ);   // a row block has at most one part to a range
   __shared__ __attribute__((aligned(16))) char smem[kBytes];
   __shared__ int s_bad[kTileWaves];
   __shared__ TilePlanLds lds;
@@ -665,8 +666,8 @@ __global__ __launch_bounds__(64 * W, 2) void tile_kernel(ScanArgs<__bf16, Tc, kT
     l = l16[0];
 
     // The offset 0 is exact where nothing overflows: SiLU >= -0.2785, so no weight is small.
-    // Row sums up to 2^100 and, in parts (at most 256 to a row block), results up to 2^119
-    // pass; else the segment is scanned again with a stabiliser that follows the scores. The
+    // Row sums up to 2^100 and, in parts, results of which all together reach 2^127 (2^119 of
+    // eight waves, 2^118 of four) pass; else the segment is scanned again with a stabiliser that follows the scores. The
     // maximum keeps a NaN (products of both signs past the range leave nothing else), which
     // is below no limit.
     float omax = 0.0f;

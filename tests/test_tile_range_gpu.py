@@ -74,3 +74,21 @@ def test_query_tiles(pages, d, H, Hkv, reqs, top):
     for x in ([m] if pages == "e4m3" else []) + [tree]:
         assert TX.tile_rows(TX.widened(x)) == 0
         TX.check_ex(x, 0.5)
+
+
+@pytest.mark.parametrize("top", [99.5, 102.0])
+@pytest.mark.parametrize("d,H,n", [(64, 8, 16), (64, 8, 32)])
+def test_parts_of_large_values(d, H, n, top):
+    """A row block in as many parts as there are ranges, of four waves (512) and of eight (256): 140,000 rows of one evidence
+    of 9 (weights of 2^13) and V about 2^top, so parts just below the range over their number, and more than the range together.
+    du as in test_joined_tiles_of_large_values."""
+    m = P.make("bf16", H, 1, d, 64, [(140000, n)], seed=1)
+    m["P1"] = torch.full_like(m["P1"], 1.0625)
+    m["cP2"] = torch.where(m["cP2"].isnan(), m["cP2"], 1.0625)
+    m["cV"] = (2.0**(top - 2) * (1.0 + 0.25 * m["cV"].float())).to(torch.bfloat16)
+    m = X.as_8bit(m)
+    assert TX.tile_rows(m) == 0
+    Y = TX.run_ex(m, 0.5)
+    assert bool(torch.isfinite(Y).all())
+    w = dict(m, cP2=torch.from_numpy(m["k64"]), cV=torch.from_numpy(m["v64"]))
+    PR.check_rows(w, Y, 0, [0, n - 1], [0, H - 1], 0.5, lambda r, s: P.bound(r, s, "bf16", 4e-5))
