@@ -22,7 +22,19 @@ __global__ __launch_bounds__(kThreads) void tree_plan_kernel(TreePlanArgs a) {
   __shared__ unsigned s_own[32 * REL_MAX_TREE_WORDS];   // those among them
   const int b = blockIdx.x, tid = threadIdx.x;
   if (b == a.S) {
-    for (int64_t t = (int64_t)max(a.cu[a.S], 0) + tid; t < a.N; t += kThreads) a.pos[t] = -1;
+    // Behind the last request; where that one ends past N, behind the last that does not.
+    int from = max(a.cu[a.S], 0);
+    if (from > a.N) {
+      from = 0;
+      for (int k = tid; k < a.S; k += kThreads) from = max(from, a.cu[k] <= a.N ? a.cu[k] : 0);
+#pragma unroll
+      for (int o = 32; o > 0; o >>= 1) from = max(from, __shfl_xor(from, o, 64));
+      if ((tid & 63) == 0) s_up[tid >> 6] = from;
+      __syncthreads();
+#pragma unroll
+      for (int w = 0; w < kThreads / 64; ++w) from = max(from, s_up[w]);
+    }
+    for (int64_t t = (int64_t)from + tid; t < a.N; t += kThreads) a.pos[t] = -1;
     return;
   }
   const int first = a.cu[b], end = a.cu[b + 1], total = a.total[b];

@@ -557,8 +557,8 @@ rel_status relation_paged_append_q8(const void* P1, const void* P2, const void* 
  *            other rows are left as they were
  *   pos    : out, device int32[N]: cached rows plus ancestors (a chunk's tokens: plus
  *            their place), the position at which the token is rotated and would stay
- *            if its path were kept; -1 for padding and for tokens of refused requests.
- *            Requests with cu outside [0, N] are skipped.
+ *            if its path were kept; -1 for padding and for tokens of refused requests,
+ *            those that run past N (and all behind them) among them
  * 1 <= tree_words <= REL_MAX_TREE_WORDS.
  */
 rel_status relation_tree_plan(const int32_t* parent, const int32_t* total,

@@ -54,7 +54,9 @@ def tree_plan(parent, total, cu, words, tree0, pos0):
     """(tree, pos); rows and entries that are left alone come from tree0 and pos0."""
     N = len(parent)
     tree, pos = np.array(tree0, dtype=np.int64), np.array(pos0, dtype=np.int64)
-    pos[max(int(cu[-1]), 0):] = -1
+    # Behind the last request; where that one ends past N, behind the last that does not.
+    last = int(cu[-1])
+    pos[max([0] + [int(c) for c in cu if c <= N]) if last > N else max(last, 0):] = -1
     for b in range(len(total)):
         f, q = int(cu[b]), int(cu[b + 1]) - int(cu[b])
         if not (0 <= f and q > 0 and f + q <= N):
