@@ -242,6 +242,14 @@ __device__ __forceinline__ void tile_barrier() {
   asm volatile("" ::: "memory");
 }
 
+// The wait states between the last products and the first read of their results.
+__device__ __forceinline__ void settle(f32x16 (&o)[2], f32x4& l) {
+  asm volatile("s_nop 15\n\ts_nop 3" : "+v"(o[0]), "+v"(o[1]), "+v"(l) : : "memory");
+}
+__device__ __forceinline__ void settle(f32x16 (&o)[4], f32x4& l) {
+  asm volatile("s_nop 15\n\ts_nop 3" : "+v"(o[0]), "+v"(o[1]), "+v"(o[2]), "+v"(o[3]), "+v"(l) : : "memory");
+}
+
 // What a block step does with the weights.
 enum : int { kNoWeights = 0, kAllSeen = 1, kMasked = 2 };
 
@@ -661,8 +669,10 @@ __global__ __launch_bounds__(64 * W, 2) void tile_kernel(ScanArgs<__bf16, Tc, kT
       }
     }
     // The compiler has left out wait states between a product and what reads it behind a
-    // branch.
-    asm volatile("s_nop 15\n\ts_nop 3\n\ts_waitcnt vmcnt(0)" ::: "memory");   // and the last direct loads
+    // branch; the results go through the wait, so that no read of them moves before it. And
+    // the last direct loads.
+    settle(o, l16);
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     l = l16[0];
 
     // The offset 0 is exact where nothing overflows: SiLU >= -0.2785, so no weight is small.
@@ -744,7 +754,7 @@ __global__ __launch_bounds__(64 * W, 2) void tile_kernel(ScanArgs<__bf16, Tc, kT
         }
         __syncthreads();
       }
-      asm volatile("s_nop 15\n\ts_nop 3" ::: "memory");
+      settle(o, l16);
       l = lane_pair_sum(l);
     }
 
