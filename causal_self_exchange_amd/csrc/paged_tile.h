@@ -11,6 +11,12 @@
 // times their scale, exactly. The products are the 32x32x16 ones of the forward: a lane
 // holds one query row's scores and weights, and no state of a row is divided between waves.
 //
+// The weights are rounded to bf16 once for the transport, and summed rounded, as in the
+// forward. Two bf16 terms a weight, as in the scan, took six chunks of 100 to 1,500 tokens of
+// 32 heads in 8 of 128 from 317 to 408 us, 48 trees of 2 to 24 tokens of 16 in 4 of 64 from 84
+// to 99, 16 of 20 to 64 over up to 30,000 rows of 32 in 8 of 128 from 324 to 398. The results
+// are off by 0.0021 to 0.0022 of their norm, with two terms by 0.0017, the rounding of Y.
+//
 // Bound by the loop's issue: a wave's tile is 36 products (1,090 cycles of the matrix unit),
 // 96 transcendentals and about 290 other instructions; a compute unit's takes 4,450 cycles
 // where the products alone would take 2,180 (with one wave to a SIMD 3,240, of 1,090). Two
@@ -853,8 +859,12 @@ __global__ __launch_bounds__(kThreads) void tile_join_kernel(ScanArgs<__bf16, Tc
                                    scan < 0 ? rows : 32, false);
 }
 
-// Where a batch's requests go, by what the host knows: kToScan, kToTiles, or kToBoth (those of
-// up to kTileRowsLeast rows to a cached head to the scan).
+// Where a batch's requests go, by what the host knows: kToScan, kToTiles (but for those of one
+// new token), or kToBoth (those of up to kTileRowsLeast rows to a cached head to the scan).
+//   Single tokens are the scan's in any batch, so that their weights have two terms whatever
+//   the other requests are. Where there are none the scan's launch takes 2 to 4 us: 48 trees of
+//   2 to 24 tokens, as below, 87 us without it and 89 with it, 65 of 60 over none 35 and 38.5,
+//   64 of 1 to 30 tokens of 32 heads of 64 in 8, some of them single, 117 and 130.
 //   Two row blocks of the scan, 64 rows, are faster than a tile: 32 requests of 64 rows over
 //   4,000 8-bit rows of 8 heads of 128 120 us by the scan, 153 on tiles; of 96 rows 172 and
 //   159, of 256 387 and 230.
@@ -881,37 +891,34 @@ enum TileUse { kToScan, kToTiles, kToBoth };
 inline TileUse tile_use(const PagedArgs& a) {
   const int G = a.H / a.H_kv;
   const int64_t most = a.max_new < a.N ? a.max_new : a.N, keys = ((int64_t)a.max_pages << a.page_shift) + kTileKeys;
-  if (!a.tiles || G > 128 || most * G <= kTileRowsLeast || !paged_chunks_possible(most, G) || (int64_t)a.N * a.H * keys < kTileWork)
+  if (!a.tiles || G > 128 || most < 2 || most * G <= kTileRowsLeast || !paged_chunks_possible(most, G) || (int64_t)a.N * a.H * keys < kTileWork)
     return kToScan;
   if (kTileLike * (int64_t)a.N >= a.S * most) return kToTiles;
   return most * G >= kTileRowsBeside ? kToBoth : kToScan;
 }
 
 template <int D, int DR, int W, typename Tc, bool kTree>
-hipError_t launch_tiles_of(const ScanArgs<__bf16, Tc, kTree>& a, const HeadParams& hp, bool both, hipStream_t s) {
+hipError_t launch_tiles_of(const ScanArgs<__bf16, Tc, kTree>& a, const HeadParams& hp, int few, hipStream_t s) {
   int cu = 0;
   hipError_t e = device_cu_count(&cu);
   if (e != hipSuccess) return e;
   const int groups = cu * 8 / W < tile_groups(32 * W) ? cu * 8 / W : tile_groups(32 * W);
-  // The scan takes requests of up to `few` tokens (none where one token has more rows).
+  // The scan takes requests of up to `few` tokens, one at least.
   ScanArgs<__bf16, Tc, kTree> small = a;
-  const int few = both ? kTileRowsLeast / (a.H / a.H_kv) : 0;
   small.max_new = few < a.max_new ? few : a.max_new;
   int scan_groups = cu * Geom<Tc, DR, 2>::kPerCu;
-  scan_groups = few == 0 ? 0 : (scan_groups < kScanGroups / 2 ? scan_groups : kScanGroups / 2);
+  scan_groups = scan_groups < kScanGroups / 2 ? scan_groups : kScanGroups / 2;
   if (a.S > kPlanInline) {
-    hipLaunchKernelGGL(tile_plan_kernel, dim3(few == 0 ? 1 : 2), dim3(256), 0, s, (const PagedArgs&)a, 32 * W, few);
+    hipLaunchKernelGGL(tile_plan_kernel, dim3(2), dim3(256), 0, s, (const PagedArgs&)a, 32 * W, few);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
   hipLaunchKernelGGL((tile_kernel<D, DR, W, Tc, kTree>), dim3(groups), dim3(64 * W), 0, s, a, hp, few);
   e = hipGetLastError();
   if (e != hipSuccess) return e;
-  if (few > 0) {
-    hipLaunchKernelGGL((scan_kernel<__bf16, DR, 2, Tc, kTree>), dim3(scan_groups), dim3(kThreads), 0, s, small, hp, 0, 0);
-    e = hipGetLastError();
-    if (e != hipSuccess) return e;
-  }
+  hipLaunchKernelGGL((scan_kernel<__bf16, DR, 2, Tc, kTree>), dim3(scan_groups), dim3(kThreads), 0, s, small, hp, 0, 0);
+  e = hipGetLastError();
+  if (e != hipSuccess) return e;
   hipLaunchKernelGGL((tile_join_kernel<DR, Tc, kTree>), dim3(groups * 2 * W + scan_groups * 2), dim3(kThreads), 0, s, a, hp, 32 * W,
                      groups);
   return hipGetLastError();
@@ -921,11 +928,12 @@ template <int D, int DR, typename Tc, bool kTree>
 hipError_t launch_tiles(const ScanArgs<__bf16, Tc, kTree>& a, const HeadParams& hp, bool both, hipStream_t s) {
   // Up to 128 rows to a cached head: work-groups of four waves, two to a compute unit, where
   // the LDS holds both.
+  const int G = a.H / a.H_kv, few = both && kTileRowsLeast > G ? kTileRowsLeast / G : 1;
   if constexpr (D == 64) {
     const int64_t most = a.max_new < a.N ? a.max_new : a.N;
-    if (most * (a.H / a.H_kv) <= 128) return launch_tiles_of<D, DR, 4, Tc, kTree>(a, hp, false, s);
+    if (most * G <= 128) return launch_tiles_of<D, DR, 4, Tc, kTree>(a, hp, few, s);
   }
-  return launch_tiles_of<D, DR, 8, Tc, kTree>(a, hp, both, s);
+  return launch_tiles_of<D, DR, 8, Tc, kTree>(a, hp, few, s);
 }
 
 }  // namespace

@@ -582,10 +582,11 @@ rel_status relation_tree_plan(const int32_t* parent, const int32_t* total,
  * scale times value is a normal bf16 number; a scale exponent of 0 reads as 0, and
  * 255, which is no scale, as 254); a row that is used may not hold NaN (they reach
  * other rows of its request, of a tree's other branches too). Weights enter the
- * transport as two bf16 terms, but for requests on query tiles, whose weights are
- * rounded to bf16 once (2^-8 of each) and summed so: of bf16 trees and of 8-bit pages,
- * in batches with much work (N H max_pages page_size), those of more than 64 rows (new
- * tokens times H / H_kv), and where max_new is at most 4 N / S all of them.
+ * transport as two bf16 terms, those of single tokens always, but for requests on
+ * query tiles, whose weights are rounded to bf16 once (2^-8 of each) and summed so: of
+ * bf16 trees and of 8-bit pages, in batches with much work (N H max_pages page_size),
+ * those of more than 64 rows (new tokens times H / H_kv), and where max_new is at most
+ * 4 N / S all of more than one token.
  * relation_select_kernels with REL_KERNEL_SCAN for the forward keeps them off the
  * tiles. A max_new close to the batch's own tells batches apart that the tiles speed up.
  */

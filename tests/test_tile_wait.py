@@ -12,7 +12,7 @@ UNIT = """
 #include "paged_tile.h"
 namespace rel {
 hipError_t unit(const PagedExArgs& a, const HeadParams& hp, hipStream_t s) {
-  return launch_tiles_of<64, 64, 4, __bf16, true>(a, hp, false, s);
+  return launch_tiles<64, 64, __bf16, true>(a, hp, false, s);
 }
 }
 """
