@@ -17,6 +17,7 @@ constexpr int kThreads = 64 * kWaves;
 // stay below n 2^8 max |V|. 2^32 overflowed for V from 2^96 on, where the outputs are
 // finite (decode_batch and decode_long 455 and 219 us at either).
 constexpr float kLazy = 8.0f;
+constexpr float kHeadroom = 0x1p8f;
 
 // A work-group barrier for LDS data alone: outstanding vector memory operations
 // (the next segment's loads) are not waited for.
@@ -57,7 +58,8 @@ __global__ __launch_bounds__(kThreads) void plan_kernel(PagedArgs a, int row_blo
 // 8-bit pages (Tc = e4m3): as the 16-bit ones, with the operands formed in registers:
 // v_cvt_scalef32_pk_bf16_fp8 gives two bf16 values, exact, times a power of two, which
 // for a P2 row is its scale; V's scales multiply the weights instead (a lane's V operand
-// has eight keys). An A operand of P2 is 8 consecutive bytes a lane, two to a 16-byte
+// has eight keys), over 2^8, which the values take: a weight may be 2^8 (kLazy) and a scale
+// 2^127. An A operand of P2 is 8 consecutive bytes a lane, two to a 16-byte
 // read where the row has whole groups of four chunks; V^T comes from ds_read_b64_tr_b8:
 // lane i of a group of 16 receives byte i % 8 of the 8-byte rows that lanes i / 8 + 2 k
 // address, k = 0 .. 7, so one read has all eight keys of the lane's column. The 32
@@ -270,7 +272,7 @@ __global__ __launch_bounds__(kThreads, (Geom<Tc, D, NB>::kPerCu)) void scan_kern
           ksc[hb] = scale_of(sc[li]);
           const unsigned x = *reinterpret_cast<const unsigned*>(sc + 16 + 4 * lj);
 #pragma unroll
-          for (int rr = 0; rr < 4; ++rr) vsc[hb][rr] = scale_of(x >> (8 * rr) & 255u);
+          for (int rr = 0; rr < 4; ++rr) vsc[hb][rr] = scale_of(x >> (8 * rr) & 255u) * (1.0f / kHeadroom);
         }
         const int k = li >> 1, q = 4 * lj + (k & 3);
         const char* const v = slot + (C::kHalves + (k >> 2)) * C::kHalf + q * D + 8 * (li & 1);
@@ -383,7 +385,7 @@ __global__ __launch_bounds__(kThreads, (Geom<Tc, D, NB>::kPerCu)) void scan_kern
       }
       if constexpr (kBf) {
         auto v_of = [&](int db) __attribute__((always_inline)) -> bf16x8 {
-          if constexpr (C::k8) return __builtin_bit_cast(bf16x8, e4m3_to_bf16(vb8[db], 1.0f));
+          if constexpr (C::k8) return __builtin_bit_cast(bf16x8, e4m3_to_bf16(vb8[db], kHeadroom));
           else return vb[db];
         };
         // The transport's operand: each weight as two bf16 terms, itself rounded and what that

@@ -484,13 +484,14 @@ size_t relation_paged_workspace_bytes(int N, int S, int H, int H_kv, int d_h);
  * Rows at or past total[b] may hold anything and are not used; a row that is
  * used may not hold NaN or infinities (they reach other rows of its request,
  * never another request's).
- * Numerics: evidence scaled in fp32, row sums and states in fp32; the same call
- * gives the same bits. In bf16 each weight enters the transport as two bf16
- * terms, at most 2^-16 of it off, so a single token is as exact as
- * relation_decode's (which has fp32 weights). Batches with much work put
- * requests with many rows on query tiles, with relation_fwd's weights: rounded to
- * bf16 once (2^-8 of each), and summed so. relation_select_kernels with
- * REL_KERNEL_SCAN for the forward keeps all rows off the tiles.
+ * Numerics: evidence scaled in fp32, row sums and states in fp32, right while
+ * n 2^8 max |V| is below 2^127 for a row that sees n; the same call gives the same
+ * bits. In bf16 each weight enters the transport as two bf16 terms, at most 2^-16
+ * of it off, so a single token is as exact as relation_decode's (which has fp32
+ * weights). Batches with much work put requests with many rows on query tiles,
+ * with relation_fwd's weights: rounded to bf16 once (2^-8 of each), and summed so.
+ * relation_select_kernels with REL_KERNEL_SCAN for the forward keeps all rows off
+ * the tiles.
  */
 rel_status relation_paged_fwd(const void* P1, int64_t ld1, const void* cache_P2,
                               const void* cache_V, const int32_t* block_table,
@@ -580,7 +581,8 @@ rel_status relation_tree_plan(const int32_t* parent, const int32_t* total,
  * this equals, bit for bit, for REL_F32 and REL_BF16 pages without a tree.
  * Numerics: as there, on the values that 8-bit rows stand for (exact in bf16 where
  * scale times value is a normal bf16 number; a scale exponent of 0 reads as 0, and
- * 255, which is no scale, as 254); a row that is used may not hold NaN (they reach
+ * 255, which is no scale, as 254; scales of V below 2^-100, the append's least, cost the
+ * weights of a scan bits); a row that is used may not hold NaN or infinities (they reach
  * other rows of its request, of a tree's other branches too). Weights enter the
  * transport as two bf16 terms, those of single tokens always, but for requests on
  * query tiles, whose weights are rounded to bf16 once (2^-8 of each) and summed so: of
