@@ -535,7 +535,8 @@ rel_status relation_paged_fwd(const void* P1, int64_t ld1, const void* cache_P2,
  *   cache_scale : out, as above; written for the rows that are
  *   theta       : host double[H_kv / 2]: an angle in fp32 is far enough from the one that
  *                 is meant to store the farther of two e4m3 neighbours now and then
- * Other arguments as in relation_paged_append.
+ * Other arguments as in relation_paged_append, but that no two tokens may have the same
+ * slot: its row may then hold one's values under the other's scale.
  */
 rel_status relation_paged_append_q8(const void* P1, const void* P2, const void* I,
                                     int64_t ld1, int64_t ld2, int64_t ldi,
