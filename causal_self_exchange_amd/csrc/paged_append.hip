@@ -254,36 +254,50 @@ __device__ __forceinline__ float2 split(double x) {
   return make_float2(hi, (float)(x - hi));
 }
 
-// turn for a row that is quantised, by split cosines and sines: each sum of exact products is
-// rounded once, and again with what the rests give, so that its error is a few steps of the
-// result also where a pair nearly cancels.
+// kTogether pairs u(e), v(e) of a row that is quantised turned by factors(e), a split cosine
+// and sine: each sum of exact products is rounded once, and again with what the rests give, so
+// that its error is a few steps of the result also where a pair nearly cancels.
+struct Factors { float2 c, n; };
+template <typename U, typename V, typename F>
+__device__ __forceinline__ void turn_together(U u, V v, F factors) {
+  float p[kTogether], q[kTogether];
+  bool near = false;
+#pragma unroll
+  for (int e = 0; e < kTogether; ++e) {
+    const auto [c, n] = factors(e);
+    p[e] = u(e);
+    q[e] = v(e);
+    u(e) = fmaf(c.x, p[e], -n.x * q[e]) + fmaf(c.y, p[e], -n.y * q[e]);
+    v(e) = fmaf(n.x, p[e], c.x * q[e]) + fmaf(n.y, p[e], c.y * q[e]);
+    near |= near_tie(u(e));
+    near |= near_tie(v(e));
+  }
+  if (near) {
+#pragma unroll
+    for (int e = 0; e < kTogether; ++e) {
+      const auto [c, n] = factors(e);
+      const double cd = (double)c.x + c.y, nd = (double)n.x + n.y;
+      u(e) = beside_tie(cd * p[e] - nd * q[e]);
+      v(e) = beside_tie(nd * p[e] + cd * q[e]);
+    }
+  }
+}
+
+// turn for a row that is quantised.
 template <int kRope>
 __device__ __forceinline__ void turn_q8(const float2* cs, const float2* sn, float (&x)[8], float (&y)[8]) {
 #pragma unroll
   for (int e0 = 0; e0 < 8; e0 += kTogether) {
-    float p[kTogether], q[kTogether];
-    bool near = false;
-#pragma unroll
-    for (int e = 0; e < kTogether; ++e) {
-      const int k = e0 + e;
-      float &u = kRope == 2 ? x[k] : (k < 4 ? x[2 * k] : y[2 * k - 8]), &v = kRope == 2 ? y[k] : (k < 4 ? x[2 * k + 1] : y[2 * k - 7]);
-      p[e] = u;
-      q[e] = v;
-      const float2 c = cs[k], n = sn[k];
-      u = fmaf(c.x, p[e], -n.x * q[e]) + fmaf(c.y, p[e], -n.y * q[e]);
-      v = fmaf(n.x, p[e], c.x * q[e]) + fmaf(n.y, p[e], c.y * q[e]);
-      near |= near_tie(u) | near_tie(v);
-    }
-    if (near) {
-#pragma unroll
-      for (int e = 0; e < kTogether; ++e) {
-        const int k = e0 + e;
-        float &u = kRope == 2 ? x[k] : (k < 4 ? x[2 * k] : y[2 * k - 8]), &v = kRope == 2 ? y[k] : (k < 4 ? x[2 * k + 1] : y[2 * k - 7]);
-        const double c = (double)cs[k].x + cs[k].y, n = (double)sn[k].x + sn[k].y;
-        u = beside_tie(c * p[e] - n * q[e]);
-        v = beside_tie(n * p[e] + c * q[e]);
-      }
-    }
+    turn_together(
+        [&](int e) __attribute__((always_inline)) -> float& {
+          const int k = e0 + e;
+          return kRope == 2 ? x[k] : (k < 4 ? x[2 * k] : y[2 * k - 8]);
+        },
+        [&](int e) __attribute__((always_inline)) -> float& {
+          const int k = e0 + e;
+          return kRope == 2 ? y[k] : (k < 4 ? x[2 * k + 1] : y[2 * k - 7]);
+        },
+        [&](int e) __attribute__((always_inline)) { return Factors{cs[e0 + e], sn[e0 + e]}; });
   }
 }
 
@@ -354,7 +368,7 @@ __global__ __launch_bounds__(kThreads) void paged_append_q8_kernel(PagedAppendAr
       if (a.mix) {
         const int ha = a.pairing == 0 ? 2 * k : 2 * k + 1, hb = (ha + 1) % a.H_kv;
         if (g < kGroups) {
-          const float c = pp.cos_theta[k], s = pp.sin_theta[k], cr = qp.cos_rest[k], sr = qp.sin_rest[k];
+          const Factors by{{pp.cos_theta[k], qp.cos_rest[k]}, {pp.sin_theta[k], qp.sin_rest[k]}};
 #pragma unroll
           for (int w = 0; w < 2; ++w) {
             load8(src + (size_t)ha * D + 8 * w, x[w]);
@@ -362,26 +376,9 @@ __global__ __launch_bounds__(kThreads) void paged_append_q8_kernel(PagedAppendAr
           }
 #pragma unroll
           for (int e0 = 0; e0 < 16; e0 += kTogether) {
-            float p[kTogether], q[kTogether];
-            bool near = false;
-#pragma unroll
-            for (int e = 0; e < kTogether; ++e) {
-              float &u = x[(e0 + e) >> 3][(e0 + e) & 7], &v = y[(e0 + e) >> 3][(e0 + e) & 7];
-              p[e] = u;
-              q[e] = v;
-              // As in turn_q8.
-              u = fmaf(c, p[e], -s * q[e]) + fmaf(cr, p[e], -sr * q[e]);
-              v = fmaf(s, p[e], c * q[e]) + fmaf(sr, p[e], cr * q[e]);
-              near |= near_tie(u) | near_tie(v);
-            }
-            if (near) {
-              const double cd = (double)c + cr, sd = (double)s + sr;
-#pragma unroll
-              for (int e = 0; e < kTogether; ++e) {
-                x[(e0 + e) >> 3][(e0 + e) & 7] = beside_tie(cd * p[e] - sd * q[e]);
-                y[(e0 + e) >> 3][(e0 + e) & 7] = beside_tie(sd * p[e] + cd * q[e]);
-              }
-            }
+            turn_together([&](int e) __attribute__((always_inline)) -> float& { return x[(e0 + e) >> 3][(e0 + e) & 7]; },
+                          [&](int e) __attribute__((always_inline)) -> float& { return y[(e0 + e) >> 3][(e0 + e) & 7]; },
+                          [&](int) __attribute__((always_inline)) { return by; });
           }
         }
         store_row(1, ha, g, 16 * g, 16 * g + 8, x[0], x[1]);
