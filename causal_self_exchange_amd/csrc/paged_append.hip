@@ -161,12 +161,13 @@ __global__ __launch_bounds__(kThreads) void paged_append_kernel(PagedAppendArgs 
 // elements each), so that its maximum is a few exchanges between lanes.
 //
 // The row is rounded once, from the fp32 of its rotation or mixing, as above but for the
-// cosines and sines, which are fp64 ones in two parts (the mixing's from fp64 angles). A value that is near the middle between two steps then (one in
-// 60,000) is formed again in fp64, so that the nearest is stored. All rotations and mixings in
-// fp64 took 16,384 tokens of 32 + 8 heads of 128 from 75 to 105 us.
+// cosines and sines, which are fp64 ones in two parts (the mixing's from fp64 angles). A value
+// of 2^-6 2^k and more that is near the middle between two steps then (one in 60,000) is formed
+// again in fp64, so that the nearest is stored. All rotations and mixings in fp64 took 16,384
+// tokens of 32 + 8 heads of 128 from 75 to 105 us.
 //
-// Bound by memory: those tokens read 201 MB and write 168 MB in 85 us, 4.3 TB/s (a copy of
-// 4 GB 4.7; without the values formed again 77 us); 64 tokens of 32 + 32 heads take 7.5 us.
+// Bound by memory: those tokens read 201 MB and write 168 MB in 83 to 85 us, 4.4 TB/s (a copy
+// of 4 GB 4.7; without the values formed again 77 us); 64 tokens of 32 + 32 heads take 7.5 us.
 constexpr int kLowScale = -100, kHighScale = 119;
 constexpr float kMostE4m3 = 448.0f;
 

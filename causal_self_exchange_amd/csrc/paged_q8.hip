@@ -5,7 +5,7 @@
 // The scan is bound by memory: 64 tokens over 1,024 to 4,096 rows of 32 heads of 128 (1.35
 // GB) take 248 us, 5.4 TB/s, of 16-bit pages 451; one token over 300 rows of 8 heads of 64
 // takes 10 us, the latency of its dependent loads. Six chunks of 100 to 1,500 tokens over up
-// to 6,000 rows of 32 heads of 128 in 8 take 687 us by the scan and 300 to 318 on tiles.
+// to 6,000 rows of 32 heads of 128 in 8 take 680 us by the scan and 295 to 330 on tiles.
 #include "paged_scan.h"
 #include "paged_tile.h"
 

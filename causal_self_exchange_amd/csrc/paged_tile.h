@@ -19,9 +19,10 @@
 //
 // Bound by the loop's issue: a wave's tile is 36 products (1,090 cycles of the matrix unit),
 // 96 transcendentals and about 290 other instructions; a compute unit's takes 4,450 cycles
-// where the products alone would take 2,180 (with one wave to a SIMD 3,240, of 1,090). Two
-// chunks of 4,000 tokens of 32 heads of 128 in 4, over up to 4,000 8-bit rows, take 540 us,
-// 0.84 PFLOP/s (a large bf16 product by the library 1.32).
+// where the products alone would take 2,180 (with one wave to a SIMD 3,240, of 1,090). Those
+// six chunks, over up to 6,000 8-bit rows, take 295 to 330 us, 0.65 to 0.73 PFLOP/s; two of
+// 4,000 of 32 heads in 4, whose segments are longer, 550 us, 0.82 (a large bf16 product by the
+// library 1.32). A segment costs about eight tiles beside its keys (kTileExtra).
 //
 // The keys of all row blocks are cut into equal ranges as in the scan (paged_device.h);
 // here a row block counts its own keys, so early blocks of a prompt take less of a range
@@ -683,9 +684,9 @@ __global__ __launch_bounds__(64 * W, 2) void tile_kernel(ScanArgs<__bf16, Tc, kT
 
     // The offset 0 is exact where nothing overflows: SiLU >= -0.2785, so no weight is small.
     // Row sums up to 2^100 and, in parts, results of which all together reach 2^127 (2^119 of
-    // eight waves, 2^118 of four) pass; else the segment is scanned again with a stabiliser that follows the scores. The
-    // maximum keeps a NaN (products of both signs past the range leave nothing else), which
-    // is below no limit.
+    // eight waves, 2^118 of four) pass; else the segment is scanned again with a stabiliser
+    // that follows the scores. The maximum keeps a NaN (products of both signs past the range
+    // leave nothing else), which is below no limit.
     float omax = 0.0f;
 #pragma unroll
     for (int db = 0; db < L::kDb; ++db)
@@ -862,9 +863,9 @@ __global__ __launch_bounds__(kThreads) void tile_join_kernel(ScanArgs<__bf16, Tc
 // Where a batch's requests go, by what the host knows: kToScan, kToTiles (but for those of one
 // new token), or kToBoth (those of up to kTileRowsLeast rows to a cached head to the scan).
 //   Single tokens are the scan's in any batch, so that their weights have two terms whatever
-//   the other requests are. Where there are none the scan's launch takes 2 to 4 us: 48 trees of
-//   2 to 24 tokens, as below, 87 us without it and 89 with it, 65 of 60 over none 35 and 38.5,
-//   64 of 1 to 30 tokens of 32 heads of 64 in 8, some of them single, 117 and 130.
+//   the other requests are. Where there are none the scan's launch adds 2 to 4 us to a call:
+//   48 trees of 2 to 24 tokens, as below, 87 us without it and 89 with it, 65 of 60 over none
+//   35 and 38.5, 64 of 1 to 30 of 32 heads of 64 in 8, some of them single, 117 and 130.
 //   Two row blocks of the scan, 64 rows, are faster than a tile: 32 requests of 64 rows over
 //   4,000 8-bit rows of 8 heads of 128 120 us by the scan, 153 on tiles; of 96 rows 172 and
 //   159, of 256 387 and 230.
@@ -876,11 +877,12 @@ __global__ __launch_bounds__(kThreads) void tile_join_kernel(ScanArgs<__bf16, Tc
 //   tables' width, not the lengths: short requests in wide tables lose up to 10 us.
 //   Where the requests have like numbers of tokens (kTileLike: the average is a quarter of the
 //   most), tiles for all are fastest, scan, both and tiles: 48 trees of 2 to 24 tokens of 16
-//   heads of 64 in 4 110, 98 and 85 us, 64 of 1 to 60 of 32 of 128 in 8 315, 232 and 220.
+//   heads of 64 in 4 110, 98 and 89 us.
 //   Where few have many, tiles of few rows are slow, and those few alone are worth launches
 //   of their own from some 500 rows on. 62 tokens over 1,024 to 4,096 rows beside two chunks
 //   of 512, 32 heads of 128: 387, 357 and 707 us, in 8 cached heads 190, 177 and 216; 60
-//   beside four of 60, 16 heads in 4: 65, 88 and 98.
+//   beside four of 60, 16 heads in 4: 65, 88 and 98. (The tiles' figures of ragged batches are
+//   of single tokens on tiles.)
 // And the workspace has to have the chunks' part.
 constexpr int kTileRowsLeast = 64;
 constexpr int kTileRowsBeside = 512;

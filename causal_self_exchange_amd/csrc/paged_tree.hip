@@ -3,8 +3,8 @@
 // per token, or for bf16 batches with many rows and much work (tile_use) the query tiles
 // of paged_tile.h. Only the steps that hold new tokens look at the bits.
 //
-// 48 trees of 2 to 24 tokens over 200 to 9,000 rows of 16 heads of 64 in 4 take 106 us by
-// the scan and 85 on tiles (their reads 38); six of 5 to 40 tokens over up to 2,000 fp32 rows
+// 48 trees of 2 to 24 tokens over 200 to 9,000 rows of 16 heads of 64 in 4 take 110 us by
+// the scan and 89 on tiles (their reads 38); six of 5 to 40 tokens over up to 2,000 fp32 rows
 // of 8 heads of 48 in 2 take 19 us and 5 for the join, by the latency of a few steps.
 #include "paged_scan.h"
 #include "paged_tile.h"
